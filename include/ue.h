@@ -32,7 +32,9 @@
  *  - A context is not thread-safe: one host thread at a time. Its routing
  *    calls (ue_load, ue_plan, ue_reroute, ue_rebalance) use the context's
  *    workspace and must not overlap one another in time on different
- *    streams. ue_weight_sync, ue_grad_reduce and ue_gather_rows use no
+ *    streams, nor ue_moe_tokens (whose workspace is its own) itself.
+ *    ue_weight_sync, ue_grad_reduce, ue_gather_rows, ue_gate,
+ *    ue_gate_backward, ue_quantize_rows and ue_matmul_i8 use no
  *    workspace and may run on another stream beside them (the next layer's
  *    rebalance beside this layer's sync), while kernel timing is off and
  *    the registered tables are not replaced meanwhile.
@@ -387,6 +389,148 @@ int ue_grad_reduce(ue_ctx *ctx, const int32_t *rep_off, const int32_t *rep_buf,
  * Positions outside [0, T*k) are skipped. */
 int ue_gather_rows(ue_ctx *ctx, const void *x, const int32_t *inv_perm,
                    int32_t T, int32_t k, int32_t H, void *out, void *stream);
+
+/* ---------------------------------------------------------------------
+ * The expert layer around a rebalance: the router's choice, which makes the
+ * routing the calls above take; products of 8-bit integers over the rows of
+ * a dispatch; and the whole layer for a few tokens, where a rebalance does
+ * not pay. Rows of a matrix argument are `ld` elements apart and contiguous
+ * inside. */
+enum {
+    UE_F32 = 0,
+    UE_BF16 = 1,
+    UE_I8 = 2
+};
+
+enum {
+    UE_SCORE_SOFTMAX = 0,      /* p = softmax(logits); ranked by the logit   */
+    UE_SCORE_SIGMOID = 1       /* p = 1/(1+exp(-logit)); ranked by p + bias  */
+};
+
+/* Expert choice from router logits (E and k are the context's). Per token:
+ *   ids      the k experts with the highest rank, best first, equal ranks
+ *            lowest id first; an expert whose logit is -inf or NaN (or
+ *            whose p + bias is) is never taken, and where fewer than k are
+ *            left the remaining ids are -1 (ue_load counts such ids as
+ *            invalid) and their weights 0
+ *   weights  scale * p_j, or with renorm scale * p_j / sum over the chosen
+ *            (sigmoid: that sum plus 1e-20)
+ * A logit of +inf counts as the largest float in the softmax. A NaN among a
+ * token's logits makes that token's weights NaN.
+ *   logits   device, [T] rows of E, UE_F32 or UE_BF16, ld apart (ld >= E)
+ *   bias     device, fp32 [E], added to the sigmoid's p for the ranking only;
+ *            may be NULL; must be NULL with the softmax
+ *   ids      device, int32 [T, k] out: a layer's routing for ue_load
+ *   weights  device, fp32 [T, k] out
+ * T in 0..max_tokens. Scores and sums are fp32. Errors: UE_EINVAL, UE_ESHAPE. */
+int ue_gate(ue_ctx *ctx, const void *logits, int32_t type, int64_t ld,
+            int32_t T, int32_t score, int32_t renorm, float scale,
+            const float *bias, int32_t *ids, float *weights, void *stream);
+
+/* Gradient of the logits from the gradient of ue_gate's weights, at the
+ * choice `ids` (not differentiated; ids outside [0, E) take no part, and a
+ * token's ids must be distinct). Every element of dlogits is written: 0
+ * where nothing flows (an expert not chosen, except for the softmax without
+ * renorm, whose denominator holds every logit).
+ *   dweights  device, fp32 [T, k]
+ *   dlogits   device, out, [T] rows of E of the logits' type, ld_out apart */
+int ue_gate_backward(ue_ctx *ctx, const void *logits, int32_t type, int64_t ld,
+                     int32_t T, int32_t score, int32_t renorm, float scale,
+                     const int32_t *ids, const float *dweights, void *dlogits,
+                     int64_t ld_out, void *stream);
+
+/* Rows as 8-bit integers: with top = max |x| of a row, q = rint(x * (127 /
+ * top)) (to even) and scale = top / 127; a row of zeros (or one so small
+ * that 127 / top overflows) has q = 0 and scale 0. A row that holds an infinity or a NaN has q = 0 and scale NaN, so that its
+ * products are NaN.
+ *   x      device, [M] rows of K, UE_F32 or UE_BF16, ldx apart
+ *   q      device, int8, out, 16-byte aligned rows ldq apart (ldq a multiple
+ *          of 16, at least K rounded up to 16; bytes K .. that are set to 0)
+ *   scale  device, fp32 [M] out
+ * K in 1..65536. */
+int ue_quantize_rows(ue_ctx *ctx, const void *x, int32_t type, int64_t ldx,
+                     int32_t M, int32_t K, int8_t *q, int64_t ldq,
+                     float *scale, void *stream);
+
+/* Product of 8-bit integers with a scale per row and per channel:
+ *   out[m, n] = a_scale[r] * w_scale[e, n] * sum_k a[r, k] * w[e, n, k]
+ * The sums are exact. Row m uses row r of a: m, or with `index` row
+ * index[m] / index_div (a dispatch permutation and its top-k: the gather of
+ * tokens into dispatch order happens inside; an entry outside a's rows gives
+ * a row of zeros). Rows are grouped by `offsets` (a placement block's
+ * slot_off, or any prefix sums): rows offsets[g] .. offsets[g+1]-1 use matrix
+ * e = expert_of[g] (slot_expert), or g without it; rows of a group whose e is
+ * outside [0, n_mats), and rows no group holds, are left as they are. Groups
+ * may be empty or of any length; entries are clamped to 0..M, and should not
+ * decrease (rows two groups claim are undefined). Without offsets all
+ * rows use matrix 0. With `gated`, w has 2 N channels, gate then up, and
+ *   out[m, n] = silu(gate) * up,  silu(v) = v / (1 + exp(-v)).
+ *   a        device, int8, 16-byte aligned rows, lda a multiple of 16
+ *   w        device, int8, likewise; matrices w_stride apart (multiple of 16)
+ *   w_scale  device, fp32, matrices ws_stride apart
+ * For a and w the bytes of a row up to K rounded up to 16 must be readable.
+ * out is UE_BF16 or UE_F32, ldo >= N. K in 1..65536; rows of out times
+ * channels are limited by a launch of 2^31 workgroups (UE_ESHAPE). */
+typedef struct ue_i8_product {
+    const int8_t *a;
+    const float *a_scale;
+    const int8_t *w;
+    const float *w_scale;
+    const int32_t *offsets;     /* int32 [groups + 1] or NULL */
+    const int32_t *expert_of;   /* int32 [groups] or NULL     */
+    const int32_t *index;       /* int32 [M] or NULL          */
+    void *out;
+    int64_t lda, ldw, w_stride, ws_stride, ldo;
+    int32_t a_rows, n_mats, groups, index_div;
+    int32_t M, N, K;
+    int32_t gated, out_type;
+} ue_i8_product;
+
+int ue_matmul_i8(ue_ctx *ctx, const ue_i8_product *p, void *stream);
+
+/* The layer of ue_moe_tokens: the context's E experts with their router.
+ *   router     device, bf16 [E, hidden]
+ *   gate_up    device, [E] matrices [2 inter, hidden] (gate rows, then up
+ *              rows), gate_up_stride elements apart
+ *   down       device, [E] matrices [hidden, inter], down_stride apart
+ *   weight_type  UE_BF16, or UE_I8 with gate_up_scale fp32 [E, 2 inter] and
+ *              down_scale fp32 [E, hidden] (the weights of ue_matmul_i8)
+ *   bias, score, renorm, scale   as in ue_gate
+ * All matrices 16-byte aligned; hidden and inter multiples of 8 (bf16) or 16
+ * (int8), strides likewise. The memory stays the caller's; the context keeps
+ * the pointers until the next registration or ue_destroy, and allocates a
+ * workspace for min(max_tokens, UE_MOE_MAX_TOKENS) tokens. */
+#define UE_MOE_MAX_TOKENS 64
+typedef struct ue_layer {
+    const void *router;
+    const float *bias;
+    const void *gate_up, *down;
+    const float *gate_up_scale, *down_scale;
+    int64_t gate_up_stride, down_stride;
+    int32_t hidden, inter, weight_type;
+    int32_t score, renorm;
+    float scale;
+} ue_layer;
+
+int ue_register_layer(ue_ctx *ctx, const ue_layer *layer);
+
+/* A mixture-of-experts layer for a few tokens (the decode step of a served
+ * model), from the registered layer:
+ *   logits = x router^T;  (ids, weights) = ue_gate(logits)
+ *   out_t = sum_j weights_tj (silu(x_t G^T) * (x_t U^T)) D^T
+ * over the matrices of expert ids_tj; ids of -1 add nothing. Sums are fp32,
+ * also between the products; out is rounded once. The result does not depend
+ * on timing (no atomics on values).
+ *   x        device, bf16 [T] rows of hidden, 16-byte aligned, ldx apart
+ *            (a multiple of 8)
+ *   out      device, bf16, ldo apart
+ *   ids      device, int32 [T, k] out: the routing, as ue_load takes it
+ *   weights  device, fp32 [T, k] out
+ * T in 0..min(max_tokens, UE_MOE_MAX_TOKENS). UE_ESTATE without a registered
+ * layer. Uses the context's workspace. */
+int ue_moe_tokens(ue_ctx *ctx, const void *x, int64_t ldx, int32_t T,
+                  void *out, int64_t ldo, int32_t *ids, float *weights,
+                  void *stream);
 
 #ifdef __cplusplus
 }

@@ -59,6 +59,31 @@ class ue_placement_layout(ctypes.Structure):
 
 # Every symbol the header declares, with its ctypes signature.
 _vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+_f32 = ctypes.c_float
+
+F32, BF16, I8 = 0, 1, 2
+_TYPES = {torch.float32: F32, torch.bfloat16: BF16}
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+class ue_i8_product(ctypes.Structure):
+    _fields_ = ([(f, _vp) for f in ("a", "a_scale", "w", "w_scale", "offsets",
+                                    "expert_of", "index", "out")] +
+                [(f, _i64) for f in ("lda", "ldw", "w_stride", "ws_stride",
+                                     "ldo")] +
+                [(f, _i32) for f in ("a_rows", "n_mats", "groups", "index_div",
+                                     "M", "N", "K", "gated", "out_type")])
+
+
+class ue_layer(ctypes.Structure):
+    _fields_ = ([(f, _vp) for f in ("router", "bias", "gate_up", "down",
+                                    "gate_up_scale", "down_scale")] +
+                [(f, _i64) for f in ("gate_up_stride", "down_stride")] +
+                [(f, _i32) for f in ("hidden", "inter", "weight_type",
+                                     "score", "renorm")] +
+                [("scale", _f32)])
+
+
 SIGNATURES = {
     "ue_create": (ctypes.c_int, [ctypes.POINTER(ue_config),
                                  ctypes.POINTER(_vp)]),
@@ -89,6 +114,17 @@ SIGNATURES = {
                                       _vp]),
     "ue_stale_loads": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _vp]),
     "ue_set_wait_limit": (ctypes.c_int, [_vp, ctypes.c_uint32]),
+    "ue_gate": (ctypes.c_int, [_vp, _vp, _i32, _i64, _i32, _i32, _i32, _f32,
+                               _vp, _vp, _vp, _vp]),
+    "ue_gate_backward": (ctypes.c_int, [_vp, _vp, _i32, _i64, _i32, _i32,
+                                        _i32, _f32, _vp, _vp, _vp, _i64,
+                                        _vp]),
+    "ue_quantize_rows": (ctypes.c_int, [_vp, _vp, _i32, _i64, _i32, _i32, _vp,
+                                        _i64, _vp, _vp]),
+    "ue_matmul_i8": (ctypes.c_int, [_vp, ctypes.POINTER(ue_i8_product), _vp]),
+    "ue_register_layer": (ctypes.c_int, [_vp, ctypes.POINTER(ue_layer)]),
+    "ue_moe_tokens": (ctypes.c_int, [_vp, _vp, _i64, _i32, _vp, _i64, _vp,
+                                     _vp, _vp]),
     "ue_rebalance_static": (ctypes.c_int, [ctypes.POINTER(ue_config), _vp,
                                            _i32, _i32, _vp, _vp, _vp, _vp,
                                            _vp, _vp, _vp, _vp, _vp]),
@@ -227,6 +263,24 @@ class Context:
 
     def gather_rows(self, x, inv_perm, out=None, stream=None):
         return ue_gather_rows(self, x, inv_perm, out, stream)
+
+    def gate(self, logits, **kw):
+        return ue_gate(self, logits, **kw)
+
+    def gate_backward(self, logits, ids, dweights, **kw):
+        return ue_gate_backward(self, logits, ids, dweights, **kw)
+
+    def quantize_rows(self, x, **kw):
+        return ue_quantize_rows(self, x, **kw)
+
+    def matmul_i8(self, a, a_scale, w, w_scale, **kw):
+        return ue_matmul_i8(self, a, a_scale, w, w_scale, **kw)
+
+    def register_layer(self, router, gate_up, down, *scales, **kw):
+        return ue_register_layer(self, router, gate_up, down, *scales, **kw)
+
+    def moe_tokens(self, x, **kw):
+        return ue_moe_tokens(self, x, **kw)
 
 
 def ue_create(num_experts, num_ranks, spare_per_rank, topk, max_tokens,
@@ -536,3 +590,267 @@ def ue_gather_rows(ctx: Context, x, inv_perm, out=None, stream=None):
                                   H, _ptr(out), _stream(stream, ctx.device))
     ctx._check(rc, "ue_gather_rows")
     return out
+
+
+# ---- the expert layer around a rebalance ----------------------------------
+
+def _rows(t, name, device, types, cols=None):
+    """A matrix [rows, cols] whose rows are contiguous; returns the distance
+    between rows in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype not in types:
+        raise TypeError(f"{name} must be one of {list(types)}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must be [rows, {cols or 'cols'}], is "
+                         f"{tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if t.shape[0] <= 1:
+        # a single row has no distance to the next: any that is long enough
+        return max(t.stride(0), (t.shape[1] + 15) // 16 * 16)
+    return t.stride(0)
+
+
+def _new(shape, dtype, ctx, stream):
+    """An output tensor whose memory belongs to the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=ctx.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=ctx.device)
+
+
+def _use(stream, *tensors):
+    """Keeps tensors of another stream from being reused under this call."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _score(score):
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {list(SCORES)}, got {score!r}")
+    return SCORES[score]
+
+
+def ue_gate(ctx: Context, logits, bias=None, score="softmax", renorm=True,
+            scale=1.0, ids=None, weights=None, stream=None):
+    """Expert choice from router logits [T, E] (fp32 or bf16, rows may be
+    apart): ids int32 [T, k], best first, and weights fp32 [T, k]. ``ids`` is
+    a layer's routing for :func:`ue_load` and :func:`ue_rebalance`."""
+    ld = _rows(logits, "logits", ctx.device, _TYPES, ctx.E)
+    T = logits.shape[0]
+    if bias is not None:
+        _need(bias, "bias", torch.float32, ctx.device, ctx.E)
+    if ids is None:
+        ids = _new((T, ctx.k), torch.int32, ctx, stream)
+    else:
+        _need(ids, "ids", torch.int32, ctx.device, T * ctx.k)
+    if weights is None:
+        weights = _new((T, ctx.k), torch.float32, ctx, stream)
+    else:
+        _need(weights, "weights", torch.float32, ctx.device, T * ctx.k)
+    _use(stream, logits, bias, ids, weights)
+    rc = library().ue_gate(ctx._h, _ptr(logits), _TYPES[logits.dtype], ld, T,
+                           _score(score), bool(renorm), scale, _ptr(bias),
+                           _ptr(ids), _ptr(weights),
+                           _stream(stream, ctx.device))
+    ctx._check(rc, "ue_gate")
+    return ids, weights
+
+
+def ue_gate_backward(ctx: Context, logits, ids, dweights, score="softmax",
+                     renorm=True, scale=1.0, dlogits=None, stream=None):
+    """Gradient of the logits [T, E] (their type) from the gradient of
+    :func:`ue_gate`'s weights, at the same choice and settings."""
+    ld = _rows(logits, "logits", ctx.device, _TYPES, ctx.E)
+    T = logits.shape[0]
+    _need(ids, "ids", torch.int32, ctx.device, T * ctx.k)
+    _need(dweights, "dweights", torch.float32, ctx.device, T * ctx.k)
+    if dlogits is None:
+        dlogits = _new((T, ctx.E), logits.dtype, ctx, stream)
+    ldo = _rows(dlogits, "dlogits", ctx.device, (logits.dtype,), ctx.E)
+    if dlogits.shape[0] != T:
+        raise ValueError(f"dlogits must have {T} rows")
+    _use(stream, logits, ids, dweights, dlogits)
+    rc = library().ue_gate_backward(
+        ctx._h, _ptr(logits), _TYPES[logits.dtype], ld, T, _score(score),
+        bool(renorm), scale, _ptr(ids), _ptr(dweights), _ptr(dlogits), ldo,
+        _stream(stream, ctx.device))
+    ctx._check(rc, "ue_gate_backward")
+    return dlogits
+
+
+def ue_quantize_rows(ctx: Context, x, q=None, scale=None, stream=None):
+    """Rows of x [M, K] (fp32 or bf16) as int8 [M, K] and scales fp32 [M]. The
+    int8 rows are 16-byte aligned (a view of rows padded to a multiple of 16,
+    the padding zero)."""
+    ldx = _rows(x, "x", ctx.device, _TYPES)
+    M, K = x.shape
+    if q is None:
+        q = _new((M, (K + 15) // 16 * 16), torch.int8, ctx, stream)[:, :K]
+    ldq = _i8_rows(q, "q", ctx.device, K)
+    if q.shape[0] != M:
+        raise ValueError(f"q must have {M} rows")
+    if scale is None:
+        scale = _new((M,), torch.float32, ctx, stream)
+    else:
+        _need(scale, "scale", torch.float32, ctx.device, M)
+    _use(stream, x, q, scale)
+    rc = library().ue_quantize_rows(ctx._h, _ptr(x), _TYPES[x.dtype], ldx, M,
+                                    K, _ptr(q), ldq, _ptr(scale),
+                                    _stream(stream, ctx.device))
+    ctx._check(rc, "ue_quantize_rows")
+    return q, scale
+
+
+def _i8_rows(t, name, device, cols=None):
+    """Distance between int8 rows, whose storage must reach the end of the
+    last row's last 16-byte piece."""
+    ld = _rows(t, name, device, (torch.int8,), cols)
+    _i8_reach(t, name, (t.shape[0] - 1) * ld if t.shape[0] else 0, t.shape[1])
+    return ld
+
+
+def _i8_reach(t, name, last_row, cols):
+    end = t.storage_offset() + last_row + (cols + 15) // 16 * 16
+    if t.numel() and end > t.untyped_storage().nbytes():
+        raise ValueError(f"{name}: the last row must be readable up to a "
+                         "multiple of 16 bytes")
+
+
+def ue_matmul_i8(ctx: Context, a, a_scale, w, w_scale, offsets=None,
+                 expert_of=None, index=None, index_div=1, gated=False,
+                 out=None, out_dtype=torch.bfloat16, stream=None):
+    """Product of int8 rows a [rows, K] (scales [rows]) with int8 matrices w
+    [N, K] or [experts, N, K] (scales [..., N]); see ``ue_matmul_i8`` in ue.h
+    for the row groups (``offsets``, ``expert_of``), the row index and the
+    gated form (w with 2 N channels). Rows that no group holds are left as
+    they are in ``out``."""
+    dev = ctx.device
+    lda = _i8_rows(a, "a", dev)
+    rows, K = a.shape
+    _need(a_scale, "a_scale", torch.float32, dev, rows)
+    w3 = w if w.dim() == 3 else w.unsqueeze(0)
+    if w3.dim() != 3 or w3.dtype != torch.int8 or w3.device != dev:
+        raise TypeError(f"w must be int8 [N, {K}] or [experts, N, {K}] on {dev}")
+    n_mats, channels = w3.shape[0], w3.shape[1]
+    if n_mats < 1 or w3.shape[2] != K:
+        raise ValueError(f"w must be [N, {K}] or [experts, N, {K}], is "
+                         f"{tuple(w.shape)}")
+    ldw = _rows(w3[0], "w", dev, (torch.int8,), K)
+    w_stride = w3.stride(0) if n_mats > 1 else 0
+    _i8_reach(w3, "w", (n_mats - 1) * w_stride + max(channels - 1, 0) * ldw, K)
+    _need(w_scale, "w_scale", torch.float32, dev, n_mats * channels)
+    if gated and channels % 2:
+        raise ValueError("gated: w needs as many up as gate channels")
+    N = channels // 2 if gated else channels
+    groups = 0
+    if offsets is not None:
+        _need(offsets, "offsets", torch.int32, dev)
+        groups = offsets.numel() - 1
+        if groups < 0:
+            raise ValueError("offsets must hold groups + 1 entries")
+        if expert_of is not None:
+            _need(expert_of, "expert_of", torch.int32, dev, groups)
+    elif expert_of is not None:
+        raise ValueError("expert_of needs offsets")
+    if index is not None:
+        _need(index, "index", torch.int32, dev)
+        M = index.numel()
+    else:
+        M = rows
+    if out is None:
+        out = _new((M, N), out_dtype, ctx, stream)
+    ldo = _rows(out, "out", dev, _TYPES, N)
+    if out.shape[0] != M:
+        raise ValueError(f"out must have {M} rows")
+    _use(stream, a, a_scale, w, w_scale, offsets, expert_of, index, out)
+    p = ue_i8_product(_ptr(a), _ptr(a_scale), _ptr(w3), _ptr(w_scale),
+                      _ptr(offsets), _ptr(expert_of), _ptr(index), _ptr(out),
+                      lda, ldw, w_stride, channels, ldo, rows, n_mats, groups,
+                      int(index_div), M, N, K, bool(gated),
+                      _TYPES[out.dtype])
+    rc = library().ue_matmul_i8(ctx._h, ctypes.byref(p),
+                                _stream(stream, dev))
+    ctx._check(rc, "ue_matmul_i8")
+    return out
+
+
+def ue_register_layer(ctx: Context, router, gate_up, down, gate_up_scale=None,
+                      down_scale=None, bias=None, score="softmax",
+                      renorm=True, scale=1.0):
+    """Registers the layer :func:`ue_moe_tokens` runs: router bf16 [E, H],
+    gate_up [E, 2 I, H] (gate rows, then up rows) and down [E, H, I], both
+    bf16 or both int8 with channel scales [E, 2 I] and [E, H]. The experts'
+    matrices may lie apart (strided in their first dimension)."""
+    dev = ctx.device
+    _need(router, "router", torch.bfloat16, dev)
+    if router.dim() != 2 or router.shape[0] != ctx.E:
+        raise ValueError(f"router must be [{ctx.E}, H]")
+    H = router.shape[1]
+    if gate_up.dtype not in (torch.bfloat16, torch.int8) or \
+            down.dtype != gate_up.dtype:
+        raise TypeError("gate_up and down must both be bf16 or both int8")
+    I = down.shape[-1]
+    for t, name, shape in ((gate_up, "gate_up", (ctx.E, 2 * I, H)),
+                           (down, "down", (ctx.E, H, I))):
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {shape}, is {tuple(t.shape)}")
+        if not t[0].is_contiguous():
+            raise ValueError(f"{name}'s matrices must be contiguous")
+    i8 = gate_up.dtype == torch.int8
+    if i8:
+        _need(gate_up_scale, "gate_up_scale", torch.float32, dev, ctx.E * 2 * I)
+        _need(down_scale, "down_scale", torch.float32, dev, ctx.E * H)
+    elif gate_up_scale is not None or down_scale is not None:
+        raise ValueError("scales belong to int8 weights")
+    if bias is not None:
+        _need(bias, "bias", torch.float32, dev, ctx.E)
+
+    def apart(t):
+        return t.stride(0) if ctx.E > 1 else t[0].numel()
+
+    layer = ue_layer(_ptr(router), _ptr(bias), _ptr(gate_up), _ptr(down),
+                     _ptr(gate_up_scale), _ptr(down_scale), apart(gate_up),
+                     apart(down), H, I, I8 if i8 else BF16, _score(score),
+                     bool(renorm), scale)
+    with torch.cuda.device(dev):
+        rc = library().ue_register_layer(ctx._h, ctypes.byref(layer))
+    ctx._check(rc, "ue_register_layer")
+    # keep the tensors alive while the library holds their pointers
+    ctx._layer = (router, gate_up, down, gate_up_scale, down_scale, bias)
+    ctx.hidden = H
+
+
+def ue_moe_tokens(ctx: Context, x, out=None, ids=None, weights=None,
+                  stream=None):
+    """The registered layer for x bf16 [T, H], T up to 64: returns (out bf16
+    [T, H], ids int32 [T, k], weights fp32 [T, k])."""
+    H = getattr(ctx, "hidden", None)
+    ldx = _rows(x, "x", ctx.device, (torch.bfloat16,), H)
+    T = x.shape[0]
+    if out is None:
+        out = _new((T, x.shape[1]), torch.bfloat16, ctx, stream)
+    ldo = _rows(out, "out", ctx.device, (torch.bfloat16,), x.shape[1])
+    if out.shape[0] != T:
+        raise ValueError(f"out must have {T} rows")
+    if ids is None:
+        ids = _new((T, ctx.k), torch.int32, ctx, stream)
+    else:
+        _need(ids, "ids", torch.int32, ctx.device, T * ctx.k)
+    if weights is None:
+        weights = _new((T, ctx.k), torch.float32, ctx, stream)
+    else:
+        _need(weights, "weights", torch.float32, ctx.device, T * ctx.k)
+    _use(stream, x, out, ids, weights)
+    rc = library().ue_moe_tokens(ctx._h, _ptr(x), ldx, T, _ptr(out), ldo,
+                                 _ptr(ids), _ptr(weights),
+                                 _stream(stream, ctx.device))
+    ctx._check(rc, "ue_moe_tokens")
+    return out, ids, weights

@@ -12,10 +12,7 @@
 
 #include "ue_internal.h"
 
-namespace {
-
-int fail(ue_ctx *c, int code, const char *fmt, ...)
-    __attribute__((format(printf, 3, 4)));
+namespace ue {
 
 int fail(ue_ctx *c, int code, const char *fmt, ...) {
     if (c) {
@@ -33,19 +30,12 @@ int hip_fail(ue_ctx *c, hipError_t e, const char *what) {
     return fail(c, UE_EHIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-int bits_for(int n) {   // smallest b with (1 << b) >= n
-    int b = 0;
-    while ((1 << b) < n) ++b;
-    return b;
-}
-
 bool aligned(const void *p, size_t a) {
     return (reinterpret_cast<uintptr_t>(p) % a) == 0;
 }
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
-// Kernel timing: tbegin() before a call's first launch, tmark() after each.
 void tbegin(ue_ctx *c, hipStream_t s) {
     if (!c->timing) return;
     c->n_ev = 0;
@@ -54,6 +44,23 @@ void tbegin(ue_ctx *c, hipStream_t s) {
 void tmark(ue_ctx *c, hipStream_t s) {
     if (!c->timing || c->n_ev == 0 || c->n_ev >= ue_ctx::kMaxEvents) return;
     if (hipEventRecord(c->ev[c->n_ev], s) == hipSuccess) ++c->n_ev;
+}
+
+}  // namespace ue
+
+namespace {
+
+using ue::aligned;
+using ue::fail;
+using ue::hip_fail;
+using ue::round_up;
+using ue::tbegin;
+using ue::tmark;
+
+int bits_for(int n) {   // smallest b with (1 << b) >= n
+    int b = 0;
+    while ((1 << b) < n) ++b;
+    return b;
 }
 
 }  // namespace
@@ -243,6 +250,7 @@ void ue_destroy(ue_ctx *ctx) {
     (void)hipDeviceSynchronize();
     if (ctx->ws) (void)hipFree(ctx->ws);
     if (ctx->reg_tables) (void)hipFree(ctx->reg_tables);
+    if (ctx->layer_ws) (void)hipFree(ctx->layer_ws);
     for (auto &e : ctx->ev)
         if (e) (void)hipEventDestroy(e);
     delete ctx;

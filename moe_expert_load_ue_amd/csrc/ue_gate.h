@@ -1,0 +1,168 @@
+// Choice of the k best experts of one token by one wave, shared by the gate
+// kernel and the few-token layer.
+//
+// Ranks are compared as 32-bit keys that order like the floats they come
+// from (negative values with all bits flipped, others with the sign bit
+// set). -0 counts as +0, so that the two tie; -inf and NaN are below every
+// key a round may take. Expert e = lane * V + i sits in slot i of its lane,
+// so the lowest id among equal keys is the lowest lane's lowest slot.
+#pragma once
+
+#include "ue_internal.h"
+
+namespace ue {
+
+constexpr uint32_t kKeyNegInf = 0x007FFFFFu;   // key of -inf: not taken
+
+__device__ __forceinline__ uint32_t rank_key(float x) {
+    const uint32_t b = __float_as_uint(x + 0.0f);          // -0 -> +0
+    const uint32_t k = b ^ ((b & 0x80000000u) ? 0xFFFFFFFFu : 0x80000000u);
+    return x != x ? 0u : k;
+}
+
+__device__ __forceinline__ float bf16_to_f32(uint16_t v) {
+    return __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
+
+// Round to nearest even; NaN stays NaN.
+__device__ __forceinline__ uint16_t f32_to_bf16(float f) {
+    const uint32_t u = __float_as_uint(f);
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u)
+        return static_cast<uint16_t>((u >> 16) | 0x40u);
+    return static_cast<uint16_t>((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+}
+
+// 1 / (1 + exp(-x)), and its slope without the cancellation of 1 - p.
+__device__ __forceinline__ float sigmoid_of(float x) {
+    return 1.0f / (1.0f + expf(-x));
+}
+__device__ __forceinline__ float sigmoid_slope(float x) {
+    const float e = expf(-fabsf(x));
+    return e / ((1.0f + e) * (1.0f + e));
+}
+
+// Maximum over the 64 lanes, wave-uniform.
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+    return ~wave_min_u32(~v);
+}
+
+// Sum over the 64 lanes in a fixed order, the same in every lane.
+__device__ __forceinline__ float wave_sum_f32(float v) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+    return v;
+}
+
+// One round per expert taken: the largest key of the wave, its lowest id.
+// `emit(r, id)` is called with wave-uniform arguments. Returns how many were
+// taken (fewer than k when the rest are -inf or NaN). The keys are consumed.
+template <int V, class Emit>
+__device__ __forceinline__ int take_best(uint32_t (&key)[V], int k, Emit emit) {
+    const int lane = lane_id();
+    for (int r = 0; r < k; ++r) {
+        uint32_t m = key[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) m = key[i] > m ? key[i] : m;
+        m = wave_max_u32(m);
+        if (m <= kKeyNegInf) return r;
+        uint64_t at[V], any = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            at[i] = __ballot(key[i] == m);
+            any |= at[i];
+        }
+        const int L = __builtin_ctzll(any);
+        int id = -1;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const bool hit = id < 0 && ((at[i] >> L) & 1);
+            if (hit) id = L * V + i;
+            if (hit && lane == L) key[i] = 0;
+        }
+        emit(r, id);
+    }
+    return k;
+}
+
+// +inf as the largest float (so that it can be subtracted from itself).
+__device__ __forceinline__ float finite_top(float x) {
+    return x > __FLT_MAX__ ? __FLT_MAX__ : x;
+}
+
+// Largest of the lanes' values that is no NaN, made finite above.
+__device__ __forceinline__ float wave_top(float v) {
+    const uint32_t m = wave_max_u32(rank_key(v));
+    return finite_top(__uint_as_float((m & 0x80000000u) ? m ^ 0x80000000u : ~m));
+}
+
+// One token's choice by one wave. `x`: its logits, slot i of lane l expert
+// l V + i, -inf past the last; `logit(id)` reads one again; `ids`, `weights`:
+// its k results; `taken(id)` is called, wave-uniform, for each expert taken.
+template <int V, class Logit, class Taken>
+__device__ __forceinline__ void gate_row(const GateRule &g, const float (&x)[V],
+                                         Logit logit, int32_t *ids,
+                                         float *weights, Taken taken) {
+    const int lane = lane_id();
+    bool nan = false;
+    uint32_t key[V];
+    float top = -__builtin_inff(), all = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        nan |= x[i] != x[i];
+        top = x[i] > top ? x[i] : top;
+    }
+    if (g.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane * V + i;
+            const float b = g.bias && e < g.E ? g.bias[e] : 0.f;
+            key[i] = x[i] == -__builtin_inff() ? 0u
+                                               : rank_key(sigmoid_of(x[i]) + b);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = rank_key(x[i]);
+        top = wave_top(top);
+        if (!g.renorm) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                all += x[i] == -__builtin_inff()
+                           ? 0.f : expf(finite_top(x[i]) - top);
+            all = wave_sum_f32(all);
+        }
+    }
+    const bool poisoned = __ballot(nan) != 0;
+    // lane j keeps rounds j, j + 64, ...: the last one in a register, with
+    // more than 64 rounds all of them in `ids`
+    int my = -1;
+    const bool many = g.k > 64;
+    const int got = take_best<V>(key, g.k, [&](int r, int id) {
+        if (lane == (r & 63)) {
+            my = id;
+            if (many) ids[r] = id;
+        }
+        taken(id);
+    });
+    auto score = [&](int id) {
+        const float v = logit(id);
+        return g.sigmoid ? sigmoid_of(v) : expf(finite_top(v) - top);
+    };
+    float sum = 0.f, p = 0.f;
+    for (int r = lane; r < got; r += 64) {
+        p = score(many ? ids[r] : my);
+        sum += p;
+    }
+    // (the softmax's own denominator cancels in the renormalised weights)
+    float n = 1.f;
+    if (g.renorm) n = wave_sum_f32(sum) + (g.sigmoid ? 1e-20f : 0.f);
+    else if (!g.sigmoid) n = all;
+    for (int r = lane; r < g.k; r += 64) {
+        const bool have = r < got;
+        if (have && many) p = score(ids[r]);
+        const float w = have ? p / n * g.scale : 0.f;
+        weights[r] = poisoned ? __builtin_nanf("") : w;
+        if (!many || !have) ids[r] = have ? my : -1;
+    }
+}
+
+}  // namespace ue

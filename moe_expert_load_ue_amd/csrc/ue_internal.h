@@ -5,7 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
-#include <string>
+#include <cstring>
 
 #include "../../include/ue.h"
 
@@ -26,6 +26,28 @@ constexpr int kRerouteTile = kBlock * kRerouteItems;
 constexpr int kLoadItems = kRerouteItems;
 constexpr int kLoadTile = kRerouteTile;
 constexpr int kLoadGroup = 16384 / kLoadTile;   // tiles per load workgroup
+
+// Last error message: fixed storage, so that recording one cannot throw
+// through the C entry points.
+struct ErrText {
+    char s[512] = {};
+    void clear() { s[0] = 0; }
+    void operator=(const char *t) {
+        std::strncpy(s, t, sizeof(s) - 1);
+        s[sizeof(s) - 1] = 0;
+    }
+    const char *c_str() const { return s; }
+};
+
+// A few tokens' worth of the layer: tokens of one expert are a 64-bit set.
+constexpr int kMoeTokens = UE_MOE_MAX_TOKENS;
+static_assert(kMoeTokens == 64, "one bit per token");
+
+struct MoeExpert {
+    unsigned long long tokens;   // bit t: token t chose it
+    int32_t expert;
+    int32_t base;                // its first row among all chosen rows
+};
 
 }  // namespace ue
 
@@ -86,13 +108,27 @@ struct ue_ctx {
     void **d_spare_w = nullptr;
     float **d_spare_g = nullptr;
 
+    // Registered layer (ue_register_layer) and its workspace: logits, the
+    // experts in use, and per chosen (expert, token) row its weight, token
+    // and hidden activations. Every word a call reads it has written itself.
+    bool has_layer = false;
+    ue_layer layer{};
+    int layer_tokens = 0;          // most tokens of one call
+    void *layer_ws = nullptr;
+    float *moe_logits = nullptr;   // [layer_tokens][E]
+    int32_t *moe_n_active = nullptr;
+    ue::MoeExpert *moe_active = nullptr;   // [E]
+    float *moe_row_weight = nullptr;       // [layer_tokens * k]
+    int32_t *moe_row_token = nullptr;      // [layer_tokens * k]
+    uint16_t *moe_h = nullptr;     // [2][layer_tokens * k][inter]
+
     // Kernel timing (off unless ue_set_timing enabled it).
     static constexpr int kMaxEvents = 8;
     bool timing = false;
     hipEvent_t ev[kMaxEvents] = {};
     int n_ev = 0;
 
-    std::string err;
+    ue::ErrText err;
 };
 
 namespace ue {
@@ -135,6 +171,105 @@ hipError_t launch_stale(const ue_ctx &c, const int32_t *placement,
 hipError_t launch_gather_rows(const ue_ctx &c, const void *x,
                               const int32_t *inv_perm, int T, int k, int H,
                               void *out, hipStream_t s);
+
+struct GateRule {
+    int E, k, sigmoid, renorm;
+    float scale;
+    const float *bias;          // [E] or null (sigmoid only)
+};
+struct GateArgs {
+    const void *logits;         // [T] rows, ld elements apart
+    int64_t ld;
+    bool bf16, vec;             // vec: a lane's logits may load at once
+    int T;
+    GateRule rule;
+    int32_t *ids;
+    float *weights;
+};
+struct GateBackArgs {
+    const void *logits;
+    int64_t ld;
+    bool bf16, vec;
+    int T;
+    GateRule rule;
+    const int32_t *ids;
+    const float *dweights;
+    void *dlogits;
+    int64_t ld_out;
+};
+// Slots per lane that hold E experts in a wave: a power of two.
+int lane_slots(int E);
+hipError_t launch_gate(const ue_ctx &c, const GateArgs &g, hipStream_t s);
+hipError_t launch_gate_backward(const ue_ctx &c, const GateBackArgs &g,
+                                hipStream_t s);
+
+struct QuantArgs {
+    const void *x;              // [M] rows, ldx elements apart
+    int64_t ldx;
+    bool bf16, vec;             // vec: rows start 16-byte aligned
+    int M, K, Kpad;             // Kpad: K up to a multiple of 16
+    int8_t *q;
+    int64_t ldq;
+    float *scale;
+};
+hipError_t launch_quantize(const QuantArgs &g, hipStream_t s);
+
+struct I8Args {
+    const int8_t *a;            // [a_rows] rows, lda apart
+    int64_t lda;
+    const float *a_scale;
+    int a_rows;
+    const int8_t *w;            // [n_mats] matrices w_stride apart, rows ldw apart
+    int64_t ldw, w_stride;
+    const float *w_scale;
+    int64_t ws_stride;
+    int n_mats;
+    const int32_t *offsets, *expert_of;   // [G + 1], [G]; may be null
+    int G;
+    const int32_t *index;       // [M] or null
+    int index_div;
+    int M, N, K;
+    bool gated, out_f32;
+    void *out;
+    int64_t ldo;
+};
+hipError_t launch_matmul_i8(const ue_ctx &c, const I8Args &g, hipStream_t s);
+
+struct MoeArgs {
+    int T, H, I;
+    const uint16_t *x;
+    int64_t ldx;
+    const uint16_t *router;
+    GateRule rule;
+    bool i8;
+    const void *gate_up, *down;
+    int64_t gate_up_stride, down_stride;   // elements
+    const float *gate_up_scale, *down_scale;
+    float *logits;
+    int32_t *n_active;
+    MoeExpert *active;
+    float *row_weight;
+    int32_t *row_token;
+    uint16_t *h_hi, *h_lo;
+    uint16_t *out;
+    int64_t ldo;
+    int32_t *ids;
+    float *weights;
+};
+// In order: router and choice, gate and up, down and weighted sum.
+hipError_t launch_moe_route(const MoeArgs &g, hipStream_t s);
+hipError_t launch_moe_up(const MoeArgs &g, hipStream_t s);
+hipError_t launch_moe_down(const MoeArgs &g, hipStream_t s);
+
+// Error text and kernel timing, shared by the entry points' files.
+int fail(ue_ctx *c, int code, const char *fmt, ...)
+    __attribute__((format(printf, 3, 4)));
+int hip_fail(ue_ctx *c, hipError_t e, const char *what);
+bool aligned(const void *p, size_t a);
+size_t round_up(size_t v, size_t a);
+// tbegin before a call's first launch, tmark after each.
+void tbegin(ue_ctx *c, hipStream_t s);
+void tmark(ue_ctx *c, hipStream_t s);
 
 // What the kernels need to know of a device.
 struct DeviceInfo {
