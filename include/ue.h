@@ -469,8 +469,9 @@ int ue_quantize_rows(ue_ctx *ctx, const void *x, int32_t type, int64_t ldx,
  *   w        device, int8, likewise; matrices w_stride apart (multiple of 16)
  *   w_scale  device, fp32, matrices ws_stride apart
  * For a and w the bytes of a row up to K rounded up to 16 must be readable.
- * out is UE_BF16 or UE_F32, ldo >= N. K in 1..65536; rows of out times
- * channels are limited by a launch of 2^31 workgroups (UE_ESHAPE). */
+ * out is UE_BF16 or UE_F32, ldo >= N. K in 1..65536; one matrix of w is below
+ * 4 GiB and lda below 16 MiB; rows of out times channels are limited by a
+ * launch of 2^31 workgroups (UE_ESHAPE). */
 typedef struct ue_i8_product {
     const int8_t *a;
     const float *a_scale;

@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -121,7 +122,7 @@ SIGNATURES = {
                                         _vp]),
     "ue_quantize_rows": (ctypes.c_int, [_vp, _vp, _i32, _i64, _i32, _i32, _vp,
                                         _i64, _vp, _vp]),
-    "ue_matmul_i8": (ctypes.c_int, [_vp, ctypes.POINTER(ue_i8_product), _vp]),
+    "ue_matmul_i8": (ctypes.c_int, [_vp, _vp, _vp]),
     "ue_register_layer": (ctypes.c_int, [_vp, ctypes.POINTER(ue_layer)]),
     "ue_moe_tokens": (ctypes.c_int, [_vp, _vp, _i64, _i32, _vp, _i64, _vp,
                                      _vp, _vp]),
@@ -199,11 +200,14 @@ class Context:
         if rc != UE_OK:
             raise UEError(rc, "ue_create refused the configuration")
         self._h = h
+        self._index = (self.device.index if self.device.index is not None
+                       else torch.cuda.current_device())
         lay = ue_placement_layout()
         library().ue_get_placement_layout(self._h, ctypes.byref(lay))
         self.layout = {f: getattr(lay, f) for f in PLACEMENT_FIELDS}
         self.placement_words = lay.words
         self._registered = None
+        self.hidden = None          # of the registered layer
 
     # -- lifetime ----------------------------------------------------------
     def close(self):
@@ -593,25 +597,43 @@ def ue_gather_rows(ctx: Context, x, inv_perm, out=None, stream=None):
 
 
 # ---- the expert layer around a rebalance ----------------------------------
+# These calls also serve single tokens, where the time on the host counts:
+# arguments are checked with few attribute reads and passed as plain integers.
+
+_FLOATS = (torch.float32, torch.bfloat16)
+_raw_stream = torch._C._cuda_getCurrentRawStream \
+    if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 
 def _rows(t, name, device, types, cols=None):
-    """A matrix [rows, cols] whose rows are contiguous; returns the distance
-    between rows in elements."""
+    """A matrix [rows, cols] whose rows are contiguous; returns (rows, cols,
+    distance between rows in elements)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype not in types:
         raise TypeError(f"{name} must be one of {list(types)}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
+    shape = t.shape
+    if len(shape) != 2 or (cols is not None and shape[1] != cols):
         raise ValueError(f"{name} must be [rows, {cols or 'cols'}], is "
-                         f"{tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+                         f"{tuple(shape)}")
+    n, c = shape
+    ld, one = t.stride()
+    if c > 1 and one != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if t.shape[0] <= 1:
+    if n <= 1:
         # a single row has no distance to the next: any that is long enough
-        return max(t.stride(0), (t.shape[1] + 15) // 16 * 16)
-    return t.stride(0)
+        ld = max(ld, (c + 15) // 16 * 16)
+    return n, c, ld
+
+
+def _flat(t, name, dtype, device, numel):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or \
+            t.device != device or t.numel() != numel or not t.is_contiguous():
+        _need(t, name, dtype, device, numel)
+    return t.data_ptr()
 
 
 def _new(shape, dtype, ctx, stream):
@@ -622,12 +644,15 @@ def _new(shape, dtype, ctx, stream):
         return torch.empty(shape, dtype=dtype, device=ctx.device)
 
 
-def _use(stream, *tensors):
-    """Keeps tensors of another stream from being reused under this call."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _on(ctx, stream, *tensors):
+    """The stream's handle; keeps tensors of another stream from being reused
+    under this call."""
+    if stream is None:
+        return _raw_stream(ctx._index)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
 
 
 def _score(score):
@@ -636,29 +661,34 @@ def _score(score):
     return SCORES[score]
 
 
+def _choice(ctx, T, ids, weights, stream):
+    """ids and weights of T tokens, made if not given: (ids, weights)."""
+    if ids is None:
+        ids = _new((T, ctx.k), torch.int32, ctx, stream)
+    else:
+        _flat(ids, "ids", torch.int32, ctx.device, T * ctx.k)
+    if weights is None:
+        weights = _new((T, ctx.k), torch.float32, ctx, stream)
+    else:
+        _flat(weights, "weights", torch.float32, ctx.device, T * ctx.k)
+    return ids, weights
+
+
 def ue_gate(ctx: Context, logits, bias=None, score="softmax", renorm=True,
             scale=1.0, ids=None, weights=None, stream=None):
     """Expert choice from router logits [T, E] (fp32 or bf16, rows may be
     apart): ids int32 [T, k], best first, and weights fp32 [T, k]. ``ids`` is
     a layer's routing for :func:`ue_load` and :func:`ue_rebalance`."""
-    ld = _rows(logits, "logits", ctx.device, _TYPES, ctx.E)
-    T = logits.shape[0]
-    if bias is not None:
-        _need(bias, "bias", torch.float32, ctx.device, ctx.E)
-    if ids is None:
-        ids = _new((T, ctx.k), torch.int32, ctx, stream)
-    else:
-        _need(ids, "ids", torch.int32, ctx.device, T * ctx.k)
-    if weights is None:
-        weights = _new((T, ctx.k), torch.float32, ctx, stream)
-    else:
-        _need(weights, "weights", torch.float32, ctx.device, T * ctx.k)
-    _use(stream, logits, bias, ids, weights)
-    rc = library().ue_gate(ctx._h, _ptr(logits), _TYPES[logits.dtype], ld, T,
-                           _score(score), bool(renorm), scale, _ptr(bias),
-                           _ptr(ids), _ptr(weights),
-                           _stream(stream, ctx.device))
-    ctx._check(rc, "ue_gate")
+    T, _, ld = _rows(logits, "logits", ctx.device, _FLOATS, ctx.E)
+    b = None if bias is None else _flat(bias, "bias", torch.float32,
+                                        ctx.device, ctx.E)
+    ids, weights = _choice(ctx, T, ids, weights, stream)
+    rc = library().ue_gate(ctx._h, logits.data_ptr(), _TYPES[logits.dtype],
+                           ld, T, _score(score), bool(renorm), scale, b,
+                           ids.data_ptr(), weights.data_ptr(),
+                           _on(ctx, stream, logits, bias, ids, weights))
+    if rc:
+        ctx._check(rc, "ue_gate")
     return ids, weights
 
 
@@ -666,21 +696,21 @@ def ue_gate_backward(ctx: Context, logits, ids, dweights, score="softmax",
                      renorm=True, scale=1.0, dlogits=None, stream=None):
     """Gradient of the logits [T, E] (their type) from the gradient of
     :func:`ue_gate`'s weights, at the same choice and settings."""
-    ld = _rows(logits, "logits", ctx.device, _TYPES, ctx.E)
-    T = logits.shape[0]
-    _need(ids, "ids", torch.int32, ctx.device, T * ctx.k)
-    _need(dweights, "dweights", torch.float32, ctx.device, T * ctx.k)
+    dev = ctx.device
+    T, _, ld = _rows(logits, "logits", dev, _FLOATS, ctx.E)
+    i = _flat(ids, "ids", torch.int32, dev, T * ctx.k)
+    g = _flat(dweights, "dweights", torch.float32, dev, T * ctx.k)
     if dlogits is None:
         dlogits = _new((T, ctx.E), logits.dtype, ctx, stream)
-    ldo = _rows(dlogits, "dlogits", ctx.device, (logits.dtype,), ctx.E)
-    if dlogits.shape[0] != T:
+    n, _, ldo = _rows(dlogits, "dlogits", dev, (logits.dtype,), ctx.E)
+    if n != T:
         raise ValueError(f"dlogits must have {T} rows")
-    _use(stream, logits, ids, dweights, dlogits)
     rc = library().ue_gate_backward(
-        ctx._h, _ptr(logits), _TYPES[logits.dtype], ld, T, _score(score),
-        bool(renorm), scale, _ptr(ids), _ptr(dweights), _ptr(dlogits), ldo,
-        _stream(stream, ctx.device))
-    ctx._check(rc, "ue_gate_backward")
+        ctx._h, logits.data_ptr(), _TYPES[logits.dtype], ld, T, _score(score),
+        bool(renorm), scale, i, g, dlogits.data_ptr(), ldo,
+        _on(ctx, stream, logits, ids, dweights, dlogits))
+    if rc:
+        ctx._check(rc, "ue_gate_backward")
     return dlogits
 
 
@@ -688,38 +718,46 @@ def ue_quantize_rows(ctx: Context, x, q=None, scale=None, stream=None):
     """Rows of x [M, K] (fp32 or bf16) as int8 [M, K] and scales fp32 [M]. The
     int8 rows are 16-byte aligned (a view of rows padded to a multiple of 16,
     the padding zero)."""
-    ldx = _rows(x, "x", ctx.device, _TYPES)
-    M, K = x.shape
+    M, K, ldx = _rows(x, "x", ctx.device, _FLOATS)
     if q is None:
-        q = _new((M, (K + 15) // 16 * 16), torch.int8, ctx, stream)[:, :K]
-    ldq = _i8_rows(q, "q", ctx.device, K)
-    if q.shape[0] != M:
-        raise ValueError(f"q must have {M} rows")
+        ldq = (K + 15) // 16 * 16
+        q = _new((M, ldq), torch.int8, ctx, stream)
+        if ldq != K:
+            q = q[:, :K]
+    else:
+        n, _, ldq = _i8_rows(q, "q", ctx.device, K)
+        if n != M:
+            raise ValueError(f"q must have {M} rows")
     if scale is None:
         scale = _new((M,), torch.float32, ctx, stream)
     else:
-        _need(scale, "scale", torch.float32, ctx.device, M)
-    _use(stream, x, q, scale)
-    rc = library().ue_quantize_rows(ctx._h, _ptr(x), _TYPES[x.dtype], ldx, M,
-                                    K, _ptr(q), ldq, _ptr(scale),
-                                    _stream(stream, ctx.device))
-    ctx._check(rc, "ue_quantize_rows")
+        _flat(scale, "scale", torch.float32, ctx.device, M)
+    rc = library().ue_quantize_rows(ctx._h, x.data_ptr(), _TYPES[x.dtype], ldx,
+                                    M, K, q.data_ptr(), ldq, scale.data_ptr(),
+                                    _on(ctx, stream, x, q, scale))
+    if rc:
+        ctx._check(rc, "ue_quantize_rows")
     return q, scale
 
 
 def _i8_rows(t, name, device, cols=None):
-    """Distance between int8 rows, whose storage must reach the end of the
-    last row's last 16-byte piece."""
-    ld = _rows(t, name, device, (torch.int8,), cols)
-    _i8_reach(t, name, (t.shape[0] - 1) * ld if t.shape[0] else 0, t.shape[1])
-    return ld
+    """As _rows; the storage must reach the end of the last row's last
+    16-byte piece."""
+    n, c, ld = _rows(t, name, device, (torch.int8,), cols)
+    if c % 16 and n:
+        _i8_reach(t, name, (n - 1) * ld, c)
+    return n, c, ld
 
 
 def _i8_reach(t, name, last_row, cols):
     end = t.storage_offset() + last_row + (cols + 15) // 16 * 16
-    if t.numel() and end > t.untyped_storage().nbytes():
+    if end > t.untyped_storage().nbytes():
         raise ValueError(f"{name}: the last row must be readable up to a "
                          "multiple of 16 bytes")
+
+
+_PRODUCT = struct.Struct("@8P5q9i")          # ue_i8_product
+assert _PRODUCT.size <= ctypes.sizeof(ue_i8_product) < _PRODUCT.size + 8
 
 
 def ue_matmul_i8(ctx: Context, a, a_scale, w, w_scale, offsets=None,
@@ -731,52 +769,60 @@ def ue_matmul_i8(ctx: Context, a, a_scale, w, w_scale, offsets=None,
     gated form (w with 2 N channels). Rows that no group holds are left as
     they are in ``out``."""
     dev = ctx.device
-    lda = _i8_rows(a, "a", dev)
-    rows, K = a.shape
-    _need(a_scale, "a_scale", torch.float32, dev, rows)
-    w3 = w if w.dim() == 3 else w.unsqueeze(0)
-    if w3.dim() != 3 or w3.dtype != torch.int8 or w3.device != dev:
-        raise TypeError(f"w must be int8 [N, {K}] or [experts, N, {K}] on {dev}")
-    n_mats, channels = w3.shape[0], w3.shape[1]
-    if n_mats < 1 or w3.shape[2] != K:
+    rows, K, lda = _i8_rows(a, "a", dev)
+    sa = _flat(a_scale, "a_scale", torch.float32, dev, rows)
+    if not isinstance(w, torch.Tensor) or w.dtype != torch.int8 or \
+            w.device != dev:
+        raise TypeError(f"w must be an int8 tensor on {dev}")
+    shape, strides = w.shape, w.stride()
+    if len(shape) == 2:
+        shape, strides = (1, *shape), (0, *strides)
+    if len(shape) != 3 or shape[0] < 1 or shape[2] != K:
         raise ValueError(f"w must be [N, {K}] or [experts, N, {K}], is "
                          f"{tuple(w.shape)}")
-    ldw = _rows(w3[0], "w", dev, (torch.int8,), K)
-    w_stride = w3.stride(0) if n_mats > 1 else 0
-    _i8_reach(w3, "w", (n_mats - 1) * w_stride + max(channels - 1, 0) * ldw, K)
-    _need(w_scale, "w_scale", torch.float32, dev, n_mats * channels)
-    if gated and channels % 2:
-        raise ValueError("gated: w needs as many up as gate channels")
-    N = channels // 2 if gated else channels
-    groups = 0
+    n_mats, channels, _ = shape
+    w_stride, ldw, one = strides
+    if K > 1 and one != 1:
+        raise ValueError("w must have contiguous rows")
+    if channels <= 1:
+        ldw = max(ldw, (K + 15) // 16 * 16)
+    if n_mats == 1:
+        w_stride = 0
+    if K % 16 and channels:
+        _i8_reach(w, "w", (n_mats - 1) * w_stride + (channels - 1) * ldw, K)
+    sw = _flat(w_scale, "w_scale", torch.float32, dev, n_mats * channels)
+    N = channels
+    if gated:
+        if channels % 2:
+            raise ValueError("gated: w needs as many up as gate channels")
+        N //= 2
+    groups, po, pe, pi, M = 0, 0, 0, 0, rows
     if offsets is not None:
-        _need(offsets, "offsets", torch.int32, dev)
         groups = offsets.numel() - 1
         if groups < 0:
             raise ValueError("offsets must hold groups + 1 entries")
+        po = _flat(offsets, "offsets", torch.int32, dev, groups + 1)
         if expert_of is not None:
-            _need(expert_of, "expert_of", torch.int32, dev, groups)
+            pe = _flat(expert_of, "expert_of", torch.int32, dev, groups)
     elif expert_of is not None:
         raise ValueError("expert_of needs offsets")
     if index is not None:
-        _need(index, "index", torch.int32, dev)
         M = index.numel()
-    else:
-        M = rows
+        pi = _flat(index, "index", torch.int32, dev, M)
     if out is None:
         out = _new((M, N), out_dtype, ctx, stream)
-    ldo = _rows(out, "out", dev, _TYPES, N)
-    if out.shape[0] != M:
+    n, _, ldo = _rows(out, "out", dev, _FLOATS, N)
+    if n != M:
         raise ValueError(f"out must have {M} rows")
-    _use(stream, a, a_scale, w, w_scale, offsets, expert_of, index, out)
-    p = ue_i8_product(_ptr(a), _ptr(a_scale), _ptr(w3), _ptr(w_scale),
-                      _ptr(offsets), _ptr(expert_of), _ptr(index), _ptr(out),
-                      lda, ldw, w_stride, channels, ldo, rows, n_mats, groups,
-                      int(index_div), M, N, K, bool(gated),
+    p = _PRODUCT.pack(a.data_ptr(), sa, w.data_ptr(), sw, po, pe, pi,
+                      out.data_ptr(), lda, ldw, w_stride, channels, ldo, rows,
+                      n_mats, groups, index_div, M, N, K, bool(gated),
                       _TYPES[out.dtype])
-    rc = library().ue_matmul_i8(ctx._h, ctypes.byref(p),
-                                _stream(stream, dev))
-    ctx._check(rc, "ue_matmul_i8")
+    rc = library().ue_matmul_i8(ctx._h, p,
+                                _on(ctx, stream, a, a_scale, w, w_scale,
+                                    offsets, expert_of, index, out))
+    if rc:
+        ctx._check(rc, "ue_matmul_i8")
     return out
 
 
@@ -832,25 +878,16 @@ def ue_moe_tokens(ctx: Context, x, out=None, ids=None, weights=None,
                   stream=None):
     """The registered layer for x bf16 [T, H], T up to 64: returns (out bf16
     [T, H], ids int32 [T, k], weights fp32 [T, k])."""
-    H = getattr(ctx, "hidden", None)
-    ldx = _rows(x, "x", ctx.device, (torch.bfloat16,), H)
-    T = x.shape[0]
+    T, H, ldx = _rows(x, "x", ctx.device, (torch.bfloat16,), ctx.hidden)
     if out is None:
-        out = _new((T, x.shape[1]), torch.bfloat16, ctx, stream)
-    ldo = _rows(out, "out", ctx.device, (torch.bfloat16,), x.shape[1])
-    if out.shape[0] != T:
+        out = _new((T, H), torch.bfloat16, ctx, stream)
+    n, _, ldo = _rows(out, "out", ctx.device, (torch.bfloat16,), H)
+    if n != T:
         raise ValueError(f"out must have {T} rows")
-    if ids is None:
-        ids = _new((T, ctx.k), torch.int32, ctx, stream)
-    else:
-        _need(ids, "ids", torch.int32, ctx.device, T * ctx.k)
-    if weights is None:
-        weights = _new((T, ctx.k), torch.float32, ctx, stream)
-    else:
-        _need(weights, "weights", torch.float32, ctx.device, T * ctx.k)
-    _use(stream, x, out, ids, weights)
-    rc = library().ue_moe_tokens(ctx._h, _ptr(x), ldx, T, _ptr(out), ldo,
-                                 _ptr(ids), _ptr(weights),
-                                 _stream(stream, ctx.device))
-    ctx._check(rc, "ue_moe_tokens")
+    ids, weights = _choice(ctx, T, ids, weights, stream)
+    rc = library().ue_moe_tokens(ctx._h, x.data_ptr(), ldx, T, out.data_ptr(),
+                                 ldo, ids.data_ptr(), weights.data_ptr(),
+                                 _on(ctx, stream, x, out, ids, weights))
+    if rc:
+        ctx._check(rc, "ue_moe_tokens")
     return out, ids, weights

@@ -18,6 +18,8 @@
 // second: a lane then holds channels of one row. The matrix's rows are laid
 // in LDS so that row 4 q + i of fragment f is channel 4 F q + 4 f + i of the
 // wave's F fragments: lane group q then holds 4 F consecutive channels.
+#include <type_traits>
+
 #include "ue_gate.h"
 
 namespace ue {
@@ -27,19 +29,28 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kStep = 128;               // bytes of K per stage
 
-// Rows [lo, hi) of group `tile` of the launch's row tiles: group g has
-// ceil(rows / BM) tiles, groups in order. Offsets are clamped to [0, M], so
-// that no table can send a tile outside. False: no such tile.
+// Waits until at most N of this wave's loads are on their way and its LDS
+// reads are done.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+// The tile of a workgroup: rows [lo, hi) of a group, channels from n0.
+struct Tile {
+    int group, lo, hi, col;
+};
+
+// Group g has ceil(rows / BM) row tiles, groups in order; offsets are clamped
+// to [0, M], so that no table can send a tile outside. The launch has room
+// for any table; how many tiles there are is counted here, and only those are
+// dealt to the XCDs. Tiles go in blocks of kBlockM row tiles by all column
+// tiles, row tiles first, each XCD a contiguous run: the tiles an XCD has at
+// once then share both operands' rows in its L2. False: no tile left.
+constexpr int kBlockM = 8;
 template <int THREADS>
-__device__ __forceinline__ bool find_tile(const I8Args &g, int tile, int BM,
-                                          int *sh, int &group, int &lo,
-                                          int &hi) {
-    if (!g.offsets) {
-        group = 0;
-        lo = tile * BM;
-        hi = g.M;
-        return lo < g.M;
-    }
+__device__ __forceinline__ bool find_tile(const I8Args &g, int BM, int ncol,
+                                          int *sh, Tile &t) {
     const int tid = threadIdx.x;
     const int per = (g.G + THREADS - 1) / THREADS;
     const int first = tid * per;
@@ -49,39 +60,59 @@ __device__ __forceinline__ bool find_tile(const I8Args &g, int tile, int BM,
         a = a < 0 ? 0 : a > g.M ? g.M : a;
         b = b < a ? a : b > g.M ? g.M : b;
     };
-    int n = 0;
-    for (int i = first; i < first + per && i < g.G; ++i) {
-        int a, b;
-        bounds(i, a, b);
-        n += (b - a + BM - 1) / BM;
+    int n = 0, before = 0, rows = (g.M + BM - 1) / BM;
+    if (g.offsets) {
+        for (int i = first; i < first + per && i < g.G; ++i) {
+            int a, b;
+            bounds(i, a, b);
+            n += (b - a + BM - 1) / BM;
+        }
+        // tiles before this thread's groups, and of all
+        const int incl = wave_inclusive_sum(n);
+        if (lane_id() == 63) sh[tid >> 6] = incl;
+        __syncthreads();
+        before = incl - n;
+        rows = 0;
+        for (int w = 0; w < THREADS / 64; ++w) {
+            before += w < (tid >> 6) ? sh[w] : 0;
+            rows += sh[w];
+        }
     }
-    // tiles before this thread's groups
-    const int incl = wave_inclusive_sum(n);
-    if (tid == 0) sh[16] = -1;
-    if (lane_id() == 63) sh[tid >> 6] = incl;
-    __syncthreads();
-    int before = incl - n;
-    for (int w = 0; w < (tid >> 6); ++w) before += sh[w];
+    // (a table whose groups overlap may ask for more tiles than there is room)
+    const int room = gridDim.x / ncol;
+    rows = rows < room ? rows : room;
+    if (static_cast<int>(blockIdx.x) >= rows * ncol) return false;
+    const int id = xcd_order(blockIdx.x, rows * ncol);
+    const int blk = id / (kBlockM * ncol), in = id - blk * kBlockM * ncol;
+    const int bm = rows - blk * kBlockM < kBlockM ? rows - blk * kBlockM : kBlockM;
+    t.col = in / bm;
+    const int tile = blk * kBlockM + in % bm;
+    if (!g.offsets) {
+        t.group = 0;
+        t.lo = tile * BM;
+        t.hi = g.M;
+        return true;
+    }
     if (tile >= before && tile < before + n) {
-        int t = tile - before;
+        int left = tile - before;
         for (int i = first;; ++i) {
             int a, b;
             bounds(i, a, b);
             const int nt = (b - a + BM - 1) / BM;
-            if (t < nt) {
+            if (left < nt) {
                 sh[16] = i;
-                sh[17] = a + t * BM;
+                sh[17] = a + left * BM;
                 sh[18] = b;
                 break;
             }
-            t -= nt;
+            left -= nt;
         }
     }
     __syncthreads();
-    group = sh[16];
-    lo = sh[17];
-    hi = sh[18];
-    return group >= 0;
+    t.group = sh[16];
+    t.lo = sh[17];
+    t.hi = sh[18];
+    return true;
 }
 
 __device__ __forceinline__ void store_out(float *p, float v) { *p = v; }
@@ -89,38 +120,87 @@ __device__ __forceinline__ void store_out(uint16_t *p, float v) {
     *p = f32_to_bf16(v);
 }
 
+// N consecutive results: 16 bytes at a time (or all of them, if that is
+// less) when `whole`, else those of the first `left` one by one.
+template <int N, typename OUT>
+__device__ __forceinline__ void store_run(OUT *p, const float (&v)[N], bool whole,
+                                          int left) {
+    constexpr int kBytes = N * static_cast<int>(sizeof(OUT));
+    constexpr int kEach = kBytes < 16 ? N : 16 / static_cast<int>(sizeof(OUT));
+    if (whole) {
+        struct alignas(kBytes < 16 ? kBytes : 16) Pack { OUT o[kEach]; };
+#pragma unroll
+        for (int c = 0; c < N; c += kEach) {
+            Pack k;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) store_out(&k.o[e], v[c + e]);
+            *reinterpret_cast<Pack *>(p + c) = k;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (e < left) store_out(p + e, v[e]);
+    }
+}
+
+// The row of activations of output row m (-1: none).
+__device__ __forceinline__ int act_row(const I8Args &g, int m) {
+    if (!g.index) return m;
+    const int i = g.index[m];
+    if (i < 0) return -1;
+    const int r = i / g.index_div;
+    return r < g.a_rows ? r : -1;
+}
+
+// Zeroes the bytes of a 16-byte piece from `left` on. Zero activations are
+// enough where a row ends: in integers what they meet does not matter.
+__device__ __forceinline__ i32x4 keep_bytes(i32x4 v, int left) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const int nb = left - 4 * w;
+        const uint32_t keep =
+            nb >= 4 ? 0xFFFFFFFFu : nb <= 0 ? 0u : (1u << (8 * nb)) - 1u;
+        v[w] &= static_cast<int>(keep);
+    }
+    return v;
+}
+
 // FM, FN: 16-row fragments of activations and of the matrix per wave;
-// WM, WN: waves along each.
-template <int FM, int FN, int WM, int WN, bool GATED, typename OUT>
-__global__ __launch_bounds__(WM *WN * 64) void k_matmul_i8(I8Args g) {
+// WM, WN: waves along each; NS: stages in LDS.
+//
+// A stage is two halves of 64 bytes of K. While a half's products run, the
+// operands of the next half are on their way from LDS. At the end of a
+// stage's first half its second half has been read, so the stage's LDS is
+// free: one barrier there tells that every wave is done with it and that the
+// next stage has landed, and the stage NS ahead is loaded into it.
+template <int FM, int FN, int WM, int WN, int NS, bool GATED, typename OUT,
+          typename OFF>
+__global__ __launch_bounds__(WM *WN * 64, FM * FN > 32 ? 1 : 2) void k_matmul_i8(I8Args g) {
     constexpr int kThreads = WM * WN * 64;
     constexpr int BM = WM * FM * 16, BN = WN * FN * 16;   // rows in LDS
     constexpr int kOut = GATED ? BN / 2 : BN;             // channels out
     constexpr int kChunks = (BM + BN) / 8 / (WM * WN);    // of 8 rows, a wave
+    constexpr int kStage = (BM + BN) * kStep;
     static_assert((BM + BN) / 8 % (WM * WN) == 0, "whole chunks per wave");
     extern __shared__ __align__(16) char lds[];
     __shared__ int sh[20];
     const int tid = threadIdx.x, lane = lane_id();
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-    const int ncol = (g.N + kOut - 1) / kOut;
-    const int id = xcd_order(blockIdx.x, gridDim.x);
-    const int n0 = (id % ncol) * kOut;
-    int group, m0, m_end;
-    if (!find_tile<kThreads>(g, id / ncol, BM, sh, group, m0, m_end)) return;
-    const int mat = g.expert_of ? g.expert_of[group] : group;
+    Tile tile;
+    if (!find_tile<kThreads>(g, BM, (g.N + kOut - 1) / kOut, sh, tile)) return;
+    const int m0 = __builtin_amdgcn_readfirstlane(tile.lo);
+    const int m_end = __builtin_amdgcn_readfirstlane(tile.hi);
+    const int n0 = tile.col * kOut;
+    const int mat = __builtin_amdgcn_readfirstlane(
+        g.expert_of ? g.expert_of[tile.group] : tile.group);
     if (static_cast<uint32_t>(mat) >= static_cast<uint32_t>(g.n_mats)) return;
 
-    // the row of activations of output row m (-1: none)
-    auto act_row = [&](int m) {
-        if (!g.index) return m;
-        const int i = g.index[m];
-        if (i < 0) return -1;
-        const int r = i / g.index_div;
-        return r < g.a_rows ? r : -1;
-    };
-    // global address of this lane's piece of each chunk it loads
-    const int8_t *src[kChunks];
+    // offset of this lane's piece of each chunk it loads, from the matrix or
+    // the activations (without an index, from the tile's first row)
+    const int8_t *const abase = g.index ? g.a : g.a + static_cast<int64_t>(m0) * g.lda;
+    const int8_t *const wbase = g.w + mat * g.w_stride;
+    OFF src[kChunks];
     const int piece = (lane & 7) ^ (lane >> 3);     // row & 7 = lane >> 3
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
@@ -128,8 +208,8 @@ __global__ __launch_bounds__(WM *WN * 64) void k_matmul_i8(I8Args g) {
         if (r < BM) {
             int m = m0 + r;
             m = m < m_end ? m : m_end - 1;
-            const int a = act_row(m);
-            src[c] = g.a + static_cast<int64_t>(a < 0 ? 0 : a) * g.lda;
+            const int a = g.index ? act_row(g, m) : m - m0;
+            src[c] = static_cast<OFF>(a < 0 ? 0 : a) * static_cast<OFF>(g.lda);
         } else {
             // row b of the tile's matrix: row l of fragment j of wave w's
             // block takes channel 4 F (l >> 2) + 4 j + (l & 3) of the block
@@ -146,23 +226,23 @@ __global__ __launch_bounds__(WM *WN * 64) void k_matmul_i8(I8Args g) {
                 n = n0 + w * FN * 16 + 4 * FN * (l >> 2) + 4 * j + (l & 3);
                 n = n < g.N ? n : g.N - 1;
             }
-            src[c] = g.w + mat * g.w_stride + static_cast<int64_t>(n) * g.ldw;
+            src[c] = static_cast<OFF>(n) * static_cast<OFF>(g.ldw);
         }
+        src[c] += piece * 16;
     }
     const int kbytes = (g.K + 15) & ~15;
-    auto load_stage = [&](int buf, int k0) {
+    const int steps = (g.K + kStep - 1) / kStep;
+    // one chunk of the stage at k0, into the LDS of stage `buf`
+    auto load_chunk = [&](int c, int buf, int k0) {
         // pieces past the row's end are read from its start: the last
         // stage's products mask them
-        int k = k0 + piece * 16;
-        k = k < kbytes ? k : 0;
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            char *dst = lds + buf * (BM + BN) * kStep +
-                        (wv * kChunks + c) * 8 * kStep;
-            __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void *)(src[c] + k),
-                (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
-        }
+        const OFF k = static_cast<OFF>(k0 + piece * 16 < kbytes ? k0 : -piece * 16);
+        const int8_t *from = ((wv * kChunks + c) * 8 < BM ? abase : wbase) +
+                             static_cast<OFF>(src[c] + k);
+        char *to = lds + buf * kStage + (wv * kChunks + c) * 8 * kStep;
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void *)from,
+            (__attribute__((address_space(3))) void *)to, 16, 0, 0);
     };
 
     i32x4 acc[FM][FN];
@@ -172,123 +252,324 @@ __global__ __launch_bounds__(WM *WN * 64) void k_matmul_i8(I8Args g) {
         for (int j = 0; j < FN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
     const int wm = wv / WN, wn = wv % WN;
     const int q = lane >> 4, l16 = lane & 15;
-    // rows of this lane's operand reads
+    // rows of this lane's operand reads, and its pieces of the two halves
     const int arow = wm * FM * 16 + l16;
     const int brow = wn * FN * 16 + l16;
-    auto products = [&](int buf, int k0, bool mask) {
-        const char *A = lds + buf * (BM + BN) * kStep;
-        const char *B = A + BM * kStep;
-#pragma unroll
-        for (int h = 0; h < kStep / 64; ++h) {
-            const int c = h * 4 + q;
-            i32x4 a[FM], b[FN];
-#pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                a[i] = *reinterpret_cast<const i32x4 *>(
-                    A + (arow + i * 16) * kStep + ((c ^ (arow & 7)) << 4));
-            }
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-                b[j] = *reinterpret_cast<const i32x4 *>(
-                    B + (brow + j * 16) * kStep + ((c ^ (brow & 7)) << 4));
-            if (mask) {
-                // zero activations past K (integers: what they meet in the
-                // matrix then does not matter)
-                const int left = g.K - (k0 + c * 16);
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const int nb = left - 4 * w;
-                    const uint32_t keep =
-                        nb >= 4 ? 0xFFFFFFFFu
-                                : nb <= 0 ? 0u : (1u << (8 * nb)) - 1u;
-#pragma unroll
-                    for (int i = 0; i < FM; ++i)
-                        a[i][w] &= static_cast<int>(keep);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
-                        b[j], a[i], acc[i][j], 0, 0, 0);
-        }
+    const char *la = lds + arow * kStep, *lb = lds + (BM + brow) * kStep;
+    struct Half { i32x4 a[FM], b[FN]; };
+    // operand read t of half h: the matrix's fragments, then the activations'
+    auto read_part = [&](Half &f, int t, int buf, int h) {
+        const int at = buf * kStage + (((h * 4 + q) ^ (l16 & 7)) << 4);
+        if (t < FN)
+            f.b[t] = *reinterpret_cast<const i32x4 *>(lb + at + t * 16 * kStep);
+        else
+            f.a[t - FN] = *reinterpret_cast<const i32x4 *>(la + at + (t - FN) * 16 * kStep);
     };
+    // The products of one half, with `tasks` calls of work(t) spread between
+    // them: a wave issues in order, so loads issued in one go would hold the
+    // matrix instructions behind them until the memory pipes have taken them
+    // all.
+    auto products = [&](Half &f, auto tasks, auto work) {
+        constexpr int kTasks = decltype(tasks)::value, kAll = FM * FN;
+        int done = 0;
+#pragma unroll
+        for (int p = 0; p < kAll; ++p) {
+#pragma unroll
+            for (; done < kTasks && done * kAll < p * kTasks; ++done) work(done);
+            __builtin_amdgcn_sched_barrier(0);
+            const int i = p / FN, j = p % FN;
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                f.b[j], f.a[i], acc[i][j], 0, 0, 0);
+        }
+#pragma unroll
+        for (; done < kTasks; ++done) work(done);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    constexpr int kReads = FM + FN;
+    typedef std::integral_constant<int, kReads> Reads;
+    typedef std::integral_constant<int, kReads + kChunks> ReadsAndLoads;
+    typedef std::integral_constant<int, 0> None;
 
-    const int steps = (g.K + kStep - 1) / kStep;
-    load_stage(0, 0);
-    __syncthreads();
-    for (int s = 0; s < steps; ++s) {
-        if (s + 1 < steps) load_stage((s + 1) & 1, (s + 1) * kStep);
-        products(s & 1, s * kStep, (s + 1) * kStep > g.K);
-        __syncthreads();
-    }
+    for (int s = 0; s < NS && s < steps; ++s)
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) load_chunk(c, s, s * kStep);
+    // every stage but the first may still be on its way
+    if (steps >= NS) wait_loads<(NS - 1) * kChunks>();
+    else wait_loads<0>();
+    __builtin_amdgcn_s_barrier();
+    Half f0, f1;
+#pragma unroll
+    for (int t = 0; t < kReads; ++t) read_part(f0, t, 0, 0);
+    int buf = 0, st = 0;
+    // all stages but the last NS load ahead, the next ones only use what was
+    // loaded, the last one masks what lies past K
+    auto stage = [&](auto loads) {
+        constexpr bool kLoads = decltype(loads)::value;
+        products(f0, Reads{}, [&](int t) { read_part(f1, t, buf, 1); });
+        wait_loads<kLoads ? (NS - 2) * kChunks : 0>();
+        __builtin_amdgcn_s_barrier();
+        const int old = buf;
+        buf = buf + 1 == NS ? 0 : buf + 1;
+        if constexpr (kLoads)
+            products(f1, ReadsAndLoads{}, [&](int t) {
+                if (t < kReads) read_part(f0, t, buf, 0);
+                else load_chunk(t - kReads, old, (st + NS) * kStep);
+            });
+        else
+            products(f1, Reads{}, [&](int t) { read_part(f0, t, buf, 0); });
+    };
+    for (; st + NS < steps; ++st) stage(std::true_type{});
+    for (; st + 1 < steps; ++st) stage(std::false_type{});
+#pragma unroll
+    for (int t = 0; t < kReads; ++t) read_part(f1, t, buf, 1);
+    auto mask_half = [&](Half &f, int k0) {
+        const int left = g.K - (k0 + q * 16);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) f.a[i] = keep_bytes(f.a[i], left);
+    };
+    mask_half(f0, st * kStep);
+    mask_half(f1, st * kStep + 64);
+    products(f0, None{}, [](int) {});
+    products(f1, None{}, [](int) {});
 
+    // scales first, all loads together, then the rows' outputs
+    constexpr int kRun = GATED ? FN * 2 : FN * 4;   // channels a lane holds
+    const int nb = n0 + wn * kRun * 4 + kRun * q;
     const float *ws = g.w_scale + mat * g.ws_stride;
+    float sw[kRun], su[kRun], sa[FM];
+#pragma unroll
+    for (int e = 0; e < kRun; ++e) {
+        const int n = nb + e < g.N ? nb + e : g.N - 1;
+        sw[e] = ws[n];
+        if (GATED) su[e] = ws[g.N + n];
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int m = m0 + arow + i * 16;
+        const int ar = act_row(g, m < m_end ? m : m_end - 1);
+        sa[i] = ar < 0 ? 0.f : g.a_scale[ar];
+    }
+    const bool whole = g.vec_out && nb + kRun <= g.N;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int m = m0 + arow + i * 16;
         if (m >= m_end) continue;
-        const int ar = act_row(m);
-        const float as = ar < 0 ? 0.f : g.a_scale[ar];
-        OUT *out = static_cast<OUT *>(g.out) + static_cast<int64_t>(m) * g.ldo;
-        if (GATED) {
-            constexpr int P = FN / 2;
-            const int base = n0 + wn * FN * 8 + 4 * P * q;
+        float v[kRun];
 #pragma unroll
-            for (int p = 0; p < P; ++p)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int n = base + 4 * p + e;
-                    if (n >= g.N) continue;
-                    const float gt = static_cast<float>(acc[i][2 * p][e]) * as * ws[n];
-                    const float up = static_cast<float>(acc[i][2 * p + 1][e]) * as * ws[g.N + n];
-                    store_out(out + n, gt / (1.0f + expf(-gt)) * up);
-                }
-        } else {
-            const int base = n0 + wn * FN * 16 + 4 * FN * q;
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int n = base + 4 * j + e;
-                    if (n >= g.N) continue;
-                    store_out(out + n, static_cast<float>(acc[i][j][e]) * as * ws[n]);
-                }
+        for (int e = 0; e < kRun; ++e) {
+            if (GATED) {
+                const float gt = static_cast<float>(acc[i][e / 4 * 2][e % 4]) * sa[i] * sw[e];
+                const float up = static_cast<float>(acc[i][e / 4 * 2 + 1][e % 4]) * sa[i] * su[e];
+                v[e] = gt / (1.0f + expf(-gt)) * up;
+            } else {
+                v[e] = static_cast<float>(acc[i][e / 4][e % 4]) * sa[i] * sw[e];
+            }
         }
+        store_run<kRun>(static_cast<OUT *>(g.out) + static_cast<int64_t>(m) * g.ldo + nb,
+                        v, whole, g.N - nb);
     }
 }
 
-template <int FM, int FN, int WM, int WN>
-hipError_t tiled(const I8Args &g, hipStream_t s) {
+// Few rows per matrix: the matrix's bytes bound the product. 16 channels (and
+// their 16 up channels) per workgroup, K split over its waves; each wave reads
+// its part of the matrix from HBM straight into its operand registers, kAhead
+// pieces at a time, for up to 16 RT rows at once.
+constexpr int kRowWaves = 8;
+
+template <int RT, bool GATED, typename OUT>
+__global__ __launch_bounds__(kRowWaves * 64) void k_rows_i8(I8Args g) {
+    constexpr int NW = GATED ? 2 : 1;
+    constexpr int kAhead = 8 / (RT > NW ? RT : NW);
+    __shared__ i32x4 part[kRowWaves][NW][RT][64];
+    const int lane = lane_id(), l16 = lane & 15, q = lane >> 4;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n0 = blockIdx.x * 16, group = blockIdx.y;
+    int lo = 0, hi = g.M;
+    if (g.offsets) {
+        lo = g.offsets[group];
+        hi = g.offsets[group + 1];
+        lo = lo < 0 ? 0 : lo > g.M ? g.M : lo;
+        hi = hi < lo ? lo : hi > g.M ? g.M : hi;
+    }
+    const int mat = g.expert_of ? g.expert_of[group] : group;
+    if (static_cast<uint32_t>(mat) >= static_cast<uint32_t>(g.n_mats)) return;
+    const int kbytes = (g.K + 15) & ~15;
+    const int n = n0 + l16 < g.N ? n0 + l16 : g.N - 1;
+    const int8_t *w[NW];
+#pragma unroll
+    for (int c = 0; c < NW; ++c)
+        w[c] = g.w + mat * g.w_stride +
+               (static_cast<int64_t>(c) * g.N + n) * g.ldw;
+    // this wave's part of K, in whole pieces of 64
+    const int pieces = (kbytes + 63) / 64;
+    const int per = (pieces + kRowWaves - 1) / kRowWaves;
+    const int p0 = wv * per, p1 = p0 + per < pieces ? p0 + per : pieces;
+
+    for (int m0 = lo; m0 < hi; m0 += 16 * RT) {
+        const int8_t *a[RT];
+        int row[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const int m = m0 + r * 16 + l16;
+            row[r] = act_row(g, m < hi ? m : hi - 1);
+            a[r] = g.a + static_cast<int64_t>(row[r] < 0 ? 0 : row[r]) * g.lda;
+        }
+        i32x4 acc[NW][RT] = {};
+        for (int p = p0; p < p1; p += kAhead) {
+            i32x4 wf[kAhead][NW], af[kAhead][RT];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                // pieces past this wave's part, or past K, are read from the
+                // row's start and masked
+                const int k = (p + u) * 64 + q * 16;
+                const int at = p + u < p1 && k < kbytes ? k : 0;
+#pragma unroll
+                for (int c = 0; c < NW; ++c)
+                    wf[u][c] = *reinterpret_cast<const i32x4 *>(w[c] + at);
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+                    af[u][r] = *reinterpret_cast<const i32x4 *>(a[r] + at);
+            }
+            if (p + kAhead > p1 || (p + kAhead) * 64 > g.K) {
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+                        af[u][r] = keep_bytes(
+                            af[u][r], p + u < p1 ? g.K - ((p + u) * 64 + q * 16) : 0);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+                for (int c = 0; c < NW; ++c)
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+                        acc[c][r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                            wf[u][c], af[u][r], acc[c][r], 0, 0, 0);
+        }
+#pragma unroll
+        for (int c = 0; c < NW; ++c)
+#pragma unroll
+            for (int r = 0; r < RT; ++r) part[wv][c][r][lane] = acc[c][r];
+        __syncthreads();
+        // wave r joins and writes rows 16 r ..
+        for (int r = wv; r < RT; r += kRowWaves) {
+            i32x4 sum[NW];
+#pragma unroll
+            for (int c = 0; c < NW; ++c) {
+                sum[c] = part[0][c][r][lane];
+                for (int v = 1; v < kRowWaves; ++v) sum[c] += part[v][c][r][lane];
+            }
+            const int m = m0 + r * 16 + l16;
+            if (m >= hi) continue;
+            const int ar = act_row(g, m);
+            const float sa = ar < 0 ? 0.f : g.a_scale[ar];
+            const float *ws = g.w_scale + mat * g.ws_stride;
+            const int nb = n0 + 4 * q;
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int nn = nb + e < g.N ? nb + e : g.N - 1;
+                const float gt = static_cast<float>(sum[0][e]) * sa * ws[nn];
+                v[e] = gt;
+                if constexpr (GATED) {
+                    const float up = static_cast<float>(sum[1][e]) * sa * ws[g.N + nn];
+                    v[e] = gt / (1.0f + expf(-gt)) * up;
+                }
+            }
+            store_run<4>(static_cast<OUT *>(g.out) + static_cast<int64_t>(m) * g.ldo + nb,
+                         v, g.vec_out && nb + 4 <= g.N, g.N - nb);
+        }
+        __syncthreads();
+    }
+}
+
+template <int RT, bool GATED, typename OUT>
+hipError_t rows_as(const I8Args &g, hipStream_t s) {
+    hipLaunchKernelGGL((k_rows_i8<RT, GATED, OUT>), dim3((g.N + 15) / 16, g.G),
+                       dim3(kRowWaves * 64), 0, s, g);
+    return hipGetLastError();
+}
+
+template <int RT>
+hipError_t rows(const I8Args &g, hipStream_t s) {
+    if (g.gated)
+        return g.out_f32 ? rows_as<RT, true, float>(g, s)
+                         : rows_as<RT, true, uint16_t>(g, s);
+    return g.out_f32 ? rows_as<RT, false, float>(g, s)
+                     : rows_as<RT, false, uint16_t>(g, s);
+}
+
+template <int FM, int FN, int WM, int WN, int NS, bool GATED, typename OUT,
+          typename OFF>
+hipError_t tiled_as(const I8Args &g, hipStream_t s) {
     constexpr int BM = WM * FM * 16, BN = WN * FN * 16;
-    const int kout = g.gated ? BN / 2 : BN;
-    const int64_t ncol = (g.N + kout - 1) / kout;
+    constexpr int kOut = GATED ? BN / 2 : BN;
+    constexpr int kLds = NS * (BM + BN) * kStep;
+    const int64_t ncol = (g.N + kOut - 1) / kOut;
     int64_t mt = (static_cast<int64_t>(g.M) + BM - 1) / BM;
     if (g.offsets) mt += g.G;       // each group's last tile may be partial
     const int64_t grid = ncol * mt;
     if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-    const size_t lds = 2 * (BM + BN) * kStep;
-    const dim3 gr(static_cast<uint32_t>(grid)), bl(WM * WN * 64);
-#define UE_I8_LAUNCH(GATED, OUT)                                               \
-    hipLaunchKernelGGL((k_matmul_i8<FM, FN, WM, WN, GATED, OUT>), gr, bl, lds, \
-                       s, g)
-    if (g.gated) {
-        if (g.out_f32) UE_I8_LAUNCH(true, float);
-        else UE_I8_LAUNCH(true, uint16_t);
-    } else {
-        if (g.out_f32) UE_I8_LAUNCH(false, float);
-        else UE_I8_LAUNCH(false, uint16_t);
+    const auto kernel = k_matmul_i8<FM, FN, WM, WN, NS, GATED, OUT, OFF>;
+    if constexpr (kLds > 65536) {
+        const hipError_t he = hipFuncSetAttribute(
+            reinterpret_cast<const void *>(kernel),
+            hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+        if (he != hipSuccess) return he;
     }
-#undef UE_I8_LAUNCH
+    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid)),
+                       dim3(WM * WN * 64), kLds, s, g);
     return hipGetLastError();
+}
+
+template <int FM, int FN, int WM, int WN, int NS, typename OFF = uint32_t>
+hipError_t tiled(const I8Args &g, hipStream_t s) {
+    if (g.gated)
+        return g.out_f32 ? tiled_as<FM, FN, WM, WN, NS, true, float, OFF>(g, s)
+                         : tiled_as<FM, FN, WM, WN, NS, true, uint16_t, OFF>(g, s);
+    return g.out_f32 ? tiled_as<FM, FN, WM, WN, NS, false, float, OFF>(g, s)
+                     : tiled_as<FM, FN, WM, WN, NS, false, uint16_t, OFF>(g, s);
 }
 
 }  // namespace
 
+#ifndef UE_I8_NO_LAUNCH
+// Which kernel, by what each measured on an MI355X (us; columns: rows x K x
+// channels, G: groups):
+//                     256x256  128x128   64x64   32x64  k_rows_i8<1>
+//   8192x7168x4096        222      238     379     541
+//   1000x2048x2048         28     13.1    10.0    14.7
+//   333x1900x1002          38     14.4     7.8     7.0
+//   128x7168x4096          71     44.0    17.5    15.9          72
+//   32x7168x4096           62     26.6    14.7    14.5        19.4
+//   16x7168x4096           60     25.6    14.7    14.4        10.8
+//   1x7168x4096            60     25.1    14.4    14.1         8.0
+//   G=72: 32768x1024x4096 277      297     483     741
+//   G=64: 4096x1024x4096   79     69.7    80.7     112
+//   G=64: 2048x4096x2048  142      138     119     114         227
+// Larger tiles read each operand less often and cost less energy (with random
+// data the power limit, not the issue rate, sets the clock); smaller ones give
+// the launch enough workgroups. So: the largest tile that groups of the mean
+// length at least half fill and that makes three workgroups for every four
+// CUs; up to 16 rows go to the row kernel.
 hipError_t launch_matmul_i8(const ue_ctx &c, const I8Args &g, hipStream_t s) {
     if (g.M == 0 || g.N == 0) return hipSuccess;
-    return tiled<4, 4, 2, 2>(g, s);
+    if (g.M <= 16 && g.G <= 65535) return rows<1>(g, s);
+    const int64_t channels = g.gated ? 2 * static_cast<int64_t>(g.N) : g.N;
+    auto fits = [&](int bm, int bn) {
+        const int64_t tiles = ((g.M + bm - 1) / bm + (g.offsets ? g.G / 2 : 0)) *
+                              ((channels + bn - 1) / bn);
+        return g.M / g.G >= bm / 2 && tiles >= c.num_cu * 3 / 4;
+    };
+    // offsets of an indexed row past 32 bits: one kernel has them in 64
+    if (g.index && static_cast<int64_t>(g.a_rows) * g.lda > 0xFFFFFFFFll)
+        return tiled<2, 2, 2, 2, 4, uint64_t>(g, s);
+    if (fits(256, 256)) return tiled<8, 4, 2, 4, 2>(g, s);
+    if (fits(128, 128)) return tiled<4, 2, 2, 4, 2>(g, s);
+    if (fits(64, 64)) return tiled<2, 2, 2, 2, 4>(g, s);
+    return tiled<1, 2, 2, 2, 6>(g, s);
 }
+#endif
 
 }  // namespace ue

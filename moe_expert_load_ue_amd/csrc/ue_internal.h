@@ -229,7 +229,7 @@ struct I8Args {
     const int32_t *index;       // [M] or null
     int index_div;
     int M, N, K;
-    bool gated, out_f32;
+    bool gated, out_f32, vec_out;         // vec_out: out's rows are 16-byte aligned
     void *out;
     int64_t ldo;
 };

@@ -173,6 +173,11 @@ int ue_matmul_i8(ue_ctx *ctx, const ue_i8_product *p, void *stream) {
                     static_cast<long long>(p->w_stride),
                     static_cast<long long>(p->ws_stride),
                     static_cast<long long>(p->ldo));
+    // (the kernels address a matrix, and 256 rows of a, with 32 bits)
+    if ((p->gated ? 2 : 1) * static_cast<int64_t>(p->N) > 0xFFFFFFFFll / p->ldw ||
+        p->lda > 0xFFFFFF)
+        return fail(ctx, UE_ESHAPE, "ue_matmul_i8: a matrix of 4 GiB, or lda=%lld of 16 MiB",
+                    static_cast<long long>(p->lda));
     if (p->out_type != UE_F32 && p->out_type != UE_BF16)
         return fail(ctx, UE_EINVAL, "ue_matmul_i8: out must be UE_F32 or UE_BF16");
     if (p->offsets ? p->groups < 0 || p->groups > 0xFFFFF
@@ -214,6 +219,7 @@ int ue_matmul_i8(ue_ctx *ctx, const ue_i8_product *p, void *stream) {
     g.K = p->K;
     g.gated = p->gated != 0;
     g.out_f32 = p->out_type == UE_F32;
+    g.vec_out = rows_aligned(p->out, p->ldo, es, 16);
     g.out = p->out;
     g.ldo = p->ldo;
     hipStream_t s = static_cast<hipStream_t>(stream);
