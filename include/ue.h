@@ -498,7 +498,7 @@ int ue_matmul_i8(ue_ctx *ctx, const ue_i8_product *p, void *stream);
  *              down_scale fp32 [E, hidden] (the weights of ue_matmul_i8)
  *   bias, score, renorm, scale   as in ue_gate
  * All matrices 16-byte aligned; hidden and inter multiples of 8 (bf16) or 16
- * (int8), strides likewise. The memory stays the caller's; the context keeps
+ * (int8), strides likewise, an expert's gate_up below 4 GiB. The memory stays the caller's; the context keeps
  * the pointers until the next registration or ue_destroy, and allocates a
  * workspace for min(max_tokens, UE_MOE_MAX_TOKENS) tokens. */
 #define UE_MOE_MAX_TOKENS 64
@@ -523,7 +523,7 @@ int ue_register_layer(ue_ctx *ctx, const ue_layer *layer);
  * also between the products; out is rounded once. The result does not depend
  * on timing (no atomics on values).
  *   x        device, bf16 [T] rows of hidden, 16-byte aligned, ldx apart
- *            (a multiple of 8)
+ *            (a multiple of 8, at most 2^24)
  *   out      device, bf16, ldo apart
  *   ids      device, int32 [T, k] out: the routing, as ue_load takes it
  *   weights  device, fp32 [T, k] out

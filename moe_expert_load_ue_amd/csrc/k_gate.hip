@@ -67,9 +67,7 @@ __global__ __launch_bounds__(kBlock) void k_gate(GateArgs g) {
         const int64_t o = static_cast<int64_t>(t) * g.rule.k;
         float x[V];
         load_row<T, V>(g.logits, row, g.rule.E, g.vec, x);
-        gate_row<V>(
-            g.rule, x, [&](int id) { return load_logit<T>(g.logits, row + id); },
-            g.ids + o, g.weights + o, [](int) {});
+        gate_row<V>(g.rule, x, g.ids + o, g.weights + o, [](int) {});
     }
 }
 

@@ -18,114 +18,10 @@
 // multiplied on its own: the second product's operands then carry 16 bits
 // of h, and the layer's result is rounded once, at the end. The extra matrix
 // instructions are free while bytes bound the kernel.
-#include "ue_gate.h"
+#include "ue_rows.h"
 
 namespace ue {
 namespace {
-
-typedef short bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 hbf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-__device__ __forceinline__ f32x4 mfma(u32x4 w, u32x4 x, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-        __builtin_bit_cast(hbf16x8, w), __builtin_bit_cast(hbf16x8, x), c, 0, 0, 0);
-}
-
-// Four int8 as bf16 (exact: 8 bits fit the significand).
-__device__ __forceinline__ u32x2 widen4(uint32_t v) {
-    const float f0 = static_cast<float>(static_cast<int8_t>(v));
-    const float f1 = static_cast<float>(static_cast<int8_t>(v >> 8));
-    const float f2 = static_cast<float>(static_cast<int8_t>(v >> 16));
-    const float f3 = static_cast<float>(static_cast<int8_t>(v >> 24));
-    // the low halves are zero: take the high ones
-    return u32x2{__builtin_amdgcn_perm(__float_as_uint(f1), __float_as_uint(f0),
-                                       0x07060302u),
-                 __builtin_amdgcn_perm(__float_as_uint(f3), __float_as_uint(f2),
-                                       0x07060302u)};
-}
-
-// A wave's pass over K of 16 matrix rows (this lane's row starts at w) for
-// RT tiles of 16 tokens (this lane's rows at x[], and x2[] where the
-// activations are sums of two parts). One step covers kK elements of K: a
-// lane group q reads the 16 bytes of the matrix at q * 16 of each 64. `k`
-// runs from k0 to k1, a multiple of the step apart but for the last.
-template <bool I8>
-struct Weights;
-template <>
-struct Weights<false> {
-    static constexpr int kK = 32;             // elements per load of 64 bytes
-    typedef u32x4 Frag;                       // 8 bf16
-    static __device__ __forceinline__ Frag load(const char *row, int k, int q) {
-        return *reinterpret_cast<const u32x4 *>(row + 2 * (k + 8 * q));
-    }
-};
-template <>
-struct Weights<true> {
-    static constexpr int kK = 64;
-    typedef u32x4 Frag;                       // 16 int8
-    static __device__ __forceinline__ Frag load(const char *row, int k, int q) {
-        return *reinterpret_cast<const u32x4 *>(row + k + 16 * q);
-    }
-};
-
-// NW matrix streams against RT token tiles of P parts each, K in [k0, k1).
-template <bool I8, int NW, int RT, int P>
-__device__ __forceinline__ void stream(const char *const (&w)[NW],
-                                       const uint16_t *const (&x)[RT][P],
-                                       int k0, int k1, int K,
-                                       f32x4 (&acc)[NW][RT]) {
-    constexpr int kK = Weights<I8>::kK;
-    constexpr int kEl = I8 ? 16 : 8;          // elements a lane holds
-    const int q = lane_id() >> 4;
-    for (int k = k0; k < k1; k += kK) {
-        // a lane past K reads the row's start and multiplies by zero
-        const bool in = k + q * kEl < K;
-        const int kk = in ? k : -q * kEl;
-        u32x4 wf[NW];
-#pragma unroll
-        for (int n = 0; n < NW; ++n) wf[n] = Weights<I8>::load(w[n], kk, q);
-        if constexpr (!I8) {
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    u32x4 xf = *reinterpret_cast<const u32x4 *>(x[r][p] + kk + 8 * q);
-                    if (!in) xf = u32x4{0, 0, 0, 0};
-#pragma unroll
-                    for (int n = 0; n < NW; ++n) {
-                        u32x4 v = wf[n];
-                        if (!in) v = u32x4{0, 0, 0, 0};
-                        acc[n][r] = mfma(v, xf, acc[n][r]);
-                    }
-                }
-        } else {
-            u32x4 lo[NW], hi[NW];
-#pragma unroll
-            for (int n = 0; n < NW; ++n) {
-                const u32x2 a = widen4(wf[n].x), b = widen4(wf[n].y);
-                const u32x2 c = widen4(wf[n].z), d = widen4(wf[n].w);
-                lo[n] = u32x4{a.x, a.y, b.x, b.y};
-                hi[n] = u32x4{c.x, c.y, d.x, d.y};
-            }
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    const u32x4 *xp = reinterpret_cast<const u32x4 *>(x[r][p] + kk + 16 * q);
-                    u32x4 x0 = xp[0], x1 = xp[1];
-                    if (!in) x0 = x1 = u32x4{0, 0, 0, 0};
-#pragma unroll
-                    for (int n = 0; n < NW; ++n) {
-                        acc[n][r] = mfma(lo[n], x0, acc[n][r]);
-                        acc[n][r] = mfma(hi[n], x1, acc[n][r]);
-                    }
-                }
-        }
-    }
-}
 
 // K split over W waves in whole steps: wave v's share.
 __device__ __forceinline__ void share(int K, int step, int W, int v, int &k0,
@@ -138,73 +34,126 @@ __device__ __forceinline__ void share(int K, int step, int W, int v, int &k0,
 }
 
 // ---- router ---------------------------------------------------------------
-// Logits of 16 experts per workgroup, K split over the waves.
-constexpr int kRouterWaves = 8;
+// Part sums of the logits of 16 experts per workgroup: K is split over the
+// workgroups of a column of the grid and their waves, for enough loads in
+// flight (256 experts alone make 16 workgroups: 16 us at K = 7168 and one
+// token, against 5 split). The choice adds the parts in order.
+constexpr int kRouterWaves = 4;
+constexpr int kRouterK = 1024;           // of K per workgroup
 
-template <int RT>
+template <int FOLD, int RT>
 __global__ __launch_bounds__(kRouterWaves * 64) void k_router(MoeArgs g) {
-    __shared__ f32x4 part[kRouterWaves][RT][64];
-    const int lane = lane_id(), l16 = lane & 15, q = lane >> 4;
-    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int e = blockIdx.x * 16 + l16;
-    const char *w[1] = {reinterpret_cast<const char *>(
-        g.router + static_cast<int64_t>(e < g.rule.E ? e : g.rule.E - 1) * g.H)};
-    const uint16_t *x[RT][1];
+    typedef RowStream<Bf16Rows, 1, FOLD, RT, 1> S;
+    __shared__ f32x4 part[kRouterWaves][S::kAcc][64];
+    const int tid = threadIdx.x, lane = lane_id();
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int E = g.rule.E, e0 = blockIdx.x * 16;
+    const char *w[1] = {reinterpret_cast<const char *>(g.router)};
+    const char *x[1] = {reinterpret_cast<const char *>(g.x)};
+    uint32_t wo[S::LD], xo[RT];
+#pragma unroll
+    for (int j = 0; j < S::LD; ++j) {
+        const int e = e0 + S::row(j);
+        wo[j] = 2u * (e < E ? e : E - 1) * g.H;
+    }
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-        const int t = r * 16 + l16;
-        x[r][0] = g.x + static_cast<int64_t>(t < g.T ? t : g.T - 1) * g.ldx;
+        const int t = S::token(r);
+        xo[r] = 2u * (t < g.T ? t : g.T - 1) * static_cast<uint32_t>(g.ldx);
     }
-    f32x4 acc[1][RT] = {};
-    int k0, k1;
-    share(g.H, 32, kRouterWaves, wv, k0, k1);
-    stream<false, 1, RT, 1>(w, x, k0, k1, g.H, acc);
+    f32x4 acc[1][S::kAcc] = {};
+    const int k0 = blockIdx.y * kRouterK + wv * (kRouterK / kRouterWaves);
+    const int k1 = k0 + kRouterK / kRouterWaves;
+    S::run(w, wo, x, xo, k0, k1 < g.H ? k1 : g.H, g.H, acc);
 #pragma unroll
-    for (int r = 0; r < RT; ++r) part[wv][r][lane] = acc[0][r];
+    for (int r = 0; r < S::kAcc; ++r) part[wv][r][lane] = acc[0][r];
     __syncthreads();
-    for (int r = wv; r < RT; r += kRouterWaves) {
-        f32x4 s = part[0][r][lane];
-        for (int v = 1; v < kRouterWaves; ++v) {
-            const f32x4 b = part[v][r][lane];
-            s.x += b.x; s.y += b.y; s.z += b.z; s.w += b.w;
-        }
-        const int t = r * 16 + l16;
-        if (t >= g.T) continue;
+    const float *f = reinterpret_cast<const float *>(part);
+    for (int i = tid; i < 16 * g.T; i += kRouterWaves * 64) {
+        const int n = i & 15, t = i >> 4;
+        if (e0 + n >= E) continue;
+        float sum = 0.f;
+        for (int v = 0; v < kRouterWaves; ++v)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int ee = blockIdx.x * 16 + 4 * q + i;
-            if (ee < g.rule.E) g.logits[static_cast<int64_t>(t) * g.rule.E + ee] = s[i];
-        }
+            for (int b = 0; b < S::kParts; ++b) {
+                int a, at;
+                S::where(n, t, b, a, at);
+                sum += f[(v * S::kAcc + a) * 256 + at];
+            }
+        g.logits[(static_cast<int64_t>(blockIdx.y) * g.T + t) * E + e0 + n] = sum;
     }
 }
 
 // ---- choice ----------------------------------------------------------------
-// One workgroup: every token's experts and weights, then the experts in use
-// with their tokens, as one 64-bit set per expert.
-constexpr int kChooseWaves = 16;
+// Every token's experts and weights, one wave per token; the workgroup that
+// ends last then lists the experts in use with their tokens (one 64-bit set
+// per expert) and the rows of all chosen (expert, token) pairs.
+constexpr int kChooseWaves = 4;
+
+__host__ __device__ inline int router_parts(int hidden) {
+    return (hidden + kRouterK - 1) / kRouterK;
+}
 
 template <int V>
 __global__ __launch_bounds__(kChooseWaves * 64) void k_choose(MoeArgs g) {
     __shared__ unsigned long long set[kMaxExperts];
     __shared__ int base[kMaxExperts];
+    __shared__ bool last;
+    // one workgroup's choices stay here until they are listed
+    __shared__ int32_t some_ids[kChooseWaves * 64];
+    __shared__ float some_weights[kChooseWaves * 64];
     const int tid = threadIdx.x, lane = lane_id(), wv = tid >> 6;
-    const int E = g.rule.E;
-    for (int e = tid; e < E; e += kChooseWaves * 64) set[e] = 0;
-    __syncthreads();
-    for (int t = wv; t < g.T; t += kChooseWaves) {
+    const int E = g.rule.E, k = g.rule.k, parts = router_parts(g.H);
+    constexpr int kBatch = V <= 4 ? 8 : 32 / V;      // parts loaded together
+    const int t = blockIdx.x * kChooseWaves + wv;
+    const bool one = gridDim.x == 1 && k <= 64;
+    int32_t *ids = one ? some_ids : g.ids;
+    float *weights = one ? some_weights : g.weights;
+    if (t < g.T) {
         const float *lg = g.logits + static_cast<int64_t>(t) * E;
-        const int64_t o = static_cast<int64_t>(t) * g.rule.k;
         float x[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane * V + i;
-            x[i] = e < E ? lg[e] : -__builtin_inff();
+        for (int i = 0; i < V; ++i)
+            x[i] = lane * V + i < E ? 0.f : -__builtin_inff();
+        for (int p0 = 0; p0 < parts; p0 += kBatch) {
+            float v[kBatch][V];
+#pragma unroll
+            for (int p = 0; p < kBatch; ++p)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int e = lane * V + i;
+                    v[p][i] = p0 + p < parts && e < E
+                                  ? lg[static_cast<int64_t>(p0 + p) * g.T * E + e]
+                                  : 0.f;
+                }
+#pragma unroll
+            for (int p = 0; p < kBatch; ++p)
+#pragma unroll
+                for (int i = 0; i < V; ++i) x[i] += v[p][i];
         }
-        gate_row<V>(
-            g.rule, x, [&](int id) { return lg[id]; }, g.ids + o, g.weights + o,
-            [&](int id) {
-                if (lane == 0) atomicOr(&set[id], 1ull << t);
-            });
+        gate_row<V>(g.rule, x, ids + t * k, weights + t * k, [](int) {});
+    }
+    if (gridDim.x > 1) {
+        // (the counter returns to zero: the next call, or replay, starts anew)
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+            last = atomicAdd(g.done, 1u) == gridDim.x - 1;
+            if (last) *g.done = 0;
+        }
+        __syncthreads();
+        if (!last) return;
+        __threadfence();
+    }
+    for (int e = tid; e < E; e += kChooseWaves * 64) set[e] = 0;
+    __syncthreads();
+    for (int a = tid; a < g.T * k; a += kChooseWaves * 64) {
+        const int e = ids[a];
+        if (one) {
+            g.ids[a] = e;
+            g.weights[a] = weights[a];
+        }
+        if (e >= 0) atomicOr(&set[e], 1ull << (a / k));
     }
     __syncthreads();
     // experts in use, in id order, and where their tokens start: one wave,
@@ -218,13 +167,8 @@ __global__ __launch_bounds__(kChooseWaves * 64) void k_choose(MoeArgs g) {
             const uint64_t used = __ballot(c > 0);
             const int incl = wave_inclusive_sum(c);
             if (e < E) base[e] = rows + incl - c;
-            if (c > 0) {
-                MoeExpert a;
-                a.tokens = s;
-                a.expert = e;
-                a.base = rows + incl - c;
-                g.active[n_act + mask_rank(used)] = a;
-            }
+            if (c > 0)
+                g.active[n_act + mask_rank(used)] = MoeExpert{s, e, rows + incl - c};
             n_act += __popcll(used);
             rows += __builtin_amdgcn_readlane(incl, 63);
         }
@@ -232,13 +176,12 @@ __global__ __launch_bounds__(kChooseWaves * 64) void k_choose(MoeArgs g) {
     }
     __syncthreads();
     // the weight of each (expert, token) row, and the token
-    for (int a = tid; a < g.T * g.rule.k; a += kChooseWaves * 64) {
-        const int t = a / g.rule.k;
-        const int e = g.ids[a];
+    for (int a = tid; a < g.T * k; a += kChooseWaves * 64) {
+        const int e = ids[a], tok = a / k;
         if (e < 0) continue;
-        const int r = base[e] + __popcll(set[e] & ((1ull << t) - 1));
-        g.row_weight[r] = g.weights[a];
-        g.row_token[r] = t;
+        const int r = base[e] + __popcll(set[e] & ((1ull << tok) - 1));
+        g.row_weight[r] = weights[a];
+        g.row_token[r] = tok;
     }
 }
 
@@ -246,181 +189,307 @@ __global__ __launch_bounds__(kChooseWaves * 64) void k_choose(MoeArgs g) {
 // 16 channels of one expert per workgroup, K split over the waves.
 constexpr int kUpWaves = 4;
 
-template <bool I8, int RT>
+template <bool I8>
+struct KindOf { typedef Bf16Rows type; };
+template <>
+struct KindOf<true> { typedef WideRows type; };
+
+template <bool I8, int FOLD, int RT>
 __device__ __forceinline__ void up_tile(const MoeArgs &g, const MoeExpert &a,
                                         int cnt, int n0, f32x4 *part) {
-    const int lane = lane_id(), l16 = lane & 15, q = lane >> 4;
-    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    typedef RowStream<typename KindOf<I8>::type, 2, FOLD, RT, 1> S;
+    const int tid = threadIdx.x, lane = lane_id();
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     constexpr int kB = I8 ? 1 : 2;
-    const int n = n0 + l16 < g.I ? n0 + l16 : g.I - 1;
     const char *mat = static_cast<const char *>(g.gate_up) +
                       a.expert * g.gate_up_stride * kB;
-    const char *w[2] = {mat + static_cast<int64_t>(n) * g.H * kB,
-                        mat + (static_cast<int64_t>(g.I) + n) * g.H * kB};
-    const uint16_t *x[RT][1];
+    const char *w[2] = {mat, mat + static_cast<int64_t>(g.I) * g.H * kB};
+    const char *x[1] = {reinterpret_cast<const char *>(g.x)};
+    uint32_t wo[S::LD], xo[RT];
+#pragma unroll
+    for (int j = 0; j < S::LD; ++j) {
+        const int n = n0 + S::row(j) < g.I ? n0 + S::row(j) : g.I - 1;
+        wo[j] = static_cast<uint32_t>(kB) * n * g.H;
+    }
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-        const int i = r * 16 + l16;
-        const int t = g.row_token[a.base + (i < cnt ? i : cnt - 1)];
-        x[r][0] = g.x + static_cast<int64_t>(t) * g.ldx;
+        // the i-th token of the set, the last one past the end
+        const int i = S::token(r);
+        unsigned long long left = a.tokens;
+        for (int c = 1; c < cnt; ++c)
+            if (c <= i) left &= left - 1;
+        xo[r] = 2u * __builtin_ctzll(left) * static_cast<uint32_t>(g.ldx);
     }
-    f32x4 acc[2][RT] = {};
+    f32x4 acc[2][S::kAcc] = {};
     int k0, k1;
-    share(g.H, Weights<I8>::kK, kUpWaves, wv, k0, k1);
-    stream<I8, 2, RT, 1>(w, x, k0, k1, g.H, acc);
+    share(g.H, S::kWindow, kUpWaves, wv, k0, k1);
+    S::run(w, wo, x, xo, k0, k1, g.H, acc);
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
-            part[((wv * 2 + m) * RT + r) * 64 + lane] = acc[m][r];
+        for (int r = 0; r < S::kAcc; ++r)
+            part[((wv * 2 + m) * S::kAcc + r) * 64 + lane] = acc[m][r];
     __syncthreads();
-    for (int r = wv; r < RT; r += kUpWaves) {
-        f32x4 s[2];
+    const float *f = reinterpret_cast<const float *>(part);
+    for (int o = tid; o < 16 * cnt; o += kUpWaves * 64) {
+        const int n = o & 15, t = o >> 4, nn = n0 + n;
+        if (nn >= g.I) continue;
+        float v[2];
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-            s[m] = part[(m * RT + r) * 64 + lane];
-            for (int v = 1; v < kUpWaves; ++v) {
-                const f32x4 b = part[((v * 2 + m) * RT + r) * 64 + lane];
-                s[m].x += b.x; s[m].y += b.y; s[m].z += b.z; s[m].w += b.w;
-            }
-        }
-        const int i = r * 16 + l16;
-        if (i >= cnt) continue;
-        const int64_t row = static_cast<int64_t>(a.base + i) * g.I;
+            v[m] = 0.f;
+            for (int u = 0; u < kUpWaves; ++u)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int nn = n0 + 4 * q + c;
-            if (nn >= g.I) continue;
-            float gt = s[0][c], up = s[1][c];
-            if (I8) {
-                const float *sc = g.gate_up_scale + static_cast<int64_t>(a.expert) * 2 * g.I;
-                gt *= sc[nn];
-                up *= sc[g.I + nn];
-            }
-            const float h = gt / (1.0f + expf(-gt)) * up;
-            const uint16_t hi = f32_to_bf16(h);
-            const float rest = h - bf16_to_f32(hi);
-            g.h_hi[row + nn] = hi;
-            // (an infinite h has no finite rest)
-            g.h_lo[row + nn] = fabsf(h) <= __FLT_MAX__ ? f32_to_bf16(rest) : 0;
+                for (int b = 0; b < S::kParts; ++b) {
+                    int c, at;
+                    S::where(n, t, b, c, at);
+                    v[m] += f[((u * 2 + m) * S::kAcc + c) * 256 + at];
+                }
         }
+        if (I8) {
+            const float *sc = g.gate_up_scale + static_cast<int64_t>(a.expert) * 2 * g.I;
+            v[0] *= sc[nn];
+            v[1] *= sc[g.I + nn];
+        }
+        const float h = v[0] / (1.0f + expf(-v[0])) * v[1];
+        const uint16_t hi = f32_to_bf16(h);
+        const int64_t at = static_cast<int64_t>(a.base + t) * g.I + nn;
+        g.h_hi[at] = hi;
+        // (an infinite h has no finite rest)
+        g.h_lo[at] = fabsf(h) <= __FLT_MAX__ ? f32_to_bf16(h - bf16_to_f32(hi)) : 0;
     }
 }
 
-template <bool I8>
-__global__ __launch_bounds__(kUpWaves * 64) void k_moe_up(MoeArgs g) {
+// MOST: tokens of the call at most 4, 8 or any number; one expert's tokens
+// choose the product's form below that. (An instance for few tokens keeps its
+// registers: with every form in it, it spilled.)
+template <bool I8, int MOST>
+__global__ __launch_bounds__(kUpWaves * 64, 4) void k_moe_up(MoeArgs g) {
+    // (most: two matrices times four results)
     __shared__ f32x4 part[kUpWaves * 2 * 4 * 64];
-    const int a = blockIdx.y;
-    if (a >= *g.n_active) return;
-    const MoeExpert ex = g.active[a];
+    // (the table has room for every blockIdx.y: both reads at once)
+    const MoeExpert ex = g.active[blockIdx.y];
+    if (static_cast<int>(blockIdx.y) >= *g.n_active) return;
     const int cnt = __popcll(ex.tokens);
     const int n0 = blockIdx.x * 16;
-    if (cnt <= 16) up_tile<I8, 1>(g, ex, cnt, n0, part);
-    else if (cnt <= 32) up_tile<I8, 2>(g, ex, cnt, n0, part);
-    else up_tile<I8, 4>(g, ex, cnt, n0, part);
+    if (MOST <= 4 || cnt <= 4) {
+        up_tile<I8, 4, 1>(g, ex, cnt, n0, part);
+    } else if (MOST <= 8 || cnt <= 8) {
+        if constexpr (MOST > 4) up_tile<I8, 2, 1>(g, ex, cnt, n0, part);
+    } else if constexpr (MOST > 8) {
+        for (int t0 = 0; t0 < cnt; t0 += 16) {
+            MoeExpert some = ex;
+            some.base += t0;
+            for (int c = 0; c < t0; ++c) some.tokens &= some.tokens - 1;
+            if (t0) __syncthreads();            // part is free again
+            up_tile<I8, 1, 1>(g, some, cnt - t0 < 16 ? cnt - t0 : 16, n0, part);
+        }
+    }
 }
 
 // ---- down and weighted sum -----------------------------------------------------
-// 16 output channels per workgroup. A unit is an expert and a share of its K;
-// each wave adds its units' weighted rows to its own sums (LDS), which are
-// joined in wave order: no atomics, so the result does not depend on timing.
+// A workgroup makes 16 (or 8) output channels of every token, from the
+// experts in use (or a share of them, blockIdx.y). A unit is an expert and a
+// share of its K; each wave adds its units' weighted rows to its own sums
+// (LDS), which are joined in wave order: no atomics, so the result does not
+// depend on timing. With several shares of the experts their sums are joined
+// by k_moe_join.
 constexpr int kDownWaves = 8;
 
-template <bool I8, int RT>
+// REGIONS: sums of a wave that a folded product's parts may go to at once (4,
+// or 1: the parts are added one after another). ROWS: channels of the
+// workgroup.
+template <bool I8, int FOLD, int ROWS, int REGIONS>
 __device__ __forceinline__ void down_unit(const MoeArgs &g, const MoeExpert &a,
-                                          int cnt, int n0, int k0, int k1,
+                                          int cnt, int n0, int split, int part,
                                           f32x4 *sum) {
+    typedef RowStream<typename KindOf<I8>::type, 1, FOLD, 1, 2,
+                      FOLD == 1 ? 0 : ROWS * FOLD / 16> S;
     const int lane = lane_id(), l16 = lane & 15, q = lane >> 4;
     constexpr int kB = I8 ? 1 : 2;
-    const int n = n0 + l16 < g.H ? n0 + l16 : g.H - 1;
     const char *w[1] = {static_cast<const char *>(g.down) +
-                        (a.expert * g.down_stride +
-                         static_cast<int64_t>(n) * g.I) * kB};
-    const uint16_t *x[RT][2];
+                        a.expert * g.down_stride * kB};
+    const int64_t first = static_cast<int64_t>(a.base) * g.I;
+    const char *x[2] = {reinterpret_cast<const char *>(g.h_hi + first),
+                        reinterpret_cast<const char *>(g.h_lo + first)};
+    uint32_t wo[S::LD], xo[1];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        const int i = r * 16 + l16;
-        const int64_t row = static_cast<int64_t>(a.base + (i < cnt ? i : cnt - 1)) * g.I;
-        x[r][0] = g.h_hi + row;
-        x[r][1] = g.h_lo + row;
+    for (int j = 0; j < S::LD; ++j) {
+        const int n = n0 + S::row(j) < g.H ? n0 + S::row(j) : g.H - 1;
+        wo[j] = static_cast<uint32_t>(kB) * n * g.I;
     }
-    f32x4 acc[1][RT] = {};
-    stream<I8, 1, RT, 2>(w, x, k0, k1, g.I, acc);
-    f32x4 sc = {1.f, 1.f, 1.f, 1.f};
+    // this lane's token among the expert's, its weight, and the scales of the
+    // channels it will hold: on their way while the products are made
+    const int i = S::token(0), row = a.base + (i < cnt ? i : cnt - 1);
+    xo[0] = 2u * (row - a.base) * g.I;
+    const int t = g.row_token[row];
+    const float wt = g.row_weight[row];
+    // channel of value 0 in accumulator r: folded, the lanes whose row and
+    // column parts agree hold 4 channels of a token
+    constexpr int kRows = S::kRows;
+    const int c0 = FOLD == 1 ? 4 * q : 4 * q % kRows;
+    f32x4 scale[S::kAcc];
     if (I8) {
+        const float *sc = g.down_scale + static_cast<int64_t>(a.expert) * g.H;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int nn = n0 + 4 * q + c;
-            sc[c] = g.down_scale[static_cast<int64_t>(a.expert) * g.H +
-                                 (nn < g.H ? nn : g.H - 1)];
-        }
+        for (int r = 0; r < S::kAcc; ++r)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int n = n0 + r * kRows + c0 + e;
+                scale[r][e] = sc[n < g.H ? n : g.H - 1];
+            }
     }
+    f32x4 acc[1][S::kAcc] = {};
+    int k0, k1;
+    share(g.I, S::kWindow, split, part, k0, k1);
+    S::run(w, wo, x, xo, k0, k1, g.I, acc);
+    const int b = FOLD == 1 ? 0 : l16 / kRows;
+    const bool mine = (FOLD == 1 || 4 * q / kRows == b) && i < cnt;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        const int i = r * 16 + l16;
-        if (i >= cnt) continue;
-        const int t = g.row_token[a.base + i];
-        const float wt = g.row_weight[a.base + i];
-        f32x4 &s = sum[t * 4 + q];
-        f32x4 v = s;
+    for (int turn = 0; turn < (REGIONS == 1 ? S::kParts : 1); ++turn) {
+        if (mine && (REGIONS > 1 || b == turn)) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] += acc[0][r][c] * sc[c] * wt;
-        s = v;
+            for (int r = 0; r < S::kAcc; ++r) {
+                f32x4 v = acc[0][r];
+                if (I8) v *= scale[r];
+                f32x4 &y = sum[((REGIONS > 1 ? b * g.T : 0) + t) * (ROWS / 4) +
+                               (r * kRows + c0) / 4];
+                y += v * wt;
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
-template <bool I8>
-__global__ __launch_bounds__(kDownWaves * 64) void k_moe_down(MoeArgs g) {
-    extern __shared__ f32x4 sums[];               // [waves][T][4]
+// A row whose weights are NaN (a NaN logit) is NaN, also where no expert
+// could be chosen.
+__device__ __forceinline__ void store_token(const MoeArgs &g, int t, int n, float s) {
+    const float w = g.weights[t * g.rule.k];
+    g.out[static_cast<int64_t>(t) * g.ldo + n] =
+        f32_to_bf16(w != w ? __builtin_nanf("") : s);
+}
+
+// MOST as in k_moe_up; ROWS: channels a workgroup makes.
+template <bool I8, int MOST, int ROWS>
+__global__ __launch_bounds__(kDownWaves * 64, 4) void k_moe_down(MoeArgs g, int most) {
+    constexpr int kRows = ROWS, kRegions = MOST <= 8 ? 4 : 1;
+    // sums [waves][regions][T][kRows / 4], then this share's experts (read
+    // once: a read before each unit would hold its first loads back)
+    extern __shared__ f32x4 sums[];
+    MoeExpert *experts = reinterpret_cast<MoeExpert *>(
+        sums + kDownWaves * kRegions * g.T * (kRows / 4));
     const int tid = threadIdx.x, lane = lane_id();
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n0 = blockIdx.x * 16;
-    f32x4 *mine = sums + wv * g.T * 4;
-    for (int i = lane; i < g.T * 4; i += 64) mine[i] = f32x4{0, 0, 0, 0};
-    const int n_act = *g.n_active;
+    const int n0 = blockIdx.x * kRows, each = kRegions * g.T * (kRows / 4);
+    f32x4 *mine = sums + wv * each;
+    for (int i = lane; i < each; i += 64) mine[i] = f32x4{0, 0, 0, 0};
+    // this share of the experts (a single share reads the table without
+    // waiting for how many entries count: it has `most`)
+    if (gridDim.y == 1)
+        for (int i = tid; i < most; i += kDownWaves * 64) experts[i] = g.active[i];
+    const int n_all = *g.n_active, per = (n_all + gridDim.y - 1) / gridDim.y;
+    const int a0 = blockIdx.y * per, left = n_all - a0;
+    const int n_act = left < per ? (left > 0 ? left : 0) : per;
+    if (gridDim.y > 1)
+        for (int i = tid; i < n_act; i += kDownWaves * 64)
+            experts[i] = g.active[a0 + i];
+    __syncthreads();
     // shares of K so that few experts still occupy every wave
     int split = 1;
     while (n_act * split < kDownWaves && split < kDownWaves) split *= 2;
     for (int u = wv; u < n_act * split; u += kDownWaves) {
-        const MoeExpert ex = g.active[u / split];
-        const int cnt = __popcll(ex.tokens);
-        int k0, k1;
-        share(g.I, Weights<I8>::kK, split, u % split, k0, k1);
-        if (cnt <= 16) down_unit<I8, 1>(g, ex, cnt, n0, k0, k1, mine);
-        else if (cnt <= 32) down_unit<I8, 2>(g, ex, cnt, n0, k0, k1, mine);
-        else down_unit<I8, 4>(g, ex, cnt, n0, k0, k1, mine);
+        MoeExpert ex = experts[u / split];
+        ex.expert = __builtin_amdgcn_readfirstlane(ex.expert);
+        ex.base = __builtin_amdgcn_readfirstlane(ex.base);
+        const int cnt = __popcll(ex.tokens), part = u % split;
+        if (MOST <= 4 || cnt <= 4) {
+            down_unit<I8, 4, ROWS, kRegions>(g, ex, cnt, n0, split, part, mine);
+        } else if (MOST <= 8 || cnt <= 8) {
+            if constexpr (MOST > 4) down_unit<I8, 2, ROWS, kRegions>(g, ex, cnt, n0, split, part, mine);
+        } else if constexpr (MOST > 8) {
+            for (int t0 = 0; t0 < cnt; t0 += 16) {
+                MoeExpert some = ex;
+                some.base += t0;
+                down_unit<I8, 1, ROWS, kRegions>(g, some, cnt - t0 < 16 ? cnt - t0 : 16, n0,
+                                    split, part, mine);
+            }
+        }
     }
     __syncthreads();
     const float *fs = reinterpret_cast<const float *>(sums);
-    for (int i = tid; i < g.T * 16; i += kDownWaves * 64) {
+    for (int i = tid; i < g.T * kRows; i += kDownWaves * 64) {
         float s = 0.f;
-        for (int v = 0; v < kDownWaves; ++v) s += fs[v * g.T * 16 + i];
-        const int t = i >> 4, n = n0 + (i & 15);
-        // a row whose weights are NaN (a NaN logit) is NaN, also where no
-        // expert could be chosen
-        if (g.weights[t * g.rule.k] != g.weights[t * g.rule.k])
-            s = __builtin_nanf("");
-        if (n < g.H) g.out[static_cast<int64_t>(t) * g.ldo + n] = f32_to_bf16(s);
+        for (int v = 0; v < kDownWaves * kRegions; ++v) s += fs[v * g.T * kRows + i];
+        const int t = i / kRows, n = n0 + i % kRows;
+        if (n >= g.H) continue;
+        if (gridDim.y > 1)
+            g.part[(static_cast<int64_t>(blockIdx.y) * g.T + t) * g.H + n] = s;
+        else
+            store_token(g, t, n, s);
     }
+}
+
+__global__ __launch_bounds__(kBlock) void k_moe_join(MoeArgs g, int shares) {
+    const int n = blockIdx.x * kBlock + threadIdx.x, t = blockIdx.y;
+    if (n >= g.H) return;
+    float s = 0.f;
+    for (int p = 0; p < shares; ++p)
+        s += g.part[(static_cast<int64_t>(p) * g.T + t) * g.H + n];
+    store_token(g, t, n, s);
+}
+
+template <bool I8>
+hipError_t up_any(const MoeArgs &g, dim3 gr, dim3 bl, hipStream_t s) {
+    if (g.T <= 4) hipLaunchKernelGGL((k_moe_up<I8, 4>), gr, bl, 0, s, g);
+    else if (g.T <= 8) hipLaunchKernelGGL((k_moe_up<I8, 8>), gr, bl, 0, s, g);
+    else hipLaunchKernelGGL((k_moe_up<I8, kMoeTokens>), gr, bl, 0, s, g);
+    return hipGetLastError();
+}
+
+template <bool I8, int MOST, int ROWS>
+hipError_t down_as(const MoeArgs &g, int shares, hipStream_t s) {
+    const int rows = g.T * g.rule.k;
+    const int most = g.rule.E < rows ? g.rule.E : rows;   // experts in use
+    const size_t lds = sizeof(float) * ROWS * kDownWaves * (MOST <= 8 ? 4 : 1) * g.T +
+                       sizeof(MoeExpert) * ((most + shares - 1) / shares);
+    hipLaunchKernelGGL((k_moe_down<I8, MOST, ROWS>),
+                       dim3((g.H + ROWS - 1) / ROWS, shares),
+                       dim3(kDownWaves * 64), lds, s, g, most);
+    return hipGetLastError();
+}
+
+template <bool I8>
+hipError_t down_any(const ue_ctx &c, const MoeArgs &g, int shares, hipStream_t s) {
+    if (g.T > 8) return down_as<I8, kMoeTokens, 16>(g, shares, s);
+    // 8 channels a workgroup where 16 would leave CUs without one
+    const bool narrow = (g.H + 15) / 16 < 4 * c.num_cu;
+    if (g.T > 4)
+        return narrow ? down_as<I8, 8, 8>(g, shares, s)
+                      : down_as<I8, 8, 16>(g, shares, s);
+    return narrow ? down_as<I8, 4, 8>(g, shares, s)
+                  : down_as<I8, 4, 16>(g, shares, s);
 }
 
 }  // namespace
 
+int moe_router_parts(int hidden) { return router_parts(hidden); }
+
 hipError_t launch_moe_route(const MoeArgs &g, hipStream_t s) {
-    const int rt = (g.T + 15) / 16;
-    const dim3 rg((g.rule.E + 15) / 16), rb(kRouterWaves * 64);
-    if (rt == 1) hipLaunchKernelGGL((k_router<1>), rg, rb, 0, s, g);
-    else if (rt == 2) hipLaunchKernelGGL((k_router<2>), rg, rb, 0, s, g);
-    else hipLaunchKernelGGL((k_router<4>), rg, rb, 0, s, g);
+    const dim3 rg((g.rule.E + 15) / 16, moe_router_parts(g.H)), rb(kRouterWaves * 64);
+    if (g.T <= 4) hipLaunchKernelGGL((k_router<4, 1>), rg, rb, 0, s, g);
+    else if (g.T <= 8) hipLaunchKernelGGL((k_router<2, 1>), rg, rb, 0, s, g);
+    else if (g.T <= 16) hipLaunchKernelGGL((k_router<1, 1>), rg, rb, 0, s, g);
+    else if (g.T <= 32) hipLaunchKernelGGL((k_router<1, 2>), rg, rb, 0, s, g);
+    else hipLaunchKernelGGL((k_router<1, 4>), rg, rb, 0, s, g);
     hipError_t he = hipGetLastError();
     if (he != hipSuccess) return he;
-    const dim3 cb(kChooseWaves * 64);
+    const dim3 cg((g.T + kChooseWaves - 1) / kChooseWaves), cb(kChooseWaves * 64);
     switch (lane_slots(g.rule.E)) {
-        case 1: hipLaunchKernelGGL((k_choose<1>), dim3(1), cb, 0, s, g); break;
-        case 2: hipLaunchKernelGGL((k_choose<2>), dim3(1), cb, 0, s, g); break;
-        case 4: hipLaunchKernelGGL((k_choose<4>), dim3(1), cb, 0, s, g); break;
-        case 8: hipLaunchKernelGGL((k_choose<8>), dim3(1), cb, 0, s, g); break;
-        default: hipLaunchKernelGGL((k_choose<16>), dim3(1), cb, 0, s, g); break;
+        case 1: hipLaunchKernelGGL((k_choose<1>), cg, cb, 0, s, g); break;
+        case 2: hipLaunchKernelGGL((k_choose<2>), cg, cb, 0, s, g); break;
+        case 4: hipLaunchKernelGGL((k_choose<4>), cg, cb, 0, s, g); break;
+        case 8: hipLaunchKernelGGL((k_choose<8>), cg, cb, 0, s, g); break;
+        default: hipLaunchKernelGGL((k_choose<16>), cg, cb, 0, s, g); break;
     }
     return hipGetLastError();
 }
@@ -429,16 +498,26 @@ hipError_t launch_moe_up(const MoeArgs &g, hipStream_t s) {
     const int rows = g.T * g.rule.k;
     const int most = g.rule.E < rows ? g.rule.E : rows;   // experts in use
     const dim3 gr((g.I + 15) / 16, most), bl(kUpWaves * 64);
-    if (g.i8) hipLaunchKernelGGL((k_moe_up<true>), gr, bl, 0, s, g);
-    else hipLaunchKernelGGL((k_moe_up<false>), gr, bl, 0, s, g);
-    return hipGetLastError();
+    return g.i8 ? up_any<true>(g, gr, bl, s) : up_any<false>(g, gr, bl, s);
 }
 
-hipError_t launch_moe_down(const MoeArgs &g, hipStream_t s) {
-    const dim3 gr((g.H + 15) / 16), bl(kDownWaves * 64);
-    const size_t lds = sizeof(float) * 16 * kDownWaves * g.T;
-    if (g.i8) hipLaunchKernelGGL((k_moe_down<true>), gr, bl, lds, s, g);
-    else hipLaunchKernelGGL((k_moe_down<false>), gr, bl, lds, s, g);
+// Shares of the experts in the second product: with more than 8 tokens many
+// experts are in use, and enough workgroups for every CU several times over
+// level their load.
+int moe_down_shares(int hidden, int T, int num_cu) {
+    if (T <= 8) return 1;
+    const int cols = (hidden + 15) / 16;
+    const int want = (4 * num_cu + cols - 1) / cols;
+    return want < 1 ? 1 : want > 8 ? 8 : want;
+}
+
+hipError_t launch_moe_down(const ue_ctx &c, const MoeArgs &g, hipStream_t s) {
+    const int shares = moe_down_shares(g.H, g.T, c.num_cu);
+    hipError_t he = g.i8 ? down_any<true>(c, g, shares, s)
+                         : down_any<false>(c, g, shares, s);
+    if (he != hipSuccess || shares == 1) return he;
+    hipLaunchKernelGGL(k_moe_join, dim3((g.H + kBlock - 1) / kBlock, g.T),
+                       dim3(kBlock), 0, s, g, shares);
     return hipGetLastError();
 }
 

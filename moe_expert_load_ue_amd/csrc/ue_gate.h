@@ -51,7 +51,8 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
 }
 
 // One round per expert taken: the largest key of the wave, its lowest id.
-// `emit(r, id)` is called with wave-uniform arguments. Returns how many were
+// `emit(r, id, slot)` is called with wave-uniform arguments (id = L V + slot
+// of lane L). Returns how many were
 // taken (fewer than k when the rest are -inf or NaN). The keys are consumed.
 template <int V, class Emit>
 __device__ __forceinline__ int take_best(uint32_t (&key)[V], int k, Emit emit) {
@@ -76,7 +77,7 @@ __device__ __forceinline__ int take_best(uint32_t (&key)[V], int k, Emit emit) {
             if (hit) id = L * V + i;
             if (hit && lane == L) key[i] = 0;
         }
-        emit(r, id);
+        emit(r, id, id & (V - 1));
     }
     return k;
 }
@@ -93,12 +94,11 @@ __device__ __forceinline__ float wave_top(float v) {
 }
 
 // One token's choice by one wave. `x`: its logits, slot i of lane l expert
-// l V + i, -inf past the last; `logit(id)` reads one again; `ids`, `weights`:
-// its k results; `taken(id)` is called, wave-uniform, for each expert taken.
-template <int V, class Logit, class Taken>
+// l V + i, -inf past the last; `ids`, `weights`: its k results; `taken(id)` is called, wave-uniform, for each expert taken.
+template <int V, class Taken>
 __device__ __forceinline__ void gate_row(const GateRule &g, const float (&x)[V],
-                                         Logit logit, int32_t *ids,
-                                         float *weights, Taken taken) {
+                                         int32_t *ids, float *weights,
+                                         Taken taken) {
     const int lane = lane_id();
     bool nan = false;
     uint32_t key[V];
@@ -129,24 +129,32 @@ __device__ __forceinline__ void gate_row(const GateRule &g, const float (&x)[V],
         }
     }
     const bool poisoned = __ballot(nan) != 0;
-    // lane j keeps rounds j, j + 64, ...: the last one in a register, with
-    // more than 64 rounds all of them in `ids`
+    // lane j keeps the ids and logits of rounds j, j + 64, ...: the last one in
+    // registers, with more than 64 rounds all of them in `ids` and `weights`
     int my = -1;
+    float mine = 0.f;
     const bool many = g.k > 64;
-    const int got = take_best<V>(key, g.k, [&](int r, int id) {
+    const int got = take_best<V>(key, g.k, [&](int r, int id, int slot) {
+        float v = x[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) v = slot == i ? x[i] : v;
+        v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), id / V));
         if (lane == (r & 63)) {
             my = id;
-            if (many) ids[r] = id;
+            mine = v;
+            if (many) {
+                ids[r] = id;
+                weights[r] = v;
+            }
         }
         taken(id);
     });
-    auto score = [&](int id) {
-        const float v = logit(id);
+    auto score = [&](float v) {
         return g.sigmoid ? sigmoid_of(v) : expf(finite_top(v) - top);
     };
     float sum = 0.f, p = 0.f;
     for (int r = lane; r < got; r += 64) {
-        p = score(many ? ids[r] : my);
+        p = score(many ? weights[r] : mine);
         sum += p;
     }
     // (the softmax's own denominator cancels in the renormalised weights)
@@ -155,7 +163,7 @@ __device__ __forceinline__ void gate_row(const GateRule &g, const float (&x)[V],
     else if (!g.sigmoid) n = all;
     for (int r = lane; r < g.k; r += 64) {
         const bool have = r < got;
-        if (have && many) p = score(ids[r]);
+        if (have && many) p = score(weights[r]);
         const float w = have ? p / n * g.scale : 0.f;
         weights[r] = poisoned ? __builtin_nanf("") : w;
         if (!many || !have) ids[r] = have ? my : -1;

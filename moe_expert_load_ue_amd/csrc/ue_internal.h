@@ -110,13 +110,16 @@ struct ue_ctx {
 
     // Registered layer (ue_register_layer) and its workspace: logits, the
     // experts in use, and per chosen (expert, token) row its weight, token
-    // and hidden activations. Every word a call reads it has written itself.
+    // and hidden activations. Every word a call reads it has
+    // written itself, but for a counter that is zero between calls.
     bool has_layer = false;
     ue_layer layer{};
     int layer_tokens = 0;          // most tokens of one call
     void *layer_ws = nullptr;
-    float *moe_logits = nullptr;   // [layer_tokens][E]
+    float *moe_logits = nullptr;   // [parts][layer_tokens][E]
+    uint32_t *moe_done = nullptr;
     int32_t *moe_n_active = nullptr;
+    float *moe_part = nullptr;     // [shares][layer_tokens][hidden]
     ue::MoeExpert *moe_active = nullptr;   // [E]
     float *moe_row_weight = nullptr;       // [layer_tokens * k]
     int32_t *moe_row_token = nullptr;      // [layer_tokens * k]
@@ -246,20 +249,26 @@ struct MoeArgs {
     int64_t gate_up_stride, down_stride;   // elements
     const float *gate_up_scale, *down_scale;
     float *logits;
+    uint32_t *done;             // workgroups of the choice that ended; 0 between calls
     int32_t *n_active;
     MoeExpert *active;
     float *row_weight;
     int32_t *row_token;
     uint16_t *h_hi, *h_lo;
+    float *part;                // [shares][T][H]
     uint16_t *out;
     int64_t ldo;
     int32_t *ids;
     float *weights;
 };
+// Parts a router's sum over `hidden` is made in.
+int moe_router_parts(int hidden);
+// Shares of the experts the second product's sums are made in.
+int moe_down_shares(int hidden, int T, int num_cu);
 // In order: router and choice, gate and up, down and weighted sum.
 hipError_t launch_moe_route(const MoeArgs &g, hipStream_t s);
 hipError_t launch_moe_up(const MoeArgs &g, hipStream_t s);
-hipError_t launch_moe_down(const MoeArgs &g, hipStream_t s);
+hipError_t launch_moe_down(const ue_ctx &c, const MoeArgs &g, hipStream_t s);
 
 // Error text and kernel timing, shared by the entry points' files.
 int fail(ue_ctx *c, int code, const char *fmt, ...)

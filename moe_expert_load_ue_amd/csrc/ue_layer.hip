@@ -249,6 +249,11 @@ int ue_register_layer(ue_ctx *ctx, const ue_layer *l) {
         return fail(ctx, UE_ESHAPE, "ue_register_layer: strides %lld and %lld",
                     static_cast<long long>(l->gate_up_stride),
                     static_cast<long long>(l->down_stride));
+    // the kernels address one expert's matrix, the router and an expert's
+    // hidden rows with 32 bits
+    if (2 * mat * (i8 ? 1 : 2) > 0xFFFFFFFFll ||
+        2ll * ctx->E * l->hidden > 0xFFFFFFFFll)
+        return fail(ctx, UE_ESHAPE, "ue_register_layer: a matrix of 4 GiB");
     if (int rc = check_rule(ctx, "ue_register_layer", l->score, l->bias)) return rc;
     if (!l->router || !l->gate_up || !l->down ||
         (i8 && (!l->gate_up_scale || !l->down_scale)))
@@ -268,8 +273,11 @@ int ue_register_layer(ue_ctx *ctx, const ue_layer *l) {
         off = round_up(off + bytes, 256);
         return o;
     };
-    const size_t o_logits = take(sizeof(float) * T * ctx->E);
+    const size_t o_logits = take(sizeof(float) * ue::moe_router_parts(l->hidden) * T * ctx->E);
     const size_t o_n = take(sizeof(int32_t));
+    const size_t o_done = take(sizeof(uint32_t));
+    const size_t o_part = take(sizeof(float) * l->hidden * T *
+                               ue::moe_down_shares(l->hidden, T, ctx->num_cu));
     const size_t o_act = take(sizeof(ue::MoeExpert) * ctx->E);
     const size_t o_w = take(sizeof(float) * rows);
     const size_t o_t = take(sizeof(int32_t) * rows);
@@ -277,13 +285,21 @@ int ue_register_layer(ue_ctx *ctx, const ue_layer *l) {
     void *ws = nullptr;
     if (hipMalloc(&ws, off) != hipSuccess)
         return fail(ctx, UE_ENOMEM, "ue_register_layer: %zu bytes of workspace", off);
+    char *b = static_cast<char *>(ws);
+    hipError_t he = hipMemset(b + o_done, 0, sizeof(uint32_t));
+    if (he == hipSuccess) he = hipDeviceSynchronize();
+    if (he != hipSuccess) {
+        (void)hipFree(ws);
+        return hip_fail(ctx, he, "ue_register_layer: workspace");
+    }
     if (ctx->layer_ws) {
         (void)hipDeviceSynchronize();
         (void)hipFree(ctx->layer_ws);
     }
-    char *b = static_cast<char *>(ws);
     ctx->layer_ws = ws;
     ctx->moe_logits = reinterpret_cast<float *>(b + o_logits);
+    ctx->moe_done = reinterpret_cast<uint32_t *>(b + o_done);
+    ctx->moe_part = reinterpret_cast<float *>(b + o_part);
     ctx->moe_n_active = reinterpret_cast<int32_t *>(b + o_n);
     ctx->moe_active = reinterpret_cast<ue::MoeExpert *>(b + o_act);
     ctx->moe_row_weight = reinterpret_cast<float *>(b + o_w);
@@ -306,7 +322,8 @@ int ue_moe_tokens(ue_ctx *ctx, const void *x, int64_t ldx, int32_t T,
     if (T < 0 || T > ctx->layer_tokens)
         return fail(ctx, UE_ESHAPE, "ue_moe_tokens: T=%d outside 0..%d", T,
                     ctx->layer_tokens);
-    if (ldx < l.hidden || ldx % 8 || ldo < l.hidden)
+    // (64 rows of x are addressed with 32 bits)
+    if (ldx < l.hidden || ldx % 8 || ldx > (1 << 24) || ldo < l.hidden)
         return fail(ctx, UE_ESHAPE, "ue_moe_tokens: ldx=%lld ldo=%lld hidden=%d",
                     static_cast<long long>(ldx), static_cast<long long>(ldo),
                     l.hidden);
@@ -332,6 +349,8 @@ int ue_moe_tokens(ue_ctx *ctx, const void *x, int64_t ldx, int32_t T,
     g.gate_up_scale = l.gate_up_scale;
     g.down_scale = l.down_scale;
     g.logits = ctx->moe_logits;
+    g.done = ctx->moe_done;
+    g.part = ctx->moe_part;
     g.n_active = ctx->moe_n_active;
     g.active = ctx->moe_active;
     g.row_weight = ctx->moe_row_weight;
@@ -350,7 +369,7 @@ int ue_moe_tokens(ue_ctx *ctx, const void *x, int64_t ldx, int32_t T,
     he = ue::launch_moe_up(g, s);
     if (he != hipSuccess) return hip_fail(ctx, he, "k_moe_up launch");
     tmark(ctx, s);
-    he = ue::launch_moe_down(g, s);
+    he = ue::launch_moe_down(*ctx, g, s);
     tmark(ctx, s);
     return he == hipSuccess ? UE_OK : hip_fail(ctx, he, "k_moe_down launch");
 }
