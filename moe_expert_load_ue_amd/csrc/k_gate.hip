@@ -62,12 +62,14 @@ __device__ __forceinline__ void load_row(const void *logits, int64_t row, int E,
 template <typename T, int V>
 __global__ __launch_bounds__(kBlock) void k_gate(GateArgs g) {
     const int waves = gridDim.x * kWaves;
+    float bias[V];
+    load_bias<V>(g.rule, bias);
     for (int t = blockIdx.x * kWaves + (threadIdx.x >> 6); t < g.T; t += waves) {
         const int64_t row = static_cast<int64_t>(t) * g.ld;
         const int64_t o = static_cast<int64_t>(t) * g.rule.k;
         float x[V];
         load_row<T, V>(g.logits, row, g.rule.E, g.vec, x);
-        gate_row<V>(g.rule, x, g.ids + o, g.weights + o, [](int) {});
+        gate_row<V>(g.rule, x, bias, g.ids + o, g.weights + o, [](int) {});
     }
 }
 

@@ -33,15 +33,142 @@ __device__ __forceinline__ void share(int K, int step, int W, int v, int &k0,
     k1 = k1 < n * step ? k1 : n * step;
 }
 
+// ---- choice ----------------------------------------------------------------
+// Every token's experts and weights, one wave per token; the workgroup that
+// ends last then lists the experts in use with their tokens (one 64-bit set
+// per expert) and the rows of all chosen (expert, token) pairs. Up to
+// kChooseWaves tokens are chosen by the router's last workgroup, without a
+// launch of their own.
+constexpr int kChooseWaves = 4;
+constexpr int kRouterK = 1024;           // of K per workgroup of the router
+
+__host__ __device__ inline int router_parts(int hidden) {
+    return (hidden + kRouterK - 1) / kRouterK;
+}
+
+// Whether this workgroup is the last of `all` to get here; what the others
+// wrote before is then visible. (The counter returns to zero: the next call,
+// or graph replay, starts anew.)
+// One wave releases and acquires for the workgroup, on either side of a
+// barrier: a fence writes back or invalidates a whole L2, and one in every
+// wave made the choice 11 us instead of 5.
+__device__ __forceinline__ bool ends_last(uint32_t *done, uint32_t all, int *sh) {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const bool last = __hip_atomic_fetch_add(done, 1u, __ATOMIC_ACQ_REL,
+                                                 __HIP_MEMORY_SCOPE_AGENT) == all - 1;
+        if (last)
+            __hip_atomic_store(done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        *sh = last;
+    }
+    __syncthreads();
+    return *sh;
+}
+
+struct ChooseLds {
+    unsigned long long set[kMaxExperts];
+    int base[kMaxExperts];
+    // one workgroup's choices stay here until they are listed
+    int32_t ids[kChooseWaves * 64];
+    float weights[kChooseWaves * 64];
+    int last;
+};
+
+// The choice of tokens t0 .. t0 + kChooseWaves - 1 by one workgroup of
+// `blocks`.
+template <int V>
+__device__ __forceinline__ void choose(const MoeArgs &g, int t0, int blocks,
+                                       ChooseLds &sh) {
+    const int tid = threadIdx.x, lane = lane_id(), wv = tid >> 6;
+    const int E = g.rule.E, k = g.rule.k, parts = router_parts(g.H);
+    constexpr int kBatch = V <= 4 ? 8 : 32 / V;      // parts loaded together
+    const int t = t0 + wv;
+    const bool one = blocks == 1 && k <= 64;
+    int32_t *ids = one ? sh.ids : g.ids;
+    float *weights = one ? sh.weights : g.weights;
+    if (t < g.T) {
+        const float *lg = g.logits + static_cast<int64_t>(t) * E;
+        float x[V], bias[V];
+        load_bias<V>(g.rule, bias);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            x[i] = lane * V + i < E ? 0.f : -__builtin_inff();
+        for (int p0 = 0; p0 < parts; p0 += kBatch) {
+            float v[kBatch][V];
+#pragma unroll
+            for (int p = 0; p < kBatch; ++p)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int e = lane * V + i;
+                    v[p][i] = p0 + p < parts && e < E
+                                  ? lg[static_cast<int64_t>(p0 + p) * g.T * E + e]
+                                  : 0.f;
+                }
+#pragma unroll
+            for (int p = 0; p < kBatch; ++p)
+#pragma unroll
+                for (int i = 0; i < V; ++i) x[i] += v[p][i];
+        }
+        gate_row<V>(g.rule, x, bias, ids + t * k, weights + t * k, [](int) {});
+    }
+    if (blocks > 1 && !ends_last(g.done, blocks, &sh.last)) return;
+    for (int e = tid; e < E; e += kChooseWaves * 64) sh.set[e] = 0;
+    __syncthreads();
+    for (int a = tid; a < g.T * k; a += kChooseWaves * 64) {
+        const int e = ids[a];
+        if (one) {
+            g.ids[a] = e;
+            g.weights[a] = weights[a];
+        }
+        if (e >= 0) atomicOr(&sh.set[e], 1ull << (a / k));
+    }
+    __syncthreads();
+    // experts in use, in id order, and where their tokens start: one wave,
+    // 64 experts at a time
+    if (wv == 0) {
+        int n_act = 0, rows = 0;
+        for (int e0 = 0; e0 < E; e0 += 64) {
+            const int e = e0 + lane;
+            const unsigned long long s = e < E ? sh.set[e] : 0;
+            const int c = __popcll(s);
+            const uint64_t used = __ballot(c > 0);
+            const int incl = wave_inclusive_sum(c);
+            if (e < E) sh.base[e] = rows + incl - c;
+            if (c > 0)
+                g.active[n_act + mask_rank(used)] = MoeExpert{s, e, rows + incl - c};
+            n_act += __popcll(used);
+            rows += __builtin_amdgcn_readlane(incl, 63);
+        }
+        if (lane == 0) *g.n_active = n_act;
+    }
+    __syncthreads();
+    // the weight of each (expert, token) row, and the token
+    for (int a = tid; a < g.T * k; a += kChooseWaves * 64) {
+        const int e = ids[a], tok = a / k;
+        if (e < 0) continue;
+        const int r = sh.base[e] + __popcll(sh.set[e] & ((1ull << tok) - 1));
+        g.row_weight[r] = weights[a];
+        g.row_token[r] = tok;
+    }
+}
+
+template <int V>
+__global__ __launch_bounds__(kChooseWaves * 64) void k_choose(MoeArgs g) {
+    __shared__ ChooseLds sh;
+    choose<V>(g, blockIdx.x * kChooseWaves, gridDim.x, sh);
+}
+
 // ---- router ---------------------------------------------------------------
 // Part sums of the logits of 16 experts per workgroup: K is split over the
 // workgroups of a column of the grid and their waves, for enough loads in
 // flight (256 experts alone make 16 workgroups: 16 us at K = 7168 and one
 // token, against 5 split). The choice adds the parts in order.
 constexpr int kRouterWaves = 4;
-constexpr int kRouterK = 1024;           // of K per workgroup
+static_assert(kRouterWaves == kChooseWaves, "the router's last workgroup chooses");
+           // of K per workgroup
 
-template <int FOLD, int RT>
+// V: lane slots of the choice made here, 0 for none (see k_choose).
+template <int FOLD, int RT, int V>
 __global__ __launch_bounds__(kRouterWaves * 64) void k_router(MoeArgs g) {
     typedef RowStream<Bf16Rows, 1, FOLD, RT, 1> S;
     __shared__ f32x4 part[kRouterWaves][S::kAcc][64];
@@ -82,106 +209,10 @@ __global__ __launch_bounds__(kRouterWaves * 64) void k_router(MoeArgs g) {
             }
         g.logits[(static_cast<int64_t>(blockIdx.y) * g.T + t) * E + e0 + n] = sum;
     }
-}
-
-// ---- choice ----------------------------------------------------------------
-// Every token's experts and weights, one wave per token; the workgroup that
-// ends last then lists the experts in use with their tokens (one 64-bit set
-// per expert) and the rows of all chosen (expert, token) pairs.
-constexpr int kChooseWaves = 4;
-
-__host__ __device__ inline int router_parts(int hidden) {
-    return (hidden + kRouterK - 1) / kRouterK;
-}
-
-template <int V>
-__global__ __launch_bounds__(kChooseWaves * 64) void k_choose(MoeArgs g) {
-    __shared__ unsigned long long set[kMaxExperts];
-    __shared__ int base[kMaxExperts];
-    __shared__ bool last;
-    // one workgroup's choices stay here until they are listed
-    __shared__ int32_t some_ids[kChooseWaves * 64];
-    __shared__ float some_weights[kChooseWaves * 64];
-    const int tid = threadIdx.x, lane = lane_id(), wv = tid >> 6;
-    const int E = g.rule.E, k = g.rule.k, parts = router_parts(g.H);
-    constexpr int kBatch = V <= 4 ? 8 : 32 / V;      // parts loaded together
-    const int t = blockIdx.x * kChooseWaves + wv;
-    const bool one = gridDim.x == 1 && k <= 64;
-    int32_t *ids = one ? some_ids : g.ids;
-    float *weights = one ? some_weights : g.weights;
-    if (t < g.T) {
-        const float *lg = g.logits + static_cast<int64_t>(t) * E;
-        float x[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            x[i] = lane * V + i < E ? 0.f : -__builtin_inff();
-        for (int p0 = 0; p0 < parts; p0 += kBatch) {
-            float v[kBatch][V];
-#pragma unroll
-            for (int p = 0; p < kBatch; ++p)
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int e = lane * V + i;
-                    v[p][i] = p0 + p < parts && e < E
-                                  ? lg[static_cast<int64_t>(p0 + p) * g.T * E + e]
-                                  : 0.f;
-                }
-#pragma unroll
-            for (int p = 0; p < kBatch; ++p)
-#pragma unroll
-                for (int i = 0; i < V; ++i) x[i] += v[p][i];
-        }
-        gate_row<V>(g.rule, x, ids + t * k, weights + t * k, [](int) {});
-    }
-    if (gridDim.x > 1) {
-        // (the counter returns to zero: the next call, or replay, starts anew)
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) {
-            last = atomicAdd(g.done, 1u) == gridDim.x - 1;
-            if (last) *g.done = 0;
-        }
-        __syncthreads();
-        if (!last) return;
-        __threadfence();
-    }
-    for (int e = tid; e < E; e += kChooseWaves * 64) set[e] = 0;
-    __syncthreads();
-    for (int a = tid; a < g.T * k; a += kChooseWaves * 64) {
-        const int e = ids[a];
-        if (one) {
-            g.ids[a] = e;
-            g.weights[a] = weights[a];
-        }
-        if (e >= 0) atomicOr(&set[e], 1ull << (a / k));
-    }
-    __syncthreads();
-    // experts in use, in id order, and where their tokens start: one wave,
-    // 64 experts at a time
-    if (wv == 0) {
-        int n_act = 0, rows = 0;
-        for (int e0 = 0; e0 < E; e0 += 64) {
-            const int e = e0 + lane;
-            const unsigned long long s = e < E ? set[e] : 0;
-            const int c = __popcll(s);
-            const uint64_t used = __ballot(c > 0);
-            const int incl = wave_inclusive_sum(c);
-            if (e < E) base[e] = rows + incl - c;
-            if (c > 0)
-                g.active[n_act + mask_rank(used)] = MoeExpert{s, e, rows + incl - c};
-            n_act += __popcll(used);
-            rows += __builtin_amdgcn_readlane(incl, 63);
-        }
-        if (lane == 0) *g.n_active = n_act;
-    }
-    __syncthreads();
-    // the weight of each (expert, token) row, and the token
-    for (int a = tid; a < g.T * k; a += kChooseWaves * 64) {
-        const int e = ids[a], tok = a / k;
-        if (e < 0) continue;
-        const int r = base[e] + __popcll(set[e] & ((1ull << tok) - 1));
-        g.row_weight[r] = weights[a];
-        g.row_token[r] = tok;
+    if constexpr (V > 0) {
+        __shared__ ChooseLds sh;
+        if (ends_last(g.done, gridDim.x * gridDim.y, &sh.last))
+            choose<V>(g, 0, 1, sh);
     }
 }
 
@@ -461,8 +492,10 @@ hipError_t down_as(const MoeArgs &g, int shares, hipStream_t s) {
 template <bool I8>
 hipError_t down_any(const ue_ctx &c, const MoeArgs &g, int shares, hipStream_t s) {
     if (g.T > 8) return down_as<I8, kMoeTokens, 16>(g, shares, s);
-    // 8 channels a workgroup where 16 would leave CUs without one
-    const bool narrow = (g.H + 15) / 16 < 4 * c.num_cu;
+    // 8 channels a workgroup where 16 would leave CUs without one (one bf16
+    // token of H=2048, I=1024: 8.2 against 13.5 us; int8, H=7168, I=2048, where
+    // it only doubles the reads of h: 32 against 24 us)
+    const bool narrow = (g.H + 15) / 16 < c.num_cu;
     if (g.T > 4)
         return narrow ? down_as<I8, 8, 8>(g, shares, s)
                       : down_as<I8, 8, 16>(g, shares, s);
@@ -474,24 +507,32 @@ hipError_t down_any(const ue_ctx &c, const MoeArgs &g, int shares, hipStream_t s
 
 int moe_router_parts(int hidden) { return router_parts(hidden); }
 
-hipError_t launch_moe_route(const MoeArgs &g, hipStream_t s) {
+template <int V>
+static hipError_t route_as(const MoeArgs &g, hipStream_t s) {
     const dim3 rg((g.rule.E + 15) / 16, moe_router_parts(g.H)), rb(kRouterWaves * 64);
-    if (g.T <= 4) hipLaunchKernelGGL((k_router<4, 1>), rg, rb, 0, s, g);
-    else if (g.T <= 8) hipLaunchKernelGGL((k_router<2, 1>), rg, rb, 0, s, g);
-    else if (g.T <= 16) hipLaunchKernelGGL((k_router<1, 1>), rg, rb, 0, s, g);
-    else if (g.T <= 32) hipLaunchKernelGGL((k_router<1, 2>), rg, rb, 0, s, g);
-    else hipLaunchKernelGGL((k_router<1, 4>), rg, rb, 0, s, g);
-    hipError_t he = hipGetLastError();
-    if (he != hipSuccess) return he;
-    const dim3 cg((g.T + kChooseWaves - 1) / kChooseWaves), cb(kChooseWaves * 64);
-    switch (lane_slots(g.rule.E)) {
-        case 1: hipLaunchKernelGGL((k_choose<1>), cg, cb, 0, s, g); break;
-        case 2: hipLaunchKernelGGL((k_choose<2>), cg, cb, 0, s, g); break;
-        case 4: hipLaunchKernelGGL((k_choose<4>), cg, cb, 0, s, g); break;
-        case 8: hipLaunchKernelGGL((k_choose<8>), cg, cb, 0, s, g); break;
-        default: hipLaunchKernelGGL((k_choose<16>), cg, cb, 0, s, g); break;
+    if (g.T <= kChooseWaves) {
+        hipLaunchKernelGGL((k_router<4, 1, V>), rg, rb, 0, s, g);
+        return hipGetLastError();
     }
+    if (g.T <= 8) hipLaunchKernelGGL((k_router<2, 1, 0>), rg, rb, 0, s, g);
+    else if (g.T <= 16) hipLaunchKernelGGL((k_router<1, 1, 0>), rg, rb, 0, s, g);
+    else if (g.T <= 32) hipLaunchKernelGGL((k_router<1, 2, 0>), rg, rb, 0, s, g);
+    else hipLaunchKernelGGL((k_router<1, 4, 0>), rg, rb, 0, s, g);
+    const hipError_t he = hipGetLastError();
+    if (he != hipSuccess) return he;
+    hipLaunchKernelGGL((k_choose<V>), dim3((g.T + kChooseWaves - 1) / kChooseWaves),
+                       dim3(kChooseWaves * 64), 0, s, g);
     return hipGetLastError();
+}
+
+hipError_t launch_moe_route(const MoeArgs &g, hipStream_t s) {
+    switch (lane_slots(g.rule.E)) {
+        case 1: return route_as<1>(g, s);
+        case 2: return route_as<2>(g, s);
+        case 4: return route_as<4>(g, s);
+        case 8: return route_as<8>(g, s);
+        default: return route_as<16>(g, s);
+    }
 }
 
 hipError_t launch_moe_up(const MoeArgs &g, hipStream_t s) {

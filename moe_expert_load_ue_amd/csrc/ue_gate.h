@@ -93,10 +93,21 @@ __device__ __forceinline__ float wave_top(float v) {
     return finite_top(__uint_as_float((m & 0x80000000u) ? m ^ 0x80000000u : ~m));
 }
 
+template <int V>
+__device__ __forceinline__ void load_bias(const GateRule &g, float (&b)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = lane_id() * V + i;
+        b[i] = g.bias && e < g.E ? g.bias[e] : 0.f;
+    }
+}
+
 // One token's choice by one wave. `x`: its logits, slot i of lane l expert
-// l V + i, -inf past the last; `ids`, `weights`: its k results; `taken(id)` is called, wave-uniform, for each expert taken.
+// l V + i, -inf past the last; `bias`: likewise, 0 where there is none (read
+// by load_bias before the logits are waited for); `ids`, `weights`: its k results; `taken(id)` is called, wave-uniform, for each expert taken.
 template <int V, class Taken>
 __device__ __forceinline__ void gate_row(const GateRule &g, const float (&x)[V],
+                                         const float (&bias)[V],
                                          int32_t *ids, float *weights,
                                          Taken taken) {
     const int lane = lane_id();
@@ -110,12 +121,9 @@ __device__ __forceinline__ void gate_row(const GateRule &g, const float (&x)[V],
     }
     if (g.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane * V + i;
-            const float b = g.bias && e < g.E ? g.bias[e] : 0.f;
-            key[i] = x[i] == -__builtin_inff() ? 0u
-                                               : rank_key(sigmoid_of(x[i]) + b);
-        }
+        for (int i = 0; i < V; ++i)
+            key[i] = x[i] == -__builtin_inff()
+                         ? 0u : rank_key(sigmoid_of(x[i]) + bias[i]);
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) key[i] = rank_key(x[i]);
