@@ -9,11 +9,27 @@
 // softmax, g p (1 - p) for the sigmoid. With the chosen scores' sum the
 // softmax's denominator drops out, so only the chosen logits matter.
 //
-// One wave per token; lane l holds experts l V .. l V + V - 1.
+// Two forms. Up to 256 experts and top-8 (top-16 backward): 16 lanes per
+// token, four tokens per wave, every reduction a few lane moves inside a row
+// of 16. Else one wave per token, lane l holding experts l V .. l V + V - 1.
+//
+// The choice by 16 lanes works on 32-bit keys: the upper 24 bits of the rank
+// (as ue_gate.h orders floats) over the expert's id, inverted so that the
+// lowest wins ties. Each lane sorts its best eight by insertion (one median
+// per place), then four steps merge the lanes' lists, the better half of a
+// bitonic merge each, until every lane has the token's best eight. Two ranks
+// may share their upper 24 bits, and the sigmoid's are made with the fast
+// exponential and reciprocal (within 3e-7). So the eight are put in order by
+// their exact ranks, each lane counting the better ones; and if an expert
+// left out is within those margins of the last one taken, the token is chosen
+// again by the rounds on exact keys (about 1 token in 300 of fp32 logits). The
+// upper 24 bits hold all of a bf16 logit.
 #include "ue_gate.h"
 
 namespace ue {
 namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 template <typename T>
 __device__ __forceinline__ float load_logit(const void *p, int64_t i);
@@ -155,33 +171,405 @@ __global__ __launch_bounds__(kBlock) void k_gate_backward(GateBackArgs g) {
     }
 }
 
-int wave_grid(int64_t T, int num_cu) {
-    const int64_t blocks = (T + kWaves - 1) / kWaves;
+// ---- 16 lanes per token --------------------------------------------------
+
+constexpr int kFastExperts = 256, kFastTopk = 8, kFastBackTopk = 16;
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t move_row(uint32_t v) {
+    // (every lane has a source: the old value and the bound bit only let the
+    // move fold into the instruction that uses it)
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
+}
+// Lane moves that pair up all 16 lanes of a row in four steps.
+constexpr int kPair1 = 0xB1, kPair2 = 0x4E, kPair4 = 0x141, kPair8 = 0x140;
+
+template <int CTRL>
+__device__ __forceinline__ float add_row(float v) {
+    return v + __uint_as_float(move_row<CTRL>(__float_as_uint(v)));
+}
+// Sum over a row's 16 lanes, in all of them, in a fixed order.
+__device__ __forceinline__ float row_sum(float v) {
+    return add_row<kPair8>(add_row<kPair4>(add_row<kPair2>(add_row<kPair1>(v))));
+}
+template <int CTRL>
+__device__ __forceinline__ float max_row(float v) {
+    const float o = __uint_as_float(move_row<CTRL>(__float_as_uint(v)));
+    return o > v ? o : v;
+}
+__device__ __forceinline__ float row_max(float v) {
+    return max_row<kPair8>(max_row<kPair4>(max_row<kPair2>(max_row<kPair1>(v))));
+}
+
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
+__device__ __forceinline__ uint32_t med3(uint32_t a, uint32_t b, uint32_t c) {
+    return umax(umin(a, b), umin(umax(a, b), c));
+}
+
+// Keeps the better half of this lane's list and its partner's, sorted again.
+template <int CTRL>
+__device__ __forceinline__ void merge_lists(uint32_t (&a)[8]) {
+    uint32_t m[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = umax(a[i], move_row<CTRL>(a[7 - i]));
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!(i & d)) {
+                const uint32_t hi = umax(m[i], m[i | d]), lo = umin(m[i], m[i | d]);
+                m[i] = hi;
+                m[i | d] = lo;
+            }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = m[i];
+}
+
+// The float a key was made from (its upper 24 bits).
+__device__ __forceinline__ float key_value(uint32_t key) {
+    const uint32_t k = key & ~0xFFu;
+    return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+__device__ __forceinline__ float fast_exp(float x) {
+    return __builtin_amdgcn_exp2f(x * kLog2e);
+}
+
+// This lane's VP logits of a row of 16 lanes' token, -inf past the last
+// expert, and their ids: four at a time when `vec`. WHOLE: 16 VP experts, in
+// rows that load so.
+template <bool WHOLE>
+__device__ __forceinline__ int slot_expert(int i, bool vec) {
+    const int l16 = lane_id() & 15;
+    return WHOLE || vec ? (i >> 2) * 64 + l16 * 4 + (i & 3) : i * 16 + l16;
+}
+template <typename T, int VP, bool WHOLE>
+__device__ __forceinline__ void load_slots(const void *logits, int64_t row, int E,
+                                           bool vec, float (&x)[VP]) {
+    const T *p = static_cast<const T *>(logits) + row;
+    if (WHOLE || vec) {
+        struct alignas(4 * sizeof(T)) Pack { T v[4]; };
+#pragma unroll
+        for (int c = 0; c < VP / 4; ++c) {
+            const int e = slot_expert<WHOLE>(4 * c, true);
+            const bool in = WHOLE || e < E;
+            const Pack q = *reinterpret_cast<const Pack *>(p + (in ? e : 0));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[4 * c + i] = in ? load_logit<T>(q.v, i) : -__builtin_inff();
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            const int e = slot_expert<false>(i, false);
+            const float v = load_logit<T>(p, e < E ? e : 0);
+            x[i] = e < E ? v : -__builtin_inff();
+        }
+    }
+}
+
+template <int N>
+__device__ __forceinline__ uint32_t rotate_row(uint32_t v) {
+    return __builtin_amdgcn_update_dpp(0, v, 0x120 + N, 0xF, 0xF, true);
+}
+// How many of the seven entries beside this lane's (eight per row, in its
+// lower and again in its upper lanes) rank higher, ties to the lower id.
+template <int N = 1>
+__device__ __forceinline__ int better_ones(uint32_t key, uint32_t id) {
+    if constexpr (N == 8) {
+        return 0;
+    } else {
+        const uint32_t ok = rotate_row<N>(key), oi = rotate_row<N>(id);
+        const int above = ok > key || (ok == key && oi < id);
+        return above + better_ones<N + 1>(key, id);
+    }
+}
+
+// VP: logits a lane holds (16 VP >= E).
+template <typename T, int VP, bool SIGMOID, bool WHOLE>
+__global__ __launch_bounds__(kBlock) void k_gate_rows(GateArgs g) {
+    constexpr int V = VP == 16 ? 4 : VP == 8 ? 2 : 1;   // slots of the rounds
+    constexpr bool kExact = sizeof(T) == 2 && !SIGMOID; // keys hold the rank
+    const int lane = lane_id(), l16 = lane & 15, quarter = lane >> 4;
+    const int E = g.rule.E, k = g.rule.k;
+    const int step = gridDim.x * kWaves * 4;
+    float bias[VP];
+#pragma unroll
+    for (int i = 0; i < VP; ++i) {
+        const int e = slot_expert<WHOLE>(i, g.vec4);
+        bias[i] = SIGMOID && g.rule.bias ? g.rule.bias[WHOLE || e < E ? e : 0] : 0.f;
+    }
+    // 0, or NaN where a bias is infinite or NaN
+    float odd_bias = 0.f;
+#pragma unroll
+    for (int i = 0; i < VP; ++i) odd_bias += bias[i] * 0.f;
+    for (int t0 = (blockIdx.x * kWaves + (threadIdx.x >> 6)) * 4; t0 < g.T; t0 += step) {
+        // (rows past the last token repeat it and write nothing)
+        const bool real = t0 + quarter < g.T;
+        const int t = real ? t0 + quarter : g.T - 1;
+        const int64_t row = static_cast<int64_t>(t) * g.ld;
+        const int64_t o = static_cast<int64_t>(t) * k;
+        float x[VP];
+        load_slots<T, VP, WHOLE>(g.logits, row, E, g.vec4, x);
+        // likewise for the logits: only then are the keys made with care for
+        // such values
+        float odd = odd_bias;
+#pragma unroll
+        for (int i = 0; i < VP; ++i) odd += x[i] * 0.f;
+        uint32_t key[VP], best[8] = {};
+        auto insert = [&](int i, uint32_t upper) {
+            key[i] = (upper & ~0xFFu) |
+                     static_cast<uint32_t>(255 - slot_expert<WHOLE>(i, g.vec4));
+#pragma unroll
+            for (int j = 7; j > 0; --j)
+                if (j <= i) best[j] = med3(best[j - 1], best[j], key[i]);
+            best[0] = umax(best[0], key[i]);
+        };
+        bool nan = false;
+        const bool careful = __ballot(odd != odd) != 0;
+        if (careful) {
+#pragma unroll
+            for (int i = 0; i < VP; ++i) {
+                nan |= x[i] != x[i];
+                float r = x[i];
+                if (SIGMOID && r != -__builtin_inff())
+                    r = __builtin_amdgcn_rcpf(1.0f + fast_exp(-r)) + bias[i];
+                insert(i, rank_key(r));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VP; ++i) {
+                float r = x[i];
+                if (SIGMOID) r = __builtin_amdgcn_rcpf(1.0f + fast_exp(-r)) + bias[i];
+                // rank_key of a number
+                const uint32_t b = __float_as_uint(r + 0.0f);
+                insert(i, b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) |
+                               0x80000000u));
+            }
+        }
+        merge_lists<kPair1>(best);
+        merge_lists<kPair2>(best);
+        merge_lists<kPair4>(best);
+        merge_lists<kPair8>(best);
+
+        bool clear = true;
+        if constexpr (!kExact) {
+            uint32_t last = best[0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) last = j < k ? best[j] : last;
+            // the least key that could belong to a rank as good as the last
+            uint32_t bar = (last & ~0xFFu) - 0x100u;
+            if (SIGMOID) bar = umin(bar, rank_key(key_value(last) - 1e-6f) & ~0xFFu);
+            int above = 0;
+#pragma unroll
+            for (int i = 0; i < VP; ++i) above += key[i] >= bar;
+            clear = row_sum(static_cast<float>(above)) == static_cast<float>(k) &&
+                    last > kKeyNegInf;
+        }
+        // lanes j and j + 8 of the row: place j of the list
+        uint32_t mine = best[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) mine = (l16 & 7) == j ? best[j] : mine;
+        const bool have = (l16 & 7) < k && mine > kKeyNegInf;
+        const int id = 255 - static_cast<int>(mine & 0xFFu);
+        float v = -__builtin_inff(), p = 0.f;
+        if (have) v = load_logit<T>(g.logits, row + id);
+        // the denominator over all experts, taken at the best logit
+        float top = 0.f, all = 1.f;
+        if (!SIGMOID) {
+            top = row_max(v);
+            if (!g.rule.renorm) {
+                all = 0.f;
+#pragma unroll
+                for (int i = 0; i < VP; ++i) all += fast_exp(x[i] - top);
+                all = row_sum(all);
+            }
+        }
+        uint32_t exact = 0;
+        if (have) {
+            p = SIGMOID ? sigmoid_of(v) : expf(v - top);
+            if (SIGMOID)
+                exact = rank_key(g.rule.bias ? p + g.rule.bias[id] : p);
+            else
+                exact = rank_key(v);
+        }
+        int place = l16 & 7;
+        if constexpr (!kExact) place = better_ones(exact, have ? id : 256 + (l16 & 7));
+        float n = all;
+        if (g.rule.renorm) {
+            n = row_sum(l16 < 8 ? p : 0.f) + (SIGMOID ? 1e-20f : 0.f);
+            if (!SIGMOID && n == 0.f) n = 1.f;
+        }
+        // an infinite logit takes the rounds too, where +inf is a number
+        if (careful) clear &= !(top > __FLT_MAX__);
+        const bool poisoned = (__ballot(nan) >> (quarter * 16)) & 0xFFFF;
+        if (clear && real && l16 < 8 && place < k) {
+            const float w = have ? p / n * g.rule.scale : 0.f;
+            g.ids[o + place] = have ? id : -1;
+            g.weights[o + place] = poisoned ? __builtin_nanf("") : w;
+        }
+        uint64_t again = __ballot(!clear && real);
+        while (again) {
+            const int which = __builtin_ctzll(again) >> 4;
+            again &= ~(0xFFFFull << (which * 16));
+            const int64_t tt = t0 + which;
+            float y[V], b[V];
+            load_bias<V>(g.rule, b);
+            load_row<T, V>(g.logits, tt * g.ld, E, false, y);
+            gate_row<V>(g.rule, y, b, g.ids + tt * k, g.weights + tt * k, [](int) {});
+        }
+    }
+}
+
+template <typename T, int VP, bool WHOLE>
+__global__ __launch_bounds__(kBlock) void k_gate_backward_rows(GateBackArgs g) {
+    // gradient of the scores by expert, one row per token
+    __shared__ __align__(16) float dense[kWaves * 4][16 * VP];
+    const int lane = lane_id(), l16 = lane & 15, quarter = lane >> 4;
+    const int wv = threadIdx.x >> 6, E = g.rule.E, k = g.rule.k;
+    float *d = dense[wv * 4 + quarter];
+    const bool full = !g.rule.sigmoid && !g.rule.renorm;   // needs every logit
+    const int step = gridDim.x * kWaves * 4;
+    for (int t0 = (blockIdx.x * kWaves + wv) * 4; t0 < g.T; t0 += step) {
+        const int t = t0 + quarter < g.T ? t0 + quarter : g.T - 1;
+        const int64_t row = static_cast<int64_t>(t) * g.ld;
+        const int64_t o = static_cast<int64_t>(t) * k;
+        const int id = l16 < k ? g.ids[o + l16] : -1;
+        const bool have = static_cast<uint32_t>(id) < static_cast<uint32_t>(E);
+        const float gk = have ? g.rule.scale * g.dweights[o + l16] : 0.f;
+        float v = have ? load_logit<T>(g.logits, row + id) : -__builtin_inff();
+        float x[VP], top = v, all = 1.f;
+        if (full) {
+            load_slots<T, VP, WHOLE>(g.logits, row, E, g.vec4, x);
+#pragma unroll
+            for (int i = 0; i < VP; ++i) top = x[i] > top ? x[i] : top;
+        }
+        top = finite_top(row_max(top));
+        if (full) {
+            all = 0.f;
+#pragma unroll
+            for (int i = 0; i < VP; ++i) {
+                x[i] = x[i] == -__builtin_inff()
+                           ? 0.f : fast_exp(finite_top(x[i]) - top);
+                all += x[i];
+            }
+            all = row_sum(all);
+            if (all == 0.f) all = 1.f;      // every expert masked: all zeros
+        }
+        float p = 0.f;
+        if (have) p = g.rule.sigmoid ? sigmoid_of(v) : expf(finite_top(v) - top) / all;
+        const float n = row_sum(p) + (g.rule.sigmoid ? 1e-20f : 0.f);
+        const float pg = row_sum(p * gk);
+        float y = gk;
+        if (g.rule.renorm && have) {
+            y = (gk - pg / n) / n;
+            if (!g.rule.sigmoid) y *= p;
+        }
+        if (g.rule.sigmoid && have) y *= sigmoid_slope(v);
+#pragma unroll
+        for (int i = 0; i < VP; i += 4)
+            *reinterpret_cast<f32x4 *>(d + l16 * VP + i) = f32x4{0, 0, 0, 0};
+        __builtin_amdgcn_wave_barrier();
+        if (have) d[id] = y;
+        __builtin_amdgcn_wave_barrier();
+        T *out = static_cast<T *>(g.dlogits) + static_cast<int64_t>(t) * g.ld_out;
+        const float rest = 1.f / all;
+        if (WHOLE || g.vec4) {
+            struct alignas(4 * sizeof(T)) Pack { T v[4]; };
+#pragma unroll
+            for (int c = 0; c < VP / 4; ++c) {
+                const int e = slot_expert<WHOLE>(4 * c, true);
+                if ((!WHOLE && e >= E) || t0 + quarter >= g.T) continue;
+                const f32x4 q = *reinterpret_cast<const f32x4 *>(d + e);
+                Pack r;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    store_logit(&r.v[i], full ? x[4 * c + i] * rest * (q[i] - pg) : q[i]);
+                *reinterpret_cast<Pack *>(out + e) = r;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VP; ++i) {
+                const int e = slot_expert<WHOLE>(i, false);
+                if (e < E && t0 + quarter < g.T)
+                    store_logit(out + e, full ? x[i] * rest * (d[e] - pg) : d[e]);
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// A workgroup's waves take `each` tokens at a time; enough workgroups to fill
+// the device, the rest in a loop.
+int wave_grid(int64_t T, int each, int num_cu) {
+    const int64_t blocks = (T + kWaves * each - 1) / (kWaves * each);
     const int64_t cap = static_cast<int64_t>(num_cu) * 8;
     return static_cast<int>(blocks < cap ? blocks : cap);
 }
 
+template <typename T, int VP>
+void gate_rows_any(const GateArgs &g, dim3 gr, dim3 bl, hipStream_t s) {
+    const bool whole = g.rule.E == 16 * VP && g.vec4;
+    if (g.rule.sigmoid) {
+        if (whole) hipLaunchKernelGGL((k_gate_rows<T, VP, true, true>), gr, bl, 0, s, g);
+        else hipLaunchKernelGGL((k_gate_rows<T, VP, true, false>), gr, bl, 0, s, g);
+    } else {
+        if (whole) hipLaunchKernelGGL((k_gate_rows<T, VP, false, true>), gr, bl, 0, s, g);
+        else hipLaunchKernelGGL((k_gate_rows<T, VP, false, false>), gr, bl, 0, s, g);
+    }
+}
+
+template <typename T, int VP>
+void back_rows_any(const GateBackArgs &g, dim3 gr, dim3 bl, hipStream_t s) {
+    if (g.rule.E == 16 * VP && g.vec4)
+        hipLaunchKernelGGL((k_gate_backward_rows<T, VP, true>), gr, bl, 0, s, g);
+    else
+        hipLaunchKernelGGL((k_gate_backward_rows<T, VP, false>), gr, bl, 0, s, g);
+}
+
 template <typename T>
-hipError_t gate_any(const GateArgs &g, int grid, hipStream_t s) {
-    const dim3 gr(grid), bl(kBlock);
-    if (g.rule.E <= 64) hipLaunchKernelGGL((k_gate<T, 1>), gr, bl, 0, s, g);
-    else if (g.rule.E <= 128) hipLaunchKernelGGL((k_gate<T, 2>), gr, bl, 0, s, g);
-    else if (g.rule.E <= 256) hipLaunchKernelGGL((k_gate<T, 4>), gr, bl, 0, s, g);
-    else if (g.rule.E <= 512) hipLaunchKernelGGL((k_gate<T, 8>), gr, bl, 0, s, g);
-    else hipLaunchKernelGGL((k_gate<T, 16>), gr, bl, 0, s, g);
+hipError_t gate_any(const ue_ctx &c, const GateArgs &g, hipStream_t s) {
+    const int E = g.rule.E;
+    const bool rows = E <= kFastExperts && g.rule.k <= kFastTopk;
+    const dim3 gr(wave_grid(g.T, rows ? 4 : 1, c.num_cu)), bl(kBlock);
+    if (rows) {
+        if (E <= 64) gate_rows_any<T, 4>(g, gr, bl, s);
+        else if (E <= 128) gate_rows_any<T, 8>(g, gr, bl, s);
+        else gate_rows_any<T, 16>(g, gr, bl, s);
+    } else {
+        switch (lane_slots(E)) {
+            case 1: hipLaunchKernelGGL((k_gate<T, 1>), gr, bl, 0, s, g); break;
+            case 2: hipLaunchKernelGGL((k_gate<T, 2>), gr, bl, 0, s, g); break;
+            case 4: hipLaunchKernelGGL((k_gate<T, 4>), gr, bl, 0, s, g); break;
+            case 8: hipLaunchKernelGGL((k_gate<T, 8>), gr, bl, 0, s, g); break;
+            default: hipLaunchKernelGGL((k_gate<T, 16>), gr, bl, 0, s, g); break;
+        }
+    }
     return hipGetLastError();
 }
 
 template <typename T>
-hipError_t back_any(const GateBackArgs &g, int grid, hipStream_t s) {
-    const dim3 gr(grid), bl(kBlock);
-    const int v = lane_slots(g.rule.E);
+hipError_t back_any(const ue_ctx &c, const GateBackArgs &g, hipStream_t s) {
+    const int E = g.rule.E;
+    const bool rows = E <= kFastExperts && g.rule.k <= kFastBackTopk;
+    const dim3 gr(wave_grid(g.T, rows ? 4 : 1, c.num_cu)), bl(kBlock);
+    const int v = lane_slots(E);
     const size_t lds = sizeof(float) * kBlock * v;
-    if (v == 1) hipLaunchKernelGGL((k_gate_backward<T, 1>), gr, bl, lds, s, g);
-    else if (v == 2) hipLaunchKernelGGL((k_gate_backward<T, 2>), gr, bl, lds, s, g);
-    else if (v == 4) hipLaunchKernelGGL((k_gate_backward<T, 4>), gr, bl, lds, s, g);
-    else if (v == 8) hipLaunchKernelGGL((k_gate_backward<T, 8>), gr, bl, lds, s, g);
-    else hipLaunchKernelGGL((k_gate_backward<T, 16>), gr, bl, lds, s, g);
+    if (rows) {
+        if (E <= 64) back_rows_any<T, 4>(g, gr, bl, s);
+        else if (E <= 128) back_rows_any<T, 8>(g, gr, bl, s);
+        else back_rows_any<T, 16>(g, gr, bl, s);
+    } else {
+        switch (v) {
+            case 1: hipLaunchKernelGGL((k_gate_backward<T, 1>), gr, bl, lds, s, g); break;
+            case 2: hipLaunchKernelGGL((k_gate_backward<T, 2>), gr, bl, lds, s, g); break;
+            case 4: hipLaunchKernelGGL((k_gate_backward<T, 4>), gr, bl, lds, s, g); break;
+            case 8: hipLaunchKernelGGL((k_gate_backward<T, 8>), gr, bl, lds, s, g); break;
+            default: hipLaunchKernelGGL((k_gate_backward<T, 16>), gr, bl, lds, s, g); break;
+        }
+    }
     return hipGetLastError();
 }
 
@@ -195,15 +583,13 @@ int lane_slots(int E) {
 
 hipError_t launch_gate(const ue_ctx &c, const GateArgs &g, hipStream_t s) {
     if (g.T == 0) return hipSuccess;
-    const int grid = wave_grid(g.T, c.num_cu);
-    return g.bf16 ? gate_any<uint16_t>(g, grid, s) : gate_any<float>(g, grid, s);
+    return g.bf16 ? gate_any<uint16_t>(c, g, s) : gate_any<float>(c, g, s);
 }
 
 hipError_t launch_gate_backward(const ue_ctx &c, const GateBackArgs &g,
                                 hipStream_t s) {
     if (g.T == 0) return hipSuccess;
-    const int grid = wave_grid(g.T, c.num_cu);
-    return g.bf16 ? back_any<uint16_t>(g, grid, s) : back_any<float>(g, grid, s);
+    return g.bf16 ? back_any<uint16_t>(c, g, s) : back_any<float>(c, g, s);
 }
 
 }  // namespace ue

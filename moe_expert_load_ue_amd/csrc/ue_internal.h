@@ -183,7 +183,8 @@ struct GateRule {
 struct GateArgs {
     const void *logits;         // [T] rows, ld elements apart
     int64_t ld;
-    bool bf16, vec;             // vec: a lane's logits may load at once
+    bool bf16, vec, vec4;       // vec: a lane's logits may load at once
+                                // vec4: four at a time
     int T;
     GateRule rule;
     int32_t *ids;
@@ -192,7 +193,7 @@ struct GateArgs {
 struct GateBackArgs {
     const void *logits;
     int64_t ld;
-    bool bf16, vec;
+    bool bf16, vec, vec4;       // vec4: of the gradient's rows too
     int T;
     GateRule rule;
     const int32_t *ids;

@@ -82,6 +82,7 @@ int ue_gate(ue_ctx *ctx, const void *logits, int32_t type, int64_t ld,
     g.ld = ld;
     g.bf16 = type == UE_BF16;
     g.vec = lane_loads(ctx, logits, type, ld);
+    g.vec4 = ctx->E % 4 == 0 && rows_aligned(logits, ld, type_bytes(type), 4 * type_bytes(type));
     g.T = T;
     g.rule = rule_of(ctx, score, renorm, scale, bias);
     g.ids = ids;
@@ -115,6 +116,9 @@ int ue_gate_backward(ue_ctx *ctx, const void *logits, int32_t type, int64_t ld,
     g.ld = ld;
     g.bf16 = type == UE_BF16;
     g.vec = lane_loads(ctx, logits, type, ld);
+    const size_t es = type_bytes(type);
+    g.vec4 = ctx->E % 4 == 0 && rows_aligned(logits, ld, es, 4 * es) &&
+             rows_aligned(dlogits, ld_out, es, 4 * es);
     g.T = T;
     g.rule = rule_of(ctx, score, renorm, scale, nullptr);
     g.ids = ids;
