@@ -226,10 +226,10 @@ __device__ __forceinline__ void merge_lists(uint32_t (&a)[8]) {
     for (int i = 0; i < 8; ++i) a[i] = m[i];
 }
 
-// The float a key was made from (its upper 24 bits).
+// The float a key was made from, with its lowest 8 bits zero.
 __device__ __forceinline__ float key_value(uint32_t key) {
-    const uint32_t k = key & ~0xFFu;
-    return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+    const uint32_t k = (key & 0x80000000u) ? key ^ 0x80000000u : ~key;
+    return __uint_as_float(k & ~0xFFu);
 }
 
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -301,18 +301,45 @@ __global__ __launch_bounds__(kBlock) void k_gate_rows(GateArgs g) {
         const int e = slot_expert<WHOLE>(i, g.vec4);
         bias[i] = SIGMOID && g.rule.bias ? g.rule.bias[WHOLE || e < E ? e : 0] : 0.f;
     }
+    // The logits again (and the biases), for the second look at the chosen
+    // ones: from LDS, so that it does not wait on memory. (A bf16 logit is in
+    // its key.)
+    __shared__ __align__(16) float seen[kExact ? 1 : kWaves * 4][16 * VP];
+    __shared__ float seen_bias[SIGMOID ? 16 * VP : 1];
+    float *const mine_seen = seen[kExact ? 0 : (threadIdx.x >> 6) * 4 + quarter];
+    if (SIGMOID) {
+        for (int e = threadIdx.x; e < E; e += kBlock)
+            seen_bias[e] = g.rule.bias ? g.rule.bias[e] : 0.f;
+        __syncthreads();
+    }
     // 0, or NaN where a bias is infinite or NaN
     float odd_bias = 0.f;
 #pragma unroll
     for (int i = 0; i < VP; ++i) odd_bias += bias[i] * 0.f;
-    for (int t0 = (blockIdx.x * kWaves + (threadIdx.x >> 6)) * 4; t0 < g.T; t0 += step) {
-        // (rows past the last token repeat it and write nothing)
+    // (rows past the last token repeat it and write nothing)
+    auto row_of = [&](int t) { return t < g.T ? t : g.T - 1; };
+    const int first = (blockIdx.x * kWaves + (threadIdx.x >> 6)) * 4;
+    float next[VP];
+    if (first < g.T)
+        load_slots<T, VP, WHOLE>(g.logits, row_of(first + quarter) * g.ld, E, g.vec4, next);
+    for (int t0 = first; t0 < g.T; t0 += step) {
         const bool real = t0 + quarter < g.T;
-        const int t = real ? t0 + quarter : g.T - 1;
-        const int64_t row = static_cast<int64_t>(t) * g.ld;
-        const int64_t o = static_cast<int64_t>(t) * k;
+        const int64_t o = static_cast<int64_t>(row_of(t0 + quarter)) * k;
         float x[VP];
-        load_slots<T, VP, WHOLE>(g.logits, row, E, g.vec4, x);
+#pragma unroll
+        for (int i = 0; i < VP; ++i) x[i] = next[i];
+        if (!kExact) {
+#pragma unroll
+            for (int i = 0; i < VP; i += 4)
+                if (WHOLE || g.vec4)
+                    *reinterpret_cast<f32x4 *>(mine_seen + slot_expert<WHOLE>(i, true)) =
+                        f32x4{x[i], x[i + 1], x[i + 2], x[i + 3]};
+                else
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mine_seen[slot_expert<false>(i + j, false)] = x[i + j];
+            __builtin_amdgcn_wave_barrier();
+        }
         // likewise for the logits: only then are the keys made with care for
         // such values
         float odd = odd_bias;
@@ -349,6 +376,10 @@ __global__ __launch_bounds__(kBlock) void k_gate_rows(GateArgs g) {
                                0x80000000u));
             }
         }
+        // the next tokens' logits, on their way while these are chosen
+        if (t0 + step < g.T)
+            load_slots<T, VP, WHOLE>(g.logits, row_of(t0 + step + quarter) * g.ld, E,
+                                     g.vec4, next);
         merge_lists<kPair1>(best);
         merge_lists<kPair2>(best);
         merge_lists<kPair4>(best);
@@ -375,7 +406,7 @@ __global__ __launch_bounds__(kBlock) void k_gate_rows(GateArgs g) {
         const bool have = (l16 & 7) < k && mine > kKeyNegInf;
         const int id = 255 - static_cast<int>(mine & 0xFFu);
         float v = -__builtin_inff(), p = 0.f;
-        if (have) v = load_logit<T>(g.logits, row + id);
+        if (have) v = kExact ? key_value(mine) : mine_seen[id];
         // the denominator over all experts, taken at the best logit
         float top = 0.f, all = 1.f;
         if (!SIGMOID) {
@@ -391,7 +422,7 @@ __global__ __launch_bounds__(kBlock) void k_gate_rows(GateArgs g) {
         if (have) {
             p = SIGMOID ? sigmoid_of(v) : expf(v - top);
             if (SIGMOID)
-                exact = rank_key(g.rule.bias ? p + g.rule.bias[id] : p);
+                exact = rank_key(p + seen_bias[id]);
             else
                 exact = rank_key(v);
         }
@@ -420,6 +451,7 @@ __global__ __launch_bounds__(kBlock) void k_gate_rows(GateArgs g) {
             load_row<T, V>(g.logits, tt * g.ld, E, false, y);
             gate_row<V>(g.rule, y, b, g.ids + tt * k, g.weights + tt * k, [](int) {});
         }
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
