@@ -9,14 +9,15 @@
 // softmax, g p (1 - p) for the sigmoid. With the chosen scores' sum the
 // softmax's denominator drops out, so only the chosen logits matter.
 //
-// Two forms. Up to 256 experts and top-8 (top-16 backward): 16 lanes per
-// token, four tokens per wave, every reduction a few lane moves inside a row
-// of 16. Else one wave per token, lane l holding experts l V .. l V + V - 1.
+// Two forms. Up to 256 experts and top-8 (top-16 backward): L = 16 lanes per
+// token, or 8 up to 128 experts, so four or eight tokens per wave, every
+// reduction a few lane moves inside a row of 16. Else one wave per token,
+// lane l holding experts l V .. l V + V - 1.
 //
-// The choice by 16 lanes works on 32-bit keys: the upper 24 bits of the rank
+// The choice by L lanes works on 32-bit keys: the upper 24 bits of the rank
 // (as ue_gate.h orders floats) over the expert's id, inverted so that the
 // lowest wins ties. Each lane sorts its best eight by insertion (one median
-// per place), then four steps merge the lanes' lists, the better half of a
+// per place), then log2 L steps merge the lanes' lists, the better half of a
 // bitonic merge each, until every lane has the token's best eight. Two ranks
 // may share their upper 24 bits, and the sigmoid's are made with the fast
 // exponential and reciprocal (within 3e-7). So the eight are put in order by
@@ -171,7 +172,7 @@ __global__ __launch_bounds__(kBlock) void k_gate_backward(GateBackArgs g) {
     }
 }
 
-// ---- 16 lanes per token --------------------------------------------------
+// ---- 8 or 16 lanes per token --------------------------------------------------
 
 constexpr int kFastExperts = 256, kFastTopk = 8, kFastBackTopk = 16;
 
@@ -181,24 +182,28 @@ __device__ __forceinline__ uint32_t move_row(uint32_t v) {
     // move fold into the instruction that uses it)
     return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
 }
-// Lane moves that pair up all 16 lanes of a row in four steps.
+// Lane moves that pair up 8 lanes in three steps, all 16 of a row in four.
 constexpr int kPair1 = 0xB1, kPair2 = 0x4E, kPair4 = 0x141, kPair8 = 0x140;
 
 template <int CTRL>
 __device__ __forceinline__ float add_row(float v) {
     return v + __uint_as_float(move_row<CTRL>(__float_as_uint(v)));
 }
-// Sum over a row's 16 lanes, in all of them, in a fixed order.
+// Sum over a token's L lanes, in all of them, in a fixed order.
+template <int L>
 __device__ __forceinline__ float row_sum(float v) {
-    return add_row<kPair8>(add_row<kPair4>(add_row<kPair2>(add_row<kPair1>(v))));
+    v = add_row<kPair4>(add_row<kPair2>(add_row<kPair1>(v)));
+    return L == 16 ? add_row<kPair8>(v) : v;
 }
 template <int CTRL>
 __device__ __forceinline__ float max_row(float v) {
     const float o = __uint_as_float(move_row<CTRL>(__float_as_uint(v)));
     return o > v ? o : v;
 }
+template <int L>
 __device__ __forceinline__ float row_max(float v) {
-    return max_row<kPair8>(max_row<kPair4>(max_row<kPair2>(max_row<kPair1>(v))));
+    v = max_row<kPair4>(max_row<kPair2>(max_row<kPair1>(v)));
+    return L == 16 ? max_row<kPair8>(v) : v;
 }
 
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
@@ -237,15 +242,15 @@ __device__ __forceinline__ float fast_exp(float x) {
     return __builtin_amdgcn_exp2f(x * kLog2e);
 }
 
-// This lane's VP logits of a row of 16 lanes' token, -inf past the last
-// expert, and their ids: four at a time when `vec`. WHOLE: 16 VP experts, in
-// rows that load so.
-template <bool WHOLE>
+// This lane's VP logits of its L lanes' token, -inf past the last expert, and
+// their ids: four at a time when `vec`. WHOLE: L VP experts, in rows that
+// load so.
+template <int L, bool WHOLE>
 __device__ __forceinline__ int slot_expert(int i, bool vec) {
-    const int l16 = lane_id() & 15;
-    return WHOLE || vec ? (i >> 2) * 64 + l16 * 4 + (i & 3) : i * 16 + l16;
+    const int l = lane_id() & (L - 1);
+    return WHOLE || vec ? (i >> 2) * 4 * L + l * 4 + (i & 3) : i * L + l;
 }
-template <typename T, int VP, bool WHOLE>
+template <typename T, int L, int VP, bool WHOLE>
 __device__ __forceinline__ void load_slots(const void *logits, int64_t row, int E,
                                            bool vec, float (&x)[VP]) {
     const T *p = static_cast<const T *>(logits) + row;
@@ -253,7 +258,7 @@ __device__ __forceinline__ void load_slots(const void *logits, int64_t row, int 
         struct alignas(4 * sizeof(T)) Pack { T v[4]; };
 #pragma unroll
         for (int c = 0; c < VP / 4; ++c) {
-            const int e = slot_expert<WHOLE>(4 * c, true);
+            const int e = slot_expert<L, WHOLE>(4 * c, true);
             const bool in = WHOLE || e < E;
             const Pack q = *reinterpret_cast<const Pack *>(p + (in ? e : 0));
 #pragma unroll
@@ -263,50 +268,57 @@ __device__ __forceinline__ void load_slots(const void *logits, int64_t row, int 
     } else {
 #pragma unroll
         for (int i = 0; i < VP; ++i) {
-            const int e = slot_expert<false>(i, false);
+            const int e = slot_expert<L, false>(i, false);
             const float v = load_logit<T>(p, e < E ? e : 0);
             x[i] = e < E ? v : -__builtin_inff();
         }
     }
 }
 
+// Lane l gets lane l ^ N of its eight.
 template <int N>
-__device__ __forceinline__ uint32_t rotate_row(uint32_t v) {
-    return __builtin_amdgcn_update_dpp(0, v, 0x120 + N, 0xF, 0xF, true);
+__device__ __forceinline__ uint32_t swap_lanes(uint32_t v) {
+    if constexpr (N & 4) v = move_row<kPair4>(v);             // l ^ 7
+    constexpr int M = N & 4 ? N ^ 7 : N;
+    if constexpr (M == 1) v = move_row<kPair1>(v);
+    if constexpr (M == 2) v = move_row<kPair2>(v);
+    if constexpr (M == 3) v = move_row<0x1B>(v);
+    return v;
 }
-// How many of the seven entries beside this lane's (eight per row, in its
-// lower and again in its upper lanes) rank higher, ties to the lower id.
+// How many of the other seven entries (one per lane of eight) rank higher,
+// ties to the lower id.
 template <int N = 1>
 __device__ __forceinline__ int better_ones(uint32_t key, uint32_t id) {
     if constexpr (N == 8) {
         return 0;
     } else {
-        const uint32_t ok = rotate_row<N>(key), oi = rotate_row<N>(id);
+        const uint32_t ok = swap_lanes<N>(key), oi = swap_lanes<N>(id);
         const int above = ok > key || (ok == key && oi < id);
         return above + better_ones<N + 1>(key, id);
     }
 }
 
-// VP: logits a lane holds (16 VP >= E).
-template <typename T, int VP, bool SIGMOID, bool WHOLE>
+// L lanes per token; VP: logits a lane holds (L VP >= E).
+template <typename T, int L, int VP, bool SIGMOID, bool WHOLE>
 __global__ __launch_bounds__(kBlock) void k_gate_rows(GateArgs g) {
-    constexpr int V = VP == 16 ? 4 : VP == 8 ? 2 : 1;   // slots of the rounds
+    constexpr int V = L * VP <= 64 ? 1 : L * VP / 64;   // slots of the rounds
+    constexpr int kEach = 64 / L;                       // tokens of a wave
     constexpr bool kExact = sizeof(T) == 2 && !SIGMOID; // keys hold the rank
-    const int lane = lane_id(), l16 = lane & 15, quarter = lane >> 4;
+    const int lane = lane_id(), at = lane & (L - 1), sub = lane / L;
     const int E = g.rule.E, k = g.rule.k;
-    const int step = gridDim.x * kWaves * 4;
+    const int step = gridDim.x * kWaves * kEach;
     float bias[VP];
 #pragma unroll
     for (int i = 0; i < VP; ++i) {
-        const int e = slot_expert<WHOLE>(i, g.vec4);
+        const int e = slot_expert<L, WHOLE>(i, g.vec4);
         bias[i] = SIGMOID && g.rule.bias ? g.rule.bias[WHOLE || e < E ? e : 0] : 0.f;
     }
     // The logits again (and the biases), for the second look at the chosen
     // ones: from LDS, so that it does not wait on memory. (A bf16 logit is in
     // its key.)
-    __shared__ __align__(16) float seen[kExact ? 1 : kWaves * 4][16 * VP];
-    __shared__ float seen_bias[SIGMOID ? 16 * VP : 1];
-    float *const mine_seen = seen[kExact ? 0 : (threadIdx.x >> 6) * 4 + quarter];
+    __shared__ __align__(16) float seen[kExact ? 1 : kWaves * kEach][L * VP];
+    __shared__ float seen_bias[SIGMOID ? L * VP : 1];
+    float *const mine_seen = seen[kExact ? 0 : (threadIdx.x >> 6) * kEach + sub];
     if (SIGMOID) {
         for (int e = threadIdx.x; e < E; e += kBlock)
             seen_bias[e] = g.rule.bias ? g.rule.bias[e] : 0.f;
@@ -318,13 +330,13 @@ __global__ __launch_bounds__(kBlock) void k_gate_rows(GateArgs g) {
     for (int i = 0; i < VP; ++i) odd_bias += bias[i] * 0.f;
     // (rows past the last token repeat it and write nothing)
     auto row_of = [&](int t) { return t < g.T ? t : g.T - 1; };
-    const int first = (blockIdx.x * kWaves + (threadIdx.x >> 6)) * 4;
+    const int first = (blockIdx.x * kWaves + (threadIdx.x >> 6)) * kEach;
     float next[VP];
     if (first < g.T)
-        load_slots<T, VP, WHOLE>(g.logits, row_of(first + quarter) * g.ld, E, g.vec4, next);
+        load_slots<T, L, VP, WHOLE>(g.logits, row_of(first + sub) * g.ld, E, g.vec4, next);
     for (int t0 = first; t0 < g.T; t0 += step) {
-        const bool real = t0 + quarter < g.T;
-        const int64_t o = static_cast<int64_t>(row_of(t0 + quarter)) * k;
+        const bool real = t0 + sub < g.T;
+        const int64_t o = static_cast<int64_t>(row_of(t0 + sub)) * k;
         float x[VP];
 #pragma unroll
         for (int i = 0; i < VP; ++i) x[i] = next[i];
@@ -332,12 +344,12 @@ __global__ __launch_bounds__(kBlock) void k_gate_rows(GateArgs g) {
 #pragma unroll
             for (int i = 0; i < VP; i += 4)
                 if (WHOLE || g.vec4)
-                    *reinterpret_cast<f32x4 *>(mine_seen + slot_expert<WHOLE>(i, true)) =
+                    *reinterpret_cast<f32x4 *>(mine_seen + slot_expert<L, WHOLE>(i, true)) =
                         f32x4{x[i], x[i + 1], x[i + 2], x[i + 3]};
                 else
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        mine_seen[slot_expert<false>(i + j, false)] = x[i + j];
+                        mine_seen[slot_expert<L, false>(i + j, false)] = x[i + j];
             __builtin_amdgcn_wave_barrier();
         }
         // likewise for the logits: only then are the keys made with care for
@@ -348,7 +360,7 @@ __global__ __launch_bounds__(kBlock) void k_gate_rows(GateArgs g) {
         uint32_t key[VP], best[8] = {};
         auto insert = [&](int i, uint32_t upper) {
             key[i] = (upper & ~0xFFu) |
-                     static_cast<uint32_t>(255 - slot_expert<WHOLE>(i, g.vec4));
+                     static_cast<uint32_t>(255 - slot_expert<L, WHOLE>(i, g.vec4));
 #pragma unroll
             for (int j = 7; j > 0; --j)
                 if (j <= i) best[j] = med3(best[j - 1], best[j], key[i]);
@@ -378,12 +390,12 @@ __global__ __launch_bounds__(kBlock) void k_gate_rows(GateArgs g) {
         }
         // the next tokens' logits, on their way while these are chosen
         if (t0 + step < g.T)
-            load_slots<T, VP, WHOLE>(g.logits, row_of(t0 + step + quarter) * g.ld, E,
+            load_slots<T, L, VP, WHOLE>(g.logits, row_of(t0 + step + sub) * g.ld, E,
                                      g.vec4, next);
         merge_lists<kPair1>(best);
         merge_lists<kPair2>(best);
         merge_lists<kPair4>(best);
-        merge_lists<kPair8>(best);
+        if constexpr (L == 16) merge_lists<kPair8>(best);
 
         bool clear = true;
         if constexpr (!kExact) {
@@ -396,26 +408,26 @@ __global__ __launch_bounds__(kBlock) void k_gate_rows(GateArgs g) {
             int above = 0;
 #pragma unroll
             for (int i = 0; i < VP; ++i) above += key[i] >= bar;
-            clear = row_sum(static_cast<float>(above)) == static_cast<float>(k) &&
+            clear = row_sum<L>(static_cast<float>(above)) == static_cast<float>(k) &&
                     last > kKeyNegInf;
         }
-        // lanes j and j + 8 of the row: place j of the list
+        // lane j (and j + 8 of 16): place j of the list
         uint32_t mine = best[0];
 #pragma unroll
-        for (int j = 1; j < 8; ++j) mine = (l16 & 7) == j ? best[j] : mine;
-        const bool have = (l16 & 7) < k && mine > kKeyNegInf;
+        for (int j = 1; j < 8; ++j) mine = (at & 7) == j ? best[j] : mine;
+        const bool have = (at & 7) < k && mine > kKeyNegInf;
         const int id = 255 - static_cast<int>(mine & 0xFFu);
         float v = -__builtin_inff(), p = 0.f;
         if (have) v = kExact ? key_value(mine) : mine_seen[id];
         // the denominator over all experts, taken at the best logit
         float top = 0.f, all = 1.f;
         if (!SIGMOID) {
-            top = row_max(v);
+            top = row_max<L>(v);
             if (!g.rule.renorm) {
                 all = 0.f;
 #pragma unroll
                 for (int i = 0; i < VP; ++i) all += fast_exp(x[i] - top);
-                all = row_sum(all);
+                all = row_sum<L>(all);
             }
         }
         uint32_t exact = 0;
@@ -426,25 +438,25 @@ __global__ __launch_bounds__(kBlock) void k_gate_rows(GateArgs g) {
             else
                 exact = rank_key(v);
         }
-        int place = l16 & 7;
-        if constexpr (!kExact) place = better_ones(exact, have ? id : 256 + (l16 & 7));
+        int place = at & 7;
+        if constexpr (!kExact) place = better_ones(exact, have ? id : 256 + (at & 7));
         float n = all;
         if (g.rule.renorm) {
-            n = row_sum(l16 < 8 ? p : 0.f) + (SIGMOID ? 1e-20f : 0.f);
+            n = row_sum<L>(at < 8 ? p : 0.f) + (SIGMOID ? 1e-20f : 0.f);
             if (!SIGMOID && n == 0.f) n = 1.f;
         }
         // an infinite logit takes the rounds too, where +inf is a number
         if (careful) clear &= !(top > __FLT_MAX__);
-        const bool poisoned = (__ballot(nan) >> (quarter * 16)) & 0xFFFF;
-        if (clear && real && l16 < 8 && place < k) {
+        const bool poisoned = (__ballot(nan) >> (sub * L)) & ((1u << L) - 1);
+        if (clear && real && at < 8 && place < k) {
             const float w = have ? p / n * g.rule.scale : 0.f;
             g.ids[o + place] = have ? id : -1;
             g.weights[o + place] = poisoned ? __builtin_nanf("") : w;
         }
         uint64_t again = __ballot(!clear && real);
         while (again) {
-            const int which = __builtin_ctzll(again) >> 4;
-            again &= ~(0xFFFFull << (which * 16));
+            const int which = __builtin_ctzll(again) / L;
+            again &= ~(((1ull << L) - 1) << (which * L));
             const int64_t tt = t0 + which;
             float y[V], b[V];
             load_bias<V>(g.rule, b);
@@ -455,30 +467,31 @@ __global__ __launch_bounds__(kBlock) void k_gate_rows(GateArgs g) {
     }
 }
 
-template <typename T, int VP, bool WHOLE>
+template <typename T, int L, int VP, bool WHOLE>
 __global__ __launch_bounds__(kBlock) void k_gate_backward_rows(GateBackArgs g) {
+    constexpr int kEach = 64 / L;                       // tokens of a wave
     // gradient of the scores by expert, one row per token
-    __shared__ __align__(16) float dense[kWaves * 4][16 * VP];
-    const int lane = lane_id(), l16 = lane & 15, quarter = lane >> 4;
+    __shared__ __align__(16) float dense[kWaves * kEach][L * VP];
+    const int lane = lane_id(), at = lane & (L - 1), sub = lane / L;
     const int wv = threadIdx.x >> 6, E = g.rule.E, k = g.rule.k;
-    float *d = dense[wv * 4 + quarter];
+    float *d = dense[wv * kEach + sub];
     const bool full = !g.rule.sigmoid && !g.rule.renorm;   // needs every logit
-    const int step = gridDim.x * kWaves * 4;
-    for (int t0 = (blockIdx.x * kWaves + wv) * 4; t0 < g.T; t0 += step) {
-        const int t = t0 + quarter < g.T ? t0 + quarter : g.T - 1;
+    const int step = gridDim.x * kWaves * kEach;
+    for (int t0 = (blockIdx.x * kWaves + wv) * kEach; t0 < g.T; t0 += step) {
+        const int t = t0 + sub < g.T ? t0 + sub : g.T - 1;
         const int64_t row = static_cast<int64_t>(t) * g.ld;
         const int64_t o = static_cast<int64_t>(t) * k;
-        const int id = l16 < k ? g.ids[o + l16] : -1;
+        const int id = at < k ? g.ids[o + at] : -1;
         const bool have = static_cast<uint32_t>(id) < static_cast<uint32_t>(E);
-        const float gk = have ? g.rule.scale * g.dweights[o + l16] : 0.f;
+        const float gk = have ? g.rule.scale * g.dweights[o + at] : 0.f;
         float v = have ? load_logit<T>(g.logits, row + id) : -__builtin_inff();
         float x[VP], top = v, all = 1.f;
         if (full) {
-            load_slots<T, VP, WHOLE>(g.logits, row, E, g.vec4, x);
+            load_slots<T, L, VP, WHOLE>(g.logits, row, E, g.vec4, x);
 #pragma unroll
             for (int i = 0; i < VP; ++i) top = x[i] > top ? x[i] : top;
         }
-        top = finite_top(row_max(top));
+        top = finite_top(row_max<L>(top));
         if (full) {
             all = 0.f;
 #pragma unroll
@@ -487,13 +500,13 @@ __global__ __launch_bounds__(kBlock) void k_gate_backward_rows(GateBackArgs g) {
                            ? 0.f : fast_exp(finite_top(x[i]) - top);
                 all += x[i];
             }
-            all = row_sum(all);
+            all = row_sum<L>(all);
             if (all == 0.f) all = 1.f;      // every expert masked: all zeros
         }
         float p = 0.f;
         if (have) p = g.rule.sigmoid ? sigmoid_of(v) : expf(finite_top(v) - top) / all;
-        const float n = row_sum(p) + (g.rule.sigmoid ? 1e-20f : 0.f);
-        const float pg = row_sum(p * gk);
+        const float n = row_sum<L>(p) + (g.rule.sigmoid ? 1e-20f : 0.f);
+        const float pg = row_sum<L>(p * gk);
         float y = gk;
         if (g.rule.renorm && have) {
             y = (gk - pg / n) / n;
@@ -502,7 +515,7 @@ __global__ __launch_bounds__(kBlock) void k_gate_backward_rows(GateBackArgs g) {
         if (g.rule.sigmoid && have) y *= sigmoid_slope(v);
 #pragma unroll
         for (int i = 0; i < VP; i += 4)
-            *reinterpret_cast<f32x4 *>(d + l16 * VP + i) = f32x4{0, 0, 0, 0};
+            *reinterpret_cast<f32x4 *>(d + at * VP + i) = f32x4{0, 0, 0, 0};
         __builtin_amdgcn_wave_barrier();
         if (have) d[id] = y;
         __builtin_amdgcn_wave_barrier();
@@ -512,8 +525,8 @@ __global__ __launch_bounds__(kBlock) void k_gate_backward_rows(GateBackArgs g) {
             struct alignas(4 * sizeof(T)) Pack { T v[4]; };
 #pragma unroll
             for (int c = 0; c < VP / 4; ++c) {
-                const int e = slot_expert<WHOLE>(4 * c, true);
-                if ((!WHOLE && e >= E) || t0 + quarter >= g.T) continue;
+                const int e = slot_expert<L, WHOLE>(4 * c, true);
+                if ((!WHOLE && e >= E) || t0 + sub >= g.T) continue;
                 const f32x4 q = *reinterpret_cast<const f32x4 *>(d + e);
                 Pack r;
 #pragma unroll
@@ -524,8 +537,8 @@ __global__ __launch_bounds__(kBlock) void k_gate_backward_rows(GateBackArgs g) {
         } else {
 #pragma unroll
             for (int i = 0; i < VP; ++i) {
-                const int e = slot_expert<WHOLE>(i, false);
-                if (e < E && t0 + quarter < g.T)
+                const int e = slot_expert<L, WHOLE>(i, false);
+                if (e < E && t0 + sub < g.T)
                     store_logit(out + e, full ? x[i] * rest * (d[e] - pg) : d[e]);
             }
         }
@@ -541,36 +554,38 @@ int wave_grid(int64_t T, int each, int num_cu) {
     return static_cast<int>(blocks < cap ? blocks : cap);
 }
 
-template <typename T, int VP>
-void gate_rows_any(const GateArgs &g, dim3 gr, dim3 bl, hipStream_t s) {
-    const bool whole = g.rule.E == 16 * VP && g.vec4;
+template <typename T, int L, int VP>
+void gate_rows_any(const ue_ctx &c, const GateArgs &g, hipStream_t s) {
+    const bool whole = g.rule.E == L * VP && g.vec4;
+    const dim3 gr(wave_grid(g.T, 64 / L, c.num_cu)), bl(kBlock);
     if (g.rule.sigmoid) {
-        if (whole) hipLaunchKernelGGL((k_gate_rows<T, VP, true, true>), gr, bl, 0, s, g);
-        else hipLaunchKernelGGL((k_gate_rows<T, VP, true, false>), gr, bl, 0, s, g);
+        if (whole) hipLaunchKernelGGL((k_gate_rows<T, L, VP, true, true>), gr, bl, 0, s, g);
+        else hipLaunchKernelGGL((k_gate_rows<T, L, VP, true, false>), gr, bl, 0, s, g);
     } else {
-        if (whole) hipLaunchKernelGGL((k_gate_rows<T, VP, false, true>), gr, bl, 0, s, g);
-        else hipLaunchKernelGGL((k_gate_rows<T, VP, false, false>), gr, bl, 0, s, g);
+        if (whole) hipLaunchKernelGGL((k_gate_rows<T, L, VP, false, true>), gr, bl, 0, s, g);
+        else hipLaunchKernelGGL((k_gate_rows<T, L, VP, false, false>), gr, bl, 0, s, g);
     }
 }
 
-template <typename T, int VP>
-void back_rows_any(const GateBackArgs &g, dim3 gr, dim3 bl, hipStream_t s) {
-    if (g.rule.E == 16 * VP && g.vec4)
-        hipLaunchKernelGGL((k_gate_backward_rows<T, VP, true>), gr, bl, 0, s, g);
+template <typename T, int L, int VP>
+void back_rows_any(const ue_ctx &c, const GateBackArgs &g, hipStream_t s) {
+    const dim3 gr(wave_grid(g.T, 64 / L, c.num_cu)), bl(kBlock);
+    if (g.rule.E == L * VP && g.vec4)
+        hipLaunchKernelGGL((k_gate_backward_rows<T, L, VP, true>), gr, bl, 0, s, g);
     else
-        hipLaunchKernelGGL((k_gate_backward_rows<T, VP, false>), gr, bl, 0, s, g);
+        hipLaunchKernelGGL((k_gate_backward_rows<T, L, VP, false>), gr, bl, 0, s, g);
 }
 
 template <typename T>
 hipError_t gate_any(const ue_ctx &c, const GateArgs &g, hipStream_t s) {
     const int E = g.rule.E;
-    const bool rows = E <= kFastExperts && g.rule.k <= kFastTopk;
-    const dim3 gr(wave_grid(g.T, rows ? 4 : 1, c.num_cu)), bl(kBlock);
-    if (rows) {
-        if (E <= 64) gate_rows_any<T, 4>(g, gr, bl, s);
-        else if (E <= 128) gate_rows_any<T, 8>(g, gr, bl, s);
-        else gate_rows_any<T, 16>(g, gr, bl, s);
+    if (E <= kFastExperts && g.rule.k <= kFastTopk) {
+        if (E <= 32) gate_rows_any<T, 8, 4>(c, g, s);
+        else if (E <= 64) gate_rows_any<T, 8, 8>(c, g, s);
+        else if (E <= 128) gate_rows_any<T, 8, 16>(c, g, s);
+        else gate_rows_any<T, 16, 16>(c, g, s);
     } else {
+        const dim3 gr(wave_grid(g.T, 1, c.num_cu)), bl(kBlock);
         switch (lane_slots(E)) {
             case 1: hipLaunchKernelGGL((k_gate<T, 1>), gr, bl, 0, s, g); break;
             case 2: hipLaunchKernelGGL((k_gate<T, 2>), gr, bl, 0, s, g); break;
@@ -585,15 +600,16 @@ hipError_t gate_any(const ue_ctx &c, const GateArgs &g, hipStream_t s) {
 template <typename T>
 hipError_t back_any(const ue_ctx &c, const GateBackArgs &g, hipStream_t s) {
     const int E = g.rule.E;
-    const bool rows = E <= kFastExperts && g.rule.k <= kFastBackTopk;
-    const dim3 gr(wave_grid(g.T, rows ? 4 : 1, c.num_cu)), bl(kBlock);
-    const int v = lane_slots(E);
-    const size_t lds = sizeof(float) * kBlock * v;
-    if (rows) {
-        if (E <= 64) back_rows_any<T, 4>(g, gr, bl, s);
-        else if (E <= 128) back_rows_any<T, 8>(g, gr, bl, s);
-        else back_rows_any<T, 16>(g, gr, bl, s);
+    if (E <= 128 && g.rule.k <= 8) {
+        if (E <= 32) back_rows_any<T, 8, 4>(c, g, s);
+        else if (E <= 64) back_rows_any<T, 8, 8>(c, g, s);
+        else back_rows_any<T, 8, 16>(c, g, s);
+    } else if (E <= kFastExperts && g.rule.k <= kFastBackTopk) {
+        back_rows_any<T, 16, 16>(c, g, s);
     } else {
+        const dim3 gr(wave_grid(g.T, 1, c.num_cu)), bl(kBlock);
+        const int v = lane_slots(E);
+        const size_t lds = sizeof(float) * kBlock * v;
         switch (v) {
             case 1: hipLaunchKernelGGL((k_gate_backward<T, 1>), gr, bl, lds, s, g); break;
             case 2: hipLaunchKernelGGL((k_gate_backward<T, 2>), gr, bl, lds, s, g); break;
