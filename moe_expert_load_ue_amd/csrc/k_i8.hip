@@ -20,12 +20,10 @@
 // wave's F fragments: lane group q then holds 4 F consecutive channels.
 #include <type_traits>
 
-#include "ue_gate.h"
+#include "ue_rows.h"
 
 namespace ue {
 namespace {
-
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kStep = 128;               // bytes of K per stage
 
@@ -47,7 +45,7 @@ struct Tile {
 // dealt to the XCDs. Tiles go in blocks of kBlockM row tiles by all column
 // tiles, row tiles first, each XCD a contiguous run: the tiles an XCD has at
 // once then share both operands' rows in its L2. False: no tile left.
-constexpr int kBlockM = 8;
+constexpr int kBlockM = 4;
 template <int THREADS>
 __device__ __forceinline__ bool find_tile(const I8Args &g, int BM, int ncol,
                                           int *sh, Tile &t) {
@@ -150,19 +148,6 @@ __device__ __forceinline__ int act_row(const I8Args &g, int m) {
     if (i < 0) return -1;
     const int r = i / g.index_div;
     return r < g.a_rows ? r : -1;
-}
-
-// Zeroes the bytes of a 16-byte piece from `left` on. Zero activations are
-// enough where a row ends: in integers what they meet does not matter.
-__device__ __forceinline__ i32x4 keep_bytes(i32x4 v, int left) {
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const int nb = left - 4 * w;
-        const uint32_t keep =
-            nb >= 4 ? 0xFFFFFFFFu : nb <= 0 ? 0u : (1u << (8 * nb)) - 1u;
-        v[w] &= static_cast<int>(keep);
-    }
-    return v;
 }
 
 // FM, FN: 16-row fragments of activations and of the matrix per wave;
@@ -325,7 +310,9 @@ __global__ __launch_bounds__(WM *WN * 64, FM * FN > 32 ? 1 : 2) void k_matmul_i8
     auto mask_half = [&](Half &f, int k0) {
         const int left = g.K - (k0 + q * 16);
 #pragma unroll
-        for (int i = 0; i < FM; ++i) f.a[i] = keep_bytes(f.a[i], left);
+        for (int i = 0; i < FM; ++i)
+            f.a[i] = __builtin_bit_cast(
+                i32x4, keep_bytes(__builtin_bit_cast(u32x4, f.a[i]), left));
     };
     mask_half(f0, st * kStep);
     mask_half(f1, st * kStep + 64);
@@ -370,19 +357,19 @@ __global__ __launch_bounds__(WM *WN * 64, FM * FN > 32 ? 1 : 2) void k_matmul_i8
     }
 }
 
-// Few rows per matrix: the matrix's bytes bound the product. 16 channels (and
-// their 16 up channels) per workgroup, K split over its waves; each wave reads
-// its part of the matrix from HBM straight into its operand registers, kAhead
-// pieces at a time, for up to 16 RT rows at once.
+// Up to 16 rows: the matrix's bytes bound the product. 16 channels (and their
+// 16 up channels) per workgroup, K split over its waves, each streaming its
+// part of the matrix from HBM straight into its operand registers (ue_rows.h).
 constexpr int kRowWaves = 8;
+constexpr int kFewRows = 16;
 
-template <int RT, bool GATED, typename OUT>
+template <int FOLD, bool GATED, typename OUT>
 __global__ __launch_bounds__(kRowWaves * 64) void k_rows_i8(I8Args g) {
     constexpr int NW = GATED ? 2 : 1;
-    constexpr int kAhead = 8 / (RT > NW ? RT : NW);
-    __shared__ i32x4 part[kRowWaves][NW][RT][64];
-    const int lane = lane_id(), l16 = lane & 15, q = lane >> 4;
-    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    typedef RowStream<I8Rows, NW, FOLD, 1, 1> S;
+    __shared__ i32x4 part[kRowWaves][NW][S::kAcc][64];
+    const int tid = threadIdx.x, lane = lane_id();
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n0 = blockIdx.x * 16, group = blockIdx.y;
     int lo = 0, hi = g.M;
     if (g.offsets) {
@@ -391,113 +378,74 @@ __global__ __launch_bounds__(kRowWaves * 64) void k_rows_i8(I8Args g) {
         lo = lo < 0 ? 0 : lo > g.M ? g.M : lo;
         hi = hi < lo ? lo : hi > g.M ? g.M : hi;
     }
+    if (lo >= hi) return;
     const int mat = g.expert_of ? g.expert_of[group] : group;
     if (static_cast<uint32_t>(mat) >= static_cast<uint32_t>(g.n_mats)) return;
-    const int kbytes = (g.K + 15) & ~15;
-    const int n = n0 + l16 < g.N ? n0 + l16 : g.N - 1;
-    const int8_t *w[NW];
+    // (hi - lo <= M <= the tokens FOLD holds)
+    const int m = lo + S::token(0), row = act_row(g, m < hi ? m : hi - 1);
+    const char *w[NW], *x[1] = {reinterpret_cast<const char *>(g.a)};
+    uint32_t wo[S::LD], xo[1] = {static_cast<uint32_t>(row < 0 ? 0 : row) *
+                                 static_cast<uint32_t>(g.lda)};
 #pragma unroll
     for (int c = 0; c < NW; ++c)
-        w[c] = g.w + mat * g.w_stride +
-               (static_cast<int64_t>(c) * g.N + n) * g.ldw;
-    // this wave's part of K, in whole pieces of 64
-    const int pieces = (kbytes + 63) / 64;
-    const int per = (pieces + kRowWaves - 1) / kRowWaves;
-    const int p0 = wv * per, p1 = p0 + per < pieces ? p0 + per : pieces;
-
-    for (int m0 = lo; m0 < hi; m0 += 16 * RT) {
-        const int8_t *a[RT];
-        int row[RT];
+        w[c] = reinterpret_cast<const char *>(
+            g.w + mat * g.w_stride + static_cast<int64_t>(c) * g.N * g.ldw);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const int m = m0 + r * 16 + l16;
-            row[r] = act_row(g, m < hi ? m : hi - 1);
-            a[r] = g.a + static_cast<int64_t>(row[r] < 0 ? 0 : row[r]) * g.lda;
-        }
-        i32x4 acc[NW][RT] = {};
-        for (int p = p0; p < p1; p += kAhead) {
-            i32x4 wf[kAhead][NW], af[kAhead][RT];
+    for (int j = 0; j < S::LD; ++j) {
+        const int n = n0 + S::row(j) < g.N ? n0 + S::row(j) : g.N - 1;
+        wo[j] = static_cast<uint32_t>(n) * static_cast<uint32_t>(g.ldw);
+    }
+    // this wave's part of K, in whole windows
+    const int windows = (g.K + S::kWindow - 1) / S::kWindow;
+    const int per = (windows + kRowWaves - 1) / kRowWaves;
+    const int w0 = wv * per, w1 = w0 + per < windows ? w0 + per : windows;
+    i32x4 acc[NW][S::kAcc] = {};
+    S::run(w, wo, x, xo, w0 * S::kWindow, w1 * S::kWindow, g.K, acc);
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                // pieces past this wave's part, or past K, are read from the
-                // row's start and masked
-                const int k = (p + u) * 64 + q * 16;
-                const int at = p + u < p1 && k < kbytes ? k : 0;
+    for (int c = 0; c < NW; ++c)
 #pragma unroll
-                for (int c = 0; c < NW; ++c)
-                    wf[u][c] = *reinterpret_cast<const i32x4 *>(w[c] + at);
-#pragma unroll
-                for (int r = 0; r < RT; ++r)
-                    af[u][r] = *reinterpret_cast<const i32x4 *>(a[r] + at);
-            }
-            if (p + kAhead > p1 || (p + kAhead) * 64 > g.K) {
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-                    for (int r = 0; r < RT; ++r)
-                        af[u][r] = keep_bytes(
-                            af[u][r], p + u < p1 ? g.K - ((p + u) * 64 + q * 16) : 0);
-            }
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-                for (int c = 0; c < NW; ++c)
-#pragma unroll
-                    for (int r = 0; r < RT; ++r)
-                        acc[c][r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
-                            wf[u][c], af[u][r], acc[c][r], 0, 0, 0);
-        }
+        for (int r = 0; r < S::kAcc; ++r) part[wv][c][r][lane] = acc[c][r];
+    __syncthreads();
+    const int *sums = reinterpret_cast<const int *>(part);
+    const float *ws = g.w_scale + mat * g.ws_stride;
+    for (int i = tid; i < 16 * (hi - lo); i += kRowWaves * 64) {
+        const int nn = i & 15, t = i >> 4, n = n0 + nn;
+        if (n >= g.N) continue;
+        int v[NW] = {};
 #pragma unroll
         for (int c = 0; c < NW; ++c)
+            for (int u = 0; u < kRowWaves; ++u)
 #pragma unroll
-            for (int r = 0; r < RT; ++r) part[wv][c][r][lane] = acc[c][r];
-        __syncthreads();
-        // wave r joins and writes rows 16 r ..
-        for (int r = wv; r < RT; r += kRowWaves) {
-            i32x4 sum[NW];
-#pragma unroll
-            for (int c = 0; c < NW; ++c) {
-                sum[c] = part[0][c][r][lane];
-                for (int v = 1; v < kRowWaves; ++v) sum[c] += part[v][c][r][lane];
-            }
-            const int m = m0 + r * 16 + l16;
-            if (m >= hi) continue;
-            const int ar = act_row(g, m);
-            const float sa = ar < 0 ? 0.f : g.a_scale[ar];
-            const float *ws = g.w_scale + mat * g.ws_stride;
-            const int nb = n0 + 4 * q;
-            float v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int nn = nb + e < g.N ? nb + e : g.N - 1;
-                const float gt = static_cast<float>(sum[0][e]) * sa * ws[nn];
-                v[e] = gt;
-                if constexpr (GATED) {
-                    const float up = static_cast<float>(sum[1][e]) * sa * ws[g.N + nn];
-                    v[e] = gt / (1.0f + expf(-gt)) * up;
+                for (int b = 0; b < S::kParts; ++b) {
+                    int a, at;
+                    S::where(nn, t, b, a, at);
+                    v[c] += sums[((u * NW + c) * S::kAcc + a) * 256 + at];
                 }
-            }
-            store_run<4>(static_cast<OUT *>(g.out) + static_cast<int64_t>(m) * g.ldo + nb,
-                         v, g.vec_out && nb + 4 <= g.N, g.N - nb);
+        const int ar = act_row(g, lo + t);
+        const float sa = ar < 0 ? 0.f : g.a_scale[ar];
+        float y = static_cast<float>(v[0]) * sa * ws[n];
+        if constexpr (GATED) {
+            const float up = static_cast<float>(v[1]) * sa * ws[g.N + n];
+            y = y / (1.0f + expf(-y)) * up;
         }
-        __syncthreads();
+        store_out(static_cast<OUT *>(g.out) + static_cast<int64_t>(lo + t) * g.ldo + n, y);
     }
 }
 
-template <int RT, bool GATED, typename OUT>
+template <int FOLD, bool GATED, typename OUT>
 hipError_t rows_as(const I8Args &g, hipStream_t s) {
-    hipLaunchKernelGGL((k_rows_i8<RT, GATED, OUT>), dim3((g.N + 15) / 16, g.G),
+    hipLaunchKernelGGL((k_rows_i8<FOLD, GATED, OUT>), dim3((g.N + 15) / 16, g.G),
                        dim3(kRowWaves * 64), 0, s, g);
     return hipGetLastError();
 }
 
-template <int RT>
+template <int FOLD>
 hipError_t rows(const I8Args &g, hipStream_t s) {
     if (g.gated)
-        return g.out_f32 ? rows_as<RT, true, float>(g, s)
-                         : rows_as<RT, true, uint16_t>(g, s);
-    return g.out_f32 ? rows_as<RT, false, float>(g, s)
-                     : rows_as<RT, false, uint16_t>(g, s);
+        return g.out_f32 ? rows_as<FOLD, true, float>(g, s)
+                         : rows_as<FOLD, true, uint16_t>(g, s);
+    return g.out_f32 ? rows_as<FOLD, false, float>(g, s)
+                     : rows_as<FOLD, false, uint16_t>(g, s);
 }
 
 template <int FM, int FN, int WM, int WN, int NS, bool GATED, typename OUT,
@@ -535,36 +483,47 @@ hipError_t tiled(const I8Args &g, hipStream_t s) {
 }  // namespace
 
 #ifndef UE_I8_NO_LAUNCH
-// Which kernel, by what each measured on an MI355X (us; columns: rows x K x
-// channels, G: groups):
-//                     256x256  128x128   64x64   32x64  k_rows_i8<1>
-//   8192x7168x4096        222      238     379     541
-//   1000x2048x2048         28     13.1    10.0    14.7
-//   333x1900x1002          38     14.4     7.8     7.0
-//   128x7168x4096          71     44.0    17.5    15.9          72
-//   32x7168x4096           62     26.6    14.7    14.5        19.4
-//   16x7168x4096           60     25.6    14.7    14.4        10.8
-//   1x7168x4096            60     25.1    14.4    14.1         8.0
-//   G=72: 32768x1024x4096 277      297     483     741
-//   G=64: 4096x1024x4096   79     69.7    80.7     112
-//   G=64: 2048x4096x2048  142      138     119     114         227
+// Which kernel, by what each measured on an MI355X (us; rows x K x channels,
+// G: groups, each with a matrix of its own):
+//                        256x256  128x256  128x128   64x64   32x64    rows
+//   8192x7168x4096           192      220      231     370     540
+//   1000x2048x2048            28       18     12.8    10.0    14.7
+//   333x1900x1002             38       23     14.4     7.8     7.0
+//   128x7168x4096             71       43     44.0    17.5    15.9
+//   32x7168x4096              62       39     26.6    14.7    14.5
+//   16x7168x4096              60       38     25.6    14.7    14.4     9.5
+//   1x7168x4096               60       38     25.1    14.4    14.1     6.6
+//   G=64, 512 rows each:
+//     32768x4096x2048        306      326      355
+//     32768x1024x4096        233      285      302
+//   G=72, 150 to 800 rows:
+//     32768x4096x2048        445      392      437
+//     32768x1024x4096        288      300      317
+//   G=64: 4096x1024x4096      79               69.7    80.7     112
+//   G=64: 2048x4096x2048     142                138     119     114
 // Larger tiles read each operand less often and cost less energy (with random
 // data the power limit, not the issue rate, sets the clock); smaller ones give
 // the launch enough workgroups. So: the largest tile that groups of the mean
 // length at least half fill and that makes three workgroups for every four
-// CUs; up to 16 rows go to the row kernel.
+// CUs; up to 16 rows go to the row kernel. Groups with long rows, whose
+// matrices come from HBM, take the tile with three stages: its loads have two
+// stages' time to arrive, and its lesser height fits uneven groups better.
 hipError_t launch_matmul_i8(const ue_ctx &c, const I8Args &g, hipStream_t s) {
     if (g.M == 0 || g.N == 0) return hipSuccess;
-    if (g.M <= 16 && g.G <= 65535) return rows<1>(g, s);
+    // offsets of an indexed row past 32 bits: one kernel has them in 64
+    const int64_t reach = static_cast<int64_t>(g.index ? g.a_rows : g.M) * g.lda;
+    const bool wide = g.index && reach > 0xFFFFFFFFll;
+    if (g.M <= kFewRows && g.G <= 65535 && !wide)
+        return g.M <= 4 ? rows<4>(g, s) : g.M <= 8 ? rows<2>(g, s) : rows<1>(g, s);
     const int64_t channels = g.gated ? 2 * static_cast<int64_t>(g.N) : g.N;
     auto fits = [&](int bm, int bn) {
         const int64_t tiles = ((g.M + bm - 1) / bm + (g.offsets ? g.G / 2 : 0)) *
                               ((channels + bn - 1) / bn);
         return g.M / g.G >= bm / 2 && tiles >= c.num_cu * 3 / 4;
     };
-    // offsets of an indexed row past 32 bits: one kernel has them in 64
-    if (g.index && static_cast<int64_t>(g.a_rows) * g.lda > 0xFFFFFFFFll)
-        return tiled<2, 2, 2, 2, 4, uint64_t>(g, s);
+    if (wide) return tiled<2, 2, 2, 2, 4, uint64_t>(g, s);
+    if (fits(256, 256) && g.offsets && g.K >= 2048)
+        return tiled<4, 4, 2, 4, 3>(g, s);
     if (fits(256, 256)) return tiled<8, 4, 2, 4, 2>(g, s);
     if (fits(128, 128)) return tiled<4, 2, 2, 4, 2>(g, s);
     if (fits(64, 64)) return tiled<2, 2, 2, 2, 4>(g, s);
