@@ -461,10 +461,11 @@ hipError_t tiled_as(const I8Args &g, hipStream_t s) {
     if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
     const auto kernel = k_matmul_i8<FM, FN, WM, WN, NS, GATED, OUT, OFF>;
     if constexpr (kLds > 65536) {
-        const hipError_t he = hipFuncSetAttribute(
+        // once per kernel: the need is a constant
+        static const hipError_t granted = hipFuncSetAttribute(
             reinterpret_cast<const void *>(kernel),
             hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-        if (he != hipSuccess) return he;
+        if (granted != hipSuccess) return granted;
     }
     hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid)),
                        dim3(WM * WN * 64), kLds, s, g);
@@ -482,7 +483,6 @@ hipError_t tiled(const I8Args &g, hipStream_t s) {
 
 }  // namespace
 
-#ifndef UE_I8_NO_LAUNCH
 // Which kernel, by what each measured on an MI355X (us; rows x K x channels,
 // G: groups, each with a matrix of its own):
 //                        256x256  128x256  128x128   64x64   32x64    rows
@@ -529,6 +529,5 @@ hipError_t launch_matmul_i8(const ue_ctx &c, const I8Args &g, hipStream_t s) {
     if (fits(64, 64)) return tiled<2, 2, 2, 2, 4>(g, s);
     return tiled<1, 2, 2, 2, 6>(g, s);
 }
-#endif
 
 }  // namespace ue

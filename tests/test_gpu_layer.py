@@ -629,3 +629,93 @@ def test_other_stream_and_graph():
         for a, b in zip(got, want):
             assert torch.equal(a, b)
     ctx.close()
+
+
+def test_matmul_i8_rows_past_4_gib():
+    """Indexed rows whose offsets do not fit 32 bits."""
+    rng = np.random.default_rng(12)
+    rows, lda, K, N = 70000, 65536, 70, 33
+    a = torch.zeros((rows, lda), dtype=torch.int8, device=DEV)
+    pick = np.array([rows - 1, 0, 65535, 65536, 65537, 69998, 12], np.int32)
+    vals = rng.integers(-128, 128, size=(pick.size, K)).astype(np.int8)
+    a[dev(pick).long(), :K] = dev(vals)
+    sa = torch.ones(rows, device=DEV)
+    w = rng.integers(-128, 128, size=(N, 80)).astype(np.int8)
+    sw = rng.random(N).astype(np.float32)
+    ctx = ctx_for()
+    for reps in (1, 40):                 # few rows, and enough for tiles
+        say("matmul_i8 past 4 GiB", reps)
+        idx = np.tile(pick, reps)
+        out = ue.ue_matmul_i8(ctx, a[:, :K], sa, dev(w)[:, :K], dev(sw),
+                              index=dev(idx), out_dtype=torch.float32)
+        want = np.tile((vals.astype(np.int64) @ w[:, :K].astype(np.int64).T) * sw.astype(np.float64), (reps, 1))
+        check_product(host(out), want, False, torch.float32)
+    ctx.close()
+
+
+def test_large_tiles_and_even_odd_groups():
+    """Sizes that take each of the tiled kernels (256 and 128 rows high, two
+    and three stages, K past several stages and ragged), against integer
+    products in float64 on the device (exact: sums below 2^53)."""
+    rng = torch.Generator(device=DEV)
+    rng.manual_seed(5)
+
+    def i8(*shape):
+        return torch.randint(-128, 128, shape, generator=rng, device=DEV, dtype=torch.int8)
+
+    ctx = ctx_for()
+    for M, K, N, groups in ((3100, 2100, 3001, None), (1500, 700, 2111, None),
+                            (5000, 2064, 1100, [0, 700, 700, 1901, 2501, 3900, 4999]),
+                            (6000, 272, 1500, [0, 1301, 1302, 3000, 4700, 6000])):
+        say("tiles", M, K, N)
+        ld = (K + 15) // 16 * 16
+        E = len(groups) - 1 if groups else 1
+        a, w = i8(M, ld)[:, :K], i8(E, N, ld)[:, :, :K]
+        sa, sw = torch.rand(M, device=DEV), torch.rand((E, N), device=DEV)
+        off = None if groups is None else torch.tensor(groups, dtype=torch.int32, device=DEV)
+        out = torch.full((M, N), -3.0, device=DEV)
+        ue.ue_matmul_i8(ctx, a, sa, w, sw, off, out=out)
+        g = groups or [0, M]
+        for e in range(len(g) - 1):
+            s = slice(g[e], g[e + 1])
+            want = (a[s].double() @ w[e].double().t()) * (sa[s].double()[:, None] * sw[e].double())
+            assert bool(((out[s].double() - want).abs() <= 4 * 2.0 ** -24 * want.abs()).all())
+        assert bool((out[g[-1]:] == -3).all())
+    ctx.close()
+
+
+def test_example_layer():
+    """The example's layer of many tokens against its layer of few, and
+    against the oracle on one token; the router's gradient against the
+    oracle's. The many-token form rounds activations twice to 8 bits: steps of
+    max/127, about 4/127 of an RMS, so 0.9% and for the heavier-tailed hidden
+    rows up to 3%; 5% bounds their sum."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                        "examples", "moe_layer.py")
+    spec = importlib.util.spec_from_file_location("moe_layer_example", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    r = m.run(tokens=777, hidden=256, inter=128, experts=32, ranks=4, spare=2,
+              topk=4, few=16)
+    assert r["same_ids"] == 1.0 and r["apart"] < 0.05
+    assert r["after"] <= r["before"]
+    lay, s = r["layer"], r["saved"]
+    x0 = r["x"][:1].double().cpu().numpy()
+    gu = scaled(lay.gate_up.cpu(), lay.gate_up_scale.cpu().numpy())
+    dn = scaled(lay.down.cpu(), lay.down_scale.cpu().numpy())
+    want, _, _ = L.moe(x0, lay.router.double().cpu().numpy(), gu, dn, 4, "sigmoid",
+                       lay.bias.double().cpu().numpy(), True, 2.5)
+    got = host(r["out"][:1])
+    assert np.linalg.norm(got - want) <= 0.05 * np.linalg.norm(want)
+    dout = torch.randn((777, 256), generator=torch.Generator().manual_seed(3)).to(DEV)
+    grad = host(lay.router_gradient(r["x"], s, dout))
+    dw = (s["rows"].double() * dout.double()[:, None, :]).sum(-1).cpu().numpy()
+    dl = L.gate_backward(s["logits"].double().cpu().numpy(), s["ids"].cpu().numpy(),
+                         dw, "sigmoid", True, 2.5)
+    want = dl.T @ r["x"].double().cpu().numpy()
+    # fp32 products over 777 tokens: u sqrt(777) of the magnitudes' product
+    mag = np.abs(dl).T @ np.abs(r["x"].double().cpu().numpy())
+    assert np.all(np.abs(grad - want) <= 2e-5 * mag + 1e-6)
+    lay.ctx.close()
