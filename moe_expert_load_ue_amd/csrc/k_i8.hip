@@ -36,7 +36,7 @@ __device__ __forceinline__ void wait_loads() {
 
 // The tile of a workgroup: rows [lo, hi) of a group, channels from n0.
 struct Tile {
-    int group, lo, hi, col;
+    int mat, lo, hi, col;               // mat: the matrix its group uses
 };
 
 // Group g has ceil(rows / BM) row tiles, groups in order; offsets are clamped
@@ -58,9 +58,15 @@ __device__ __forceinline__ bool find_tile(const I8Args &g, int BM, int ncol,
         a = a < 0 ? 0 : a > g.M ? g.M : a;
         b = b < a ? a : b > g.M ? g.M : b;
     };
-    int n = 0, before = 0, rows = (g.M + BM - 1) / BM;
+    int n = 0, before = 0, rows = (g.M + BM - 1) / BM, a1 = 0, b1 = 0, mat = first;
     if (g.offsets) {
-        for (int i = first; i < first + per && i < g.G; ++i) {
+        // (the common case of a group per thread reads everything at once)
+        if (first < g.G) {
+            if (g.expert_of) mat = g.expert_of[first];
+            bounds(first, a1, b1);
+            n = (b1 - a1 + BM - 1) / BM;
+        }
+        for (int i = first + 1; i < first + per && i < g.G; ++i) {
             int a, b;
             bounds(i, a, b);
             n += (b - a + BM - 1) / BM;
@@ -86,28 +92,23 @@ __device__ __forceinline__ bool find_tile(const I8Args &g, int BM, int ncol,
     t.col = in / bm;
     const int tile = blk * kBlockM + in % bm;
     if (!g.offsets) {
-        t.group = 0;
+        t.mat = 0;
         t.lo = tile * BM;
         t.hi = g.M;
         return true;
     }
     if (tile >= before && tile < before + n) {
-        int left = tile - before;
-        for (int i = first;; ++i) {
-            int a, b;
+        int left = tile - before, i = first, a = a1, b = b1;
+        for (int nt; left >= (nt = (b - a + BM - 1) / BM); left -= nt) {
+            ++i;
             bounds(i, a, b);
-            const int nt = (b - a + BM - 1) / BM;
-            if (left < nt) {
-                sh[16] = i;
-                sh[17] = a + left * BM;
-                sh[18] = b;
-                break;
-            }
-            left -= nt;
         }
+        sh[16] = i == first ? mat : g.expert_of ? g.expert_of[i] : i;
+        sh[17] = a + left * BM;
+        sh[18] = b;
     }
     __syncthreads();
-    t.group = sh[16];
+    t.mat = sh[16];
     t.lo = sh[17];
     t.hi = sh[18];
     return true;
@@ -169,6 +170,7 @@ __global__ __launch_bounds__(WM *WN * 64, FM * FN > 32 ? 1 : 2) void k_matmul_i8
     static_assert((BM + BN) / 8 % (WM * WN) == 0, "whole chunks per wave");
     extern __shared__ __align__(16) char lds[];
     __shared__ int sh[20];
+    __shared__ float tile_scale[BM + BN];
     const int tid = threadIdx.x, lane = lane_id();
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
 
@@ -177,8 +179,7 @@ __global__ __launch_bounds__(WM *WN * 64, FM * FN > 32 ? 1 : 2) void k_matmul_i8
     const int m0 = __builtin_amdgcn_readfirstlane(tile.lo);
     const int m_end = __builtin_amdgcn_readfirstlane(tile.hi);
     const int n0 = tile.col * kOut;
-    const int mat = __builtin_amdgcn_readfirstlane(
-        g.expert_of ? g.expert_of[tile.group] : tile.group);
+    const int mat = __builtin_amdgcn_readfirstlane(tile.mat);
     if (static_cast<uint32_t>(mat) >= static_cast<uint32_t>(g.n_mats)) return;
 
     // offset of this lane's piece of each chunk it loads, from the matrix or
@@ -275,6 +276,23 @@ __global__ __launch_bounds__(WM *WN * 64, FM * FN > 32 ? 1 : 2) void k_matmul_i8
     typedef std::integral_constant<int, kReads + kChunks> ReadsAndLoads;
     typedef std::integral_constant<int, 0> None;
 
+    // The scales of the tile's rows and channels (gated: the gate channels',
+    // then the up channels'), on their way before the stages: in order, so
+    // that no wait is for them. They go to LDS behind the last products.
+    constexpr int kScales = (BM + BN + kThreads - 1) / kThreads;
+    float scale[kScales];
+    const float *ws = g.w_scale + mat * g.ws_stride;
+#pragma unroll
+    for (int c = 0; c < kScales; ++c) {
+        const int i = c * kThreads + tid, j = i - BM;
+        if (i < BM) {
+            const int ar = m0 + i < m_end ? act_row(g, m0 + i) : -1;
+            scale[c] = ar < 0 ? 0.f : g.a_scale[ar];
+        } else {
+            const int n = n0 + j % kOut;
+            scale[c] = ws[(n < g.N ? n : g.N - 1) + (j < kOut || !GATED ? 0 : g.N)];
+        }
+    }
     for (int s = 0; s < NS && s < steps; ++s)
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) load_chunk(c, s, s * kStep);
@@ -319,37 +337,34 @@ __global__ __launch_bounds__(WM *WN * 64, FM * FN > 32 ? 1 : 2) void k_matmul_i8
     products(f0, None{}, [](int) {});
     products(f1, None{}, [](int) {});
 
-    // scales first, all loads together, then the rows' outputs
+#pragma unroll
+    for (int c = 0; c < kScales; ++c)
+        if (c * kThreads + tid < BM + BN) tile_scale[c * kThreads + tid] = scale[c];
+    __syncthreads();
+    const float *row_scale = tile_scale, *col_scale = tile_scale + BM;
     constexpr int kRun = GATED ? FN * 2 : FN * 4;   // channels a lane holds
-    const int nb = n0 + wn * kRun * 4 + kRun * q;
-    const float *ws = g.w_scale + mat * g.ws_stride;
-    float sw[kRun], su[kRun], sa[FM];
+    const int at = wn * kRun * 4 + kRun * q, nb = n0 + at;
+    float sw[kRun], su[kRun];
 #pragma unroll
     for (int e = 0; e < kRun; ++e) {
-        const int n = nb + e < g.N ? nb + e : g.N - 1;
-        sw[e] = ws[n];
-        if (GATED) su[e] = ws[g.N + n];
-    }
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-        const int m = m0 + arow + i * 16;
-        const int ar = act_row(g, m < m_end ? m : m_end - 1);
-        sa[i] = ar < 0 ? 0.f : g.a_scale[ar];
+        sw[e] = col_scale[at + e];
+        if (GATED) su[e] = col_scale[kOut + at + e];
     }
     const bool whole = g.vec_out && nb + kRun <= g.N;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int m = m0 + arow + i * 16;
         if (m >= m_end) continue;
+        const float sa = row_scale[arow + i * 16];
         float v[kRun];
 #pragma unroll
         for (int e = 0; e < kRun; ++e) {
             if (GATED) {
-                const float gt = static_cast<float>(acc[i][e / 4 * 2][e % 4]) * sa[i] * sw[e];
-                const float up = static_cast<float>(acc[i][e / 4 * 2 + 1][e % 4]) * sa[i] * su[e];
-                v[e] = gt / (1.0f + expf(-gt)) * up;
+                const float gt = static_cast<float>(acc[i][e / 4 * 2][e % 4]) * sa * sw[e];
+                const float up = static_cast<float>(acc[i][e / 4 * 2 + 1][e % 4]) * sa * su[e];
+                v[e] = silu_of(gt) * up;
             } else {
-                v[e] = static_cast<float>(acc[i][e / 4][e % 4]) * sa[i] * sw[e];
+                v[e] = static_cast<float>(acc[i][e / 4][e % 4]) * sa * sw[e];
             }
         }
         store_run<kRun>(static_cast<OUT *>(g.out) + static_cast<int64_t>(m) * g.ldo + nb,
@@ -426,7 +441,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void k_rows_i8(I8Args g) {
         float y = static_cast<float>(v[0]) * sa * ws[n];
         if constexpr (GATED) {
             const float up = static_cast<float>(v[1]) * sa * ws[g.N + n];
-            y = y / (1.0f + expf(-y)) * up;
+            y = silu_of(y) * up;
         }
         store_out(static_cast<OUT *>(g.out) + static_cast<int64_t>(lo + t) * g.ldo + n, y);
     }

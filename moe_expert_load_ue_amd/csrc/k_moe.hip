@@ -282,7 +282,7 @@ __device__ __forceinline__ void up_tile(const MoeArgs &g, const MoeExpert &a,
             v[0] *= sc[nn];
             v[1] *= sc[g.I + nn];
         }
-        const float h = v[0] / (1.0f + expf(-v[0])) * v[1];
+        const float h = silu_of(v[0]) * v[1];
         const uint16_t hi = f32_to_bf16(h);
         const int64_t at = static_cast<int64_t>(a.base + t) * g.I + nn;
         g.h_hi[at] = hi;

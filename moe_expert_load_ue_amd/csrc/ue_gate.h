@@ -38,6 +38,21 @@ __device__ __forceinline__ float sigmoid_slope(float x) {
     return e / ((1.0f + e) * (1.0f + e));
 }
 
+// v / (1 + exp(-v)) within a few ulp: the exponential through base 2, the
+// product's rounding put back as a factor of 1 + r ln 2, and the reciprocal
+// instruction (the full division and exponential took the gated product's
+// epilogue 40 instructions per value, this takes 9).
+__device__ __forceinline__ float silu_of(float v) {
+    constexpr float kLog2eHi = 1.44269502162933349609f;
+    constexpr float kLog2eLo = 1.92596299112661746888e-8f;
+    const float t = -v * kLog2eHi;
+    const float r = __builtin_fmaf(-v, kLog2eHi, -t) - v * kLog2eLo;
+    const float e = __builtin_amdgcn_exp2f(t);
+    // (an infinite e stays so, also where r is not a number)
+    const float d = e > __FLT_MAX__ ? e : __builtin_fmaf(e, r * 0.693147180559945f, e);
+    return v * __builtin_amdgcn_rcpf(1.0f + d);
+}
+
 // Maximum over the 64 lanes, wave-uniform.
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
     return ~wave_min_u32(~v);
