@@ -20,12 +20,14 @@
 // wave's F fragments: lane group q then holds 4 F consecutive channels.
 //
 // Bound: for large products the matrix units at the clock that the power
-// limit leaves them. 8192x7168x4096: 192-222 us on different boxes (2.2-2.5
-// POP/s; the library's product 233-249 us there, zeros instead of random data
-// 160 us), matrix units busy 64% of the cycles, no LDS bank conflicts. With
-// groups, the last row tile of each (a third of the 256-row tiles' rows at 455
-// rows a group) and the rounds of tiles over the CUs: 32768x4096x2048 in 72
-// uneven groups 399 us, in 64 even ones 306, in one 249.
+// limit leaves them. 8192x7168x4096: 196-225 us (2.1-2.5 POP/s) on random data,
+// 166 on zeros, which draw less power; the library's product, without scales,
+// in turn with it 204-235 and 141. Matrix units busy 64% of the cycles, no LDS
+// bank conflicts. With groups, the last row tile of each (23% of the rows of
+// 256-row tiles are empty at 263-939 rows a group, 13% of 128-row tiles) and
+// the rounds of tiles over the CUs: gated 32768x4096x2048 in 72 uneven groups
+// 403 us (128-row tiles), and with 256-row tiles 306 in 64 even groups, 250 in
+// four, 238 without groups.
 #include <type_traits>
 
 #include "ue_rows.h"

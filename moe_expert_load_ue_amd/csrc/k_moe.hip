@@ -23,8 +23,8 @@
 //
 // Bound: HBM reads, 6.9 TB/s at most on this device. Layer of 256 experts,
 // top-8, H=7168, I=2048: 32 tokens, bf16, 96 experts in use: router and choice
-// 18 us, first product 848 us (6.65 TB/s), second 494 (5.7), join 5. One token,
-// int8: 13, 42 (5.6) and 25 us (4.7), where each kernel's start and end weigh.
+// 18 us, first product 850 us (6.6 TB/s), second 495 (5.7), join 5. One token,
+// int8: 13, 43 (5.5) and 25 us (4.7), where each kernel's start and end weigh.
 // The first product reads exactly its matrices (5.64 GB of 5.64), the second 3%
 // more than its own (the hidden activations, once per L2).
 #include "ue_rows.h"
