@@ -38,19 +38,25 @@ __device__ __forceinline__ float sigmoid_slope(float x) {
     return e / ((1.0f + e) * (1.0f + e));
 }
 
-// v / (1 + exp(-v)) within a few ulp: the exponential through base 2, the
-// product's rounding put back as a factor of 1 + r ln 2, and the reciprocal
-// instruction (the full division and exponential took the gated product's
-// epilogue 40 instructions per value, this takes 9).
+// v / (1 + exp(-v)) within 8 u (u = 2^-24) where the exponential is finite:
+// through base 2, the product's rounding put back as a factor of 1 + r ln 2,
+// and the reciprocal instruction, one ulp each (the full division and
+// exponential took the gated product's epilogue 40 instructions per value,
+// this takes 10). The rest r means nothing where the product overflows: an
+// exponential of 0 or infinity (the instruction makes no subnormal numbers)
+// is taken as it is, so that v comes back for large v, also infinite. A
+// quarter of the denominator keeps its reciprocal a normal number, which is
+// all that the instruction makes.
 __device__ __forceinline__ float silu_of(float v) {
     constexpr float kLog2eHi = 1.44269502162933349609f;
     constexpr float kLog2eLo = 1.92596299112661746888e-8f;
+    constexpr int kPositiveNormal = 0x100;
     const float t = -v * kLog2eHi;
     const float r = __builtin_fmaf(-v, kLog2eHi, -t) - v * kLog2eLo;
-    const float e = __builtin_amdgcn_exp2f(t);
-    // (an infinite e stays so, also where r is not a number)
-    const float d = e > __FLT_MAX__ ? e : __builtin_fmaf(e, r * 0.693147180559945f, e);
-    return v * __builtin_amdgcn_rcpf(1.0f + d);
+    float e = __builtin_amdgcn_exp2f(t);
+    if (__builtin_amdgcn_classf(e, kPositiveNormal))
+        e = __builtin_fmaf(e, r * 0.693147180559945f, e);
+    return (0.25f * v) * __builtin_amdgcn_rcpf(__builtin_fmaf(0.25f, e, 0.25f));
 }
 
 // Maximum over the 64 lanes, wave-uniform.

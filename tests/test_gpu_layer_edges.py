@@ -1,0 +1,93 @@
+"""The expert layer's operators where they once went wrong, and at values and
+sizes that tests/test_gpu_layer.py does not reach. u = 2^-24 and u16 = 2^-8 as
+there."""
+import numpy as np
+import pytest
+import torch
+
+import moe_expert_load_ue_amd as ue
+from gpu_helpers import say
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+INF = float("inf")
+U = 2.0 ** -24
+U16 = 2.0 ** -8
+
+
+def ctx_for(E=8, k=2, T=64):
+    return ue.Context(E, 1, 0, k, T, device=DEV)
+
+
+def dev(a, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(a))
+    return (t if dtype is None else t.to(dtype)).to(DEV)
+
+
+def host(t):
+    torch.cuda.synchronize()
+    return t.double().cpu().numpy() if t.is_floating_point() else t.cpu().numpy()
+
+
+def one_expert(x, gate, up, down):
+    """A layer of one expert, hidden 16 and inter 8: x [T, 16]; channel 0 has
+    the given gate and up row (over the first entries of x) and every output
+    reads it through `down`; the other channels are zero."""
+    w13 = torch.zeros((1, 16, 16))
+    w13[0, 0, :len(gate)] = torch.tensor(gate)
+    w13[0, 8, :len(up)] = torch.tensor(up)
+    w2 = torch.zeros((1, 16, 8))
+    w2[0, :, 0] = down
+    ctx = ctx_for(1, 1, 64)
+    router = torch.zeros((1, 16), dtype=torch.bfloat16, device=DEV)
+    ue.ue_register_layer(ctx, router, w13.bfloat16().to(DEV), w2.bfloat16().to(DEV))
+    xs = torch.zeros((len(x), 16))
+    for t, row in enumerate(x):
+        xs[t, :len(row)] = torch.tensor(row)
+    out, _, _ = ue.ue_moe_tokens(ctx, xs.bfloat16().to(DEV))
+    got = host(out)
+    ctx.close()
+    return got
+
+
+# ---- silu ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("M", [1, 40])
+def test_silu_over_the_whole_range(M):
+    """Gated products whose gate is exactly v (1 * 1 * v) and whose up is 1.
+    Relative error: the exponential and the reciprocal instruction one ulp (2 u)
+    each, four roundings: 8 u. Below -88.72 the exponential overflows and the
+    result is -0 where the formula has up to 2.6e-37."""
+    low = float(np.finfo(np.float32).max)
+    v = np.array([INF, low, 3e38, 2.4e38, 2.3e38, 1e38, 1e20, 200.0, 89.0, 88.0,
+                  20.0, 3.0, 1.0, 0.5, 1e-3, 1e-30, 0.0, -0.0, -1e-30, -1e-3,
+                  -0.5, -1.0, -3.0, -20.0, -80.0, -86.0, -87.0, -87.4, -87.5,
+                  -88.0, -88.6, -88.8, -89.0, -104.0, -200.0, -1e20, -1e38,
+                  -2.3e38, -2.4e38, -3e38, -low, -INF, np.nan], np.float32)
+    v = np.concatenate([v, np.linspace(-88.7, 88.7, 1000).astype(np.float32)])
+    n = v.size
+    say("silu", M)
+    ctx = ctx_for()
+    a = torch.ones((M, 16), dtype=torch.int8, device=DEV)[:, :1]
+    w = torch.ones((2 * n, 16), dtype=torch.int8, device=DEV)[:, :1]
+    sw = dev(np.concatenate([v, np.ones(n, np.float32)]))
+    got = host(ue.ue_matmul_i8(ctx, a, torch.ones(M, device=DEV), w, sw, gated=True,
+                               out_dtype=torch.float32))
+    ctx.close()
+    with np.errstate(all="ignore"):
+        d = v.astype(np.float64)
+        want = np.where(d > 700, d, d / (1 + np.exp(-d)))
+    bad = np.isnan(want)
+    assert np.isnan(got[:, bad]).all() and not np.isnan(got[:, ~bad]).any()
+    assert (got[:, np.isposinf(want)] == INF).all()
+    fin = np.isfinite(want)
+    assert np.all(np.abs(got[:, fin] - want[fin]) <= 8 * U * np.abs(want[fin]) + 3e-37)
+
+
+def test_silu_of_large_gates_in_the_layer():
+    """A gate of 2.5e38, one that overflows to infinity, and their negatives."""
+    got = one_expert([[1, 0], [1, 1], [-1, 0]], [2.5e38, 3e38], [1e-30], 1.0)
+    bf = float(torch.tensor(2.5e38).bfloat16()) * float(torch.tensor(1e-30).bfloat16())
+    assert np.all(np.abs(got[0] - bf) <= (U16 + 8 * U) * bf)
+    assert (got[1] == INF).all()
+    assert (got[2] == 0).all()
