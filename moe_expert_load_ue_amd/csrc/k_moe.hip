@@ -60,8 +60,10 @@ __host__ __device__ inline int router_parts(int hidden) {
 // or graph replay, starts anew.)
 // One wave releases and acquires for the workgroup, on either side of a
 // barrier: a fence writes back or invalidates a whole L2, and one in every
-// wave made the choice 11 us instead of 5.
+// wave made the choice 11 us instead of 5. Each wave waits for its own stores
+// ahead of the first barrier.
 __device__ __forceinline__ bool ends_last(uint32_t *done, uint32_t all, int *sh) {
+    wait_stores();
     __syncthreads();
     if (threadIdx.x == 0) {
         const bool last = __hip_atomic_fetch_add(done, 1u, __ATOMIC_ACQ_REL,
@@ -129,7 +131,8 @@ __device__ __forceinline__ void choose(const MoeArgs &g, int t0, int blocks,
             g.ids[a] = e;
             g.weights[a] = weights[a];
         }
-        if (e >= 0) atomicOr(&sh.set[e], 1ull << (a / k));
+        if (static_cast<uint32_t>(e) < static_cast<uint32_t>(E))
+            atomicOr(&sh.set[e], 1ull << (a / k));
     }
     __syncthreads();
     // experts in use, in id order, and where their tokens start: one wave,
@@ -154,7 +157,7 @@ __device__ __forceinline__ void choose(const MoeArgs &g, int t0, int blocks,
     // the weight of each (expert, token) row, and the token
     for (int a = tid; a < g.T * k; a += kChooseWaves * 64) {
         const int e = ids[a], tok = a / k;
-        if (e < 0) continue;
+        if (static_cast<uint32_t>(e) >= static_cast<uint32_t>(E)) continue;
         const int r = sh.base[e] + __popcll(sh.set[e] & ((1ull << tok) - 1));
         g.row_weight[r] = weights[a];
         g.row_token[r] = tok;

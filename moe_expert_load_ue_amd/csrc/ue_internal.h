@@ -447,6 +447,15 @@ __device__ __forceinline__ uint64_t match_peers(int v, bool valid, int bits) {
     return peers;
 }
 
+// Waits until this wave's global stores have arrived. A barrier alone does not:
+// it is compiled without a wait for stores, and the release that one wave makes
+// behind it waits for that wave's own. So every wave whose stores a later
+// release publishes calls this ahead of the barrier. (Nothing is written back
+// here, so it costs no more than the stores' own latency.)
+__device__ __forceinline__ void wait_stores() {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
 __device__ __forceinline__ uint64_t atomic_load_agent(const uint64_t *p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
