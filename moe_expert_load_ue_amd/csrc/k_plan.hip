@@ -1131,7 +1131,9 @@ __global__ __launch_bounds__(kPlanBlock) void k_plan(
         // one device-scope fence per workgroup on each side, after the
         // barrier that orders the workgroup's own stores and loads: each
         // such fence writes back or invalidates a whole L2, so one per
-        // wave would cost a multiple of the plan
+        // wave would cost a multiple of the plan. Each wave waits for its
+        // own stores ahead of that barrier, which does not.
+        wait_stores();
         __syncthreads();
         if (tid == 0) {
             __threadfence();

@@ -45,7 +45,7 @@ def unwaited(lines):
     return found, bad
 
 
-@pytest.mark.parametrize("source", ["k_moe.hip"])
+@pytest.mark.parametrize("source", ["k_moe.hip", "k_plan.hip"])
 def test_stores_are_waited_for_before_they_are_published(source, tmp_path):
     found, bad = unwaited(device_assembly(source, tmp_path))
     assert found > 0 and bad == []
