@@ -498,9 +498,14 @@ int ue_matmul_i8(ue_ctx *ctx, const ue_i8_product *p, void *stream);
  *              down_scale fp32 [E, hidden] (the weights of ue_matmul_i8)
  *   bias, score, renorm, scale   as in ue_gate
  * All matrices 16-byte aligned; hidden and inter multiples of 8 (bf16) or 16
- * (int8), strides likewise, an expert's gate_up below 4 GiB. The memory stays the caller's; the context keeps
- * the pointers until the next registration or ue_destroy, and allocates a
- * workspace for min(max_tokens, UE_MOE_MAX_TOKENS) tokens. */
+ * (int8), strides likewise, an expert's gate_up below 4 GiB. The memory stays
+ * the caller's; the context keeps the pointers until the next registration or
+ * ue_destroy. The call waits for the device (it cannot be captured) and
+ * allocates a workspace for min(max_tokens, UE_MOE_MAX_TOKENS) tokens, unless
+ * an earlier layer's is large enough. Workspaces live until ue_destroy: a
+ * captured graph of ue_moe_tokens keeps working after further registrations,
+ * with the layer it was captured with, as long as the caller keeps that
+ * layer's memory (and replays do not overlap other calls of ue_moe_tokens). */
 #define UE_MOE_MAX_TOKENS 64
 typedef struct ue_layer {
     const void *router;

@@ -832,7 +832,9 @@ def ue_register_layer(ctx: Context, router, gate_up, down, gate_up_scale=None,
     """Registers the layer :func:`ue_moe_tokens` runs: router bf16 [E, H],
     gate_up [E, 2 I, H] (gate rows, then up rows) and down [E, H, I], both
     bf16 or both int8 with channel scales [E, 2 I] and [E, H]. The experts'
-    matrices may lie apart (strided in their first dimension)."""
+    matrices may lie apart (strided in their first dimension). The context
+    keeps the tensors until the next registration; a graph captured from
+    :func:`ue_moe_tokens` needs the caller to keep its layer's."""
     dev = ctx.device
     _need(router, "router", torch.bfloat16, dev)
     if router.dim() != 2 or router.shape[0] != ctx.E:

@@ -250,7 +250,11 @@ void ue_destroy(ue_ctx *ctx) {
     (void)hipDeviceSynchronize();
     if (ctx->ws) (void)hipFree(ctx->ws);
     if (ctx->reg_tables) (void)hipFree(ctx->reg_tables);
-    if (ctx->layer_ws) (void)hipFree(ctx->layer_ws);
+    while (ue::LayerSpace *w = ctx->layer_ws) {
+        ctx->layer_ws = w->older;
+        (void)hipFree(w->mem);
+        delete w;
+    }
     for (auto &e : ctx->ev)
         if (e) (void)hipEventDestroy(e);
     delete ctx;

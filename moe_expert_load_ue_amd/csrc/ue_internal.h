@@ -43,6 +43,13 @@ struct ErrText {
 constexpr int kMoeTokens = UE_MOE_MAX_TOKENS;
 static_assert(kMoeTokens == 64, "one bit per token");
 
+// One workspace of registered layers (device memory) and those it outgrew.
+struct LayerSpace {
+    void *mem;
+    size_t bytes;
+    LayerSpace *older;
+};
+
 struct MoeExpert {
     unsigned long long tokens;   // bit t: token t chose it
     int32_t expert;
@@ -115,7 +122,10 @@ struct ue_ctx {
     bool has_layer = false;
     ue_layer layer{};
     int layer_tokens = 0;          // most tokens of one call
-    void *layer_ws = nullptr;
+    // Workspaces live as long as the context: a captured graph writes to the
+    // one of its capture whenever it is replayed. A registration that fits the
+    // latest one uses it again; an outgrown one stays in the list.
+    ue::LayerSpace *layer_ws = nullptr;
     float *moe_logits = nullptr;   // [parts][layer_tokens][E]
     uint32_t *moe_done = nullptr;
     int32_t *moe_n_active = nullptr;

@@ -2,6 +2,8 @@
 // rows and products, and the whole layer for a few tokens. As in the other
 // entry points every host-visible argument is checked before anything is
 // launched or written.
+#include <new>
+
 #include "ue_internal.h"
 
 namespace {
@@ -277,30 +279,37 @@ int ue_register_layer(ue_ctx *ctx, const ue_layer *l) {
         off = round_up(off + bytes, 256);
         return o;
     };
+    // (the counter comes first in every layout: no layer's other data may lie
+    // over it, since it is zero between calls whichever layer they are of)
+    const size_t o_done = take(sizeof(uint32_t));
     const size_t o_logits = take(sizeof(float) * ue::moe_router_parts(l->hidden) * T * ctx->E);
     const size_t o_n = take(sizeof(int32_t));
-    const size_t o_done = take(sizeof(uint32_t));
     const size_t o_part = take(sizeof(float) * l->hidden * T *
                                ue::moe_down_shares(l->hidden, T, ctx->num_cu));
     const size_t o_act = take(sizeof(ue::MoeExpert) * ctx->E);
     const size_t o_w = take(sizeof(float) * rows);
     const size_t o_t = take(sizeof(int32_t) * rows);
     const size_t o_h = take(2 * sizeof(uint16_t) * rows * l->inter);
-    void *ws = nullptr;
-    if (hipMalloc(&ws, off) != hipSuccess)
-        return fail(ctx, UE_ENOMEM, "ue_register_layer: %zu bytes of workspace", off);
-    char *b = static_cast<char *>(ws);
-    hipError_t he = hipMemset(b + o_done, 0, sizeof(uint32_t));
-    if (he == hipSuccess) he = hipDeviceSynchronize();
-    if (he != hipSuccess) {
-        (void)hipFree(ws);
-        return hip_fail(ctx, he, "ue_register_layer: workspace");
+    if (!ctx->layer_ws || ctx->layer_ws->bytes < off) {
+        ue::LayerSpace *w = new (std::nothrow) ue::LayerSpace{nullptr, off, ctx->layer_ws};
+        if (!w || hipMalloc(&w->mem, off) != hipSuccess) {
+            delete w;
+            return fail(ctx, UE_ENOMEM, "ue_register_layer: %zu bytes of workspace", off);
+        }
+        const hipError_t he = hipMemset(static_cast<char *>(w->mem) + o_done, 0,
+                                        sizeof(uint32_t));
+        if (he != hipSuccess) {
+            (void)hipFree(w->mem);
+            delete w;
+            return hip_fail(ctx, he, "ue_register_layer: workspace");
+        }
+        ctx->layer_ws = w;
     }
-    if (ctx->layer_ws) {
-        (void)hipDeviceSynchronize();
-        (void)hipFree(ctx->layer_ws);
-    }
-    ctx->layer_ws = ws;
+    // (calls of the layer registered before have ended when this returns, so
+    // its matrices may go, and its workspace be used from another stream)
+    const hipError_t he = hipDeviceSynchronize();
+    if (he != hipSuccess) return hip_fail(ctx, he, "ue_register_layer");
+    char *b = static_cast<char *>(ctx->layer_ws->mem);
     ctx->moe_logits = reinterpret_cast<float *>(b + o_logits);
     ctx->moe_done = reinterpret_cast<uint32_t *>(b + o_done);
     ctx->moe_part = reinterpret_cast<float *>(b + o_part);

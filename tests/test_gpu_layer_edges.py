@@ -91,3 +91,67 @@ def test_silu_of_large_gates_in_the_layer():
     assert np.all(np.abs(got[0] - bf) <= (U16 + 8 * U) * bf)
     assert (got[1] == INF).all()
     assert (got[2] == 0).all()
+
+
+# ---- registrations and captured graphs ----------------------------------------------------
+
+def test_graph_outlives_further_registrations():
+    """A captured layer is replayed after larger and smaller layers were
+    registered in the same context and used: each replay, with inputs of its
+    own, equal to the eager result of the layer it was captured with."""
+    E, k, T = 16, 4, 12
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(2)
+
+    def layer(H, I):
+        r = lambda *s: (torch.randn(s, generator=gen, device=DEV) / s[-1] ** 0.5).bfloat16()  # noqa: E731
+        return r(E, H), r(E, 2 * I, H), r(E, H, I)
+
+    ctx, alone = ctx_for(E, k, 64), ctx_for(E, k, 64)
+    first, sizes = layer(64, 32), [(4096, 512), (64, 16), (8192, 64), (32, 64)]
+    ue.ue_register_layer(ctx, *first)
+    ue.ue_register_layer(alone, *first)
+    static = torch.zeros((T, 64), dtype=torch.bfloat16, device=DEV)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        ue.ue_moe_tokens(ctx, static)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        res = ue.ue_moe_tokens(ctx, static)
+    for n, (H, I) in enumerate(sizes):
+        say("registration", n, H, I)
+        other = layer(H, I)
+        ue.ue_register_layer(ctx, *other)
+        y = torch.randn((T, H), generator=gen, device=DEV).bfloat16()
+        before = ue.ue_moe_tokens(ctx, y)
+        x = torch.randn((T, 64), generator=gen, device=DEV).bfloat16()
+        static.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in res]
+        for a, b in zip(got, ue.ue_moe_tokens(alone, x)):
+            assert torch.equal(a, b)
+        # and the layer registered last is as it was
+        for a, b in zip(ue.ue_moe_tokens(ctx, y), before):
+            assert torch.equal(a, b)
+        torch.cuda.synchronize()
+    ctx.close()
+    alone.close()
+
+
+def test_registration_uses_a_workspace_again():
+    """Layers that fit the workspace there is take no more device memory."""
+    E, k = 8, 2
+    ctx = ctx_for(E, k, 64)
+    mk = lambda H, I: [torch.zeros(s, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+                       for s in ((E, H), (E, 2 * I, H), (E, H, I))]
+    big, small = mk(8192, 1024), mk(8192, 64)
+    ue.ue_register_layer(ctx, *big)
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    for _ in range(40):
+        ue.ue_register_layer(ctx, *small)
+        ue.ue_register_layer(ctx, *big)
+    assert torch.cuda.mem_get_info()[0] == free
+    ctx.close()
