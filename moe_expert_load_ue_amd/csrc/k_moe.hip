@@ -296,11 +296,14 @@ __device__ __forceinline__ void up_tile(const MoeArgs &g, const MoeExpert &a,
             v[1] *= sc[g.I + nn];
         }
         const float h = silu_of(v[0]) * v[1];
-        const uint16_t hi = f32_to_bf16(h);
+        // (a finite h that rounds to infinity takes the largest bf16 as its
+        // first half; an infinite one has no finite rest)
+        const bool finite = fabsf(h) <= __FLT_MAX__;
+        uint16_t hi = f32_to_bf16(h);
+        if (finite && (hi & 0x7FFFu) == 0x7F80u) --hi;
         const int64_t at = static_cast<int64_t>(a.base + t) * g.I + nn;
         g.h_hi[at] = hi;
-        // (an infinite h has no finite rest)
-        g.h_lo[at] = fabsf(h) <= __FLT_MAX__ ? f32_to_bf16(h - bf16_to_f32(hi)) : 0;
+        g.h_lo[at] = finite ? f32_to_bf16(h - bf16_to_f32(hi)) : 0;
     }
 }
 

@@ -155,3 +155,18 @@ def test_registration_uses_a_workspace_again():
         ue.ue_register_layer(ctx, *big)
     assert torch.cuda.mem_get_info()[0] == free
     ctx.close()
+
+
+# ---- the hidden activations' two halves --------------------------------------------
+
+def test_hidden_activation_that_rounds_past_bf16():
+    """h = 181/128 2^63 * 181/128 2^64 = 1.9996 2^127 is finite in fp32 and
+    rounds to infinity in bf16: its halves have to add up to it all the same."""
+    v = 181 / 128
+    got = one_expert([[1], [-1]], [v * 2.0 ** 63], [v * 2.0 ** 64], 2.0 ** -100)
+    want = v * v * 2.0 ** 27
+    assert np.all(np.abs(got[0] - want) <= (U16 + 16 * U) * want)
+    # (a negative gate: silu is -0)
+    assert (got[1] == 0).all()
+    got = one_expert([[1]], [v * 2.0 ** 63], [-v * 2.0 ** 64], 2.0 ** -100)
+    assert np.all(np.abs(got[0] + want) <= (U16 + 16 * U) * want)
