@@ -471,7 +471,8 @@ int ue_quantize_rows(ue_ctx *ctx, const void *x, int32_t type, int64_t ldx,
  * For a and w the bytes of a row up to K rounded up to 16 must be readable.
  * out is UE_BF16 or UE_F32, ldo >= N. K in 1..65536; one matrix of w is below
  * 4 GiB and lda below 16 MiB; rows of out times channels are limited by a
- * launch of 2^31 workgroups (UE_ESHAPE). */
+ * launch of fewer than 2^32 threads (UE_ESHAPE): 512 for a tile of 256 x 256
+ * results, 256 for a begun tile of 32 x 64 where groups are that short. */
 typedef struct ue_i8_product {
     const int8_t *a;
     const float *a_scale;

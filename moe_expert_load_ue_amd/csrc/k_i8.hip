@@ -31,6 +31,7 @@
 #include <type_traits>
 
 #include "ue_rows.h"
+#include "ue_tiles.h"
 
 namespace ue {
 namespace {
@@ -387,7 +388,6 @@ __global__ __launch_bounds__(WM *WN * 64, FM * FN > 32 ? 1 : 2) void k_matmul_i8
 // part of the matrix from HBM straight into its operand registers (ue_rows.h).
 // One row, 7168x4096: 6.6 us (29.4 MB, 4.4 TB/s; an empty launch takes 2).
 constexpr int kRowWaves = 8;
-constexpr int kFewRows = 16;
 
 template <int FOLD, bool GATED, typename OUT>
 __global__ __launch_bounds__(kRowWaves * 64) void k_rows_i8(I8Args g) {
@@ -460,6 +460,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void k_rows_i8(I8Args g) {
 
 template <int FOLD, bool GATED, typename OUT>
 hipError_t rows_as(const I8Args &g, hipStream_t s) {
+    static_assert(i8_tile(kI8Rows).bn == 16 && i8_tile(kI8Rows).threads == kRowWaves * 64);
     hipLaunchKernelGGL((k_rows_i8<FOLD, GATED, OUT>), dim3((g.N + 15) / 16, g.G),
                        dim3(kRowWaves * 64), 0, s, g);
     return hipGetLastError();
@@ -474,17 +475,13 @@ hipError_t rows(const I8Args &g, hipStream_t s) {
                      : rows_as<FOLD, false, uint16_t>(g, s);
 }
 
-template <int FM, int FN, int WM, int WN, int NS, bool GATED, typename OUT,
-          typename OFF>
-hipError_t tiled_as(const I8Args &g, hipStream_t s) {
+template <I8Kernel KIND, int FM, int FN, int WM, int WN, int NS, bool GATED,
+          typename OUT, typename OFF>
+hipError_t tiled_as(const I8Args &g, int64_t workgroups, hipStream_t s) {
     constexpr int BM = WM * FM * 16, BN = WN * FN * 16;
-    constexpr int kOut = GATED ? BN / 2 : BN;
+    static_assert(i8_tile(KIND).bm == BM && i8_tile(KIND).bn == BN &&
+                  i8_tile(KIND).threads == WM * WN * 64);
     constexpr int kLds = NS * (BM + BN) * kStep;
-    const int64_t ncol = (g.N + kOut - 1) / kOut;
-    int64_t mt = (static_cast<int64_t>(g.M) + BM - 1) / BM;
-    if (g.offsets) mt += g.G;       // each group's last tile may be partial
-    const int64_t grid = ncol * mt;
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
     const auto kernel = k_matmul_i8<FM, FN, WM, WN, NS, GATED, OUT, OFF>;
     if constexpr (kLds > 65536) {
         // once per kernel: the need is a constant
@@ -493,67 +490,47 @@ hipError_t tiled_as(const I8Args &g, hipStream_t s) {
             hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
         if (granted != hipSuccess) return granted;
     }
-    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid)),
+    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(workgroups)),
                        dim3(WM * WN * 64), kLds, s, g);
     return hipGetLastError();
 }
 
-template <int FM, int FN, int WM, int WN, int NS, typename OFF = uint32_t>
-hipError_t tiled(const I8Args &g, hipStream_t s) {
+template <I8Kernel KIND, int FM, int FN, int WM, int WN, int NS, typename OFF = uint32_t>
+hipError_t tiled(const I8Args &g, int64_t n, hipStream_t s) {
     if (g.gated)
-        return g.out_f32 ? tiled_as<FM, FN, WM, WN, NS, true, float, OFF>(g, s)
-                         : tiled_as<FM, FN, WM, WN, NS, true, uint16_t, OFF>(g, s);
-    return g.out_f32 ? tiled_as<FM, FN, WM, WN, NS, false, float, OFF>(g, s)
-                     : tiled_as<FM, FN, WM, WN, NS, false, uint16_t, OFF>(g, s);
+        return g.out_f32 ? tiled_as<KIND, FM, FN, WM, WN, NS, true, float, OFF>(g, n, s)
+                         : tiled_as<KIND, FM, FN, WM, WN, NS, true, uint16_t, OFF>(g, n, s);
+    return g.out_f32 ? tiled_as<KIND, FM, FN, WM, WN, NS, false, float, OFF>(g, n, s)
+                     : tiled_as<KIND, FM, FN, WM, WN, NS, false, uint16_t, OFF>(g, n, s);
 }
 
 }  // namespace
 
-// Which kernel, by what each measured on an MI355X (us; rows x K x channels,
-// G: groups, each with a matrix of its own):
-//                        256x256  128x256  128x128   64x64   32x64    rows
-//   8192x7168x4096           192      220      231     370     540
-//   1000x2048x2048            28       18     12.8    10.0    14.7
-//   333x1900x1002             38       23     14.4     7.8     7.0
-//   128x7168x4096             71       43     44.0    17.5    15.9
-//   32x7168x4096              62       39     26.6    14.7    14.5
-//   16x7168x4096              60       38     25.6    14.7    14.4     9.5
-//   1x7168x4096               60       38     25.1    14.4    14.1     6.6
-//   G=64, 512 rows each:
-//     32768x4096x2048        306      326      355
-//     32768x1024x4096        233      285      302
-//   G=72, 150 to 800 rows:
-//     32768x4096x2048        445      392      437
-//     32768x1024x4096        288      300      317
-//   G=64: 4096x1024x4096      79               69.7    80.7     112
-//   G=64: 2048x4096x2048     142                138     119     114
-// Larger tiles read each operand less often and cost less energy (with random
-// data the power limit, not the issue rate, sets the clock); smaller ones give
-// the launch enough workgroups. So: the largest tile that groups of the mean
-// length at least half fill and that makes three workgroups for every four
-// CUs; up to 16 rows go to the row kernel. Groups with long rows, whose
-// matrices come from HBM, take the tile with three stages: its loads have two
-// stages' time to arrive, and its lesser height fits uneven groups better.
-hipError_t launch_matmul_i8(const ue_ctx &c, const I8Args &g, hipStream_t s) {
+hipError_t launch_matmul_i8(const ue_ctx &c, const I8Args &g, hipStream_t s,
+                            bool &too_large) {
+    too_large = false;
     if (g.M == 0 || g.N == 0) return hipSuccess;
     // offsets of an indexed row past 32 bits: one kernel has them in 64
     const int64_t reach = static_cast<int64_t>(g.index ? g.a_rows : g.M) * g.lda;
-    const bool wide = g.index && reach > 0xFFFFFFFFll;
-    if (g.M <= kFewRows && g.G <= 65535 && !wide)
-        return g.M <= 4 ? rows<4>(g, s) : g.M <= 8 ? rows<2>(g, s) : rows<1>(g, s);
-    const int64_t channels = g.gated ? 2 * static_cast<int64_t>(g.N) : g.N;
-    auto fits = [&](int bm, int bn) {
-        const int64_t tiles = ((g.M + bm - 1) / bm + (g.offsets ? g.G / 2 : 0)) *
-                              ((channels + bn - 1) / bn);
-        return g.M / g.G >= bm / 2 && tiles >= c.num_cu * 3 / 4;
-    };
-    if (wide) return tiled<2, 2, 2, 2, 4, uint64_t>(g, s);
-    if (fits(256, 256) && g.offsets && g.K >= 2048)
-        return tiled<4, 4, 2, 4, 3>(g, s);
-    if (fits(256, 256)) return tiled<8, 4, 2, 4, 2>(g, s);
-    if (fits(128, 128)) return tiled<4, 2, 2, 4, 2>(g, s);
-    if (fits(64, 64)) return tiled<2, 2, 2, 2, 4>(g, s);
-    return tiled<1, 2, 2, 2, 6>(g, s);
+    const I8Size z{g.M, g.N, g.K, g.G, g.gated, g.offsets != nullptr,
+                   g.index && reach > 0xFFFFFFFFll, c.num_cu};
+    const I8Kernel kind = i8_kernel(z);
+    const int64_t n = i8_workgroups(kind, z);
+    if (n * i8_tile(kind).threads > kLaunchThreads) {
+        too_large = true;
+        return hipSuccess;
+    }
+    switch (kind) {
+        case kI8Rows:
+            return g.M <= 4 ? rows<4>(g, s) : g.M <= 8 ? rows<2>(g, s) : rows<1>(g, s);
+        case kI8Wide: return tiled<kI8Wide, 2, 2, 2, 2, 4, uint64_t>(g, n, s);
+        case kI8Tall: return tiled<kI8Tall, 8, 4, 2, 4, 2>(g, n, s);
+        case kI8Deep: return tiled<kI8Deep, 4, 4, 2, 4, 3>(g, n, s);
+        case kI8Mid: return tiled<kI8Mid, 4, 2, 2, 4, 2>(g, n, s);
+        case kI8Small: return tiled<kI8Small, 2, 2, 2, 2, 4>(g, n, s);
+        case kI8Least: break;
+    }
+    return tiled<kI8Least, 1, 2, 2, 2, 6>(g, n, s);
 }
 
 }  // namespace ue

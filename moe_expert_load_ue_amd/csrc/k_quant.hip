@@ -131,9 +131,21 @@ hipError_t quantize_any(const QuantArgs &g, hipStream_t s) {
 
 }  // namespace
 
+// In launches of at most 2^23 rows: a launch has fewer than 2^32 threads (of one
+// with more the runtime reports success and runs the rest modulo 2^32).
 hipError_t launch_quantize(const QuantArgs &g, hipStream_t s) {
-    if (g.M == 0) return hipSuccess;
-    return g.bf16 ? quantize_any<uint16_t>(g, s) : quantize_any<float>(g, s);
+    constexpr int kRows = 1 << 23;
+    for (int64_t m = 0; m < g.M; m += kRows) {
+        QuantArgs part = g;
+        part.M = static_cast<int>(g.M - m < kRows ? g.M - m : kRows);
+        part.x = static_cast<const char *>(g.x) + m * g.ldx * (g.bf16 ? 2 : 4);
+        part.q = g.q + m * g.ldq;
+        part.scale = g.scale + m;
+        const hipError_t he = g.bf16 ? quantize_any<uint16_t>(part, s)
+                                     : quantize_any<float>(part, s);
+        if (he != hipSuccess) return he;
+    }
+    return hipSuccess;
 }
 
 }  // namespace ue

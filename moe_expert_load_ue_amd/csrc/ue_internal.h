@@ -247,7 +247,9 @@ struct I8Args {
     void *out;
     int64_t ldo;
 };
-hipError_t launch_matmul_i8(const ue_ctx &c, const I8Args &g, hipStream_t s);
+// too_large: nothing was launched, the launch would have 2^32 threads or more.
+hipError_t launch_matmul_i8(const ue_ctx &c, const I8Args &g, hipStream_t s,
+                            bool &too_large);
 
 struct MoeArgs {
     int T, H, I;

@@ -230,10 +230,11 @@ int ue_matmul_i8(ue_ctx *ctx, const ue_i8_product *p, void *stream) {
     g.ldo = p->ldo;
     hipStream_t s = static_cast<hipStream_t>(stream);
     tbegin(ctx, s);
-    const hipError_t he = ue::launch_matmul_i8(*ctx, g, s);
+    bool too_large = false;
+    const hipError_t he = ue::launch_matmul_i8(*ctx, g, s, too_large);
     tmark(ctx, s);
-    if (he == hipErrorInvalidValue)
-        return fail(ctx, UE_ESHAPE, "ue_matmul_i8: more than 2^31 workgroups");
+    if (too_large)
+        return fail(ctx, UE_ESHAPE, "ue_matmul_i8: a launch of 2^32 threads or more");
     return he == hipSuccess ? UE_OK : hip_fail(ctx, he, "k_matmul_i8 launch");
 }
 

@@ -170,3 +170,44 @@ def test_hidden_activation_that_rounds_past_bf16():
     assert (got[1] == 0).all()
     got = one_expert([[1]], [v * 2.0 ** 63], [-v * 2.0 ** 64], 2.0 ** -100)
     assert np.all(np.abs(got[0] + want) <= (U16 + 16 * U) * want)
+
+
+# ---- launches of 2^32 threads ------------------------------------------------------------
+
+def test_more_rows_than_one_launch_holds():
+    """2^26 + 3 rows of one element: more than 2^32 threads at a wave per row."""
+    M = (1 << 26) + 3
+    say("quantize rows", M)
+    x = torch.zeros((M, 1), device=DEV)
+    x[-1], x[0], x[1 << 26], x[12345] = 3.0, -2.0, 0.5, INF
+    ctx = ctx_for()
+    q = torch.full((M, 16), 7, dtype=torch.int8, device=DEV)
+    _, s = ue.ue_quantize_rows(ctx, x, q=q[:, :1])
+    at = torch.tensor([M - 1, 0, 1 << 26, 12345, 5, (1 << 26) + 1], device=DEV)
+    assert q[at, 0].tolist() == [127, -127, 127, 0, 0, 0]
+    assert bool((q[:, 1:] == 0).all())
+    want = (x[at, 0] / 127).cpu()
+    got = s[at].cpu()
+    assert torch.equal(got[[0, 1, 2, 4, 5]].sign(), torch.tensor([1.0, 1, 1, 0, 0]))
+    assert torch.equal(got[[0, 2]], want[[0, 2]]) and torch.equal(got[1], -want[1])
+    assert bool(got[3].isnan())
+    assert int((s != 0).sum()) == 4
+    ctx.close()
+
+
+def test_more_channels_than_one_launch_of_the_row_kernel_holds():
+    """One row of 16 times 2^27 + 5 channels: 2 GiB, which the limits allow, but
+    2^32 threads at 16 channels a workgroup."""
+    N = (1 << 27) + 5
+    say("one row, channels", N)
+    rng = torch.Generator(device=DEV)
+    rng.manual_seed(1)
+    a = torch.randint(-127, 128, (1, 16), generator=rng, device=DEV, dtype=torch.int8)
+    w = torch.randint(-127, 128, (N, 16), generator=rng, device=DEV, dtype=torch.int8)
+    sw = torch.ones(N, device=DEV)
+    ctx = ctx_for()
+    out = ue.ue_matmul_i8(ctx, a, sw[:1], w, sw, out_dtype=torch.float32)
+    for lo in range(0, N, 1 << 24):
+        part = (w[lo:lo + (1 << 24)].float() * a.float()).sum(1)     # below 2^24: exact
+        assert torch.equal(out[0, lo:lo + (1 << 24)], part)
+    ctx.close()
