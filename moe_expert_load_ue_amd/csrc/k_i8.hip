@@ -477,18 +477,25 @@ hipError_t rows(const I8Args &g, hipStream_t s) {
 
 template <I8Kernel KIND, int FM, int FN, int WM, int WN, int NS, bool GATED,
           typename OUT, typename OFF>
-hipError_t tiled_as(const I8Args &g, int64_t workgroups, hipStream_t s) {
+hipError_t tiled_as(ue_ctx &c, const I8Args &g, int64_t workgroups, hipStream_t s) {
     constexpr int BM = WM * FM * 16, BN = WN * FN * 16;
     static_assert(i8_tile(KIND).bm == BM && i8_tile(KIND).bn == BN &&
                   i8_tile(KIND).threads == WM * WN * 64);
+    static_assert(KIND * 4 + 3 < 32, "a bit for every kernel");
     constexpr int kLds = NS * (BM + BN) * kStep;
     const auto kernel = k_matmul_i8<FM, FN, WM, WN, NS, GATED, OUT, OFF>;
     if constexpr (kLds > 65536) {
-        // once per kernel: the need is a constant
-        static const hipError_t granted = hipFuncSetAttribute(
-            reinterpret_cast<const void *>(kernel),
-            hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-        if (granted != hipSuccess) return granted;
+        // once per kernel and context (a grant is the device's, and a context
+        // belongs to one): the need is a constant. One that fails is asked for
+        // again by the next call.
+        const uint32_t bit = 1u << (KIND * 4 + GATED * 2 + (sizeof(OUT) == 4));
+        if (!(c.i8_granted & bit)) {
+            const hipError_t he = hipFuncSetAttribute(
+                reinterpret_cast<const void *>(kernel),
+                hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+            if (he != hipSuccess) return he;
+            c.i8_granted |= bit;
+        }
     }
     hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(workgroups)),
                        dim3(WM * WN * 64), kLds, s, g);
@@ -496,17 +503,17 @@ hipError_t tiled_as(const I8Args &g, int64_t workgroups, hipStream_t s) {
 }
 
 template <I8Kernel KIND, int FM, int FN, int WM, int WN, int NS, typename OFF = uint32_t>
-hipError_t tiled(const I8Args &g, int64_t n, hipStream_t s) {
+hipError_t tiled(ue_ctx &c, const I8Args &g, int64_t n, hipStream_t s) {
     if (g.gated)
-        return g.out_f32 ? tiled_as<KIND, FM, FN, WM, WN, NS, true, float, OFF>(g, n, s)
-                         : tiled_as<KIND, FM, FN, WM, WN, NS, true, uint16_t, OFF>(g, n, s);
-    return g.out_f32 ? tiled_as<KIND, FM, FN, WM, WN, NS, false, float, OFF>(g, n, s)
-                     : tiled_as<KIND, FM, FN, WM, WN, NS, false, uint16_t, OFF>(g, n, s);
+        return g.out_f32 ? tiled_as<KIND, FM, FN, WM, WN, NS, true, float, OFF>(c, g, n, s)
+                         : tiled_as<KIND, FM, FN, WM, WN, NS, true, uint16_t, OFF>(c, g, n, s);
+    return g.out_f32 ? tiled_as<KIND, FM, FN, WM, WN, NS, false, float, OFF>(c, g, n, s)
+                     : tiled_as<KIND, FM, FN, WM, WN, NS, false, uint16_t, OFF>(c, g, n, s);
 }
 
 }  // namespace
 
-hipError_t launch_matmul_i8(const ue_ctx &c, const I8Args &g, hipStream_t s,
+hipError_t launch_matmul_i8(ue_ctx &c, const I8Args &g, hipStream_t s,
                             bool &too_large) {
     too_large = false;
     if (g.M == 0 || g.N == 0) return hipSuccess;
@@ -523,14 +530,14 @@ hipError_t launch_matmul_i8(const ue_ctx &c, const I8Args &g, hipStream_t s,
     switch (kind) {
         case kI8Rows:
             return g.M <= 4 ? rows<4>(g, s) : g.M <= 8 ? rows<2>(g, s) : rows<1>(g, s);
-        case kI8Wide: return tiled<kI8Wide, 2, 2, 2, 2, 4, uint64_t>(g, n, s);
-        case kI8Tall: return tiled<kI8Tall, 8, 4, 2, 4, 2>(g, n, s);
-        case kI8Deep: return tiled<kI8Deep, 4, 4, 2, 4, 3>(g, n, s);
-        case kI8Mid: return tiled<kI8Mid, 4, 2, 2, 4, 2>(g, n, s);
-        case kI8Small: return tiled<kI8Small, 2, 2, 2, 2, 4>(g, n, s);
+        case kI8Wide: return tiled<kI8Wide, 2, 2, 2, 2, 4, uint64_t>(c, g, n, s);
+        case kI8Tall: return tiled<kI8Tall, 8, 4, 2, 4, 2>(c, g, n, s);
+        case kI8Deep: return tiled<kI8Deep, 4, 4, 2, 4, 3>(c, g, n, s);
+        case kI8Mid: return tiled<kI8Mid, 4, 2, 2, 4, 2>(c, g, n, s);
+        case kI8Small: return tiled<kI8Small, 2, 2, 2, 2, 4>(c, g, n, s);
         case kI8Least: break;
     }
-    return tiled<kI8Least, 1, 2, 2, 2, 6>(g, n, s);
+    return tiled<kI8Least, 1, 2, 2, 2, 6>(c, g, n, s);
 }
 
 }  // namespace ue

@@ -135,6 +135,9 @@ struct ue_ctx {
     int32_t *moe_row_token = nullptr;      // [layer_tokens * k]
     uint16_t *moe_h = nullptr;     // [2][layer_tokens * k][inter]
 
+    // Kernels of ue_matmul_i8 whose LDS need this context's device has granted.
+    uint32_t i8_granted = 0;
+
     // Kernel timing (off unless ue_set_timing enabled it).
     static constexpr int kMaxEvents = 8;
     bool timing = false;
@@ -248,7 +251,7 @@ struct I8Args {
     int64_t ldo;
 };
 // too_large: nothing was launched, the launch would have 2^32 threads or more.
-hipError_t launch_matmul_i8(const ue_ctx &c, const I8Args &g, hipStream_t s,
+hipError_t launch_matmul_i8(ue_ctx &c, const I8Args &g, hipStream_t s,
                             bool &too_large);
 
 struct MoeArgs {

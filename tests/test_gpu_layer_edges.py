@@ -211,3 +211,26 @@ def test_more_channels_than_one_launch_of_the_row_kernel_holds():
         part = (w[lo:lo + (1 << 24)].float() * a.float()).sum(1)     # below 2^24: exact
         assert torch.equal(out[0, lo:lo + (1 << 24)], part)
     ctx.close()
+
+
+# ---- large tiles in every context ---------------------------------------------------------
+
+def test_large_tiles_in_a_second_context():
+    """The LDS of the large tiles is granted per context: the first calls of two
+    contexts, each with both output types, plain and gated."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(9)
+    a = torch.randint(-127, 128, (4096, 256), generator=gen, device=DEV, dtype=torch.int8)
+    w = torch.randint(-127, 128, (3072, 256), generator=gen, device=DEV, dtype=torch.int8)
+    one = torch.full((4096,), 0.01, device=DEV)
+    got = []
+    for _ in range(2):
+        ctx = ctx_for()
+        for gated in (False, True):
+            for dtype in (torch.float32, torch.bfloat16):
+                got.append(ue.ue_matmul_i8(ctx, a, one, w, one[:3072], gated=gated,
+                                           out_dtype=dtype))
+        torch.cuda.synchronize()
+        ctx.close()
+    for i in range(4):
+        assert torch.equal(got[i], got[i + 4])
