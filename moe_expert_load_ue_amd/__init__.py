@@ -624,8 +624,8 @@ def _rows(t, name, device, types, cols=None):
     if c > 1 and one != 1:
         raise ValueError(f"{name} must have contiguous rows")
     if n <= 1:
-        # a single row has no distance to the next: any that is long enough
-        ld = max(ld, (c + 15) // 16 * 16)
+        # a single row has no distance to the next: one that meets every call
+        ld = (c + 15) // 16 * 16
     return n, c, ld
 
 
@@ -785,7 +785,7 @@ def ue_matmul_i8(ctx: Context, a, a_scale, w, w_scale, offsets=None,
     if K > 1 and one != 1:
         raise ValueError("w must have contiguous rows")
     if channels <= 1:
-        ldw = max(ldw, (K + 15) // 16 * 16)
+        ldw = (K + 15) // 16 * 16
     if n_mats == 1:
         w_stride = 0
     if K % 16 and channels:

@@ -234,3 +234,41 @@ def test_large_tiles_in_a_second_context():
         ctx.close()
     for i in range(4):
         assert torch.equal(got[i], got[i + 4])
+
+
+# ---- single rows -----------------------------------------------------------------------
+
+def test_a_single_row_of_any_matrix():
+    """One row has no next one, so the distance to it is no condition: rows cut
+    out of matrices whose own distance would be refused."""
+    ctx = ctx_for(8, 2, 16)
+    rng = np.random.default_rng(3)
+    wide = torch.full((3, 91), 5, dtype=torch.int8, device=DEV)
+    a = torch.empty((1, 91), dtype=torch.int8, device=DEV)
+    a.copy_(dev(rng.integers(-127, 128, size=(1, 91)).astype(np.int8)))
+    wide[:1] = a
+    w = dev(rng.integers(-127, 128, size=(5, 96)).astype(np.int8))[:, :80]
+    one = torch.ones(5, device=DEV)
+    want = (a[:, :80].double() @ w.double().t()).float()
+    say("single rows")
+    got = ue.ue_matmul_i8(ctx, wide[:1, :80], one[:1], w, one, out_dtype=torch.float32)
+    assert torch.equal(got, want)
+    # one channel of a matrix likewise
+    got = ue.ue_matmul_i8(ctx, w, one, wide[:1, :80], one[:1], out_dtype=torch.float32)
+    assert torch.equal(got, want.t())
+    # a row of activations into a row of int8
+    x = torch.randn((2, 83), device=DEV)
+    q = torch.full((2, 91), 9, dtype=torch.int8, device=DEV)
+    ue.ue_quantize_rows(ctx, x[:1, :80], q=q[:1, :80])
+    assert torch.equal(q[:1, :80], ue.ue_quantize_rows(ctx, x[:1, :80].contiguous())[0])
+    assert bool((q[0, 80:] == 9).all()) and bool((q[1] == 9).all())
+    # a token
+    router = torch.randn((8, 16), device=DEV).bfloat16()
+    gu, dn = torch.randn((8, 32, 16), device=DEV).bfloat16(), torch.randn((8, 16, 16), device=DEV).bfloat16()
+    ue.ue_register_layer(ctx, router, gu, dn)
+    tok = torch.randn((2, 19), device=DEV).bfloat16()
+    got = ue.ue_moe_tokens(ctx, tok[:1, :16])
+    want = ue.ue_moe_tokens(ctx, tok[:1, :16].contiguous())
+    for g, v in zip(got, want):
+        assert torch.equal(g, v)
+    ctx.close()
