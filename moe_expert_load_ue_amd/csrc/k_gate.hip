@@ -246,6 +246,10 @@ __device__ __forceinline__ float key_value(uint32_t key) {
     return __uint_as_float(k & ~0xFFu);
 }
 
+// exp(x) within (2 + 1.2 |x|) u: for ranks that are looked at again, and for
+// the softmax's denominator, where a term x below the top counts with its
+// weight e^x (the weighted mean of |x| over 256 terms is at most 3.4, so the
+// sum is within 7 u).
 constexpr float kLog2e = 1.44269504088896340736f;
 __device__ __forceinline__ float fast_exp(float x) {
     return __builtin_amdgcn_exp2f(x * kLog2e);
@@ -505,8 +509,11 @@ __global__ __launch_bounds__(kBlock) void k_gate_backward_rows(GateBackArgs g) {
             all = 0.f;
 #pragma unroll
             for (int i = 0; i < VP; ++i) {
-                x[i] = x[i] == -__builtin_inff()
-                           ? 0.f : fast_exp(finite_top(x[i]) - top);
+                // (an fp32 gradient shows an unlikely expert's error in full;
+                // in bf16 100 u are lost in the rounding)
+                const float below = finite_top(x[i]) - top;
+                x[i] = x[i] == -__builtin_inff() ? 0.f
+                       : sizeof(T) == 4 ? exp_of(below) : fast_exp(below);
                 all += x[i];
             }
             all = row_sum<L>(all);

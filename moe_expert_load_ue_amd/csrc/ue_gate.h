@@ -38,25 +38,28 @@ __device__ __forceinline__ float sigmoid_slope(float x) {
     return e / ((1.0f + e) * (1.0f + e));
 }
 
-// v / (1 + exp(-v)) within 8 u (u = 2^-24) where the exponential is finite:
-// through base 2, the product's rounding put back as a factor of 1 + r ln 2,
-// and the reciprocal instruction, one ulp each (the full division and
-// exponential took the gated product's epilogue 40 instructions per value,
-// this takes 10). The rest r means nothing where the product overflows: an
-// exponential of 0 or infinity (the instruction makes no subnormal numbers)
-// is taken as it is, so that v comes back for large v, also infinite. A
-// quarter of the denominator keeps its reciprocal a normal number, which is
-// all that the instruction makes.
-__device__ __forceinline__ float silu_of(float v) {
+// exp(x) within 4 u (u = 2^-24), 0 below 2^-126: through base 2, the product's
+// rounding put back as a factor of 1 + r ln 2. (The instruction alone is off by
+// 1.2 |x| u more.) The rest r means nothing where the product overflows: an
+// exponential of 0 or infinity is taken as it is.
+__device__ __forceinline__ float exp_of(float x) {
     constexpr float kLog2eHi = 1.44269502162933349609f;
     constexpr float kLog2eLo = 1.92596299112661746888e-8f;
     constexpr int kPositiveNormal = 0x100;
-    const float t = -v * kLog2eHi;
-    const float r = __builtin_fmaf(-v, kLog2eHi, -t) - v * kLog2eLo;
-    float e = __builtin_amdgcn_exp2f(t);
-    if (__builtin_amdgcn_classf(e, kPositiveNormal))
-        e = __builtin_fmaf(e, r * 0.693147180559945f, e);
-    return (0.25f * v) * __builtin_amdgcn_rcpf(__builtin_fmaf(0.25f, e, 0.25f));
+    const float t = x * kLog2eHi;
+    const float r = __builtin_fmaf(x, kLog2eHi, -t) + x * kLog2eLo;
+    const float e = __builtin_amdgcn_exp2f(t);
+    return __builtin_amdgcn_classf(e, kPositiveNormal)
+               ? __builtin_fmaf(e, r * 0.693147180559945f, e) : e;
+}
+
+// v / (1 + exp(-v)) within 8 u where the exponential is finite, by the
+// reciprocal instruction, one ulp (the full division and exponential took the
+// gated product's epilogue 40 instructions per value, this takes 10). v comes
+// back for large v, also infinite. A quarter of the denominator keeps its
+// reciprocal a normal number, which is all that the instruction makes.
+__device__ __forceinline__ float silu_of(float v) {
+    return (0.25f * v) * __builtin_amdgcn_rcpf(__builtin_fmaf(0.25f, exp_of(-v), 0.25f));
 }
 
 // Maximum over the 64 lanes, wave-uniform.

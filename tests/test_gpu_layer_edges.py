@@ -272,3 +272,32 @@ def test_a_single_row_of_any_matrix():
     for g, v in zip(got, want):
         assert torch.equal(g, v)
     ctx.close()
+
+
+# ---- the softmax's gradient far from the top ------------------------------------------
+
+@pytest.mark.parametrize("E", [60, 64, 128, 200, 256])
+def test_softmax_gradient_of_unlikely_experts(E):
+    """One expert chosen at logit 0, the others 20 to 85 below, in eighths, so
+    that differences to the top are exact. Each gradient is -p_e p_0 g: the
+    exponential 2 u, the denominator u and its reciprocal or quotient 3 u (the
+    other terms are below 256 e^-20), p_0 g with its factor 4 u, the products
+    2 u: 12 u, and 16 u here."""
+    rng = np.random.default_rng(E)
+    T = 70
+    x = -rng.integers(160, 680, size=(T, E)) / 8.0
+    top = rng.integers(0, E, size=T)
+    x[np.arange(T), top] = 0
+    dw = (rng.random((T, 1)) + 0.5).astype(np.float32)
+    say("unlikely experts", E)
+    ctx = ctx_for(E, 1, T)
+    got = host(ue.ue_gate_backward(ctx, dev(x, torch.float32), dev(top.astype(np.int32)),
+                                   dev(dw), "softmax", False, 1.5))
+    ctx.close()
+    p = np.exp(x)
+    p /= p.sum(1, keepdims=True)
+    p0 = p[np.arange(T), top]
+    want = -p * (p0 * dw[:, 0] * 1.5)[:, None]
+    # (the chosen expert's is p_0 g times the sum of the others: it cancels)
+    rest = np.arange(E)[None, :] != top[:, None]
+    assert np.all(np.abs(got - want)[rest] <= 16 * U * np.abs(want)[rest])
