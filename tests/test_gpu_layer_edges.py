@@ -7,6 +7,7 @@ import torch
 
 import moe_expert_load_ue_amd as ue
 from gpu_helpers import say
+from tile_rule import compile_rule
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -301,3 +302,105 @@ def test_softmax_gradient_of_unlikely_experts(E):
     # (the chosen expert's is p_0 g times the sum of the others: it cancels)
     rest = np.arange(E)[None, :] != top[:, None]
     assert np.all(np.abs(got - want)[rest] <= 16 * U * np.abs(want)[rest])
+
+
+# ---- every tile of the int8 product ------------------------------------------------------
+
+@pytest.fixture(scope="module")
+def rule(tmp_path_factory):
+    f = compile_rule(str(tmp_path_factory.mktemp("rule")))
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    return lambda *a: f(*a, num_cu=cus)
+
+
+def uneven(rng, M, G, low):
+    """Offsets of G groups over M rows, one of them empty, none of the others
+    below `low`, the last row in none."""
+    n = rng.random(G) + 0.3
+    n[G // 2] = 0
+    rows = np.floor(n / n.sum() * (M - 1 - low * G)).astype(np.int64) + low
+    rows[G // 2] = 0
+    rows[-1] += M - 1 - rows.sum()
+    return np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+
+
+# tile wanted, M, channels out (ungated), groups (0: none), the lengths of K
+TILED = [("256x256", 4100, 3001, 0, (16, 128, 129, 256, 300, 500, 1000)),
+         ("256x256", 6200, 2040, 7, (100, 384, 1990)),
+         ("128x256", 6200, 2040, 7, (2048, 2100, 2303)),
+         ("128x128", 1500, 2111, 0, (60, 250, 700)),
+         ("128x128", 2500, 2100, 9, (333, 2063)),
+         ("64x64", 700, 1100, 0, (128, 129, 512, 600, 1030)),
+         ("64x64", 1900, 515, 11, (90, 777)),
+         ("32x64", 130, 500, 0, (200, 900)),
+         ("32x64", 300, 390, 14, (400,))]
+
+
+@pytest.mark.parametrize("want,M,N,G,Ks", TILED)
+@pytest.mark.parametrize("gated", [False, True])
+def test_every_tile_by_value(rule, want, M, N, G, Ks, gated):
+    """Plain, gated, indexed (an index out of range among them), both output
+    types, rows of the output that are and that are not 16-byte aligned, at
+    ends of K inside and between stages, against sums in float64 (exact:
+    below 2^53). The roundings as in tests/test_gpu_layer.py: 4 u, gated
+    1.5e-5 (gates are below 100 here), bf16 u16 more."""
+    rng = np.random.default_rng(M + N + G)
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(M)
+
+    def i8(*shape):
+        return torch.randint(-128, 128, shape, generator=gen, device=DEV, dtype=torch.int8)
+
+    N = N // 2 if gated else N
+    mats = max(G, 1)
+    ctx = ctx_for()
+    for K in Ks:
+        assert rule(M, N, K, mats, gated, G > 0).name == want
+        ld = (K + 15) // 16 * 16
+        ch = 2 * N if gated else N
+        k, rows = 3, M // 2
+        w = i8(mats, ch, ld)[:, :, :K]
+        sw = (torch.rand((mats, ch), generator=gen, device=DEV) + 0.5) / (73 * K ** 0.5)
+        off = uneven(rng, M, G, 1) if G else None
+        exp = rng.permutation(mats).astype(np.int32)
+        if G:
+            exp[1] = -1                                     # a slot without expert
+        index = rng.integers(0, rows * k, size=M).astype(np.int32)
+        index[rng.integers(0, M, size=3)] = [-1, rows * k, 2 ** 31 - 1]
+        for indexed, dtype, pad in ((False, torch.float32, 0), (False, torch.bfloat16, 8 - N % 8),
+                                    (True, torch.float32, 4 - N % 4), (True, torch.bfloat16, 3)):
+            say("tile", want, M, K, N, G, gated, indexed, dtype, pad)
+            a = i8(rows if indexed else M, ld)[:, :K]
+            sa = (torch.rand(a.shape[0], generator=gen, device=DEV) + 0.5) / 127
+            out = torch.full((M, N + pad), -77.0, dtype=dtype, device=DEV)
+            ue.ue_matmul_i8(ctx, a, sa, w if G else w[0], sw if G else sw[0],
+                            dev(off) if G else None, dev(exp) if G else None,
+                            dev(index) if indexed else None, k, gated, out[:, :N])
+            r = torch.arange(M, device=DEV)
+            if indexed:
+                r = torch.div(dev(index).long(), k, rounding_mode="floor")
+            ok = (r >= 0) & (r < a.shape[0])
+            av = a[r.clamp(0, a.shape[0] - 1)].double() * ok[:, None]
+            sv = sa[r.clamp(0, a.shape[0] - 1)].double()
+            bounds = off.tolist() if G else [0, M]
+            seen = torch.zeros(M, dtype=torch.bool, device=DEV)
+            for g in range(len(bounds) - 1):
+                e = int(exp[g]) if G else 0
+                lo, hi = bounds[g], bounds[g + 1]
+                if e < 0 or lo == hi:
+                    continue
+                seen[lo:hi] = True
+                v = av[lo:hi] @ w[e].double().t()
+                v = v * sv[lo:hi, None] * sw[e].double()
+                if gated:
+                    gt = v[:, :N]
+                    assert float(gt.abs().max()) < 100
+                    v = gt / (1 + torch.exp(-gt)) * v[:, N:]
+                tol = (1.5e-5 if gated else 4 * U) * v.abs() + (1e-30 if gated else 0)
+                if dtype == torch.bfloat16:
+                    tol = tol + U16 * v.abs()
+                assert bool(((out[lo:hi, :N].double() - v).abs() <= tol).all()), (K, g)
+            assert bool((out[~seen] == -77).all())
+            assert bool((out[:, N:] == -77).all())
+            assert int(seen.sum()) > M // 2
+    ctx.close()
