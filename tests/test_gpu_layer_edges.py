@@ -7,6 +7,7 @@ import torch
 
 import moe_expert_load_ue_amd as ue
 from gpu_helpers import say
+from oracle import layer as L
 from tile_rule import compile_rule
 
 pytestmark = pytest.mark.gpu
@@ -403,4 +404,173 @@ def test_every_tile_by_value(rule, want, M, N, G, Ks, gated):
             assert bool((out[~seen] == -77).all())
             assert bool((out[:, N:] == -77).all())
             assert int(seen.sum()) > M // 2
+    ctx.close()
+
+
+# ---- the gate's approximate ranks, ties and large calls -------------------------------------
+
+def check_choice(x, bias, k, score, renorm, dtype=torch.float32, rank=None):
+    """ids, weights and gradient of one call against the oracle."""
+    T, E = x.shape
+    ctx = ctx_for(E, k, T)
+    lg = dev(x, dtype)
+    ids, w = ue.ue_gate(ctx, lg, None if bias is None else dev(bias), score, renorm, 2.5)
+    want_ids, want_w = L.gate(x, k, score, bias, renorm, 2.5, rank=rank)
+    assert np.array_equal(host(ids), want_ids)
+    nan = np.isnan(want_w)
+    assert np.array_equal(np.isnan(host(w)), nan)
+    err = np.abs(host(w) - want_w)[~nan]
+    assert np.all(err <= 5e-6 * np.abs(want_w)[~nan] + 1e-30)
+    ctx.close()
+    return want_ids
+
+
+@pytest.mark.parametrize("E,k", [(16, 8), (32, 4), (60, 6), (64, 8), (100, 7), (128, 8),
+                                 (200, 8), (256, 8), (256, 1), (300, 8)])
+def test_gate_logits_apart_in_the_low_bits_only(E, k):
+    """fp32 logits that share their upper 24 bits with others of the row, many
+    of them equal: the order by all 32 bits, ties to the lowest id."""
+    rng = np.random.default_rng(E)
+    base = rng.choice(np.array([1.5, 1.4375, -2.0], np.float32), size=(120, E), p=[.5, .3, .2])
+    x = (base.view(np.int32) & ~0xFF) + rng.integers(0, 256, size=base.shape).astype(np.int32)
+    x[::3] = (base[::3].view(np.int32) & ~0xFF) + rng.integers(0, 3, size=base[::3].shape).astype(np.int32)
+    x = x.astype(np.int32).view(np.float32)
+    say("low bits", E, k)
+    for renorm in (True, False):
+        ids = check_choice(x.astype(np.float64), None, k, "softmax", renorm)
+    assert (ids >= 0).all()
+
+
+@pytest.mark.parametrize("E,k", [(16, 8), (32, 4), (60, 6), (64, 8), (128, 8), (200, 8),
+                                 (256, 8), (300, 8), (512, 16)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gate_sigmoid_ties(E, k, dtype):
+    """Sigmoid ranks with exact ties: equal logits (with equal biases), and
+    logits so large that the fp32 score is 1. Different ranks are at least
+    1e-4 apart, so fp32 cannot confuse them; every row is live."""
+    rng = np.random.default_rng(E + k)
+    levels = np.array([-3.0, -1.25, -0.5, 0.0, 0.75, 1.5, 2.5, 30.0, 40.0, 88.0])
+    x = rng.choice(levels, size=(90, E))
+    x[0] = 0.75                                     # all equal
+    x[1] = rng.choice([20.0, 30.0, 100.0], size=E)  # all saturated
+    x[2::5][rng.random(x[2::5].shape) < 0.3] = -INF
+    biases = np.array([0.0, 0.3, -0.23, 0.0117], np.float32)
+    for bias in (None, rng.choice(biases, size=E)):
+        b = np.zeros(E, np.float32) if bias is None else bias
+        # the rank as it is defined: in fp32
+        p = np.where(x > 17.5, 1.0, L._sigmoid(x)).astype(np.float32)
+        rank = (p + b).astype(np.float32)
+        u = np.unique(rank)
+        near = np.diff(u.astype(np.float64))
+        # p rounds within u of its value whoever computes it: ranks of one
+        # level and bias are taken as equal, others must be apart
+        assert near[near > 1e-6].min() > 1e-4 and (near[near <= 1e-6]).size == 0
+        say("sigmoid ties", E, k, dtype, bias is not None)
+        for renorm in (True, False):
+            ids = check_choice(x, bias, k, "sigmoid", renorm, dtype, rank)
+        assert (ids >= 0).mean() > 0.9
+        assert ids[0].tolist() == (np.argsort(-b, kind="stable")[:k]).tolist()
+
+
+@pytest.mark.parametrize("E", [32, 60, 64, 128, 200, 256, 300])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gate_infinities_and_nan_beside_ordinary_rows(E, score, dtype):
+    """Rows with +inf, -inf, NaN, the lowest value, all of one kind, between
+    ordinary rows of the same wave, which keep their results."""
+    rng = np.random.default_rng(E)
+    T, k = 96, 8
+    x = np.stack([rng.permutation(np.arange(E)) for _ in range(T)]) * (12.0 / E) - 6
+    x = torch.from_numpy(x).to(dtype).double().numpy()
+    if score == "sigmoid":
+        # apart by more than fp32 scores can confuse, or equal (in bf16)
+        p = np.sort(L._sigmoid(x), axis=1)
+        gap = np.diff(p, axis=1)
+        assert gap[gap > 0].min() > 1e-6
+    low = float(torch.finfo(dtype).min)
+    x[3, 5] = INF
+    x[8, [2, 9, 30]] = INF
+    x[13] = -INF
+    x[14, :-2] = -INF
+    x[21, 7] = np.nan
+    x[22] = np.nan
+    x[30] = low
+    x[31, ::2] = low
+    x[40, 1], x[40, 3] = INF, np.nan
+    x[51] = INF
+    x[52, ::3], x[52, 1::3] = -INF, INF
+    say("special rows", E, score, dtype)
+    rank = None
+    if score == "sigmoid":
+        rank = np.where(x > 17.5, 1.0, L._row_scores(x, score))
+    for renorm in (True, False):
+        check_choice(x, None, k, score, renorm, dtype, rank)
+
+
+@pytest.mark.parametrize("E,k,dtype", [(256, 8, torch.float32), (256, 8, torch.bfloat16),
+                                       (128, 8, torch.float32), (128, 8, torch.bfloat16),
+                                       (200, 6, torch.float32), (60, 6, torch.float32),
+                                       (32, 8, torch.bfloat16), (256, 16, torch.bfloat16),
+                                       (300, 8, torch.float32)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_past_one_trip_of_the_grid(E, k, dtype, score):
+    """More tokens than the whole grid takes at once (eight workgroups of four
+    waves per CU; a token on 8 lanes, on 16, or on a wave), ragged: equal, bit
+    for bit, to the same rows in calls that need one trip, and on a sample to
+    the oracle."""
+    renorm = k % 4 == 0
+    lanes = 64 if E > 256 else 16 if E > 128 or k > 8 else 8
+    trip = 8 * 4 * torch.cuda.get_device_properties(0).multi_processor_count * (64 // lanes)
+    T = 2 * trip + trip // 3 + 5
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(E + k)
+    x = (torch.randn((T, E), generator=gen, device=DEV) * 2).to(dtype)
+    # a third of the rows needs a second look: logits apart in their low bits
+    if dtype == torch.float32:
+        x[::3] = (1.0 + torch.randint(0, 64, x[::3].shape, generator=gen, device=DEV) * 2.0 ** -23)
+    x[5::11].masked_fill_(torch.rand(x[5::11].shape, generator=gen, device=DEV) < 0.3, -INF)
+    x[7::97] = -INF
+    bias = torch.randn(E, generator=gen, device=DEV) * 0.1 if score == "sigmoid" else None
+    dw = torch.randn((T, k), generator=gen, device=DEV)
+    say("past one trip", E, k, dtype, score, T)
+    ctx = ctx_for(E, k, T)
+    ids, w = ue.ue_gate(ctx, x, bias, score, renorm, 2.5)
+    d = ue.ue_gate_backward(ctx, x, ids, dw, score, renorm, 2.5)
+    n = trip // 2 + 3
+    for lo in range(0, T, n):
+        s = slice(lo, min(lo + n, T))
+        i2, w2 = ue.ue_gate(ctx, x[s], bias, score, renorm, 2.5)
+        d2 = ue.ue_gate_backward(ctx, x[s], i2, dw[s], score, renorm, 2.5)
+        assert torch.equal(i2, ids[s]) and torch.equal(w2, w[s]) and torch.equal(d2, d[s]), lo
+    # every row: distinct ids, best first, nothing better left out
+    xd = x.double()
+    rank = xd if score == "softmax" else torch.where(
+        xd == -INF, xd, torch.sigmoid(xd) + bias.double())
+    got = ids >= 0
+    mine = torch.where(got, rank.gather(1, ids.clamp_min(0).long()), -INF)
+    best = rank.topk(k, dim=1).values
+    slack = 0 if score == "softmax" else 1e-6
+    assert bool(((best - mine).nan_to_num(0, 0, 0).abs() <= slack).all())
+    assert bool((got == (best > -INF)).all())
+    spread = torch.where(got, ids.long(), E + torch.arange(k, device=DEV)).sort(1).values
+    assert bool((spread[:, 1:] > spread[:, :-1]).all()) or k == 1
+    # weights and gradient of rows from every part, at the choice made
+    at = torch.cat([torch.arange(0, 40, device=DEV), torch.arange(trip - 20, trip + 20, device=DEV),
+                    torch.arange(2 * trip - 5, 2 * trip + 40, device=DEV),
+                    torch.arange(T - 40, T, device=DEV)])
+    xs, sel = xd[at].cpu().numpy(), ids[at].cpu().numpy()
+    order = np.full(xs.shape, -INF)
+    for t in range(len(sel)):
+        for j, e in enumerate(sel[t]):
+            if e >= 0:
+                order[t, e] = k - j
+    want_ids, want_w = L.gate(xs, k, score, None, renorm, 2.5, rank=order)
+    assert np.array_equal(want_ids, sel)
+    assert np.all(np.abs(host(w[at]) - want_w) <= 5e-6 * np.abs(want_w) + 1e-30)
+    dws = dw[at].cpu().numpy()
+    want = L.gate_backward(xs, sel, dws, score, renorm, 2.5)
+    tol = 2e-5 * 2.5 * np.abs(dws).max(1, keepdims=True)
+    if dtype == torch.bfloat16:
+        tol = tol + U16 * np.abs(want)
+    assert np.all(np.abs(host(d[at]) - want) <= tol)
     ctx.close()
