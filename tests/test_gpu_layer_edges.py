@@ -574,3 +574,43 @@ def test_gate_past_one_trip_of_the_grid(E, k, dtype, score):
         tol = tol + U16 * np.abs(want)
     assert np.all(np.abs(host(d[at]) - want) <= tol)
     ctx.close()
+
+
+# ---- many short rows to int8 -------------------------------------------------------------
+
+@pytest.mark.parametrize("K", [1, 8, 17, 1000, 2040, 2048])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_quantize_many_short_rows(K, dtype):
+    """2,048 rows or more of up to 2,048 elements take a wave each: to the bit
+    as the definition (float32 operations), also from unaligned rows."""
+    rng = np.random.default_rng(K)
+    M = 2051
+    v = (rng.normal(size=(M, K)) * np.exp(rng.normal(size=(M, 1)) * 4)).astype(np.float32)
+    v[5] = 0
+    v[6] = 1e-45
+    v[7, K // 2], v[1030, K - 1], v[2050, 0] = INF, np.nan, -INF
+    x = dev(v, dtype)
+    say("quantize many", K, dtype)
+    ctx = ctx_for()
+    q, s = ue.ue_quantize_rows(ctx, x)
+    f = x.float().cpu().numpy()
+    with np.errstate(all="ignore"):
+        fine = np.isfinite(f).all(1)
+        top = np.abs(f).max(1)
+        inv = np.float32(127) / top
+        live = fine & (top > 0) & np.isfinite(inv)
+        want = np.zeros((M, K), np.int8)
+        want[live] = np.rint(f[live] * inv[live, None]).astype(np.int8)
+        ws = np.where(live, top / np.float32(127), np.where(fine, 0, np.nan)).astype(np.float32)
+    assert live.sum() == M - 5
+    assert np.array_equal(host(q), want)
+    assert np.array_equal(s.cpu().numpy(), ws, equal_nan=True)
+    pad = torch.as_strided(q, (M, (K + 15) // 16 * 16), (q.stride(0), 1))[:, K:]
+    assert bool((pad == 0).all())
+    ld = K + 5
+    buf = torch.full((M * ld + 1,), 9.0, dtype=dtype, device=DEV)
+    u = buf[1:].view(M, ld)[:, :K]
+    u.copy_(x)
+    q2, s2 = ue.ue_quantize_rows(ctx, u)
+    assert torch.equal(q2, q) and np.array_equal(s2.cpu().numpy(), ws, equal_nan=True)
+    ctx.close()
