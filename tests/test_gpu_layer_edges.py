@@ -614,3 +614,58 @@ def test_quantize_many_short_rows(K, dtype):
     q2, s2 = ue.ue_quantize_rows(ctx, u)
     assert torch.equal(q2, q) and np.array_equal(s2.cpu().numpy(), ws, equal_nan=True)
     ctx.close()
+
+
+# ---- few tokens of a wide layer ----------------------------------------------------------
+
+@pytest.mark.parametrize("T", [1, 3, 4, 5, 8, 9, 20])
+@pytest.mark.parametrize("i8", [False, True])
+def test_moe_tokens_of_a_wide_layer(T, i8):
+    """A hidden size that gives every CU a workgroup of 16 output channels:
+    the second product's instances for up to 4 and up to 8 tokens, and the
+    next one. Bounds as in tests/test_gpu_layer.py."""
+    E, k, I = 6, 3, 48
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    H = 16 * cus + 32                            # (H + 15) / 16 >= cus
+    rng = np.random.default_rng(T)
+    bf = lambda v: torch.from_numpy(v).bfloat16()  # noqa: E731
+    x = bf(rng.normal(size=(T, H)))
+    router = bf(rng.normal(size=(E, H)) * 1.5 / np.sqrt(H))
+    if i8:
+        w13 = torch.from_numpy(rng.integers(-127, 128, size=(E, 2 * I, H)).astype(np.int8))
+        w2 = torch.from_numpy(rng.integers(-127, 128, size=(E, H, I)).astype(np.int8))
+        s13 = ((rng.random((E, 2 * I)) + 0.5) / (73 * np.sqrt(H))).astype(np.float32)
+        s2 = ((rng.random((E, H)) + 0.5) / (73 * np.sqrt(I))).astype(np.float32)
+        w13d = w13.double().numpy() * s13.astype(np.float64)[..., None]
+        w2d = w2.double().numpy() * s2.astype(np.float64)[..., None]
+    else:
+        w13 = bf(rng.normal(size=(E, 2 * I, H)) / np.sqrt(H))
+        w2 = bf(rng.normal(size=(E, H, I)) / np.sqrt(I))
+        s13 = s2 = None
+        w13d, w2d = w13.double().numpy(), w2.double().numpy()
+    say("wide layer", T, i8, H)
+    ctx = ctx_for(E, k, 64)
+    ue.ue_register_layer(ctx, router.to(DEV), w13.to(DEV), w2.to(DEV),
+                         None if s13 is None else dev(s13), None if s2 is None else dev(s2))
+    xs = x.to(DEV)
+    out, ids, w = ue.ue_moe_tokens(ctx, xs)
+    again, _, _ = ue.ue_moe_tokens(ctx, xs)
+    assert torch.equal(out, again)
+    out, ids, w = host(out), host(ids), host(w)
+    xd = x.double().numpy()
+    logits = xd @ router.double().numpy().T
+    # the best k of the 64-bit logits, but for what fp32 sums cannot tell apart
+    kth = np.sort(logits, 1)[:, -k]
+    at = np.arange(T)[:, None]
+    assert np.all(logits[at, ids] >= kth[:, None] - 1e-4)
+    p = np.exp(logits[at, ids] - logits.max(1, keepdims=True))
+    assert np.all(np.abs(w - p / p.sum(1, keepdims=True)) <= 2e-5)
+    want, _, _ = L.moe(xd, router.double().numpy(), w13d, w2d, k, choice=(ids, w))
+    assert (np.sort(ids, 1)[:, 1:] > np.sort(ids, 1)[:, :-1]).all() and (ids >= 0).all()
+    mag = np.zeros(want.shape)
+    for t in range(T):
+        for j in range(k):
+            gu = np.abs(w13d[ids[t, j]]) @ np.abs(xd[t])
+            mag[t] += abs(w[t, j]) * (np.abs(w2d[ids[t, j]]) @ (gu[:I] * (gu[I:] + 1)))
+    assert np.all(np.abs(out - want) <= U16 * np.abs(want) + 2e-6 * mag)
+    ctx.close()
