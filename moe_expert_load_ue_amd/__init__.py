@@ -644,9 +644,17 @@ def _new(shape, dtype, ctx, stream):
         return torch.empty(shape, dtype=dtype, device=ctx.device)
 
 
+_device = torch._C._cuda_getDevice \
+    if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
 def _on(ctx, stream, *tensors):
     """The stream's handle; keeps tensors of another stream from being reused
-    under this call."""
+    under this call. The library launches on the current device, and the
+    default stream's handle is the same on every device."""
+    if _device() != ctx._index:
+        raise ValueError(f"the current device is {_device()}, the context's "
+                         f"{ctx._index} (torch.cuda.set_device)")
     if stream is None:
         return _raw_stream(ctx._index)
     for t in tensors:
