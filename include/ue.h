@@ -32,7 +32,8 @@
  *  - A context is not thread-safe: one host thread at a time. Its routing
  *    calls (ue_load, ue_plan, ue_reroute, ue_rebalance) use the context's
  *    workspace and must not overlap one another in time on different
- *    streams, nor ue_moe_tokens (whose workspace is its own) itself.
+ *    streams. Calls of ue_moe_tokens have a workspace of their own and must
+ *    not overlap one another, replays of captured ones included.
  *    ue_weight_sync, ue_grad_reduce, ue_gather_rows, ue_gate,
  *    ue_gate_backward, ue_quantize_rows and ue_matmul_i8 use no
  *    workspace and may run on another stream beside them (the next layer's
@@ -422,7 +423,8 @@ enum {
  *            may be NULL; must be NULL with the softmax
  *   ids      device, int32 [T, k] out: a layer's routing for ue_load
  *   weights  device, fp32 [T, k] out
- * T in 0..max_tokens. Scores and sums are fp32. Errors: UE_EINVAL, UE_ESHAPE. */
+ * T in 0..max_tokens. Scores and sums are fp32: equal ranks are ranks equal in
+ * fp32 (a sigmoid above 16.7 is 1). Errors: UE_EINVAL, UE_ESHAPE. */
 int ue_gate(ue_ctx *ctx, const void *logits, int32_t type, int64_t ld,
             int32_t T, int32_t score, int32_t renorm, float scale,
             const float *bias, int32_t *ids, float *weights, void *stream);
@@ -441,8 +443,11 @@ int ue_gate_backward(ue_ctx *ctx, const void *logits, int32_t type, int64_t ld,
 
 /* Rows as 8-bit integers: with top = max |x| of a row, q = rint(x * (127 /
  * top)) (to even) and scale = top / 127; a row of zeros (or one so small
- * that 127 / top overflows) has q = 0 and scale 0. A row that holds an infinity or a NaN has q = 0 and scale NaN, so that its
- * products are NaN.
+ * that 127 / top overflows) has q = 0 and scale 0. The factor 127 / top is
+ * rounded to fp32, and so is its product with x: an x that lies half way
+ * between two steps (top / 2, common in bf16) may go to either. A row that
+ * holds an infinity or a NaN has q = 0 and scale NaN, so that its products are
+ * NaN.
  *   x      device, [M] rows of K, UE_F32 or UE_BF16, ldx apart
  *   q      device, int8, out, 16-byte aligned rows ldq apart (ldq a multiple
  *          of 16, at least K rounded up to 16; bytes K .. that are set to 0)
@@ -525,9 +530,10 @@ int ue_register_layer(ue_ctx *ctx, const ue_layer *layer);
  * model), from the registered layer:
  *   logits = x router^T;  (ids, weights) = ue_gate(logits)
  *   out_t = sum_j weights_tj (silu(x_t G^T) * (x_t U^T)) D^T
- * over the matrices of expert ids_tj; ids of -1 add nothing. Sums are fp32,
- * also between the products; out is rounded once. The result does not depend
- * on timing (no atomics on values).
+ * over the matrices of expert ids_tj; ids of -1 add nothing. Sums are fp32; the
+ * hidden activations silu() * () go from the first product to the second as
+ * a sum of two bf16 numbers, 16 bits of them; out is rounded once. The result
+ * does not depend on timing (no atomics on values).
  *   x        device, bf16 [T] rows of hidden, 16-byte aligned, ldx apart
  *            (a multiple of 8, at most 2^24)
  *   out      device, bf16, ldo apart

@@ -16,8 +16,9 @@
 //
 // h is kept as a sum of two bf16 numbers (its rounding and the rest), each
 // multiplied on its own: the second product's operands then carry 16 bits
-// of h, and the layer's result is rounded once, at the end. That costs 8% of the
-// second product's time (532 against 492 us in the batch below, three shares)
+// of h (the only sums or values of the layer held in fewer than 32), and the
+// layer's result is rounded once, at the end. That costs 8% of the second
+// product's time (532 against 492 us in the batch below, three shares)
 // and takes the layer's error from 1.4 roundings to one. An expert with more
 // than 16 tokens takes passes of 16, its matrices read again from cache.
 //
@@ -177,7 +178,6 @@ __global__ __launch_bounds__(kChooseWaves * 64) void k_choose(MoeArgs g) {
 // token, against 5 split). The choice adds the parts in order.
 constexpr int kRouterWaves = 4;
 static_assert(kRouterWaves == kChooseWaves, "the router's last workgroup chooses");
-           // of K per workgroup
 
 // V: lane slots of the choice made here, 0 for none (see k_choose).
 template <int FOLD, int RT, int V>

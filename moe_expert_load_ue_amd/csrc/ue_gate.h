@@ -76,8 +76,8 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
 
 // One round per expert taken: the largest key of the wave, its lowest id.
 // `emit(r, id, slot)` is called with wave-uniform arguments (id = L V + slot
-// of lane L). Returns how many were
-// taken (fewer than k when the rest are -inf or NaN). The keys are consumed.
+// of lane L). Returns how many were taken (fewer than k when the rest are -inf
+// or NaN). The keys are consumed.
 template <int V, class Emit>
 __device__ __forceinline__ int take_best(uint32_t (&key)[V], int k, Emit emit) {
     const int lane = lane_id();
@@ -128,7 +128,8 @@ __device__ __forceinline__ void load_bias(const GateRule &g, float (&b)[V]) {
 
 // One token's choice by one wave. `x`: its logits, slot i of lane l expert
 // l V + i, -inf past the last; `bias`: likewise, 0 where there is none (read
-// by load_bias before the logits are waited for); `ids`, `weights`: its k results; `taken(id)` is called, wave-uniform, for each expert taken.
+// by load_bias before the logits are waited for); `ids`, `weights`: its k
+// results; `taken(id)` is called, wave-uniform, for each expert taken.
 template <int V, class Taken>
 __device__ __forceinline__ void gate_row(const GateRule &g, const float (&x)[V],
                                          const float (&bias)[V],

@@ -122,9 +122,9 @@ struct RowStream {
 
     // Matrix n's first row is at w[n], this lane's row of load j wo[j] bytes
     // on; part p of the activations at x[p], its token's row of tile r xo[r]
-    // bytes on (bases are uniform: the offsets take 32 bits). K in [k0, k1), k0 and k1 whole windows but for K
-    // itself; what lies past K is read from the row's start and multiplied
-    // by zeros. (K a multiple of a piece for the bf16 kinds; for I8Rows any,
+    // bytes on (bases are uniform: the offsets take 32 bits). K in [k0, k1),
+    // k0 and k1 whole windows but for K itself; what lies past K is read from
+    // the row's start and multiplied by zeros. (K a multiple of a piece for the bf16 kinds; for I8Rows any,
     // and rows readable to the end of their last piece.)
     static __device__ __forceinline__ void run(const char *const (&w)[NW],
                                                const uint32_t (&wo)[LD],

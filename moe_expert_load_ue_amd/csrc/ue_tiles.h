@@ -34,7 +34,12 @@ constexpr int64_t kLaunchThreads = 0xFFFFFFFFll;
 // length at least half fill and that makes three workgroups for every four
 // CUs; up to 16 rows go to the row kernel. Groups with long rows, whose
 // matrices come from HBM, take the tile with three stages: its loads have two
-// stages' time to arrive, and its lesser height fits uneven groups better.
+// stages' time to arrive, and its lesser height fits uneven groups better (392
+// against 445 us above; with even groups, which the host cannot tell since the
+// offsets are on the device, it loses 326 to 306). Where between K = 1024 and
+// 4096 the two cross was not measured. From 17 to some hundred rows the times
+// are latency's (14.6 us for 17 rows, 15.6 for 128; the matrix's bytes take 6):
+// 64 to 128 workgroups, each walking all of K.
 enum I8Kernel {
     kI8Rows,        // up to 16 rows, the matrix streamed past them
     kI8Tall,        // 256 rows by 256 channels, two stages in LDS
