@@ -545,6 +545,174 @@ int ue_moe_tokens(ue_ctx *ctx, const void *x, int64_t ldx, int32_t T,
                   void *out, int64_t ldo, int32_t *ids, float *weights,
                   void *stream);
 
+/* ---------------------------------------------------------------------
+ * The training step of the expert layer: the loss that keeps the routing
+ * even, activations kept in 8 bits for the backward pass, the gradients of the
+ * slots' matrices (which ue_grad_reduce then sums into the masters'), and the
+ * sum of the experts' rows back to their tokens. None of these calls uses the
+ * context's workspace: they may run beside any other call on another stream,
+ * two calls that are given the same `workspace` excepted. */
+
+/* Balance loss of packed sequences (E and k are the context's). With p the
+ * softmax of a token's logits, or its sigmoids over their sum plus 1e-20, and
+ * for sequence s of n tokens:
+ *   counts[s, e] = number of its assignments to e (ids outside [0, E) are none)
+ *   prob[s, e]   = (1 / n) sum_t p[t, e]
+ *   loss[s]      = (E / (k n)) sum_e counts[s, e] prob[s, e]
+ * which is 1 where the choice is even. An empty sequence has 0 everywhere. An
+ * expert whose logit is -inf has p = 0, a token with no other has p = 0
+ * everywhere; +inf counts as the largest float in the softmax; a NaN among a
+ * token's logits makes its sequence's prob and loss NaN.
+ *   logits   device, [T] rows of E, UE_F32 or UE_BF16, ld apart (ld >= E)
+ *   ids      device, int32 [T, k] (from ue_gate)
+ *   offsets  device, int32 [n_seq + 1]: sequence s is tokens offsets[s] ..
+ *            offsets[s + 1] - 1; NULL: one sequence of all T tokens (n_seq 1).
+ *            Entries are clamped to 0..T and must not decrease (results are
+ *            undefined if they do). Tokens no sequence holds (padding) take no
+ *            part.
+ *   counts   device, int32 [n_seq, E] out;  prob  device, fp32 [n_seq, E] out
+ *   loss     device, fp32 [n_seq] out
+ *   workspace  device, 16-byte aligned, ue_balance_workspace(ctx, T, n_seq)
+ *            bytes, overwritten. Calls given the same one must not overlap,
+ *            replays of captured ones included.
+ * T in 0..max_tokens, n_seq in 0..2^20. Sums are fp32 in a fixed order (no
+ * atomics on values): results repeat bit for bit. */
+size_t ue_balance_workspace(const ue_ctx *ctx, int32_t T, int32_t n_seq);
+int ue_balance(ue_ctx *ctx, const void *logits, int32_t type, int64_t ld,
+               int32_t T, int32_t score, const int32_t *ids,
+               const int32_t *offsets, int32_t n_seq, int32_t *counts,
+               float *prob, float *loss, void *workspace, void *stream);
+
+/* Gradient of the logits from that of the losses (counts are constants):
+ *   d[t, e] = dloss[s] (E / (k n^2)) p_e (counts[s, e] - sum_j p_j counts[s, j])
+ * times 1 - sigmoid(logit) for the sigmoid.
+ *   counts   device, int32 [n_seq, E], from ue_balance (or summed over several
+ *            devices that share the batch, with dloss scaled to match)
+ *   dloss    device, fp32 [n_seq]
+ *   dlogits  device, of the logits' type, [T] rows of E, ld_out apart: with
+ *            `accumulate` the gradient is added to it (in fp32, rounded once;
+ *            the gradient ue_gate_backward wrote, say) and rows of tokens no
+ *            sequence holds stay as they are; else every element is written,
+ *            0 in those rows. May be the logits' own memory. */
+int ue_balance_backward(ue_ctx *ctx, const void *logits, int32_t type,
+                        int64_t ld, int32_t T, int32_t score,
+                        const int32_t *offsets, int32_t n_seq,
+                        const int32_t *counts, const float *dloss,
+                        void *dlogits, int64_t ld_out, int32_t accumulate,
+                        void *stream);
+
+/* Packed rows: 8 bits per element and one power of two per row and 32 columns
+ * (a block; the last one of a row may be shorter). With top the block's largest
+ * magnitude, e the smallest exponent from -126 with top <= 127 * 2^e:
+ *   q = rint(x / 2^e) (to even),  scale = e + 127 as a byte
+ * so |x - q 2^e| <= 2^(e-1), every quotient is exact, and q 2^e is a bf16
+ * number. A block of zeros has scale 1. A block that holds an infinity or a NaN
+ * has q = 0 and scale 255 and stands for NaNs.
+ *   x      device, [M] rows of K, UE_F32 or UE_BF16, ldx apart
+ *   q      device, int8, 16-byte aligned rows ldq apart (a multiple of 16, at
+ *          least K rounded up to 32; bytes K .. that are set to 0)
+ *   scale  device, bytes, rows of ceil(K / 32), lds apart
+ * K in 1..2^20. ue_unpack_rows writes the values q 2^e stands for. */
+#define UE_PACK_BLOCK 32
+int ue_pack_rows(ue_ctx *ctx, const void *x, int32_t type, int64_t ldx,
+                 int32_t M, int32_t K, int8_t *q, int64_t ldq, uint8_t *scale,
+                 int64_t lds, void *stream);
+int ue_unpack_rows(ue_ctx *ctx, const int8_t *q, int64_t ldq,
+                   const uint8_t *scale, int64_t lds, int32_t M, int32_t K,
+                   void *x, int32_t type, int64_t ldx, void *stream);
+
+/* Gated activation that keeps its inputs in 8 bits, and its backward pass from
+ * what was kept:
+ *   h = silu(gate) up,  silu(v) = v / (1 + exp(-v))
+ *   gu     device, [M] rows of 2 I: gate, then up; UE_F32 or UE_BF16, ldgu
+ *          apart
+ *   h      device, out, of the same type, [M] rows of I, ldh apart
+ *   q, scale  out, or both NULL (nothing is kept): gate and up as packed rows
+ *          side by side, each half padded to whole blocks: with P = I rounded up
+ *          to 32, q has gate in bytes 0 .. I-1 and up in P .. P+I-1 of a row of
+ *          2 P (ldq >= 2 P), scale P / 32 bytes for each (lds >= P / 16)
+ * Backward, with gate and up the values that q and scale stand for and s =
+ * 1 / (1 + exp(-gate)):
+ *   dgate = dh up s (1 + gate (1 - s)),  dup = dh silu(gate)
+ *   dh     device, [M] rows of I, UE_F32 or UE_BF16, lddh apart
+ *   dgu    device, out, of the same type, [M] rows of 2 I, lddgu apart
+ *   h      device, out, of the same type, ldh apart, or NULL: silu(gate) up again
+ *          (the rows that the second product's weight gradient takes)
+ * I in 1..2^19. dgu must not overlap dh, nor h gu. */
+int ue_gated(ue_ctx *ctx, const void *gu, int32_t type, int64_t ldgu, int32_t M,
+             int32_t I, void *h, int64_t ldh, int8_t *q, int64_t ldq,
+             uint8_t *scale, int64_t lds, void *stream);
+int ue_gated_backward(ue_ctx *ctx, const int8_t *q, int64_t ldq,
+                      const uint8_t *scale, int64_t lds, const void *dh,
+                      int32_t type, int64_t lddh, int32_t M, int32_t I,
+                      void *dgu, int64_t lddgu, void *h, int64_t ldh,
+                      void *stream);
+
+/* Gradients of the matrices of row groups (a plan's slots):
+ *   out[g, n, k] (+)= sum over the rows m of group g of dy[m, n] x[r(m), k]
+ * Rows are grouped by `offsets` as in ue_matmul_i8 (entries clamped to 0..M, and
+ * should not decrease); without offsets one group holds all rows. r(m) is m, or
+ * with `index` index[m] / index_div (a dispatch permutation and its top-k); an
+ * entry outside x's rows counts as a row of zeros. Sums are fp32 in a fixed
+ * order: results repeat bit for bit.
+ *   dy       device, bf16, [M] rows of N, lddy apart
+ *   x        device, [x_rows] rows of K, ldx apart: bf16, or with x_scale packed
+ *            rows (ue_pack_rows: int8, ldx a multiple of 16, 16-byte aligned)
+ *   x_scale  device, bytes, lds apart, or NULL (x is bf16)
+ *   out      device, fp32, `groups` matrices of N rows of K, rows ldo apart,
+ *            matrices out_stride apart. With `accumulate` the sums are added to
+ *            what out holds, else every element is written (0 for an empty
+ *            group).
+ *   workspace  device, 16-byte aligned, of ue_weight_grad_workspace(ctx, p)
+ *            bytes (0 for many shapes), or NULL: few matrices of many rows are
+ *            then not split over the device. Calls given the same one must not
+ *            overlap.
+ * N and K in 0..2^20; one matrix of out, and 64 rows of dy, are below 4 GiB. */
+typedef struct ue_weight_grad_product {
+    const void *dy;
+    const void *x;
+    const uint8_t *x_scale;
+    const int32_t *offsets;     /* int32 [groups + 1] or NULL */
+    const int32_t *index;       /* int32 [M] or NULL          */
+    float *out;
+    void *workspace;
+    int64_t lddy, ldx, lds, ldo, out_stride;
+    int32_t x_rows, groups, index_div;
+    int32_t M, N, K;
+    int32_t accumulate;
+} ue_weight_grad_product;
+
+size_t ue_weight_grad_workspace(const ue_ctx *ctx,
+                                const ue_weight_grad_product *p);
+int ue_weight_grad(ue_ctx *ctx, const ue_weight_grad_product *p, void *stream);
+
+/* Sum of the experts' rows back to their tokens (k is the context's):
+ *   out[t] = add[t] + sum_j weights[t, j] y[inv_perm[t, j]]
+ * in fp32, j in order, rounded once. Entries of inv_perm outside [0, rows) (an
+ * assignment that found no place: -1) add nothing. Without weights they are 1:
+ * the gradient of ue_gather_rows.
+ *   y         device, [rows] rows of H, UE_F32 or UE_BF16, ldy apart (dispatch
+ *             order)
+ *   inv_perm  device, int32 [T, k];  weights  device, fp32 [T, k] or NULL
+ *   add       device, of y's type, ldadd apart, or NULL (the shared expert's
+ *             output, the residual)
+ *   out       device, of y's type, [T] rows of H, ldo apart; may be add itself
+ * Backward:
+ *   dy[inv_perm[t, j]] = weights[t, j] dout[t]  (rows no assignment names are
+ *                        left as they are; a row named twice is undefined)
+ *   dweights[t, j] = sum_h dout[t, h] y[inv_perm[t, j], h], fp32, in a fixed
+ *                    order; 0 where the entry is outside [0, rows)
+ * dy or dweights (and then y) may be NULL. T in 0..max_tokens, H in 1..2^20. */
+int ue_combine(ue_ctx *ctx, const void *y, int32_t type, int64_t ldy,
+               int32_t rows, const int32_t *inv_perm, const float *weights,
+               const void *add, int64_t ldadd, int32_t T, int32_t H, void *out,
+               int64_t ldo, void *stream);
+int ue_combine_backward(ue_ctx *ctx, const void *dout, int32_t type,
+                        int64_t lddout, const int32_t *inv_perm,
+                        const float *weights, const void *y, int64_t ldy,
+                        int32_t rows, int32_t T, int32_t H, void *dy,
+                        int64_t lddy, float *dweights, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

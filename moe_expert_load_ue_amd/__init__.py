@@ -76,6 +76,15 @@ class ue_i8_product(ctypes.Structure):
                                      "M", "N", "K", "gated", "out_type")])
 
 
+class ue_weight_grad_product(ctypes.Structure):
+    _fields_ = ([(f, _vp) for f in ("dy", "x", "x_scale", "offsets", "index",
+                                    "out", "workspace")] +
+                [(f, _i64) for f in ("lddy", "ldx", "lds", "ldo",
+                                     "out_stride")] +
+                [(f, _i32) for f in ("x_rows", "groups", "index_div", "M", "N",
+                                     "K", "accumulate")])
+
+
 class ue_layer(ctypes.Structure):
     _fields_ = ([(f, _vp) for f in ("router", "bias", "gate_up", "down",
                                     "gate_up_scale", "down_scale")] +
@@ -126,6 +135,28 @@ SIGNATURES = {
     "ue_register_layer": (ctypes.c_int, [_vp, ctypes.POINTER(ue_layer)]),
     "ue_moe_tokens": (ctypes.c_int, [_vp, _vp, _i64, _i32, _vp, _i64, _vp,
                                      _vp, _vp]),
+    "ue_balance_workspace": (ctypes.c_size_t, [_vp, _i32, _i32]),
+    "ue_balance": (ctypes.c_int, [_vp, _vp, _i32, _i64, _i32, _i32, _vp, _vp,
+                                  _i32, _vp, _vp, _vp, _vp, _vp]),
+    "ue_balance_backward": (ctypes.c_int, [_vp, _vp, _i32, _i64, _i32, _i32,
+                                           _vp, _i32, _vp, _vp, _vp, _i64,
+                                           _i32, _vp]),
+    "ue_pack_rows": (ctypes.c_int, [_vp, _vp, _i32, _i64, _i32, _i32, _vp,
+                                    _i64, _vp, _i64, _vp]),
+    "ue_unpack_rows": (ctypes.c_int, [_vp, _vp, _i64, _vp, _i64, _i32, _i32,
+                                      _vp, _i32, _i64, _vp]),
+    "ue_gated": (ctypes.c_int, [_vp, _vp, _i32, _i64, _i32, _i32, _vp, _i64,
+                                _vp, _i64, _vp, _i64, _vp]),
+    "ue_gated_backward": (ctypes.c_int, [_vp, _vp, _i64, _vp, _i64, _vp, _i32,
+                                         _i64, _i32, _i32, _vp, _i64, _vp,
+                                         _i64, _vp]),
+    "ue_weight_grad_workspace": (ctypes.c_size_t, [_vp, _vp]),
+    "ue_weight_grad": (ctypes.c_int, [_vp, _vp, _vp]),
+    "ue_combine": (ctypes.c_int, [_vp, _vp, _i32, _i64, _i32, _vp, _vp, _vp,
+                                  _i64, _i32, _i32, _vp, _i64, _vp]),
+    "ue_combine_backward": (ctypes.c_int, [_vp, _vp, _i32, _i64, _vp, _vp, _vp,
+                                           _i64, _i32, _i32, _i32, _vp, _i64,
+                                           _vp, _vp]),
     "ue_rebalance_static": (ctypes.c_int, [ctypes.POINTER(ue_config), _vp,
                                            _i32, _i32, _vp, _vp, _vp, _vp,
                                            _vp, _vp, _vp, _vp, _vp]),
@@ -285,6 +316,33 @@ class Context:
 
     def moe_tokens(self, x, **kw):
         return ue_moe_tokens(self, x, **kw)
+
+    def balance(self, logits, ids, offsets=None, **kw):
+        return ue_balance(self, logits, ids, offsets, **kw)
+
+    def balance_backward(self, logits, counts, dloss, offsets=None, **kw):
+        return ue_balance_backward(self, logits, counts, dloss, offsets, **kw)
+
+    def pack_rows(self, x, **kw):
+        return ue_pack_rows(self, x, **kw)
+
+    def unpack_rows(self, q, scale, **kw):
+        return ue_unpack_rows(self, q, scale, **kw)
+
+    def gated(self, gu, **kw):
+        return ue_gated(self, gu, **kw)
+
+    def gated_backward(self, dh, q, scale, **kw):
+        return ue_gated_backward(self, dh, q, scale, **kw)
+
+    def weight_grad(self, dy, x, x_scale=None, **kw):
+        return ue_weight_grad(self, dy, x, x_scale, **kw)
+
+    def combine(self, y, inv_perm, weights=None, **kw):
+        return ue_combine(self, y, inv_perm, weights, **kw)
+
+    def combine_backward(self, dout, inv_perm, weights=None, **kw):
+        return ue_combine_backward(self, dout, inv_perm, weights, **kw)
 
 
 def ue_create(num_experts, num_ranks, spare_per_rank, topk, max_tokens,
@@ -901,3 +959,377 @@ def ue_moe_tokens(ctx: Context, x, out=None, ids=None, weights=None,
     if rc:
         ctx._check(rc, "ue_moe_tokens")
     return out, ids, weights
+
+
+# ---- the expert layer's training step --------------------------------------
+
+PACK_BLOCK = 32        # columns of a packed row that share a power of two
+
+
+def _sequences(ctx, offsets, name="offsets"):
+    """(pointer, sequences) of int32 [n_seq + 1] offsets, or of none."""
+    if offsets is None:
+        return None, 1
+    n = offsets.numel() - 1 if isinstance(offsets, torch.Tensor) else -1
+    if n < 0:
+        raise ValueError(f"{name} must be a tensor of n_seq + 1 entries")
+    return _flat(offsets, name, torch.int32, ctx.device, n + 1), n
+
+
+def ue_balance(ctx: Context, logits, ids, offsets=None, score="softmax",
+               counts=None, prob=None, loss=None, workspace=None, stream=None):
+    """Balance loss of packed sequences from router logits [T, E] and the
+    choice ids int32 [T, k]: (loss fp32 [n_seq], counts int32 [n_seq, E], prob
+    fp32 [n_seq, E]). ``offsets`` int32 [n_seq + 1]: where the sequences start
+    (None: all tokens are one). ``workspace``: uint8, of at least
+    :func:`ue_balance_workspace` bytes."""
+    dev = ctx.device
+    T, _, ld = _rows(logits, "logits", dev, _FLOATS, ctx.E)
+    i = _flat(ids, "ids", torch.int32, dev, T * ctx.k)
+    po, n = _sequences(ctx, offsets)
+    score = _score(score)
+    if loss is None:
+        loss = _new((n,), torch.float32, ctx, stream)
+    else:
+        _flat(loss, "loss", torch.float32, dev, n)
+    if counts is None:
+        counts = _new((n, ctx.E), torch.int32, ctx, stream)
+    else:
+        _flat(counts, "counts", torch.int32, dev, n * ctx.E)
+    if prob is None:
+        prob = _new((n, ctx.E), torch.float32, ctx, stream)
+    else:
+        _flat(prob, "prob", torch.float32, dev, n * ctx.E)
+    need = library().ue_balance_workspace(ctx._h, T, n)
+    workspace = _workspace(ctx, workspace, need, stream)
+    rc = library().ue_balance(ctx._h, logits.data_ptr(), _TYPES[logits.dtype],
+                              ld, T, score, i, po, n, counts.data_ptr(),
+                              prob.data_ptr(), loss.data_ptr(),
+                              workspace.data_ptr(),
+                              _on(ctx, stream, logits, ids, offsets, counts,
+                                  prob, loss, workspace))
+    if rc:
+        ctx._check(rc, "ue_balance")
+    return loss, counts, prob
+
+
+def ue_balance_workspace(ctx: Context, T: int, n_seq: int = 1) -> int:
+    """Bytes of workspace :func:`ue_balance` needs."""
+    return int(library().ue_balance_workspace(ctx._h, T, n_seq))
+
+
+def _workspace(ctx, t, need, stream):
+    if t is None:
+        return _new((need,), torch.uint8, ctx, stream)
+    _need(t, "workspace", torch.uint8, ctx.device)
+    if t.numel() < need:
+        raise ValueError(f"workspace must hold {need} bytes, has {t.numel()}")
+    return t
+
+
+def ue_balance_backward(ctx: Context, logits, counts, dloss, offsets=None,
+                        score="softmax", dlogits=None, accumulate=False,
+                        stream=None):
+    """Gradient of the logits [T, E] (their type) from that of the losses
+    fp32 [n_seq], at the counts of :func:`ue_balance`. With ``accumulate`` it is
+    added to ``dlogits`` (that of :func:`ue_gate_backward`, say)."""
+    dev = ctx.device
+    T, _, ld = _rows(logits, "logits", dev, _FLOATS, ctx.E)
+    po, n = _sequences(ctx, offsets)
+    c = _flat(counts, "counts", torch.int32, dev, n * ctx.E)
+    d = _flat(dloss, "dloss", torch.float32, dev, n)
+    if dlogits is None:
+        if accumulate:
+            raise ValueError("accumulate needs dlogits to add to")
+        dlogits = _new((T, ctx.E), logits.dtype, ctx, stream)
+    rows, _, ldo = _rows(dlogits, "dlogits", dev, (logits.dtype,), ctx.E)
+    if rows != T:
+        raise ValueError(f"dlogits must have {T} rows")
+    rc = library().ue_balance_backward(
+        ctx._h, logits.data_ptr(), _TYPES[logits.dtype], ld, T, _score(score),
+        po, n, c, d, dlogits.data_ptr(), ldo, bool(accumulate),
+        _on(ctx, stream, logits, counts, dloss, offsets, dlogits))
+    if rc:
+        ctx._check(rc, "ue_balance_backward")
+    return dlogits
+
+
+def _packed_new(ctx, M, columns, stream):
+    """Packed rows of whole blocks: (q int8 [M, P], scale uint8 [M, P / 32])."""
+    return (_new((M, columns), torch.int8, ctx, stream),
+            _new((M, columns // PACK_BLOCK), torch.uint8, ctx, stream))
+
+
+def _packed(ctx, q, scale, columns=None):
+    """(rows, columns, ldq, pointer of q, lds, pointer of scale)."""
+    if scale is None:
+        raise ValueError("packed rows need their scales")
+    M, K, ldq = _rows(q, "q", ctx.device, (torch.int8,), columns)
+    blocks = (K + PACK_BLOCK - 1) // PACK_BLOCK
+    n, _, lds = _rows(scale, "scale", ctx.device, (torch.uint8,), blocks)
+    if n != M:
+        raise ValueError(f"scale must have {M} rows")
+    if M <= 1:
+        # (whole blocks apart, as every call wants them)
+        ldq = blocks * PACK_BLOCK
+    return M, K, ldq, q.data_ptr(), lds, scale.data_ptr()
+
+
+def _reach(t, name, rows, ld, cols, unit):
+    """The storage must hold the last row up to a multiple of `unit` bytes."""
+    if rows and cols % unit:
+        end = t.storage_offset() + (rows - 1) * ld + (cols + unit - 1) // unit * unit
+        if end > t.untyped_storage().nbytes():
+            raise ValueError(f"{name}: the last row must reach a multiple of "
+                             f"{unit} bytes")
+
+
+def ue_pack_rows(ctx: Context, x, q=None, scale=None, stream=None):
+    """Rows of x [M, K] (fp32 or bf16) in 8 bits with a power of two per row and
+    32 columns: (q int8 [M, K], scale uint8 [M, ceil(K / 32)]). q is a view of
+    rows padded with zeros to whole blocks."""
+    M, K, ldx = _rows(x, "x", ctx.device, _FLOATS)
+    whole = (K + PACK_BLOCK - 1) // PACK_BLOCK * PACK_BLOCK
+    if (q is None) != (scale is None):
+        raise ValueError("q and scale belong together")
+    if q is None:
+        q, scale = _packed_new(ctx, M, whole, stream)
+        if whole != K:
+            q = q[:, :K]
+    m, _, ldq, pq, lds, ps = _packed(ctx, q, scale, K)
+    if m != M:
+        raise ValueError(f"q must have {M} rows")
+    _reach(q, "q", M, ldq, K, PACK_BLOCK)
+    rc = library().ue_pack_rows(ctx._h, x.data_ptr(), _TYPES[x.dtype], ldx, M,
+                                K, pq, ldq, ps, lds,
+                                _on(ctx, stream, x, q, scale))
+    if rc:
+        ctx._check(rc, "ue_pack_rows")
+    return q, scale
+
+
+def ue_unpack_rows(ctx: Context, q, scale, out=None, out_dtype=torch.bfloat16,
+                   stream=None):
+    """The values [M, K] that packed rows stand for (exact in either type)."""
+    M, K, ldq, pq, lds, ps = _packed(ctx, q, scale)
+    _reach(q, "q", M, ldq, K, PACK_BLOCK)
+    if out is None:
+        out = _new((M, K), out_dtype, ctx, stream)
+    n, _, ldx = _rows(out, "out", ctx.device, _FLOATS, K)
+    if n != M:
+        raise ValueError(f"out must have {M} rows")
+    rc = library().ue_unpack_rows(ctx._h, pq, ldq, ps, lds, M, K,
+                                  out.data_ptr(), _TYPES[out.dtype], ldx,
+                                  _on(ctx, stream, q, scale, out))
+    if rc:
+        ctx._check(rc, "ue_unpack_rows")
+    return out
+
+
+def _half(I):
+    """Bytes of gate, and of up, in a packed row of both."""
+    return (I + PACK_BLOCK - 1) // PACK_BLOCK * PACK_BLOCK
+
+
+def ue_gated(ctx: Context, gu, h=None, q=None, scale=None, keep=True,
+             stream=None):
+    """silu(gate) * up of gu [M, 2 I] (gate, then up): (h [M, I], q int8
+    [M, 2 P], scale uint8 [M, P / 16]) with P = I rounded up to 32: gate and up
+    as packed rows, gate in q[:, :I], up in q[:, P:P + I]. ``keep=False``: h
+    alone is made, q and scale are None."""
+    M, two, ldgu = _rows(gu, "gu", ctx.device, _FLOATS)
+    if two % 2:
+        raise ValueError("gu must hold as many up as gate columns")
+    I = two // 2
+    if h is None:
+        h = _new((M, I), gu.dtype, ctx, stream)
+    n, _, ldh = _rows(h, "h", ctx.device, (gu.dtype,), I)
+    if n != M:
+        raise ValueError(f"h must have {M} rows")
+    if (q is None) != (scale is None) or (q is not None and not keep):
+        raise ValueError("q and scale belong together, and to keep=True")
+    ldq = lds = 0
+    pq = ps = None
+    if keep:
+        if q is None:
+            q, scale = _packed_new(ctx, M, 2 * _half(I), stream)
+        m, _, ldq, pq, lds, ps = _packed(ctx, q, scale, 2 * _half(I))
+        if m != M:
+            raise ValueError(f"q must have {M} rows")
+    rc = library().ue_gated(ctx._h, gu.data_ptr(), _TYPES[gu.dtype], ldgu, M, I,
+                            h.data_ptr(), ldh, pq, ldq, ps, lds,
+                            _on(ctx, stream, gu, h, q, scale))
+    if rc:
+        ctx._check(rc, "ue_gated")
+    return h, q, scale
+
+
+def ue_gated_backward(ctx: Context, dh, q, scale, dgu=None, h=None,
+                      with_h=True, stream=None):
+    """Gradient [M, 2 I] of gate and up from dh [M, I] and what :func:`ue_gated`
+    kept, and (``with_h``) silu(gate) * up of the kept values [M, I]:
+    (dgu, h)."""
+    M, I, lddh = _rows(dh, "dh", ctx.device, _FLOATS)
+    m, _, ldq, pq, lds, ps = _packed(ctx, q, scale, 2 * _half(I))
+    if m != M:
+        raise ValueError(f"q must have {M} rows")
+    if dgu is None:
+        dgu = _new((M, 2 * I), dh.dtype, ctx, stream)
+    n, _, lddgu = _rows(dgu, "dgu", ctx.device, (dh.dtype,), 2 * I)
+    if n != M:
+        raise ValueError(f"dgu must have {M} rows")
+    if h is None and with_h:
+        h = _new((M, I), dh.dtype, ctx, stream)
+    ldh = 0
+    if h is not None:
+        n, _, ldh = _rows(h, "h", ctx.device, (dh.dtype,), I)
+        if n != M:
+            raise ValueError(f"h must have {M} rows")
+    rc = library().ue_gated_backward(
+        ctx._h, pq, ldq, ps, lds, dh.data_ptr(), _TYPES[dh.dtype], lddh, M, I,
+        dgu.data_ptr(), lddgu, None if h is None else h.data_ptr(), ldh,
+        _on(ctx, stream, q, scale, dh, dgu, h))
+    if rc:
+        ctx._check(rc, "ue_gated_backward")
+    return dgu, h
+
+
+_WGRAD = struct.Struct("@7P5q7i")            # ue_weight_grad_product
+assert _WGRAD.size <= ctypes.sizeof(ue_weight_grad_product) < _WGRAD.size + 8
+
+
+def ue_weight_grad(ctx: Context, dy, x, x_scale=None, offsets=None, index=None,
+                   index_div=1, out=None, accumulate=False, workspace=None,
+                   stream=None):
+    """Gradients fp32 [groups, N, K] of the matrices of row groups: the sums over
+    each group's rows of dy[m]^T x[row of m], dy bf16 [M, N], x bf16 [rows, K]
+    or packed (int8 with ``x_scale``). Groups and rows are those of
+    :func:`ue_matmul_i8` (``offsets``, ``index``, ``index_div``). With
+    ``accumulate`` the sums are added to ``out``. The matrices of ``out`` may lie
+    apart, and so may their rows."""
+    dev = ctx.device
+    M, N, lddy = _rows(dy, "dy", dev, (torch.bfloat16,))
+    if x_scale is None:
+        rows, K, ldx = _rows(x, "x", dev, (torch.bfloat16,))
+        ps, lds = 0, 0
+    else:
+        rows, K, ldx, _, lds, ps = _packed(ctx, x, x_scale)
+        _reach(x, "x", rows, ldx, K, 16)
+    groups, po, pi = 1, 0, 0
+    if offsets is not None:
+        groups = offsets.numel() - 1
+        if groups < 0:
+            raise ValueError("offsets must hold groups + 1 entries")
+        po = _flat(offsets, "offsets", torch.int32, dev, groups + 1)
+    if index is not None:
+        if index.numel() != M:
+            raise ValueError(f"index must hold {M} rows")
+        pi = _flat(index, "index", torch.int32, dev, M)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out to add to")
+        out = _new((groups, N, K), torch.float32, ctx, stream)
+    elif not isinstance(out, torch.Tensor) or out.dtype != torch.float32:
+        raise TypeError("out must be an fp32 tensor")
+    elif out.device != dev or tuple(out.shape) != (groups, N, K):
+        raise ValueError(f"out must be [{groups}, {N}, {K}] on {dev}, is "
+                         f"{tuple(out.shape)} on {out.device}")
+    out_stride, ldo, one = out.stride()
+    if K > 1 and one != 1:
+        raise ValueError("out must have contiguous rows")
+    if N <= 1:
+        ldo = (K + 3) // 4 * 4
+
+    def product(ws):
+        return _WGRAD.pack(dy.data_ptr(), x.data_ptr(), ps, po, pi,
+                           out.data_ptr(), ws, lddy, ldx, lds, ldo, out_stride,
+                           rows, groups, index_div, M, N, K, bool(accumulate))
+    p = product(0)
+    need = library().ue_weight_grad_workspace(ctx._h, p)
+    if need:
+        workspace = _workspace(ctx, workspace, need, stream)
+        p = product(workspace.data_ptr())
+    rc = library().ue_weight_grad(ctx._h, p,
+                                  _on(ctx, stream, dy, x, x_scale, offsets,
+                                      index, out, workspace))
+    if rc:
+        ctx._check(rc, "ue_weight_grad")
+    return out
+
+
+def _assigned(ctx, inv_perm, weights):
+    """(tokens, pointers) of inv_perm int32 [T, k] and weights fp32 [T, k]."""
+    if not isinstance(inv_perm, torch.Tensor) or inv_perm.numel() % ctx.k:
+        raise ValueError(f"inv_perm must be an int32 tensor [T, {ctx.k}]")
+    T = inv_perm.numel() // ctx.k
+    pi = _flat(inv_perm, "inv_perm", torch.int32, ctx.device, T * ctx.k)
+    pw = None if weights is None else _flat(weights, "weights", torch.float32,
+                                            ctx.device, T * ctx.k)
+    return T, pi, pw
+
+
+def ue_combine(ctx: Context, y, inv_perm, weights=None, add=None, out=None,
+               stream=None):
+    """out[t] = add[t] + sum_j weights[t, j] y[inv_perm[t, j]]: rows of y [rows,
+    H] (fp32 or bf16, dispatch order) back to their tokens. Entries of inv_perm
+    outside y's rows add nothing; without weights they are 1 (the gradient of
+    :func:`ue_gather_rows`)."""
+    dev = ctx.device
+    rows, H, ldy = _rows(y, "y", dev, _FLOATS)
+    T, pi, pw = _assigned(ctx, inv_perm, weights)
+    pa, lda = None, 0
+    if add is not None:
+        n, _, lda = _rows(add, "add", dev, (y.dtype,), H)
+        if n != T:
+            raise ValueError(f"add must have {T} rows")
+        pa = add.data_ptr()
+    if out is None:
+        out = _new((T, H), y.dtype, ctx, stream)
+    n, _, ldo = _rows(out, "out", dev, (y.dtype,), H)
+    if n != T:
+        raise ValueError(f"out must have {T} rows")
+    rc = library().ue_combine(ctx._h, y.data_ptr(), _TYPES[y.dtype], ldy, rows,
+                              pi, pw, pa, lda, T, H, out.data_ptr(), ldo,
+                              _on(ctx, stream, y, inv_perm, weights, add, out))
+    if rc:
+        ctx._check(rc, "ue_combine")
+    return out
+
+
+def ue_combine_backward(ctx: Context, dout, inv_perm, weights=None, y=None,
+                        dy=None, dweights=None, with_dy=True, stream=None):
+    """Gradients of :func:`ue_combine` from dout [T, H]: (dy, dweights). dy is
+    as y (or, without y, [T * k, H]); its rows that inv_perm does not name are
+    left as they are. dweights fp32 [T, k] needs y and is None without it."""
+    dev = ctx.device
+    T, H, lddo = _rows(dout, "dout", dev, _FLOATS)
+    n, pi, pw = _assigned(ctx, inv_perm, weights)
+    if n != T:
+        raise ValueError(f"inv_perm must be [{T}, {ctx.k}]")
+    if y is None and dweights is not None:
+        raise ValueError("dweights needs y")
+    rows, ldy, py = T * ctx.k, 0, None
+    if y is not None:
+        rows, _, ldy = _rows(y, "y", dev, (dout.dtype,), H)
+        py = y.data_ptr()
+        if dweights is None:
+            dweights = _new((T, ctx.k), torch.float32, ctx, stream)
+        else:
+            _flat(dweights, "dweights", torch.float32, dev, T * ctx.k)
+    lddy = 0
+    if dy is not None or with_dy:
+        if dy is None:
+            dy = _new((rows, H), dout.dtype, ctx, stream)
+        n, _, lddy = _rows(dy, "dy", dev, (dout.dtype,), H)
+        if y is None:
+            rows = n
+        elif n != rows:
+            raise ValueError(f"dy must have {rows} rows")
+    rc = library().ue_combine_backward(
+        ctx._h, dout.data_ptr(), _TYPES[dout.dtype], lddo, pi, pw, py, ldy,
+        rows, T, H, None if dy is None else dy.data_ptr(), lddy,
+        None if dweights is None else dweights.data_ptr(),
+        _on(ctx, stream, dout, inv_perm, weights, y, dy, dweights))
+    if rc:
+        ctx._check(rc, "ue_combine_backward")
+    return dy, dweights

@@ -1,0 +1,376 @@
+// Balance loss of packed sequences (ue_balance) and the gradient of the
+// router's logits (ue_balance_backward).
+//
+// With p_t the scores of token t (softmax, or sigmoids over their sum) and c_e
+// the assignments to expert e in a sequence of n tokens:
+//   loss = E / (k n^2) sum_e c_e sum_t p_te
+//   dl_te = dloss E / (k n^2) p_te (c_e - sum_j p_tj c_j) [1 - sigmoid(l_te)]
+// Counts are constants, so the forward pass is one over the logits and ids that
+// sums p and counts ids, and the backward pass one over the logits.
+//
+// L lanes share a token, VP experts each, 64 / L tokens per wave; a lane's
+// experts are the same for every token, so it adds their p in registers. Sums
+// are in a fixed order without atomics on values: a workgroup takes a share of
+// consecutive tokens and writes one row of partial sums for every sequence it
+// meets. Share c and sequence s meet in slot c + s: going along the tokens
+// either grows by one, so no two meetings share a slot, and shares + sequences
+// slots are enough for any lengths. A second launch adds a sequence's rows,
+// shares in order.
+#include "ue_train.h"
+
+namespace ue {
+namespace {
+
+template <typename T, int L, int VP>
+__device__ __forceinline__ int expert_of_slot(int at, int i, bool vec) {
+    return vec ? 4 * (at + L * (i / 4)) + i % 4 : at + L * i;
+}
+
+// The logits of one row that lane `at` holds, -inf past the last expert.
+template <typename T, int L, int VP>
+__device__ __forceinline__ void load_token(const T *row, int at, int E, bool vec,
+                                           float (&x)[VP]) {
+    if (vec) {
+        struct alignas(4 * sizeof(T)) Pack { T v[4]; };
+#pragma unroll
+        for (int c = 0; c < VP / 4; ++c) {
+            const int e = 4 * (at + L * c);
+            Pack p;
+            if (e < E) p = *reinterpret_cast<const Pack *>(row + e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[4 * c + i] = e < E ? widen<T>(p.v[i]) : -__builtin_inff();
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            const int e = at + L * i;
+            x[i] = e < E ? widen<T>(row[e]) : -__builtin_inff();
+        }
+    }
+}
+
+// Scores of a token in place of its logits, 0 where all are masked; `slope`:
+// 1 - sigmoid (untouched for the softmax).
+template <int L, int VP, bool SIGMOID, bool SLOPE>
+__device__ __forceinline__ void scores(float (&x)[VP], float (&slope)[SLOPE ? VP : 1]) {
+    float sum = 0.f;
+    if (SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            // from exp(-|x|), which never overflows
+            const float e = exp_of(-fabsf(x[i])), r = 1.0f / (1.0f + e);
+            const bool up = x[i] >= 0.f;
+            if constexpr (SLOPE) slope[i] = up ? e * r : r;
+            x[i] = up ? r : e * r;
+            sum += x[i];
+        }
+        sum = lanes_sum<L>(sum) + 1e-20f;
+    } else {
+        float top = x[0];
+#pragma unroll
+        for (int i = 1; i < VP; ++i) top = fmaxf(top, x[i]);
+        top = finite_top(lanes_max<L>(top));
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            x[i] = x[i] == -__builtin_inff() ? 0.f : exp_of(finite_top(x[i]) - top);
+            sum += x[i];
+        }
+        sum = lanes_sum<L>(sum);
+        if (sum == 0.f) sum = 1.f;
+    }
+    const float inv = 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < VP; ++i) x[i] *= inv;
+}
+
+// Bounds of sequences, clamped to the tokens there are.
+struct Sequences {
+    const int32_t *offsets;
+    int T, n;
+    __device__ __forceinline__ int begin(int s) const {
+        if (!offsets) return s ? T : 0;
+        const int o = offsets[s];
+        return o < 0 ? 0 : o > T ? T : o;
+    }
+    // the first sequence that ends behind token t
+    __device__ __forceinline__ int find(int t) const {
+        int lo = 0, hi = n;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (begin(mid + 1) > t) hi = mid;
+            else lo = mid + 1;
+        }
+        return lo;
+    }
+};
+
+template <typename T, int L, int VP, bool SIGMOID>
+__global__ __launch_bounds__(kBlock) void k_balance(BalanceArgs g) {
+    constexpr int kEach = 64 / L, kAll = L * VP;
+    __shared__ float sums[kWaves][kAll];
+    __shared__ int hist[kAll];
+    const int tid = threadIdx.x, lane = lane_id(), wv = tid >> 6;
+    const int at = lane & (L - 1), sub = lane / L, E = g.E;
+    const Sequences seqs{g.offsets, g.T, g.n_seq};
+    const int c = blockIdx.x, t0 = c * g.chunk;
+    const int t1 = g.T - t0 < g.chunk ? g.T : t0 + g.chunk;
+    const T *logits = static_cast<const T *>(g.logits);
+    for (int s = seqs.find(t0); s < g.n_seq; ++s) {
+        int a = seqs.begin(s), b = seqs.begin(s + 1);
+        if (a >= t1) break;
+        a = a > t0 ? a : t0;
+        b = b < t1 ? b : t1;
+        if (a >= b) continue;
+        for (int e = tid; e < E; e += kBlock) hist[e] = 0;
+        __syncthreads();
+        for (int i = a * g.k + tid; i < b * g.k; i += kBlock) {
+            const int id = g.ids[i];
+            if (static_cast<uint32_t>(id) < static_cast<uint32_t>(E))
+                atomicAdd(&hist[id], 1);
+        }
+        float acc[VP] = {};
+        const int step = kWaves * kEach;
+        for (int t = a + wv * kEach; t < b; t += step) {
+            const int mine = t + sub < b ? t + sub : b - 1;
+            float x[VP], none[1];
+            load_token<T, L, VP>(logits + mine * g.ld, at, E, g.vec, x);
+            scores<L, VP, SIGMOID, false>(x, none);
+            if (t + sub < b) {
+#pragma unroll
+                for (int i = 0; i < VP; ++i) acc[i] += x[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+#pragma unroll
+            for (int d = L; d < 64; d <<= 1) acc[i] += __shfl_xor(acc[i], d);
+            if (sub == 0) sums[wv][expert_of_slot<T, L, VP>(at, i, g.vec)] = acc[i];
+        }
+        __syncthreads();
+        const int64_t slot = static_cast<int64_t>(c + s) * E;
+        for (int e = tid; e < E; e += kBlock) {
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) v += sums[w][e];
+            g.part[slot + e] = v;
+            g.part_n[slot + e] = hist[e];
+        }
+        __syncthreads();
+    }
+}
+
+// Adds a sequence's rows of partial sums: wave w takes shares w, w + kEndWaves,
+// ... and 256 experts at a time.
+constexpr int kEndWaves = 16, kEndBlock = kEndWaves * 64;
+
+__global__ __launch_bounds__(kEndBlock) void k_balance_end(BalanceArgs g) {
+    __shared__ float sums[kEndWaves][256];
+    __shared__ int counts[kEndWaves][256];
+    __shared__ float terms[4];
+    const int tid = threadIdx.x, lane = lane_id(), wv = tid >> 6, E = g.E;
+    const int s = blockIdx.x;
+    const Sequences seqs{g.offsets, g.T, g.n_seq};
+    const int a = seqs.begin(s), b = seqs.begin(s + 1), n = b > a ? b - a : 0;
+    const int c0 = n ? a / g.chunk : 0, c1 = n ? (b - 1) / g.chunk + 1 : 0;
+    const float inv_n = n ? 1.0f / static_cast<float>(n) : 0.f;
+    float term = 0.f;
+    for (int e0 = 0; e0 < E; e0 += 256) {
+        float v[4] = {};
+        int m[4] = {};
+#pragma unroll 4
+        for (int c = c0 + wv; c < c1; c += kEndWaves) {
+            const int64_t slot = static_cast<int64_t>(c + s) * E + e0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = lane + 64 * i;
+                if (e0 + e < E) {
+                    v[i] += g.part[slot + e];
+                    m[i] += g.part_n[slot + e];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sums[wv][lane + 64 * i] = v[i];
+            counts[wv][lane + 64 * i] = m[i];
+        }
+        __syncthreads();
+        if (tid < 256 && e0 + tid < E) {
+            float total = 0.f;
+            int count = 0;
+#pragma unroll
+            for (int w = 0; w < kEndWaves; ++w) {
+                total += sums[w][tid];
+                count += counts[w][tid];
+            }
+            const int64_t o = static_cast<int64_t>(s) * E + e0 + tid;
+            g.counts[o] = count;
+            const float mean = total * inv_n;
+            g.prob[o] = mean;
+            term += static_cast<float>(count) * mean;
+        }
+        __syncthreads();
+    }
+    if (tid < 256) {
+        term = lanes_sum<64>(term);
+        if (lane == 0) terms[wv] = term;
+    }
+    __syncthreads();
+    if (tid == 0)
+        g.loss[s] = ((terms[0] + terms[1]) + (terms[2] + terms[3])) *
+                    (static_cast<float>(E) / static_cast<float>(g.k)) * inv_n;
+}
+
+template <typename T, int L, int VP, bool SIGMOID>
+__global__ __launch_bounds__(kBlock) void k_balance_backward(BalanceBackArgs g, int chunk) {
+    constexpr int kEach = 64 / L;
+    const int lane = lane_id(), wv = threadIdx.x >> 6;
+    const int at = lane & (L - 1), sub = lane / L, E = g.E;
+    const Sequences seqs{g.offsets, g.T, g.n_seq};
+    const int t0 = blockIdx.x * chunk;
+    const int t1 = g.T - t0 < chunk ? g.T : t0 + chunk;
+    const T *logits = static_cast<const T *>(g.logits);
+    T *out = static_cast<T *>(g.dlogits);
+    int t = t0 + wv * kEach + sub;
+    // this token's sequence; its counts times what its gradient is scaled with
+    int s = seqs.find(t), from = 0, to = -1;
+    float cw[VP] = {};
+    for (; t - sub < t1; t += kWaves * kEach) {
+        const bool real = t < t1;
+        const int mine = real ? t : t1 - 1;
+        float x[VP], slope[VP];
+        load_token<T, L, VP>(logits + mine * g.ld, at, E, g.vec, x);
+        if (real && t >= to) {
+            while (s < g.n_seq && seqs.begin(s + 1) <= t) ++s;
+            if (s < g.n_seq) {
+                from = seqs.begin(s);
+                to = seqs.begin(s + 1);
+                const float n = static_cast<float>(to - from);
+                const float f = g.dloss[s] *
+                    (static_cast<float>(E) / (static_cast<float>(g.k) * n)) / n;
+#pragma unroll
+                for (int i = 0; i < VP; ++i) {
+                    const int e = expert_of_slot<T, L, VP>(at, i, g.vec);
+                    cw[i] = e < E ? static_cast<float>(
+                                g.counts[static_cast<int64_t>(s) * E + e]) * f : 0.f;
+                }
+            } else {
+                from = to = g.T;       // behind the last sequence
+            }
+        }
+        const bool inside = real && t >= from && t < to;
+        scores<L, VP, SIGMOID, true>(x, slope);
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < VP; ++i) dot = __builtin_fmaf(x[i], cw[i], dot);
+        dot = lanes_sum<L>(dot);
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            x[i] *= cw[i] - dot;
+            if (SIGMOID) x[i] *= slope[i];
+            if (!inside) x[i] = 0.f;
+        }
+        if (!real || (g.accumulate && !inside)) continue;
+        T *row = out + t * g.ld_out;
+        if (g.vec) {
+            struct alignas(4 * sizeof(T)) Pack { T v[4]; };
+#pragma unroll
+            for (int c = 0; c < VP / 4; ++c) {
+                const int e = 4 * (at + L * c);
+                if (e >= E) continue;
+                Pack p;
+                if (g.accumulate) {
+                    p = *reinterpret_cast<const Pack *>(row + e);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[4 * c + i] += widen<T>(p.v[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p.v[i] = narrow<T>(x[4 * c + i]);
+                *reinterpret_cast<Pack *>(row + e) = p;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VP; ++i) {
+                const int e = at + L * i;
+                if (e >= E) continue;
+                if (g.accumulate) x[i] += widen<T>(row[e]);
+                row[e] = narrow<T>(x[i]);
+            }
+        }
+    }
+}
+
+// The lanes and slots that hold E experts: f<L, VP>().
+template <class F>
+void with_lanes(int E, F f) {
+    if (E <= 32) f(std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
+    else if (E <= 64) f(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{});
+    else if (E <= 128) f(std::integral_constant<int, 8>{}, std::integral_constant<int, 16>{});
+    else if (E <= 256) f(std::integral_constant<int, 16>{}, std::integral_constant<int, 16>{});
+    else if (E <= 512) f(std::integral_constant<int, 32>{}, std::integral_constant<int, 16>{});
+    else f(std::integral_constant<int, 64>{}, std::integral_constant<int, 16>{});
+}
+
+template <typename T, bool SIGMOID>
+void balance_any(const BalanceArgs &g, int shares, hipStream_t s) {
+    with_lanes(g.E, [&](auto l, auto v) {
+        hipLaunchKernelGGL((k_balance<T, decltype(l)::value, decltype(v)::value, SIGMOID>),
+                           dim3(shares), dim3(kBlock), 0, s, g);
+    });
+}
+
+template <typename T, bool SIGMOID>
+void backward_any(const BalanceBackArgs &g, int chunk, int shares, hipStream_t s) {
+    with_lanes(g.E, [&](auto l, auto v) {
+        hipLaunchKernelGGL((k_balance_backward<T, decltype(l)::value, decltype(v)::value, SIGMOID>),
+                           dim3(shares), dim3(kBlock), 0, s, g, chunk);
+    });
+}
+
+}  // namespace
+
+// Two workgroups' shares per CU, of 64 tokens at least.
+int balance_chunk(int T, int num_cu) {
+    const int each = (T + 2 * num_cu - 1) / (2 * num_cu);
+    return each <= 64 ? 64 : (each + 15) / 16 * 16;
+}
+int64_t balance_slots(int T, int n_seq, int num_cu) {
+    const int c = balance_chunk(T, num_cu);
+    return (static_cast<int64_t>(T) + c - 1) / c + n_seq;
+}
+
+hipError_t launch_balance(const ue_ctx &c, const BalanceArgs &a, hipStream_t s) {
+    if (a.n_seq == 0) return hipSuccess;
+    BalanceArgs g = a;
+    g.chunk = balance_chunk(g.T, c.num_cu);
+    const int shares = (g.T + g.chunk - 1) / g.chunk;
+    if (shares > 0) {
+        if (g.bf16)
+            g.sigmoid ? balance_any<uint16_t, true>(g, shares, s)
+                      : balance_any<uint16_t, false>(g, shares, s);
+        else
+            g.sigmoid ? balance_any<float, true>(g, shares, s)
+                      : balance_any<float, false>(g, shares, s);
+        const hipError_t he = hipGetLastError();
+        if (he != hipSuccess) return he;
+    }
+    hipLaunchKernelGGL(k_balance_end, dim3(g.n_seq), dim3(kEndBlock), 0, s, g);
+    return hipGetLastError();
+}
+
+hipError_t launch_balance_backward(const ue_ctx &c, const BalanceBackArgs &g,
+                                   hipStream_t s) {
+    if (g.T == 0) return hipSuccess;
+    const int chunk = balance_chunk(g.T, c.num_cu);
+    const int shares = (g.T + chunk - 1) / chunk;
+    if (g.bf16)
+        g.sigmoid ? backward_any<uint16_t, true>(g, chunk, shares, s)
+                  : backward_any<uint16_t, false>(g, chunk, shares, s);
+    else
+        g.sigmoid ? backward_any<float, true>(g, chunk, shares, s)
+                  : backward_any<float, false>(g, chunk, shares, s);
+    return hipGetLastError();
+}
+
+}  // namespace ue

@@ -1,0 +1,262 @@
+// Internal declarations of the expert layer's training step: kernel arguments,
+// launchers, packed rows, sums over the lanes that share a token.
+#pragma once
+
+#include "ue_gate.h"
+
+namespace ue {
+
+struct BalanceArgs {
+    const void *logits;         // [T] rows of E, ld elements apart
+    int64_t ld;
+    bool bf16, vec;             // vec: four logits load (and store) at once
+    bool sigmoid;
+    int E, k, T, n_seq;
+    const int32_t *ids;
+    const int32_t *offsets;     // [n_seq + 1] or null (one sequence)
+    int32_t *counts;
+    float *prob, *loss;
+    int chunk;                  // tokens of a workgroup's share
+    float *part;                // [slots][E] sums of p; slot: chunk + sequence
+    int32_t *part_n;            // [slots][E] assignments
+};
+struct BalanceBackArgs {
+    const void *logits;
+    int64_t ld;
+    bool bf16, vec;             // vec: of the gradient's rows too
+    bool sigmoid, accumulate;
+    int E, k, T, n_seq;
+    const int32_t *offsets, *counts;
+    const float *dloss;
+    void *dlogits;
+    int64_t ld_out;
+};
+// Tokens of a workgroup's share, and the slots of partial sums T tokens in
+// n_seq sequences may need.
+int balance_chunk(int T, int num_cu);
+int64_t balance_slots(int T, int n_seq, int num_cu);
+hipError_t launch_balance(const ue_ctx &c, const BalanceArgs &g, hipStream_t s);
+hipError_t launch_balance_backward(const ue_ctx &c, const BalanceBackArgs &g,
+                                   hipStream_t s);
+
+// Rows and their packed form. `vec`: the unpacked rows start 16-byte aligned.
+struct PackArgs {
+    const void *x;
+    void *out;                  // unpacking: where the values go
+    int64_t ldx;
+    bool bf16, vec;
+    int M, K;
+    int8_t *q;
+    const int8_t *q_in;
+    int64_t ldq;
+    uint8_t *scale;
+    const uint8_t *scale_in;
+    int64_t lds;
+};
+hipError_t launch_pack(const ue_ctx &c, const PackArgs &g, hipStream_t s);
+hipError_t launch_unpack(const ue_ctx &c, const PackArgs &g, hipStream_t s);
+
+struct GatedArgs {
+    const void *gu;             // forward: [M] rows of 2 I
+    const void *dh;             // backward: [M] rows of I
+    int64_t ldin;
+    bool bf16, vec;             // vec: every row's pieces are 16-byte aligned
+    int M, I;
+    void *h;                    // may be null backward
+    int64_t ldh;
+    void *dgu;
+    int64_t lddgu;
+    int8_t *q;                  // may be null forward
+    const int8_t *q_in;
+    int64_t ldq;
+    uint8_t *scale;
+    const uint8_t *scale_in;
+    int64_t lds;
+};
+hipError_t launch_gated(const ue_ctx &c, const GatedArgs &g, hipStream_t s);
+hipError_t launch_gated_backward(const ue_ctx &c, const GatedArgs &g, hipStream_t s);
+
+struct CombineArgs {
+    const void *y;              // [rows] rows of H
+    int64_t ldy;
+    int rows;
+    bool bf16, vec;             // vec: all rows are 16-byte aligned
+    const int32_t *inv;
+    const float *weights;       // or null (ones)
+    int T, k, H;
+    const void *add;            // or null
+    int64_t ldadd;
+    void *out;                  // forward
+    int64_t ldo;
+    const void *dout;           // backward
+    int64_t lddout;
+    void *dy;                   // or null
+    int64_t lddy;
+    float *dweights;            // or null
+};
+hipError_t launch_combine(const ue_ctx &c, const CombineArgs &g, hipStream_t s);
+hipError_t launch_combine_backward(const ue_ctx &c, const CombineArgs &g,
+                                   hipStream_t s);
+
+struct WgradArgs {
+    const uint16_t *dy;
+    int64_t lddy;
+    const void *x;
+    int64_t ldx;
+    const uint8_t *x_scale;
+    int64_t lds;
+    int x_rows;
+    const int32_t *offsets;     // [G + 1] or null
+    int G;
+    const int32_t *index;       // [M] or null
+    int index_div;
+    int M, N, K;
+    bool accumulate, vec_dy, vec_x, vec_out;   // rows in 16-byte pieces
+    float *out;
+    int64_t ldo, out_stride;
+    float *part;                // [parts][G][N][K] of a split sum, or null
+    int parts;
+};
+// too_large: nothing was launched, the launch would have 2^32 threads or more.
+hipError_t launch_wgrad(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_large);
+// Parts each group's rows are split into (1: no workspace).
+int wgrad_parts(int M, int N, int K, int G, bool packed, int num_cu);
+
+// ---------------------------------------------------------------------
+// device helpers
+
+template <typename T>
+__device__ __forceinline__ float widen(T v);
+template <>
+__device__ __forceinline__ float widen<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float widen<uint16_t>(uint16_t v) { return bf16_to_f32(v); }
+
+template <typename T>
+__device__ __forceinline__ T narrow(float v);
+template <>
+__device__ __forceinline__ float narrow<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ uint16_t narrow<uint16_t>(float v) { return f32_to_bf16(v); }
+
+// Eight elements, or those of them before `n`, at p.
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, bool vec, int n, float (&f)[8]) {
+    if (vec && n >= 8) {
+        struct alignas(16) Pack { T v[8]; };
+        const Pack k = *reinterpret_cast<const Pack *>(p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = widen<T>(k.v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = i < n ? widen<T>(p[i]) : 0.f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T *p, bool vec, int n, const float (&f)[8]) {
+    if (vec && n >= 8) {
+        struct alignas(16) Pack { T v[8]; } k;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) k.v[i] = narrow<T>(f[i]);
+        *reinterpret_cast<Pack *>(p) = k;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = narrow<T>(f[i]);
+    }
+}
+
+// The power of two of a block whose largest magnitude has these bits, biased
+// by 127: its exponent less 6, one more above 127/64 of its power of two, and
+// at least 1 (so that it and its inverse are normal numbers); 255 for a block
+// that holds an infinity or a NaN.
+__device__ __forceinline__ uint32_t block_scale(uint32_t top) {
+    if (top >= 0x7F800000u) return 255u;
+    const uint32_t e = (top + 0x1FFFFu) >> 23;
+    return e > 7u ? e - 6u : 1u;
+}
+// 2^e, infinity for 255 (which q = 0 turns into the block's NaNs).
+__device__ __forceinline__ float scale_step(uint32_t s) { return __uint_as_float(s << 23); }
+// 2^-e, 0 for 255 (254 - e is 0 only for e = 254, which no finite block has).
+__device__ __forceinline__ float scale_inverse(uint32_t s) {
+    return s >= 254u ? 0.f : __uint_as_float((254u - s) << 23);
+}
+
+// Largest of four lanes' values (the lanes of one block).
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+    uint32_t o = __builtin_amdgcn_update_dpp(v, v, 0xB1, 0xF, 0xF, false);
+    v = o > v ? o : v;
+    o = __builtin_amdgcn_update_dpp(v, v, 0x4E, 0xF, 0xF, false);
+    return o > v ? o : v;
+}
+
+// Eight elements of this lane's part of a block (four lanes) as integers;
+// returns the block's scale.
+__device__ __forceinline__ uint32_t pack8(const float (&f)[8], uint64_t &q) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t b = __float_as_uint(f[i]) & 0x7FFFFFFFu;
+        top = b > top ? b : top;
+    }
+    const uint32_t s = block_scale(quad_max(top));
+    const float inv = scale_inverse(s);
+    union { int8_t b[8]; uint64_t w; } u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        u.b[i] = static_cast<int8_t>(s == 255u ? 0 : static_cast<int>(rintf(f[i] * inv)));
+    q = u.w;
+    return s;
+}
+__device__ __forceinline__ void unpack8(uint64_t q, uint32_t s, float (&f)[8]) {
+    const float step = scale_step(s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        f[i] = static_cast<float>(static_cast<int8_t>(q >> (8 * i))) * step;
+}
+
+// Quotients of numbers below 2^31 by a divisor fixed on the host: a high
+// product, a sum and a shift.
+struct FastDiv {
+    uint32_t d, mul, shift;
+};
+inline FastDiv fast_div(uint32_t d) {
+    uint32_t l = 0;
+    while ((1ull << l) < d) ++l;
+    const uint32_t m = static_cast<uint32_t>(((1ull << 32) * ((1ull << l) - d)) / d + 1);
+    return FastDiv{d, m, l};
+}
+__device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv &f) {
+    return (__umulhi(n, f.mul) + n) >> f.shift;
+}
+
+template <int CTRL>
+__device__ __forceinline__ float lane_move(float v) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(
+        __float_as_uint(v), __float_as_uint(v), CTRL, 0xF, 0xF, false));
+}
+// Sum and maximum over L consecutive lanes, the same in each: inside a row of
+// 16 by lane moves (pairs, halves of four, mirrored eights and sixteens),
+// beyond it by exchange.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+    if (L > 1) v += lane_move<0xB1>(v);
+    if (L > 2) v += lane_move<0x4E>(v);
+    if (L > 4) v += lane_move<0x141>(v);
+    if (L > 8) v += lane_move<0x140>(v);
+    if (L > 16) v += __shfl_xor(v, 16);
+    if (L > 32) v += __shfl_xor(v, 32);
+    return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+    if (L > 1) v = fmaxf(v, lane_move<0xB1>(v));
+    if (L > 2) v = fmaxf(v, lane_move<0x4E>(v));
+    if (L > 4) v = fmaxf(v, lane_move<0x141>(v));
+    if (L > 8) v = fmaxf(v, lane_move<0x140>(v));
+    if (L > 16) v = fmaxf(v, __shfl_xor(v, 16));
+    if (L > 32) v = fmaxf(v, __shfl_xor(v, 32));
+    return v;
+}
+
+}  // namespace ue
