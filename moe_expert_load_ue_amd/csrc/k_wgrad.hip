@@ -77,24 +77,32 @@ __device__ __forceinline__ Unit load_unit(const uint16_t *p, int n) {
     return u;
 }
 
-// FN, FK: 32-column fragments of dy and of x per wave; WN, WK: waves along each;
-// ROWS: rows of a stage. WHOLE: rows are 16-byte aligned and multiples of 8
-// columns (packed x always is), so that pieces are whole or nobody's.
+// FN, FK: 32-column fragments of dy and of x per wave; WN, WK: waves along each.
+// WHOLE: rows are 16-byte aligned and multiples of 8 columns (packed x always
+// is), so that pieces are whole or nobody's.
 //
-// While a stage's products run, the next one's rows are in registers or on
-// their way to LDS, and the one after that is on its way to registers.
-template <int FN, int FK, int WN, int WK, int ROWS, bool WHOLE, bool PACKED>
-__global__ __launch_bounds__(WN *WK * 64, FN * FK > 8 ? 1 : 2) void k_wgrad(
+// A stage is four steps of 16 rows. A step's operands are read from LDS during
+// the step before; the next stage is put down during the second and third step,
+// and each of its registers is at once filled with the stage after that. So by
+// the end of the third step this stage has been read and the next one is in
+// LDS: one barrier there.
+constexpr int kStep = 16, kSteps = 4, kRows = kStep * kSteps;
+
+template <int FN, int FK, int WN, int WK, bool WHOLE, bool PACKED>
+__global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
     WgradArgs g, FastDiv div, int tiles_n, int tiles_k) {
     constexpr int kThreads = WN * WK * 64;
     constexpr int BN = WN * FN * 32, BK = WK * FK * 32;
     constexpr int UN = BN / kUnit, UK = BK / kUnit;          // units of a row
-    constexpr int kDyBytes = ROWS * BN * 2, kStage = kDyBytes + ROWS * BK * 2;
-    constexpr int kUnitsX = ROWS * UK / kThreads;            // units of a thread
-    constexpr int kUnitsDy = ROWS * UN / kThreads;
-    static_assert(kUnitsX * kThreads == ROWS * UK && kUnitsDy * kThreads == ROWS * UN,
+    constexpr int kDyBytes = kRows * BN * 2, kXBytes = kRows * BK * 2;
+    constexpr int kUnitsX = kRows * UK / kThreads;           // units of a thread
+    constexpr int kUnitsDy = kRows * UN / kThreads;
+    constexpr int kGapX = kThreads / UK, kGapDy = kThreads / UN;   // rows between them
+    static_assert(kUnitsX * kThreads == kRows * UK && kUnitsDy * kThreads == kRows * UN,
                   "whole units per thread");
-    static_assert(ROWS % 16 == 0 && UN % 8 == 0 && UK % 8 == 0);
+    static_assert((UN == 8 || UN == 16) && (UK == 8 || UK == 16));
+    // both stages of dy, then both of x: a stage is an offset that fits the
+    // instructions'
     extern __shared__ __align__(16) char lds[];
     const int tid = threadIdx.x, lane = lane_id();
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -114,91 +122,91 @@ __global__ __launch_bounds__(WN *WK * 64, FN * FK > 8 ? 1 : 2) void k_wgrad(
         lo = lo < 0 ? 0 : lo > g.M ? g.M : lo;
         hi = hi < lo ? lo : hi > g.M ? g.M : hi;
     }
-    const int steps = (hi - lo + ROWS - 1) / ROWS;
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    const int steps = (hi - lo + kRows - 1) / kRows;
+    // first row of a stage (past the last one: the last one's, read again and
+    // put where nobody reads it)
+    auto first_of = [&](int st) { return lo + (st < steps ? st : steps - 1) * kRows; };
 
     // ---- loads: rows past the group's last are read again as the last one and
-    // put down as zeros; pieces past the last column are read from the first
+    // put down as zeros; pieces past the last column are read as others
     // (results of columns that nobody stores) ----
+    const int dy_row = tid / UN, dy_n = n0 + tid % UN * kUnit;
+    const uint32_t dy_at = dy_n < g.N ? dy_n * 2 : 0;
+    const uint32_t dy_up = dy_n + 8 < g.N ? 16 : 0;
     Unit dyr[kUnitsDy];
-    auto fetch_dy = [&](int st) {
-#pragma unroll
-        for (int c = 0; c < kUnitsDy; ++c) {
-            const int i = c * kThreads + tid, n = n0 + i % UN * kUnit;
-            int m = lo + st * ROWS + i / UN;
-            m = m < hi ? m : hi - 1;
-            const uint16_t *row = g.dy + m * g.lddy;
-            if constexpr (WHOLE) {
-                dyr[c].lo = *reinterpret_cast<const u32x4 *>(row + (n < g.N ? n : 0));
-                dyr[c].hi = *reinterpret_cast<const u32x4 *>(row + (n + 8 < g.N ? n + 8 : 0));
-            } else {
-                dyr[c] = load_unit(row + n, g.N - n);
-            }
+    auto fetch_dy = [&](int st, int c) {
+        const int m0 = first_of(st), left = hi - m0;
+        const char *base = reinterpret_cast<const char *>(g.dy + m0 * g.lddy);
+        int r = c * kGapDy + dy_row;
+        if (left < kRows) r = r < left ? r : left - 1;
+        const uint32_t at = r * static_cast<uint32_t>(g.lddy * 2);
+        if constexpr (WHOLE) {
+            dyr[c].lo = *reinterpret_cast<const u32x4 *>(base + (at + dy_at));
+            dyr[c].hi = *reinterpret_cast<const u32x4 *>(base + (at + dy_at + dy_up));
+        } else {
+            dyr[c] = load_unit(reinterpret_cast<const uint16_t *>(base + at) + dy_n, g.N - dy_n);
         }
     };
-    auto put = [&](char *base, int units, int i, const Unit &u) {
-        const int r = i / units, at = (i % units) ^ (r & (units - 1));
-        u32x4 *to = reinterpret_cast<u32x4 *>(base + (r * units + at) * 32);
-        to[0] = u.lo;
-        to[1] = u.hi;
+    // LDS places of a row's units: the units' first halves side by side, then
+    // the second ones (16 lanes that put down a row meet all 64 banks), unit u at
+    // u ^ 2 (r mod 4), so that the four rows of two units that 32 lanes read meet
+    // all banks too
+    auto place = [](int units, int r, int u, int half) {
+        const int p = u ^ (2 * (r & 3));
+        return units == 16 ? (r * 32 + half * 16 + (p ^ (half * 8))) * 16
+                           : (r * 16 + (half ^ (r & 1)) * 8 + p) * 16;
     };
-    auto put_dy = [&](int st) {
-        const bool last = lo + (st + 1) * ROWS > hi;
-#pragma unroll
-        for (int c = 0; c < kUnitsDy; ++c) {
-            const int i = c * kThreads + tid;
-            Unit u = dyr[c];
-            if (last && lo + st * ROWS + i / UN >= hi) u = Unit{};
-            put(lds + (st & 1) * kStage, UN, i, u);
-        }
+    auto put = [&](char *base, int units, int r, int u, const Unit &v) {
+        *reinterpret_cast<u32x4 *>(base + place(units, r, u, 0)) = v.lo;
+        *reinterpret_cast<u32x4 *>(base + place(units, r, u, 1)) = v.hi;
+    };
+    auto put_dy = [&](int st, int buf, int c) {
+        const int left = hi - lo - st * kRows, r = c * kGapDy + dy_row;
+        if (left < kRows && r >= left) dyr[c] = Unit{};
+        put(lds + buf * kDyBytes, UN, r, tid % UN, dyr[c]);
     };
     // x: the index of a row a stage before its units
+    const int x_row = tid / UK, x_k = k0 + tid % UK * kUnit;
+    const int x_at = x_k < g.K ? x_k : 0;
+    const int x_up = x_k + 8 < g.K ? 8 : 0;
     int index[kUnitsX];
-    auto fetch_index = [&](int st) {
-#pragma unroll
-        for (int c = 0; c < kUnitsX; ++c) {
-            int m = lo + st * ROWS + (c * kThreads + tid) / UK;
-            m = m < hi ? m : hi - 1;
-            index[c] = g.index ? g.index[m] : m;
-        }
+    auto fetch_index = [&](int st, int c) {
+        const int m0 = first_of(st), left = hi - m0;
+        int r = c * kGapX + x_row;
+        if (left < kRows) r = r < left ? r : left - 1;
+        index[c] = g.index ? (g.index + m0)[r] : m0 + r;
     };
     struct Raw { u32x4 q; uint32_t s; };
     Raw xq[PACKED ? kUnitsX : 1];
     Unit xu[PACKED ? 1 : kUnitsX];
     bool live[kUnitsX];
-    auto fetch_x = [&](int st) {
-#pragma unroll
-        for (int c = 0; c < kUnitsX; ++c) {
-            const int i = c * kThreads + tid, k = k0 + i % UK * kUnit;
-            int r = index[c] < 0 ? -1 : static_cast<int>(div_by(index[c], div));
-            live[c] = r >= 0 && r < g.x_rows && lo + st * ROWS + i / UK < hi;
-            r = live[c] ? r : 0;
-            if constexpr (PACKED) {
-                // (rows are readable up to a multiple of 16)
-                const int at = k < g.K ? k : 0;
-                xq[c].q = *reinterpret_cast<const u32x4 *>(
-                    static_cast<const int8_t *>(g.x) + r * g.ldx + at);
-                xq[c].s = g.x_scale[r * g.lds + at / UE_PACK_BLOCK];
+    auto fetch_x = [&](int st, int c) {
+        const uint32_t r = div_by(index[c], div);
+        live[c] = index[c] >= 0 && r < static_cast<uint32_t>(g.x_rows) &&
+                  lo + st * kRows + c * kGapX + x_row < hi;
+        const uint64_t row = live[c] ? r : 0;
+        if constexpr (PACKED) {
+            // (rows are readable up to a multiple of 16)
+            xq[c].q = *reinterpret_cast<const u32x4 *>(
+                static_cast<const int8_t *>(g.x) + (row * static_cast<uint32_t>(g.ldx) + x_at));
+            xq[c].s = g.x_scale[row * static_cast<uint32_t>(g.lds) + x_at / UE_PACK_BLOCK];
+        } else {
+            const uint16_t *p = static_cast<const uint16_t *>(g.x) + row * static_cast<uint32_t>(g.ldx);
+            if constexpr (WHOLE) {
+                xu[c].lo = *reinterpret_cast<const u32x4 *>(p + x_at);
+                xu[c].hi = *reinterpret_cast<const u32x4 *>(p + x_at + x_up);
             } else {
-                const uint16_t *row = static_cast<const uint16_t *>(g.x) + r * g.ldx;
-                if constexpr (WHOLE) {
-                    xu[c].lo = *reinterpret_cast<const u32x4 *>(row + (k < g.K ? k : 0));
-                    xu[c].hi = *reinterpret_cast<const u32x4 *>(row + (k + 8 < g.K ? k + 8 : 0));
-                } else {
-                    xu[c] = load_unit(row + k, g.K - k);
-                }
+                xu[c] = load_unit(p + x_k, g.K - x_k);
             }
         }
     };
-    auto put_x = [&](int st) {
-        char *const base = lds + (st & 1) * kStage + kDyBytes;
-#pragma unroll
-        for (int c = 0; c < kUnitsX; ++c) {
-            if constexpr (PACKED)
-                put(base, UK, c * kThreads + tid,
-                    widen_unit(xq[c].q, live[c] ? scale_step(xq[c].s) : 0.f));
-            else
-                put(base, UK, c * kThreads + tid, live[c] ? xu[c] : Unit{});
-        }
+    auto put_x = [&](int buf, int c) {
+        Unit u;
+        if constexpr (PACKED) u = widen_unit(xq[c].q, live[c] ? scale_step(xq[c].s) : 0.f);
+        else u = live[c] ? xu[c] : Unit{};
+        put(lds + 2 * kDyBytes + buf * kXBytes, UK, c * kGapX + x_row, tid % UK, u);
     };
 
     // ---- products ----
@@ -209,102 +217,162 @@ __global__ __launch_bounds__(WN *WK * 64, FN * FK > 8 ? 1 : 2) void k_wgrad(
         for (int j = 0; j < FK; ++j) acc[i][j] = f32x16{};
     const int wn = wv / WK, wk = wv % WK;
     // where this lane reads: four rows of one unit per 16 lanes; half of a
-    // wave's lanes take rows 0-7 of sixteen, half 8-15, in two reads
+    // wave's lanes take rows 0-7 of a step, half 8-15, in two reads
     const int q = lane >> 4, sub = lane & 15;
-    int ra[FN][2], rb[FK][2];
+    const int r0 = 8 * (q >> 1) + (sub >> 2);
+    const char *ra[FN], *rb[FK];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int r = 8 * (q >> 1) + 4 * t + (sub >> 2);
+    for (int i = 0; i < FN; ++i)
+        ra[i] = lds + place(UN, r0, (wn * FN + i) * 2 + (q & 1), (sub >> 1) & 1) + (sub & 1) * 8;
 #pragma unroll
-        for (int i = 0; i < FN; ++i) {
-            const int u = wn * FN * 2 + i * 2 + (q & 1);
-            ra[i][t] = (r * UN + (u ^ (r & (UN - 1)))) * 32 + (sub & 3) * 8;
-        }
-#pragma unroll
-        for (int j = 0; j < FK; ++j) {
-            const int u = wk * FK * 2 + j * 2 + (q & 1);
-            rb[j][t] = kDyBytes + (r * UK + (u ^ (r & (UK - 1)))) * 32 + (sub & 3) * 8;
-        }
-    }
-    auto read = [&](const char *p, int a, int b) {
+    for (int j = 0; j < FK; ++j)
+        rb[j] = lds + 2 * kDyBytes +
+                place(UK, r0, (wk * FK + j) * 2 + (q & 1), (sub >> 1) & 1) + (sub & 1) * 8;
+    struct Operands { s16x4 a[FN][2], b[FK][2]; };
+    constexpr int kReads = 2 * (FN + FK);
+    auto read = [&](Operands &o, int buf, int step, int t) {
         typedef __attribute__((address_space(3))) s16x4 *P;
-        const s16x4 l = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(p + a));
-        const s16x4 h = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(p + b));
-        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(l, h, 0, 1, 2, 3, 4, 5, 6, 7));
-    };
-    auto products = [&](int st) {
-        const char *base = lds + (st & 1) * kStage;
-#pragma unroll
-        for (int ks = 0; ks < ROWS / 16; ++ks) {
-            bf16x8 a[FN], b[FK];
-#pragma unroll
-            for (int j = 0; j < FK; ++j)
-                b[j] = read(base + ks * 16 * BK * 2, rb[j][0], rb[j][1]);
-#pragma unroll
-            for (int i = 0; i < FN; ++i)
-                a[i] = read(base + ks * 16 * BN * 2, ra[i][0], ra[i][1]);
-#pragma unroll
-            for (int i = 0; i < FN; ++i)
-#pragma unroll
-                for (int j = 0; j < FK; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+        // x's fragments first, every dy fragment meets them
+        if (t < 2 * FK) {
+            const int off = buf * kXBytes + (step * kStep + t % 2 * 4) * BK * 2;
+            o.b[t / 2][t % 2] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(rb[t / 2] + off));
+        } else {
+            const int i = t / 2 - FK, off = buf * kDyBytes + (step * kStep + t % 2 * 4) * BN * 2;
+            o.a[i][t % 2] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(ra[i] + off));
         }
     };
+    auto joined = [](const s16x4 (&v)[2]) {
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    // The products of one step, with `tasks` calls of work(t) spread between
+    // them: a wave issues in order, and what stands between matrix instructions
+    // runs beside them.
+    auto products = [&](const Operands &o, auto tasks, auto work) {
+        constexpr int kTasks = decltype(tasks)::value, kAll = FN * FK;
+        int done = 0;
+#pragma unroll
+        for (int p = 0; p < kAll; ++p) {
+            const int i = p / FK, j = p % FK;
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(joined(o.a[i]), joined(o.b[j]),
+                                                                acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (; done < kTasks && done * kAll < (p + 1) * kTasks; ++done) work(done);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    constexpr int kPutsX = kUnitsX, kPutsDy = kUnitsDy;
+    typedef std::integral_constant<int, kReads> Reads;
+    typedef std::integral_constant<int, kReads + kPutsX> ReadsAndX;
+    typedef std::integral_constant<int, kReads + kPutsDy> ReadsAndDy;
+    Operands o0, o1;
+    auto stage = [&](int st, auto buffer) {
+        constexpr int buf = decltype(buffer)::value, other = 1 - buf;
+        products(o0, Reads{}, [&](int t) { read(o1, buf, 1, t); });
+        products(o1, ReadsAndX{}, [&](int t) {
+            if (t < kReads) {
+                read(o0, buf, 2, t);
+            } else {
+                put_x(other, t - kReads);
+                fetch_x(st + 2, t - kReads);
+            }
+        });
+        products(o0, ReadsAndDy{}, [&](int t) {
+            if (t < kReads) {
+                read(o1, buf, 3, t);
+            } else {
+                put_dy(st + 1, other, t - kReads);
+                fetch_dy(st + 2, t - kReads);
+            }
+        });
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        products(o1, ReadsAndX{}, [&](int t) {
+            if (t < kReads) read(o0, other, 0, t);
+            else fetch_index(st + 3, t - kReads);
+        });
+    };
+    typedef std::integral_constant<int, 0> Even;
+    typedef std::integral_constant<int, 1> Odd;
 
     // ---- stages ----
     if (steps > 0) {
-        fetch_index(0);
-        fetch_x(0);
-        fetch_dy(0);
-        fetch_index(1);
-        put_x(0);
-        put_dy(0);
-        fetch_x(1);
-        fetch_dy(1);
-        fetch_index(2);
-        for (int st = 0; st < steps; ++st) {
-            // this stage has been put down, and the other buffer is read
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            __builtin_amdgcn_s_barrier();
-            // (past the last stage: rows read again, put where nobody reads)
-            put_x(st + 1);
-            put_dy(st + 1);
-            fetch_x(st + 2);
-            fetch_dy(st + 2);
-            fetch_index(st + 3);
-            products(st);
+#pragma unroll
+        for (int c = 0; c < kUnitsX; ++c) fetch_index(0, c);
+#pragma unroll
+        for (int c = 0; c < kUnitsDy; ++c) fetch_dy(0, c);
+#pragma unroll
+        for (int c = 0; c < kUnitsX; ++c) {
+            fetch_x(0, c);
+            fetch_index(1, c);
+        }
+#pragma unroll
+        for (int c = 0; c < kUnitsDy; ++c) {
+            put_dy(0, 0, c);
+            fetch_dy(1, c);
+        }
+#pragma unroll
+        for (int c = 0; c < kUnitsX; ++c) {
+            put_x(0, c);
+            fetch_x(1, c);
+            fetch_index(2, c);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+#pragma unroll
+        for (int t = 0; t < kReads; ++t) read(o0, 0, 0, t);
+        for (int st = 0; st < steps; st += 2) {
+            stage(st, Even{});
+            if (st + 1 < steps) stage(st + 1, Odd{});
         }
     }
 
     // ---- results: lane l holds column l mod 32, rows 8 (r / 4) + 4 (l / 32) +
-    // r mod 4 of each fragment ----
-    float *out = g.out + grp * g.out_stride;
+    // r mod 4 of each fragment: whole lines of 128 bytes per store ----
+    const int nb = n0 + wn * FN * 32 + 4 * (lane >> 5), kb = k0 + wk * FK * 32 + (lane & 31);
+    float *const out = g.out + grp * g.out_stride + nb * g.ldo + kb;
+    auto results = [&](auto inside, auto add) {
+        constexpr bool kInside = decltype(inside)::value, kAdd = decltype(add)::value;
 #pragma unroll
-    for (int i = 0; i < FN; ++i)
+        for (int i = 0; i < FN; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int n = n0 + (wn * FN + i) * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
-            if (n >= g.N) continue;
+            for (int h = 0; h < 16; h += 8) {
+                auto each = [&](auto f) {
 #pragma unroll
-            for (int j = 0; j < FK; ++j) {
-                const int k = k0 + (wk * FK + j) * 32 + (lane & 31);
-                if (k >= g.K) continue;
-                float *p = out + n * g.ldo + k;
-                *p = g.accumulate ? *p + acc[i][j][r] : acc[i][j][r];
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = h + e, n = i * 32 + 8 * (r / 4) + r % 4;
+#pragma unroll
+                        for (int j = 0; j < FK; ++j)
+                            if (kInside || (nb + n < g.N && kb + j * 32 < g.K))
+                                f(out + n * g.ldo + j * 32, e, j, acc[i][j][r]);
+                    }
+                };
+                float old[8][FK];
+                if (kAdd) each([&](float *p, int e, int j, float) { old[e][j] = *p; });
+                each([&](float *p, int e, int j, float v) { *p = kAdd ? old[e][j] + v : v; });
             }
-        }
+    };
+    typedef std::true_type Yes;
+    typedef std::false_type No;
+    if (n0 + BN <= g.N && k0 + BK <= g.K) {
+        if (g.accumulate) results(Yes{}, Yes{});
+        else results(Yes{}, No{});
+    } else {
+        if (g.accumulate) results(No{}, Yes{});
+        else results(No{}, No{});
+    }
 }
 
 constexpr int64_t kLaunchThreads = 0xFFFFFFFFll;
 
-template <int FN, int FK, int WN, int WK, int ROWS, bool WHOLE, bool PACKED>
+template <int FN, int FK, int WN, int WK, bool WHOLE, bool PACKED>
 hipError_t wgrad_as(const WgradArgs &g, hipStream_t s, bool &too_large) {
     constexpr int BN = WN * FN * 32, BK = WK * FK * 32, kThreads = WN * WK * 64;
-    constexpr int kLds = 2 * ROWS * (BN + BK) * 2;
+    constexpr int kLds = 2 * kRows * (BN + BK) * 2;
     const int64_t tn = (g.N + BN - 1) / BN, tk = (g.K + BK - 1) / BK;
     too_large = tn * tk * g.G > kLaunchThreads / kThreads;
     if (too_large) return hipSuccess;
-    const auto kernel = k_wgrad<FN, FK, WN, WK, ROWS, WHOLE, PACKED>;
+    const auto kernel = k_wgrad<FN, FK, WN, WK, WHOLE, PACKED>;
     if (kLds > 65536) {
         const hipError_t he = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                                   hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
@@ -316,14 +384,14 @@ hipError_t wgrad_as(const WgradArgs &g, hipStream_t s, bool &too_large) {
     return hipGetLastError();
 }
 
-template <int FN, int FK, int WN, int WK, int ROWS>
+template <int FN, int FK, int WN, int WK>
 hipError_t wgrad_any(const WgradArgs &g, hipStream_t s, bool &too_large) {
     const bool whole = g.vec_dy && g.N % 8 == 0 && (g.x_scale || (g.vec_x && g.K % 8 == 0));
     if (g.x_scale)
-        return whole ? wgrad_as<FN, FK, WN, WK, ROWS, true, true>(g, s, too_large)
-                     : wgrad_as<FN, FK, WN, WK, ROWS, false, true>(g, s, too_large);
-    return whole ? wgrad_as<FN, FK, WN, WK, ROWS, true, false>(g, s, too_large)
-                 : wgrad_as<FN, FK, WN, WK, ROWS, false, false>(g, s, too_large);
+        return whole ? wgrad_as<FN, FK, WN, WK, true, true>(g, s, too_large)
+                     : wgrad_as<FN, FK, WN, WK, false, true>(g, s, too_large);
+    return whole ? wgrad_as<FN, FK, WN, WK, true, false>(g, s, too_large)
+                 : wgrad_as<FN, FK, WN, WK, false, false>(g, s, too_large);
 }
 
 }  // namespace
@@ -334,8 +402,8 @@ hipError_t launch_wgrad(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_
     too_large = false;
     if (g.N == 0 || g.K == 0 || g.G == 0) return hipSuccess;
     const int64_t large = static_cast<int64_t>((g.N + 255) / 256) * ((g.K + 255) / 256) * g.G;
-    if (large >= c.num_cu) return wgrad_any<4, 2, 2, 4, 32>(g, s, too_large);
-    return wgrad_any<2, 2, 2, 2, 32>(g, s, too_large);
+    if (large >= c.num_cu) return wgrad_any<4, 2, 2, 4>(g, s, too_large);
+    return wgrad_any<2, 2, 2, 2>(g, s, too_large);
 }
 
 }  // namespace ue
