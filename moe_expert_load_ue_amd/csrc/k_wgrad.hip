@@ -30,31 +30,12 @@ constexpr int kUnit = 16;                // columns of a unit: 32 bytes in LDS
 // Sixteen columns of a row as bf16.
 struct Unit { u32x4 lo, hi; };
 
-// Four int8 times a power of two as bf16: the product's low half is zero.
-__device__ __forceinline__ void widen_packed(uint32_t v, float step, uint32_t &a, uint32_t &b) {
+// The two low int8 of v times a power of two as bf16: the products' low halves
+// are zero.
+__device__ __forceinline__ uint32_t widen_pair(uint32_t v, float step) {
     const float f0 = static_cast<float>(static_cast<int8_t>(v)) * step;
     const float f1 = static_cast<float>(static_cast<int8_t>(v >> 8)) * step;
-    const float f2 = static_cast<float>(static_cast<int8_t>(v >> 16)) * step;
-    const float f3 = static_cast<float>(static_cast<int8_t>(v >> 24)) * step;
-    a = __builtin_amdgcn_perm(__float_as_uint(f1), __float_as_uint(f0), 0x07060302u);
-    b = __builtin_amdgcn_perm(__float_as_uint(f3), __float_as_uint(f2), 0x07060302u);
-}
-__device__ __forceinline__ Unit widen_unit(u32x4 q, float step) {
-    Unit u;
-    uint32_t a, b;
-    widen_packed(q[0], step, a, b);
-    u.lo[0] = a;
-    u.lo[1] = b;
-    widen_packed(q[1], step, a, b);
-    u.lo[2] = a;
-    u.lo[3] = b;
-    widen_packed(q[2], step, a, b);
-    u.hi[0] = a;
-    u.hi[1] = b;
-    widen_packed(q[3], step, a, b);
-    u.hi[2] = a;
-    u.hi[3] = b;
-    return u;
+    return __builtin_amdgcn_perm(__float_as_uint(f1), __float_as_uint(f0), 0x07060302u);
 }
 
 // The first `n` of 16 bf16 at p (zeros past them); whole pieces by 16-byte loads
@@ -88,7 +69,7 @@ __device__ __forceinline__ Unit load_unit(const uint16_t *p, int n) {
 // LDS: one barrier there.
 constexpr int kStep = 16, kSteps = 4, kRows = kStep * kSteps;
 
-template <int FN, int FK, int WN, int WK, bool WHOLE, bool PACKED>
+template <int FN, int FK, int WN, int WK, bool WHOLE, bool PACKED, bool INDEXED>
 __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
     WgradArgs g, FastDiv div, int tiles_n, int tiles_k) {
     constexpr int kThreads = WN * WK * 64;
@@ -171,21 +152,22 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
     const int x_row = tid / UK, x_k = k0 + tid % UK * kUnit;
     const int x_at = x_k < g.K ? x_k : 0;
     const int x_up = x_k + 8 < g.K ? 8 : 0;
-    int index[kUnitsX];
+    int index[kUnitsX] = {};
     auto fetch_index = [&](int st, int c) {
         const int m0 = first_of(st), left = hi - m0;
         int r = c * kGapX + x_row;
         if (left < kRows) r = r < left ? r : left - 1;
-        index[c] = g.index ? (g.index + m0)[r] : m0 + r;
+        if constexpr (INDEXED) index[c] = (g.index + m0)[r];
     };
     struct Raw { u32x4 q; uint32_t s; };
     Raw xq[PACKED ? kUnitsX : 1];
     Unit xu[PACKED ? 1 : kUnitsX];
     bool live[kUnitsX];
     auto fetch_x = [&](int st, int c) {
-        const uint32_t r = div_by(index[c], div);
-        live[c] = index[c] >= 0 && r < static_cast<uint32_t>(g.x_rows) &&
-                  lo + st * kRows + c * kGapX + x_row < hi;
+        const int m = lo + st * kRows + c * kGapX + x_row;
+        const int i = INDEXED ? index[c] : m;
+        const uint32_t r = INDEXED ? div_by(i, div) : i;
+        live[c] = i >= 0 && r < static_cast<uint32_t>(g.x_rows) && m < hi;
         const uint64_t row = live[c] ? r : 0;
         if constexpr (PACKED) {
             // (rows are readable up to a multiple of 16)
@@ -202,11 +184,24 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
             }
         }
     };
+    // A unit is made ready in kParts parts: two columns each, or at once.
+    constexpr int kParts = 8;
+    Unit ready;
+    auto ready_x = [&](int c, int part) {
+        uint32_t v;
+        if constexpr (PACKED) {
+            // (or the compiler takes bytes out of a load as soon as it is issued)
+            if (part == 0) asm volatile("" : "+v"(xq[c].q), "+v"(xq[c].s));
+            const float step = live[c] ? scale_step(xq[c].s) : 0.f;
+            v = widen_pair(xq[c].q[part / 2] >> (16 * (part & 1)), step);
+        } else {
+            v = live[c] ? (part < 4 ? xu[c].lo[part & 3] : xu[c].hi[part & 3]) : 0u;
+        }
+        if (part < 4) ready.lo[part & 3] = v;
+        else ready.hi[part & 3] = v;
+    };
     auto put_x = [&](int buf, int c) {
-        Unit u;
-        if constexpr (PACKED) u = widen_unit(xq[c].q, live[c] ? scale_step(xq[c].s) : 0.f);
-        else u = live[c] ? xu[c] : Unit{};
-        put(lds + 2 * kDyBytes + buf * kXBytes, UK, c * kGapX + x_row, tid % UK, u);
+        put(lds + 2 * kDyBytes + buf * kXBytes, UK, c * kGapX + x_row, tid % UK, ready);
     };
 
     // ---- products ----
@@ -244,54 +239,64 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
     auto joined = [](const s16x4 (&v)[2]) {
         return __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
     };
-    // The products of one step, with `tasks` calls of work(t) spread between
-    // them: a wave issues in order, and what stands between matrix instructions
-    // runs beside them.
-    auto products = [&](const Operands &o, auto tasks, auto work) {
-        constexpr int kTasks = decltype(tasks)::value, kAll = FN * FK;
-        int done = 0;
+    // The products of one step: work(p) stands behind the p-th matrix
+    // instruction. A wave issues in order, and what stands between matrix
+    // instructions runs beside them.
+    constexpr int kAll = FN * FK;
+    auto products = [&](const Operands &o, auto work) {
 #pragma unroll
         for (int p = 0; p < kAll; ++p) {
             const int i = p / FK, j = p % FK;
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(joined(o.a[i]), joined(o.b[j]),
                                                                 acc[i][j], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (; done < kTasks && done * kAll < (p + 1) * kTasks; ++done) work(done);
+            work(p);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    constexpr int kPutsX = kUnitsX, kPutsDy = kUnitsDy;
-    typedef std::integral_constant<int, kReads> Reads;
-    typedef std::integral_constant<int, kReads + kPutsX> ReadsAndX;
-    typedef std::integral_constant<int, kReads + kPutsDy> ReadsAndDy;
+    // the p-th share of a step's operand reads
+    auto reads = [&](Operands &o, int buf, int step, int p) {
+#pragma unroll
+        for (int t = p * kReads / kAll; t < (p + 1) * kReads / kAll; ++t) read(o, buf, step, t);
+    };
     Operands o0, o1;
     auto stage = [&](int st, auto buffer) {
         constexpr int buf = decltype(buffer)::value, other = 1 - buf;
-        products(o0, Reads{}, [&](int t) { read(o1, buf, 1, t); });
-        products(o1, ReadsAndX{}, [&](int t) {
-            if (t < kReads) {
-                read(o0, buf, 2, t);
-            } else {
-                put_x(other, t - kReads);
-                fetch_x(st + 2, t - kReads);
+        // units of x that are made ready behind the instructions of step n
+        auto x_step = [&](int n, int p) {
+#pragma unroll
+            for (int c = n; c < kUnitsX; c += 2) {
+#pragma unroll
+                for (int part = p * kParts / kAll; part < (p + 1) * kParts / kAll; ++part)
+                    ready_x(c, part);
+                if (p + 1 == kAll) {
+                    put_x(other, c);
+                    fetch_x(st + 2, c);
+                    fetch_index(st + 3, c);
+                }
             }
+        };
+        products(o0, [&](int p) {
+            reads(o1, buf, 1, p);
+            x_step(0, p);
         });
-        products(o0, ReadsAndDy{}, [&](int t) {
-            if (t < kReads) {
-                read(o1, buf, 3, t);
-            } else {
-                put_dy(st + 1, other, t - kReads);
-                fetch_dy(st + 2, t - kReads);
+        products(o1, [&](int p) {
+            reads(o0, buf, 2, p);
+            x_step(1, p);
+        });
+        products(o0, [&](int p) {
+            reads(o1, buf, 3, p);
+#pragma unroll
+            for (int c = p * kUnitsDy / kAll; c < (p + 1) * kUnitsDy / kAll; ++c) {
+                put_dy(st + 1, other, c);
+                fetch_dy(st + 2, c);
             }
         });
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
-        products(o1, ReadsAndX{}, [&](int t) {
-            if (t < kReads) read(o0, other, 0, t);
-            else fetch_index(st + 3, t - kReads);
-        });
+        products(o1, [&](int p) { reads(o0, other, 0, p); });
     };
+    static_assert(kUnitsX <= 2, "a unit a step");
     typedef std::integral_constant<int, 0> Even;
     typedef std::integral_constant<int, 1> Odd;
 
@@ -313,6 +318,8 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
         }
 #pragma unroll
         for (int c = 0; c < kUnitsX; ++c) {
+#pragma unroll
+            for (int part = 0; part < kParts; ++part) ready_x(c, part);
             put_x(0, c);
             fetch_x(1, c);
             fetch_index(2, c);
@@ -365,33 +372,39 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
 
 constexpr int64_t kLaunchThreads = 0xFFFFFFFFll;
 
-template <int FN, int FK, int WN, int WK, bool WHOLE, bool PACKED>
+template <int FN, int FK, int WN, int WK, bool WHOLE, bool PACKED, bool INDEXED>
 hipError_t wgrad_as(const WgradArgs &g, hipStream_t s, bool &too_large) {
     constexpr int BN = WN * FN * 32, BK = WK * FK * 32, kThreads = WN * WK * 64;
     constexpr int kLds = 2 * kRows * (BN + BK) * 2;
     const int64_t tn = (g.N + BN - 1) / BN, tk = (g.K + BK - 1) / BK;
     too_large = tn * tk * g.G > kLaunchThreads / kThreads;
     if (too_large) return hipSuccess;
-    const auto kernel = k_wgrad<FN, FK, WN, WK, WHOLE, PACKED>;
+    const auto kernel = k_wgrad<FN, FK, WN, WK, WHOLE, PACKED, INDEXED>;
     if (kLds > 65536) {
         const hipError_t he = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                                   hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
         if (he != hipSuccess) return he;
     }
     hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(tn * tk * g.G)), dim3(kThreads), kLds,
-                       s, g, fast_div(g.index ? g.index_div : 1), static_cast<int>(tn),
+                       s, g, fast_div(INDEXED ? g.index_div : 1), static_cast<int>(tn),
                        static_cast<int>(tk));
     return hipGetLastError();
+}
+
+template <int FN, int FK, int WN, int WK, bool WHOLE, bool PACKED>
+hipError_t wgrad_rows(const WgradArgs &g, hipStream_t s, bool &too_large) {
+    return g.index ? wgrad_as<FN, FK, WN, WK, WHOLE, PACKED, true>(g, s, too_large)
+                   : wgrad_as<FN, FK, WN, WK, WHOLE, PACKED, false>(g, s, too_large);
 }
 
 template <int FN, int FK, int WN, int WK>
 hipError_t wgrad_any(const WgradArgs &g, hipStream_t s, bool &too_large) {
     const bool whole = g.vec_dy && g.N % 8 == 0 && (g.x_scale || (g.vec_x && g.K % 8 == 0));
     if (g.x_scale)
-        return whole ? wgrad_as<FN, FK, WN, WK, true, true>(g, s, too_large)
-                     : wgrad_as<FN, FK, WN, WK, false, true>(g, s, too_large);
-    return whole ? wgrad_as<FN, FK, WN, WK, true, false>(g, s, too_large)
-                 : wgrad_as<FN, FK, WN, WK, false, false>(g, s, too_large);
+        return whole ? wgrad_rows<FN, FK, WN, WK, true, true>(g, s, too_large)
+                     : wgrad_rows<FN, FK, WN, WK, false, true>(g, s, too_large);
+    return whole ? wgrad_rows<FN, FK, WN, WK, true, false>(g, s, too_large)
+                 : wgrad_rows<FN, FK, WN, WK, false, false>(g, s, too_large);
 }
 
 }  // namespace
