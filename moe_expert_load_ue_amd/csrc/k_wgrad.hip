@@ -74,7 +74,7 @@ __device__ __forceinline__ Unit load_unit(const uint16_t *p, int n) {
 // the step before, and the next stage is put down during the first three. So by
 // the end of the third step this stage has been read and the next one is in
 // LDS: one barrier there.
-constexpr int kStep = 16, kSteps = 4, kRows = kStep * kSteps;
+constexpr int kStep = 16;
 
 // A stage of a tile: rows m0 .. of the group, `left` of them in the group still
 // (0: none, for a group without rows, or behind the last tile).
@@ -83,15 +83,17 @@ struct Stage {
     bool real;
 };
 
-template <int FN, int FK, int WN, int WK, bool WHOLE, bool PACKED, bool INDEXED>
+template <int FN, int FK, int WN, int WK, int STEPS, bool WHOLE, bool PACKED, bool INDEXED>
 __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
     WgradArgs g, FastDiv div, int tiles_n, int tiles_k) {
-    constexpr int kThreads = WN * WK * 64;
+    constexpr int kThreads = WN * WK * 64, kRows = STEPS * kStep;
     constexpr int BN = WN * FN * 32, BK = WK * FK * 32;
     constexpr int UN = BN / kUnit, UK = BK / kUnit;          // units of a row
     constexpr int kDyBytes = kRows * BN * 2, kXBytes = kRows * BK * 2;
     constexpr int kGapX = kThreads / UK, kGapDy = kThreads / UN;
-    static_assert(kGapX * 2 == kRows && kGapDy * 2 == kRows, "two units per thread, of rows kGap apart");
+    // units of a thread, of rows kGap apart
+    constexpr int kUnitsX = kRows / kGapX, kUnitsDy = kRows / kGapDy;
+    static_assert(kUnitsX >= 1 && kUnitsX <= 2 && kUnitsDy >= 1 && kUnitsDy <= 2);
     static_assert((UN == 8 || UN == 16) && (UK == 8 || UK == 16));
     // both stages of dy, then both of x
     extern __shared__ __align__(16) char lds[];
@@ -101,19 +103,26 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
     // ---- the stream of stages: tiles in launch order, those of a group side by
     // side along n first, so that an XCD (every eighth workgroup) keeps to some
     // columns of dy and every XCD has a share of every group ----
-    const int per = tiles_n * tiles_k, total = per * g.G;
+    const int per = tiles_n * tiles_k, total = per * g.G * g.parts;
     auto begin_tile = [&](int id) {
         Stage s;
         s.grp = id / per;
         const int in = id - s.grp * per;
         s.n0 = in % tiles_n * BN;
         s.k0 = in / tiles_n * BK;
+        const int part = s.grp / g.G, grp = s.grp - part * g.G;
         int lo = 0, hi = g.M;
         if (g.offsets) {
-            lo = g.offsets[s.grp];
-            hi = g.offsets[s.grp + 1];
+            lo = g.offsets[grp];
+            hi = g.offsets[grp + 1];
             lo = lo < 0 ? 0 : lo > g.M ? g.M : lo;
             hi = hi < lo ? lo : hi > g.M ? g.M : hi;
+        }
+        if (g.parts > 1) {
+            // whole stages, but for the group's end
+            const int len = ((hi - lo) / g.parts + kRows) / kRows * kRows;
+            lo = (hi - lo) / len >= part ? lo + part * len : hi;
+            hi = hi - lo > len ? lo + len : hi;
         }
         s.left = __builtin_amdgcn_readfirstlane(hi - lo);
         // (rows that are not there are read as some other row)
@@ -145,7 +154,7 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
     // are read as others (results of columns that nobody stores) ----
     const int dy_row = tid / UN, dy_col = tid % UN * kUnit;
     const int x_row = tid / UK, x_col = tid % UK * kUnit;
-    Unit dyr[2];
+    Unit dyr[kUnitsDy];
     auto fetch_dy = [&](const Stage &s, int c, int half) {
         const char *base = reinterpret_cast<const char *>(g.dy + s.m0 * g.lddy);
         const uint32_t at = row_in(s, c * kGapDy + dy_row) * static_cast<uint32_t>(g.lddy * 2);
@@ -159,15 +168,15 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
             dyr[c] = load_unit(reinterpret_cast<const uint16_t *>(base + at) + n, g.N - n);
         }
     };
-    int index[2] = {};
+    int index[kUnitsX] = {};
     auto fetch_index = [&](const Stage &s, int c) {
         if constexpr (INDEXED) index[c] = (g.index + s.m0)[row_in(s, c * kGapX + x_row)];
     };
     struct Raw { u32x4 q; uint32_t s; };
-    Raw xq[PACKED ? 2 : 1];
-    Unit xu[PACKED ? 1 : 2];
-    bool live[2];
-    uint32_t x_of[2];
+    Raw xq[PACKED ? kUnitsX : 1];
+    Unit xu[PACKED ? 1 : kUnitsX];
+    bool live[kUnitsX];
+    uint32_t x_of[kUnitsX];
     auto fetch_x = [&](const Stage &s, int c, int half) {
         if (half == 0) {
             const int r = c * kGapX + x_row, i = INDEXED ? index[c] : s.m0 + r;
@@ -295,8 +304,9 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
     // its registers filled again, a load or a store at a time. Loads are waited
     // for in their order, so each is used after about as many others.
     auto at_place = [&](int at) {
+        constexpr int x1 = kUnitsX - 1, dy1 = kUnitsDy - 1;
         if (at < kParts) ready_x(0, at);
-        else if (at < 2 * kParts) ready_x(1, at - kParts);
+        else if (kUnitsX > 1 && at < 2 * kParts) ready_x(x1, at - kParts);
         switch (at) {
             case 1: put_dy(put_of, 0, 0); break;
             case 2: fetch_dy(fetch_of, 0, 0); break;
@@ -305,19 +315,26 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
             case 6: fetch_dy(fetch_of, 0, 1); break;
             case 7: put_x(0, 1); break;
             case 8: fetch_x(fetch_of, 0, 0); break;
-            case 9: put_dy(put_of, 1, 0); fetch_x(fetch_of, 0, 1); fetch_index(index_of, 0); break;
-            case 10: fetch_dy(fetch_of, 1, 0); break;
-            case 12: put_x(1, 0); break;
-            case 13: put_dy(put_of, 1, 1); break;
-            case 14: fetch_dy(fetch_of, 1, 1); break;
-            case 15: put_x(1, 1); break;
-            case 16: fetch_x(fetch_of, 1, 0); break;
-            case 17: fetch_x(fetch_of, 1, 1); fetch_index(index_of, 1); break;
+            case 9: fetch_x(fetch_of, 0, 1); fetch_index(index_of, 0); break;
+            default: break;
+        }
+        if (kUnitsDy > 1) switch (at) {
+            case 9: put_dy(put_of, dy1, 0); break;
+            case 10: fetch_dy(fetch_of, dy1, 0); break;
+            case 13: put_dy(put_of, dy1, 1); break;
+            case 14: fetch_dy(fetch_of, dy1, 1); break;
+            default: break;
+        }
+        if (kUnitsX > 1) switch (at) {
+            case 12: put_x(x1, 0); break;
+            case 15: put_x(x1, 1); break;
+            case 16: fetch_x(fetch_of, x1, 0); break;
+            case 17: fetch_x(fetch_of, x1, 1); fetch_index(index_of, x1); break;
             default: break;
         }
     };
-    constexpr int kEach = 32 / (kSteps * kAll);
-    static_assert(kEach * kSteps * kAll == 32);
+    constexpr int kEach = 32 / (STEPS * kAll);
+    static_assert(kEach * STEPS * kAll == 32 && (STEPS == 2 || STEPS == 4));
     // The products of one step on `use`, while the operands of `step` are read
     // into `load`. A wave issues in order, and what stands between matrix
     // instructions runs beside them.
@@ -396,20 +413,20 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
     index_of = fetch_of;
     next_stage(index_of);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) fetch_index(now, c);
+    for (int c = 0; c < kUnitsX; ++c) fetch_index(now, c);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) fetch_dy(now, c / 2, c % 2);
+    for (int c = 0; c < 2 * kUnitsDy; ++c) fetch_dy(now, c / 2, c % 2);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) fetch_x(now, c / 2, c % 2);
+    for (int c = 0; c < 2 * kUnitsX; ++c) fetch_x(now, c / 2, c % 2);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) fetch_index(put_of, c);
+    for (int c = 0; c < kUnitsX; ++c) fetch_index(put_of, c);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < 2 * kUnitsDy; ++c) {
         put_dy(now, c / 2, c % 2);
         fetch_dy(put_of, c / 2, c % 2);
     }
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < kUnitsX; ++c) {
 #pragma unroll
         for (int part = 0; part < kParts; ++part) ready_x(c, part);
         put_x(c, 0);
@@ -431,8 +448,10 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
 
     while (now.real) {
         products(0, o0, o1, 1);
-        products(1, o1, o0, 2);
-        products(2, o0, o1, 3);
+        if constexpr (STEPS == 4) {
+            products(1, o1, o0, 2);
+            products(2, o0, o1, 3);
+        }
         // this stage has been read by every wave, the next one been put down
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
@@ -440,7 +459,7 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
         delta_dy = -delta_dy;
         delta_x = -delta_x;
         flip_puts();
-        products(3, o1, o0, 0);
+        products(STEPS - 1, o1, o0, 0);
         if (now.left <= kRows) {
             results(now);
             clear();
@@ -452,6 +471,22 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
     }
 }
 
+// ---- which tile ----
+enum WgradTile { kTile256, kTile256x128, kTile128 };
+
+int64_t tiles_of(int N, int K, int bn, int bk) {
+    return static_cast<int64_t>((N + bn - 1) / bn) * ((K + bk - 1) / bk);
+}
+constexpr int kPartRows = 256, kMaxParts = 64;
+
+WgradTile wgrad_tile(int M, int N, int K, int64_t G, int num_cu) {
+#ifdef FORCE_TILE
+    return FORCE_TILE;
+#endif
+    if (tiles_of(N, K, 256, 256) * G >= num_cu) return kTile256;
+    return kTile128;
+}
+
 // Matrices of groups without any rows at all.
 __global__ __launch_bounds__(kBlock) void k_wgrad_zero(WgradArgs g) {
     const int64_t rows = static_cast<int64_t>(g.G) * g.N;
@@ -461,16 +496,30 @@ __global__ __launch_bounds__(kBlock) void k_wgrad_zero(WgradArgs g) {
     }
 }
 
-template <int FN, int FK, int WN, int WK, bool WHOLE, bool PACKED, bool INDEXED>
+// The parts of split sums, added in order.
+__global__ __launch_bounds__(kBlock) void k_wgrad_join(WgradArgs g) {
+    const int64_t rows = static_cast<int64_t>(g.G) * g.N, all = rows * g.K;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        float *out = g.out + r / g.N * g.out_stride + r % g.N * g.ldo;
+        const float *part = g.part + r * g.K;
+        for (int k = threadIdx.x; k < g.K; k += kBlock) {
+            float v = g.accumulate ? out[k] : 0.f;
+            for (int p = 0; p < g.parts; ++p) v += part[p * all + k];
+            out[k] = v;
+        }
+    }
+}
+
+template <int FN, int FK, int WN, int WK, int STEPS, bool WHOLE, bool PACKED, bool INDEXED>
 hipError_t wgrad_as(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_large) {
     constexpr int BN = WN * FN * 32, BK = WK * FK * 32, kThreads = WN * WK * 64;
-    constexpr int kLds = 2 * kRows * (BN + BK) * 2;
-    // as many workgroups as fit at once (LDS: one of 128 KB, two of 64)
-    constexpr int kPerCu = kLds > 65536 ? 1 : 2;
-    const int64_t tn = (g.N + BN - 1) / BN, tk = (g.K + BK - 1) / BK, total = tn * tk * g.G;
+    constexpr int kLds = 2 * STEPS * kStep * (BN + BK) * 2;
+    // as many workgroups as fit at once: two waves per SIMD
+    constexpr int kPerCu = 512 / kThreads;
+    const int64_t tn = (g.N + BN - 1) / BN, tk = (g.K + BK - 1) / BK, total = tn * tk * g.G * g.parts;
     too_large = total > 0x7FFFFFFF - kPerCu * c.num_cu;
     if (too_large) return hipSuccess;
-    const auto kernel = k_wgrad<FN, FK, WN, WK, WHOLE, PACKED, INDEXED>;
+    const auto kernel = k_wgrad<FN, FK, WN, WK, STEPS, WHOLE, PACKED, INDEXED>;
     if (kLds > 65536) {
         const hipError_t he = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                                   hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
@@ -483,39 +532,61 @@ hipError_t wgrad_as(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_larg
     return hipGetLastError();
 }
 
-template <int FN, int FK, int WN, int WK, bool WHOLE, bool PACKED>
+template <int FN, int FK, int WN, int WK, int STEPS, bool WHOLE, bool PACKED>
 hipError_t wgrad_rows(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_large) {
-    return g.index ? wgrad_as<FN, FK, WN, WK, WHOLE, PACKED, true>(c, g, s, too_large)
-                   : wgrad_as<FN, FK, WN, WK, WHOLE, PACKED, false>(c, g, s, too_large);
+    return g.index ? wgrad_as<FN, FK, WN, WK, STEPS, WHOLE, PACKED, true>(c, g, s, too_large)
+                   : wgrad_as<FN, FK, WN, WK, STEPS, WHOLE, PACKED, false>(c, g, s, too_large);
 }
 
-template <int FN, int FK, int WN, int WK>
+template <int FN, int FK, int WN, int WK, int STEPS>
 hipError_t wgrad_any(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_large) {
     const bool whole = g.vec_dy && g.N % 8 == 0 && (g.x_scale || (g.vec_x && g.K % 8 == 0));
     if (g.x_scale)
-        return whole ? wgrad_rows<FN, FK, WN, WK, true, true>(c, g, s, too_large)
-                     : wgrad_rows<FN, FK, WN, WK, false, true>(c, g, s, too_large);
-    return whole ? wgrad_rows<FN, FK, WN, WK, true, false>(c, g, s, too_large)
-                 : wgrad_rows<FN, FK, WN, WK, false, false>(c, g, s, too_large);
+        return whole ? wgrad_rows<FN, FK, WN, WK, STEPS, true, true>(c, g, s, too_large)
+                     : wgrad_rows<FN, FK, WN, WK, STEPS, false, true>(c, g, s, too_large);
+    return whole ? wgrad_rows<FN, FK, WN, WK, STEPS, true, false>(c, g, s, too_large)
+                 : wgrad_rows<FN, FK, WN, WK, STEPS, false, false>(c, g, s, too_large);
+}
+
+hipError_t wgrad_tiles(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_large) {
+    switch (wgrad_tile(g.M, g.N, g.K, static_cast<int64_t>(g.G) * g.parts, c.num_cu)) {
+        case kTile256: return wgrad_any<4, 2, 2, 4, 4>(c, g, s, too_large);
+        case kTile256x128: return wgrad_any<4, 2, 2, 2, 2>(c, g, s, too_large);
+        default: return wgrad_any<2, 2, 2, 2, 4>(c, g, s, too_large);
+    }
 }
 
 }  // namespace
 
-int wgrad_parts(int, int, int, int, bool, int) { return 1; }
+int wgrad_parts(int M, int N, int K, int G, bool, int num_cu) {
+    const int64_t tiles = tiles_of(N, K, 128, 128) * G;
+    const int64_t slots = 2 * num_cu, rows = M / G;
+    int64_t parts = slots / tiles;
+    if (parts > rows / kPartRows) parts = rows / kPartRows;
+    if (parts > kMaxParts) parts = kMaxParts;
+    return parts > 1 ? static_cast<int>(parts) : 1;
+}
 
-hipError_t launch_wgrad(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_large) {
+hipError_t launch_wgrad(ue_ctx &c, const WgradArgs &a, hipStream_t s, bool &too_large) {
     too_large = false;
-    if (g.N == 0 || g.K == 0 || g.G == 0) return hipSuccess;
+    if (a.N == 0 || a.K == 0 || a.G == 0) return hipSuccess;
+    WgradArgs g = a;
+    const int64_t rows = static_cast<int64_t>(g.G) * g.N, most = 64 * c.num_cu;
+    const dim3 per_row(static_cast<uint32_t>(rows < most ? rows : most));
     if (g.M == 0) {
         if (g.accumulate) return hipSuccess;
-        const int64_t rows = static_cast<int64_t>(g.G) * g.N, most = 64 * c.num_cu;
-        hipLaunchKernelGGL(k_wgrad_zero, dim3(static_cast<uint32_t>(rows < most ? rows : most)),
-                           dim3(kBlock), 0, s, g);
+        hipLaunchKernelGGL(k_wgrad_zero, per_row, dim3(kBlock), 0, s, g);
         return hipGetLastError();
     }
-    const int64_t large = static_cast<int64_t>((g.N + 255) / 256) * ((g.K + 255) / 256) * g.G;
-    if (large >= c.num_cu) return wgrad_any<4, 2, 2, 4>(c, g, s, too_large);
-    return wgrad_any<2, 2, 2, 2>(c, g, s, too_large);
+    if (g.parts == 1) return wgrad_tiles(c, g, s, too_large);
+    g.out = g.part;
+    g.ldo = g.K;
+    g.out_stride = static_cast<int64_t>(g.N) * g.K;
+    g.accumulate = false;
+    const hipError_t he = wgrad_tiles(c, g, s, too_large);
+    if (he != hipSuccess || too_large) return he;
+    hipLaunchKernelGGL(k_wgrad_join, per_row, dim3(kBlock), 0, s, a);
+    return hipGetLastError();
 }
 
 }  // namespace ue
