@@ -14,6 +14,7 @@
 // different banks.
 #include "ue_train.h"
 
+#include <atomic>
 #include <type_traits>
 
 namespace ue {
@@ -38,25 +39,29 @@ __device__ __forceinline__ uint32_t widen_pair(uint32_t v, float step) {
     return __builtin_amdgcn_perm(__float_as_uint(f1), __float_as_uint(f0), 0x07060302u);
 }
 
-// The first `n` of 16 bf16 at p (zeros past them); whole pieces by 16-byte loads
-// at any 2-byte alignment.
-__device__ __forceinline__ Unit load_unit(const uint16_t *p, int n) {
+// Rows at any 2-byte alignment are read in pieces of eight elements all the
+// same, past their end too (results of columns that nobody stores); but a piece
+// that would pass the end of the whole matrix is read back from that end, and
+// moved to its place when it is put down.
+__device__ __forceinline__ u32x4 load_piece(const void *p) {
     struct __attribute__((packed, aligned(2))) Piece { u32x4 v; };
-    Unit u{};
-    if (n >= 8) u.lo = reinterpret_cast<const Piece *>(p)->v;
-    if (n >= 16) u.hi = reinterpret_cast<const Piece *>(p + 8)->v;
-    if (n > 0 && n < 16 && n != 8) {
-        const int from = n > 8 ? 8 : 0;
-        u32x4 t{};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (from + i < n)
-                t[i / 2] |= static_cast<uint32_t>(p[from + i]) << (16 * (i & 1));
-        if (from) u.hi = t;
-        else u.lo = t;
-    }
-    return u;
+    return static_cast<const Piece *>(p)->v;
 }
+__device__ __forceinline__ u32x4 moved_down(u32x4 v, int elements) {
+    uint64_t lo = static_cast<uint64_t>(v[1]) << 32 | v[0];
+    uint64_t hi = static_cast<uint64_t>(v[3]) << 32 | v[2];
+    const int bits = 16 * elements;
+    if (bits >= 64) {
+        lo = hi >> (bits & 63);
+        hi = 0;
+    } else if (bits > 0) {
+        lo = lo >> bits | hi << (64 - bits);
+        hi >>= bits;
+    }
+    return u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32),
+                 static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)};
+}
+constexpr int kPiece = 8;
 
 // FN, FK: 32-column fragments of dy and of x per wave; WN, WK: waves along each.
 // WHOLE: rows are 16-byte aligned and multiples of 8 columns (packed x always
@@ -74,7 +79,7 @@ __device__ __forceinline__ Unit load_unit(const uint16_t *p, int n) {
 // the step before, and the next stage is put down during the first three. So by
 // the end of the third step this stage has been read and the next one is in
 // LDS: one barrier there.
-constexpr int kStep = 16;
+constexpr int kStep = 16, kSteps = 4, kRows = kStep * kSteps;
 
 // A stage of a tile: rows m0 .. of the group, `left` of them in the group still
 // (0: none, for a group without rows, or behind the last tile).
@@ -83,17 +88,15 @@ struct Stage {
     bool real;
 };
 
-template <int FN, int FK, int WN, int WK, int STEPS, bool WHOLE, bool PACKED, bool INDEXED>
+template <int FN, int FK, int WN, int WK, bool WHOLE, bool PACKED, bool INDEXED>
 __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
     WgradArgs g, FastDiv div, int tiles_n, int tiles_k) {
-    constexpr int kThreads = WN * WK * 64, kRows = STEPS * kStep;
+    constexpr int kThreads = WN * WK * 64;
     constexpr int BN = WN * FN * 32, BK = WK * FK * 32;
     constexpr int UN = BN / kUnit, UK = BK / kUnit;          // units of a row
     constexpr int kDyBytes = kRows * BN * 2, kXBytes = kRows * BK * 2;
     constexpr int kGapX = kThreads / UK, kGapDy = kThreads / UN;
-    // units of a thread, of rows kGap apart
-    constexpr int kUnitsX = kRows / kGapX, kUnitsDy = kRows / kGapDy;
-    static_assert(kUnitsX >= 1 && kUnitsX <= 2 && kUnitsDy >= 1 && kUnitsDy <= 2);
+    static_assert(kGapX * 2 == kRows && kGapDy * 2 == kRows, "two units of a thread, kGap rows apart");
     static_assert((UN == 8 || UN == 16) && (UK == 8 || UK == 16));
     // both stages of dy, then both of x
     extern __shared__ __align__(16) char lds[];
@@ -143,40 +146,49 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
             s.real = false;
         }
     };
+    // Stages: of the products, of what is put down, of units on their way, and
+    // of row numbers.
+    Stage now, put_of, fetch_of, index_of;
     // row r of a stage; past the last one, that one
     auto row_in = [](const Stage &s, int r) {
         return s.left >= kRows ? r : r < s.left ? r : s.left > 0 ? s.left - 1 : 0;
     };
 
     // ---- loads: two units of dy and of x per thread, a half at a time. Rows
-    // that are not the stage's are put down as zeros; whole units are read with
-    // the second half, when the first has been put down too; pieces past the last column
+    // that are not the stage's are put down as zeros; pieces past the last column
     // are read as others (results of columns that nobody stores) ----
     const int dy_row = tid / UN, dy_col = tid % UN * kUnit;
     const int x_row = tid / UK, x_col = tid % UK * kUnit;
-    Unit dyr[kUnitsDy];
+    Unit dyr[2];
     auto fetch_dy = [&](const Stage &s, int c, int half) {
-        const char *base = reinterpret_cast<const char *>(g.dy + s.m0 * g.lddy);
-        const uint32_t at = row_in(s, c * kGapDy + dy_row) * static_cast<uint32_t>(g.lddy * 2);
-        const int n = s.n0 + dy_col;
+        // (a piece before the stage's first row: what is read back from the end
+        // may begin there, and offsets are unsigned)
+        const int64_t first = s.m0 * g.lddy - (WHOLE ? 0 : kPiece);
+        const uint32_t at = row_in(s, c * kGapDy + dy_row) * static_cast<uint32_t>(g.lddy);
+        const int n = s.n0 + dy_col + half * kPiece;
+        uint32_t from = at + (n < g.N ? n : 0);
+        const uint16_t *p = g.dy + first;
+        u32x4 v;
         if constexpr (WHOLE) {
-            const int h = n + half * 8;
-            const u32x4 v = *reinterpret_cast<const u32x4 *>(base + (at + (h < g.N ? h * 2 : 0)));
-            if (half) dyr[c].hi = v;
-            else dyr[c].lo = v;
-        } else if (half) {
-            dyr[c] = load_unit(reinterpret_cast<const uint16_t *>(base + at) + n, g.N - n);
+            v = *reinterpret_cast<const u32x4 *>(p + from);
+        } else {
+            const int64_t last = (g.M - 1) * g.lddy + g.N - kPiece - first;
+            const uint32_t most = last < 0x7FFFFFFF ? static_cast<uint32_t>(last) : 0x7FFFFFFFu;
+            from += kPiece;
+            v = load_piece(p + (from < most ? from : most));
         }
+        if (half) dyr[c].hi = v;
+        else dyr[c].lo = v;
     };
-    int index[kUnitsX] = {};
+    int index[2] = {};
     auto fetch_index = [&](const Stage &s, int c) {
         if constexpr (INDEXED) index[c] = (g.index + s.m0)[row_in(s, c * kGapX + x_row)];
     };
     struct Raw { u32x4 q; uint32_t s; };
-    Raw xq[PACKED ? kUnitsX : 1];
-    Unit xu[PACKED ? 1 : kUnitsX];
-    bool live[kUnitsX];
-    uint32_t x_of[kUnitsX];
+    Raw xq[PACKED ? 2 : 1];
+    Unit xu[PACKED ? 1 : 2];
+    bool live[2];
+    uint32_t x_of[2];
     auto fetch_x = [&](const Stage &s, int c, int half) {
         if (half == 0) {
             const int r = c * kGapX + x_row, i = INDEXED ? index[c] : s.m0 + r;
@@ -194,14 +206,18 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
                 static_cast<const int8_t *>(g.x) + (row * static_cast<uint32_t>(g.ldx) + at));
         } else {
             const uint16_t *p = static_cast<const uint16_t *>(g.x) + row * static_cast<uint32_t>(g.ldx);
+            const int h = k + half * kPiece;
+            u32x4 v;
             if constexpr (WHOLE) {
-                const int h = k + half * 8;
-                const u32x4 v = *reinterpret_cast<const u32x4 *>(p + (h < g.K ? h : 0));
-                if (half) xu[c].hi = v;
-                else xu[c].lo = v;
-            } else if (half) {
-                xu[c] = load_unit(p + k, g.K - k);
+                v = *reinterpret_cast<const u32x4 *>(p + (h < g.K ? h : 0));
+            } else {
+                p += h < g.K ? h : 0;
+                const uint16_t *last = static_cast<const uint16_t *>(g.x) +
+                                       (g.x_rows - 1) * g.ldx + g.K - kPiece;
+                v = load_piece(p < last ? p : last);
             }
+            if (half) xu[c].hi = v;
+            else xu[c].lo = v;
         }
     };
 
@@ -230,6 +246,14 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
     };
     auto put_dy = [&](const Stage &s, int c, int half) {
         u32x4 v = half ? dyr[c].hi : dyr[c].lo;
+        if constexpr (!WHOLE) {
+            if (s.m0 + kRows + kPiece > g.M) {
+                const int n = s.n0 + dy_col + half * kPiece;
+                const int64_t over = (s.m0 + row_in(s, c * kGapDy + dy_row) + 1 - g.M) * g.lddy +
+                                     (n < g.N ? n : 0) + kPiece - g.N;
+                if (over > 0) v = moved_down(v, static_cast<int>(over));
+            }
+        }
         if (s.left < kRows && c * kGapDy + dy_row >= s.left) v = u32x4{};
         put(wd[half] + c * kGapDy * BN * 2, v);
     };
@@ -244,6 +268,18 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
             const float step = live[c] ? scale_step(xq[c].s) : 0.f;
             v = widen_pair(xq[c].q[part / 2] >> (16 * (part & 1)), step);
         } else {
+            if constexpr (!WHOLE) {
+                // (x_of and the stage are still those of this unit)
+                if (part % 4 == 0 && x_of[c] + kPiece >= static_cast<uint32_t>(g.x_rows)) {
+                    const int k = put_of.k0 + x_col + part / 4 * kPiece;
+                    const int64_t over = (static_cast<int64_t>(x_of[c]) + 1 - g.x_rows) * g.ldx +
+                                         (k < g.K ? k : 0) + kPiece - g.K;
+                    if (over > 0) {
+                        u32x4 &u = part ? xu[c].hi : xu[c].lo;
+                        u = moved_down(u, static_cast<int>(over));
+                    }
+                }
+            }
             v = live[c] ? (part < 4 ? xu[c].lo[part & 3] : xu[c].hi[part & 3]) : 0u;
         }
         if (part < 4) ready.lo[part & 3] = v;
@@ -297,16 +333,12 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
 #pragma unroll
         for (int j = 0; j < FK; ++j) rb[j] += delta_x;
     };
-    // Stages: of the products, of what is put down, of units on their way, and
-    // of row numbers.
-    Stage now, put_of, fetch_of, index_of;
     // What stands at 32 places of a stage: a unit is made ready and put down and
     // its registers filled again, a load or a store at a time. Loads are waited
     // for in their order, so each is used after about as many others.
     auto at_place = [&](int at) {
-        constexpr int x1 = kUnitsX - 1, dy1 = kUnitsDy - 1;
         if (at < kParts) ready_x(0, at);
-        else if (kUnitsX > 1 && at < 2 * kParts) ready_x(x1, at - kParts);
+        else if (at < 2 * kParts) ready_x(1, at - kParts);
         switch (at) {
             case 1: put_dy(put_of, 0, 0); break;
             case 2: fetch_dy(fetch_of, 0, 0); break;
@@ -315,26 +347,19 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
             case 6: fetch_dy(fetch_of, 0, 1); break;
             case 7: put_x(0, 1); break;
             case 8: fetch_x(fetch_of, 0, 0); break;
-            case 9: fetch_x(fetch_of, 0, 1); fetch_index(index_of, 0); break;
-            default: break;
-        }
-        if (kUnitsDy > 1) switch (at) {
-            case 9: put_dy(put_of, dy1, 0); break;
-            case 10: fetch_dy(fetch_of, dy1, 0); break;
-            case 13: put_dy(put_of, dy1, 1); break;
-            case 14: fetch_dy(fetch_of, dy1, 1); break;
-            default: break;
-        }
-        if (kUnitsX > 1) switch (at) {
-            case 12: put_x(x1, 0); break;
-            case 15: put_x(x1, 1); break;
-            case 16: fetch_x(fetch_of, x1, 0); break;
-            case 17: fetch_x(fetch_of, x1, 1); fetch_index(index_of, x1); break;
+            case 9: put_dy(put_of, 1, 0); fetch_x(fetch_of, 0, 1); fetch_index(index_of, 0); break;
+            case 10: fetch_dy(fetch_of, 1, 0); break;
+            case 12: put_x(1, 0); break;
+            case 13: put_dy(put_of, 1, 1); break;
+            case 14: fetch_dy(fetch_of, 1, 1); break;
+            case 15: put_x(1, 1); break;
+            case 16: fetch_x(fetch_of, 1, 0); break;
+            case 17: fetch_x(fetch_of, 1, 1); fetch_index(index_of, 1); break;
             default: break;
         }
     };
-    constexpr int kEach = 32 / (STEPS * kAll);
-    static_assert(kEach * STEPS * kAll == 32 && (STEPS == 2 || STEPS == 4));
+    constexpr int kEach = 32 / (kSteps * kAll);
+    static_assert(kEach * kSteps * kAll == 32);
     // The products of one step on `use`, while the operands of `step` are read
     // into `load`. A wave issues in order, and what stands between matrix
     // instructions runs beside them.
@@ -404,40 +429,43 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
         }
     };
 
-    // ---- the first stages ----
-    now = begin_tile(id);
-    put_of = now;
-    next_stage(put_of);
+    // ---- the first stages: the first one is put down, two more are on their
+    // way ----
+    put_of = begin_tile(id);
     fetch_of = put_of;
     next_stage(fetch_of);
     index_of = fetch_of;
     next_stage(index_of);
 #pragma unroll
-    for (int c = 0; c < kUnitsX; ++c) fetch_index(now, c);
+    for (int c = 0; c < 2; ++c) fetch_index(put_of, c);
 #pragma unroll
-    for (int c = 0; c < 2 * kUnitsDy; ++c) fetch_dy(now, c / 2, c % 2);
+    for (int c = 0; c < 4; ++c) fetch_dy(put_of, c / 2, c % 2);
 #pragma unroll
-    for (int c = 0; c < 2 * kUnitsX; ++c) fetch_x(now, c / 2, c % 2);
+    for (int c = 0; c < 4; ++c) fetch_x(put_of, c / 2, c % 2);
 #pragma unroll
-    for (int c = 0; c < kUnitsX; ++c) fetch_index(put_of, c);
+    for (int c = 0; c < 2; ++c) fetch_index(fetch_of, c);
 #pragma unroll
-    for (int c = 0; c < 2 * kUnitsDy; ++c) {
-        put_dy(now, c / 2, c % 2);
-        fetch_dy(put_of, c / 2, c % 2);
+    for (int c = 0; c < 4; ++c) {
+        put_dy(put_of, c / 2, c % 2);
+        fetch_dy(fetch_of, c / 2, c % 2);
     }
 #pragma unroll
-    for (int c = 0; c < kUnitsX; ++c) {
+    for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int part = 0; part < kParts; ++part) ready_x(c, part);
         put_x(c, 0);
         put_x(c, 1);
-        fetch_x(put_of, c, 0);
-        fetch_x(put_of, c, 1);
-        fetch_index(fetch_of, c);
+        fetch_x(fetch_of, c, 0);
+        fetch_x(fetch_of, c, 1);
+        fetch_index(index_of, c);
         // (a byte that is known to be one from here on would be cut to it in the
         // loop, at a place that waits for it too soon)
         if constexpr (PACKED) asm volatile("" : "+v"(xq[c].s));
     }
+    now = put_of;
+    put_of = fetch_of;
+    fetch_of = index_of;
+    next_stage(index_of);
     flip_puts();
     clear();
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -448,10 +476,8 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
 
     while (now.real) {
         products(0, o0, o1, 1);
-        if constexpr (STEPS == 4) {
-            products(1, o1, o0, 2);
-            products(2, o0, o1, 3);
-        }
+        products(1, o1, o0, 2);
+        products(2, o0, o1, 3);
         // this stage has been read by every wave, the next one been put down
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
@@ -459,7 +485,7 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
         delta_dy = -delta_dy;
         delta_x = -delta_x;
         flip_puts();
-        products(STEPS - 1, o1, o0, 0);
+        products(3, o1, o0, 0);
         if (now.left <= kRows) {
             results(now);
             clear();
@@ -471,21 +497,31 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
     }
 }
 
-// ---- which tile ----
-enum WgradTile { kTile256, kTile256x128, kTile128 };
+// Tiles of 256 x 256 on eight waves, one workgroup per CU, or of 128 x 128 on
+// four, two per CU. By what each measured (us, packed x, groups of uneven length;
+// mean rows x N x K):
+//                            256    128
+//    72 of  455x2048x4096     794   1119
+//     5 of 1638x4096x7168     593    682
+//    64 of  256x1024x2048     119    158
+//     8 of  256x1024x2048      22     26
+//     8 of  748x 316x3650      46     57   (240 tiles of 256)
+//     3 of 4000x 760x3640     155    136   (135)
+//     4 of 2048x1024x2048      87     67   (128)
+//     8 of  600x 480x 352      30     23   (32)
+//          32768x 128x 256      50     41   (in parts)
+// So the large ones when they make work for three CUs of four.
+enum WgradTile { kTile256, kTile128 };
 
-int64_t tiles_of(int N, int K, int bn, int bk) {
-    return static_cast<int64_t>((N + bn - 1) / bn) * ((K + bk - 1) / bk);
+int64_t tiles_of(int N, int K, int b) {
+    return static_cast<int64_t>((N + b - 1) / b) * ((K + b - 1) / b);
 }
+WgradTile wgrad_tile(int N, int K, int64_t G, int num_cu) {
+    return tiles_of(N, K, 256) * G >= num_cu * 3 / 4 ? kTile256 : kTile128;
+}
+// A part has at least kPartRows rows (on average), so that what it writes and
+// reads again, 128 KB for a tile of 128, is less than the rows it saves others.
 constexpr int kPartRows = 256, kMaxParts = 64;
-
-WgradTile wgrad_tile(int M, int N, int K, int64_t G, int num_cu) {
-#ifdef FORCE_TILE
-    return FORCE_TILE;
-#endif
-    if (tiles_of(N, K, 256, 256) * G >= num_cu) return kTile256;
-    return kTile128;
-}
 
 // Matrices of groups without any rows at all.
 __global__ __launch_bounds__(kBlock) void k_wgrad_zero(WgradArgs g) {
@@ -493,6 +529,35 @@ __global__ __launch_bounds__(kBlock) void k_wgrad_zero(WgradArgs g) {
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
         float *out = g.out + r / g.N * g.out_stride + r % g.N * g.ldo;
         for (int k = threadIdx.x; k < g.K; k += kBlock) out[k] = 0.f;
+    }
+}
+
+// Matrices too small to be read in pieces: a thread per result.
+__global__ __launch_bounds__(kBlock) void k_wgrad_tiny(WgradArgs g) {
+    const int64_t each = static_cast<int64_t>(g.N) * g.K, all = each * g.G;
+    for (int64_t i = blockIdx.x * kBlock + threadIdx.x; i < all; i += gridDim.x * kBlock) {
+        const int grp = static_cast<int>(i / each), k = static_cast<int>(i % g.K);
+        const int n = static_cast<int>(i / g.K % g.N);
+        int lo = 0, hi = g.M;
+        if (g.offsets) {
+            lo = g.offsets[grp];
+            hi = g.offsets[grp + 1];
+            lo = lo < 0 ? 0 : lo > g.M ? g.M : lo;
+            hi = hi < lo ? lo : hi > g.M ? g.M : hi;
+        }
+        float sum = 0.f;
+        for (int m = lo; m < hi; ++m) {
+            int r = m;
+            if (g.index) r = g.index[m] < 0 ? -1 : g.index[m] / g.index_div;
+            float v = 0.f;
+            if (r >= 0 && r < g.x_rows)
+                v = g.x_scale ? static_cast<float>(static_cast<const int8_t *>(g.x)[r * g.ldx + k]) *
+                                    scale_step(g.x_scale[r * g.lds + k / UE_PACK_BLOCK])
+                              : bf16_to_f32(static_cast<const uint16_t *>(g.x)[r * g.ldx + k]);
+            sum = __builtin_fmaf(bf16_to_f32(g.dy[m * g.lddy + n]), v, sum);
+        }
+        float *p = g.out + grp * g.out_stride + n * g.ldo + k;
+        *p = g.accumulate ? *p + sum : sum;
     }
 }
 
@@ -510,20 +575,28 @@ __global__ __launch_bounds__(kBlock) void k_wgrad_join(WgradArgs g) {
     }
 }
 
-template <int FN, int FK, int WN, int WK, int STEPS, bool WHOLE, bool PACKED, bool INDEXED>
+template <int FN, int FK, int WN, int WK, bool WHOLE, bool PACKED, bool INDEXED>
 hipError_t wgrad_as(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_large) {
     constexpr int BN = WN * FN * 32, BK = WK * FK * 32, kThreads = WN * WK * 64;
-    constexpr int kLds = 2 * STEPS * kStep * (BN + BK) * 2;
+    constexpr int kLds = 2 * kRows * (BN + BK) * 2;
     // as many workgroups as fit at once: two waves per SIMD
     constexpr int kPerCu = 512 / kThreads;
     const int64_t tn = (g.N + BN - 1) / BN, tk = (g.K + BK - 1) / BK, total = tn * tk * g.G * g.parts;
     too_large = total > 0x7FFFFFFF - kPerCu * c.num_cu;
     if (too_large) return hipSuccess;
-    const auto kernel = k_wgrad<FN, FK, WN, WK, STEPS, WHOLE, PACKED, INDEXED>;
+    const auto kernel = k_wgrad<FN, FK, WN, WK, WHOLE, PACKED, INDEXED>;
     if (kLds > 65536) {
-        const hipError_t he = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                                  hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-        if (he != hipSuccess) return he;
+        // once per kernel and device (a grant is the device's); one that fails is
+        // asked for again by the next call
+        static std::atomic<uint64_t> granted{0};
+        const uint64_t bit = 1ull << (c.device & 63);
+        if (c.device > 63 || !(granted.load(std::memory_order_relaxed) & bit)) {
+            const hipError_t he = hipFuncSetAttribute(
+                reinterpret_cast<const void *>(kernel),
+                hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+            if (he != hipSuccess) return he;
+            granted.fetch_or(bit, std::memory_order_relaxed);
+        }
     }
     const int64_t grid = total < kPerCu * c.num_cu ? total : kPerCu * c.num_cu;
     hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid)), dim3(kThreads), kLds, s, g,
@@ -532,34 +605,33 @@ hipError_t wgrad_as(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_larg
     return hipGetLastError();
 }
 
-template <int FN, int FK, int WN, int WK, int STEPS, bool WHOLE, bool PACKED>
+template <int FN, int FK, int WN, int WK, bool WHOLE, bool PACKED>
 hipError_t wgrad_rows(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_large) {
-    return g.index ? wgrad_as<FN, FK, WN, WK, STEPS, WHOLE, PACKED, true>(c, g, s, too_large)
-                   : wgrad_as<FN, FK, WN, WK, STEPS, WHOLE, PACKED, false>(c, g, s, too_large);
+    return g.index ? wgrad_as<FN, FK, WN, WK, WHOLE, PACKED, true>(c, g, s, too_large)
+                   : wgrad_as<FN, FK, WN, WK, WHOLE, PACKED, false>(c, g, s, too_large);
 }
 
-template <int FN, int FK, int WN, int WK, int STEPS>
+template <int FN, int FK, int WN, int WK>
 hipError_t wgrad_any(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_large) {
     const bool whole = g.vec_dy && g.N % 8 == 0 && (g.x_scale || (g.vec_x && g.K % 8 == 0));
     if (g.x_scale)
-        return whole ? wgrad_rows<FN, FK, WN, WK, STEPS, true, true>(c, g, s, too_large)
-                     : wgrad_rows<FN, FK, WN, WK, STEPS, false, true>(c, g, s, too_large);
-    return whole ? wgrad_rows<FN, FK, WN, WK, STEPS, true, false>(c, g, s, too_large)
-                 : wgrad_rows<FN, FK, WN, WK, STEPS, false, false>(c, g, s, too_large);
+        return whole ? wgrad_rows<FN, FK, WN, WK, true, true>(c, g, s, too_large)
+                     : wgrad_rows<FN, FK, WN, WK, false, true>(c, g, s, too_large);
+    return whole ? wgrad_rows<FN, FK, WN, WK, true, false>(c, g, s, too_large)
+                 : wgrad_rows<FN, FK, WN, WK, false, false>(c, g, s, too_large);
 }
 
 hipError_t wgrad_tiles(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_large) {
-    switch (wgrad_tile(g.M, g.N, g.K, static_cast<int64_t>(g.G) * g.parts, c.num_cu)) {
-        case kTile256: return wgrad_any<4, 2, 2, 4, 4>(c, g, s, too_large);
-        case kTile256x128: return wgrad_any<4, 2, 2, 2, 2>(c, g, s, too_large);
-        default: return wgrad_any<2, 2, 2, 2, 4>(c, g, s, too_large);
-    }
+    if (wgrad_tile(g.N, g.K, static_cast<int64_t>(g.G) * g.parts, c.num_cu) == kTile256)
+        return wgrad_any<4, 2, 2, 4>(c, g, s, too_large);
+    return wgrad_any<2, 2, 2, 2>(c, g, s, too_large);
 }
 
 }  // namespace
 
-int wgrad_parts(int M, int N, int K, int G, bool, int num_cu) {
-    const int64_t tiles = tiles_of(N, K, 128, 128) * G;
+// As many as give every CU two tiles of 128.
+int wgrad_parts(int M, int N, int K, int G, int num_cu) {
+    const int64_t tiles = tiles_of(N, K, 128) * G;
     const int64_t slots = 2 * num_cu, rows = M / G;
     int64_t parts = slots / tiles;
     if (parts > rows / kPartRows) parts = rows / kPartRows;
@@ -576,6 +648,15 @@ hipError_t launch_wgrad(ue_ctx &c, const WgradArgs &a, hipStream_t s, bool &too_
     if (g.M == 0) {
         if (g.accumulate) return hipSuccess;
         hipLaunchKernelGGL(k_wgrad_zero, per_row, dim3(kBlock), 0, s, g);
+        return hipGetLastError();
+    }
+    auto tiny = [](int64_t rows, int64_t ld, int cols) {
+        return (rows - 1) * ld + cols < kPiece;
+    };
+    if (tiny(g.M, g.lddy, g.N) || (!g.x_scale && tiny(g.x_rows, g.ldx, g.K))) {
+        const int64_t blocks = (rows * g.K + kBlock - 1) / kBlock;
+        hipLaunchKernelGGL(k_wgrad_tiny, dim3(static_cast<uint32_t>(blocks < most ? blocks : most)),
+                           dim3(kBlock), 0, s, a);
         return hipGetLastError();
     }
     if (g.parts == 1) return wgrad_tiles(c, g, s, too_large);

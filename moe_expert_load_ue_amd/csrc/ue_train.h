@@ -120,7 +120,7 @@ struct WgradArgs {
 // too_large: nothing was launched, the launch would have 2^32 threads or more.
 hipError_t launch_wgrad(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_large);
 // Parts each group's rows are split into (1: no workspace).
-int wgrad_parts(int M, int N, int K, int G, bool packed, int num_cu);
+int wgrad_parts(int M, int N, int K, int G, int num_cu);
 
 // ---------------------------------------------------------------------
 // device helpers

@@ -318,8 +318,7 @@ int ue_gated_backward(ue_ctx *ctx, const int8_t *q, int64_t ldq, const uint8_t *
 
 size_t ue_weight_grad_workspace(const ue_ctx *ctx, const ue_weight_grad_product *p) {
     if (!ctx || !p || p->M < 0 || p->N < 1 || p->K < 1 || p->groups < 1) return 0;
-    const int parts = ue::wgrad_parts(p->M, p->N, p->K, p->groups, p->x_scale != nullptr,
-                                      ctx->num_cu);
+    const int parts = ue::wgrad_parts(p->M, p->N, p->K, p->groups, ctx->num_cu);
     return parts > 1 ? static_cast<size_t>(parts) * p->groups * p->N * p->K * 4 : 0;
 }
 
@@ -356,8 +355,7 @@ int ue_weight_grad(ue_ctx *ctx, const ue_weight_grad_product *p, void *stream) {
     g.out = p->out;
     g.ldo = p->ldo;
     g.out_stride = p->out_stride;
-    g.parts = p->workspace ? ue::wgrad_parts(p->M, p->N, p->K, p->groups,
-                                             p->x_scale != nullptr, ctx->num_cu)
+    g.parts = p->workspace ? ue::wgrad_parts(p->M, p->N, p->K, p->groups, ctx->num_cu)
                            : 1;
     g.part = static_cast<float *>(p->workspace);
     hipStream_t s = static_cast<hipStream_t>(stream);
