@@ -21,6 +21,8 @@
 namespace ue {
 namespace {
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 template <typename T, int L, int VP>
 __device__ __forceinline__ int expert_of_slot(int at, int i, bool vec) {
     return vec ? 4 * (at + L * (i / 4)) + i % 4 : at + L * i;
@@ -58,11 +60,11 @@ __device__ __forceinline__ void scores(float (&x)[VP], float (&slope)[SLOPE ? VP
     if (SIGMOID) {
 #pragma unroll
         for (int i = 0; i < VP; ++i) {
-            // from exp(-|x|), which never overflows
-            const float e = exp_of(-fabsf(x[i])), r = 1.0f / (1.0f + e);
-            const bool up = x[i] >= 0.f;
-            if constexpr (SLOPE) slope[i] = up ? e * r : r;
-            x[i] = up ? r : e * r;
+            // (an infinite exponential leaves a score of 0; the slope is 1 there,
+            // and where the reciprocal is no normal number)
+            const float e = exp_of(-x[i]), r = __builtin_amdgcn_rcpf(1.0f + e);
+            if constexpr (SLOPE) slope[i] = e > 0x1p125f ? 1.0f : e * r;
+            x[i] = r;
             sum += x[i];
         }
         sum = lanes_sum<L>(sum) + 1e-20f;
@@ -105,10 +107,12 @@ struct Sequences {
     }
 };
 
+constexpr int kFwdWaves = 8, kFwdBlock = kFwdWaves * 64;
+
 template <typename T, int L, int VP, bool SIGMOID>
-__global__ __launch_bounds__(kBlock) void k_balance(BalanceArgs g) {
+__global__ __launch_bounds__(kFwdBlock) void k_balance(BalanceArgs g) {
     constexpr int kEach = 64 / L, kAll = L * VP;
-    __shared__ float sums[kWaves][kAll];
+    __shared__ float sums[kFwdWaves][kAll];
     __shared__ int hist[kAll];
     const int tid = threadIdx.x, lane = lane_id(), wv = tid >> 6;
     const int at = lane & (L - 1), sub = lane / L, E = g.E;
@@ -122,24 +126,32 @@ __global__ __launch_bounds__(kBlock) void k_balance(BalanceArgs g) {
         a = a > t0 ? a : t0;
         b = b < t1 ? b : t1;
         if (a >= b) continue;
-        for (int e = tid; e < E; e += kBlock) hist[e] = 0;
+        for (int e = tid; e < E; e += kFwdBlock) hist[e] = 0;
         __syncthreads();
-        for (int i = a * g.k + tid; i < b * g.k; i += kBlock) {
+        for (int i = a * g.k + tid; i < b * g.k; i += kFwdBlock) {
             const int id = g.ids[i];
             if (static_cast<uint32_t>(id) < static_cast<uint32_t>(E))
                 atomicAdd(&hist[id], 1);
         }
         float acc[VP] = {};
-        const int step = kWaves * kEach;
-        for (int t = a + wv * kEach; t < b; t += step) {
+        constexpr int kStep = kFwdWaves * kEach;
+        // a token's logits are on their way while the one before is summed
+        float x[VP], next[VP], none[1];
+        auto load = [&](int t, float (&to)[VP]) {
             const int mine = t + sub < b ? t + sub : b - 1;
-            float x[VP], none[1];
-            load_token<T, L, VP>(logits + mine * g.ld, at, E, g.vec, x);
+            load_token<T, L, VP>(logits + mine * g.ld, at, E, g.vec, to);
+        };
+        int t = a + wv * kEach;
+        if (t < b) load(t, x);
+        for (; t < b; t += kStep) {
+            if (t + kStep < b) load(t + kStep, next);
             scores<L, VP, SIGMOID, false>(x, none);
             if (t + sub < b) {
 #pragma unroll
                 for (int i = 0; i < VP; ++i) acc[i] += x[i];
             }
+#pragma unroll
+            for (int i = 0; i < VP; ++i) x[i] = next[i];
         }
 #pragma unroll
         for (int i = 0; i < VP; ++i) {
@@ -149,10 +161,10 @@ __global__ __launch_bounds__(kBlock) void k_balance(BalanceArgs g) {
         }
         __syncthreads();
         const int64_t slot = static_cast<int64_t>(c + s) * E;
-        for (int e = tid; e < E; e += kBlock) {
+        for (int e = tid; e < E; e += kFwdBlock) {
             float v = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) v += sums[w][e];
+            for (int w = 0; w < kFwdWaves; ++w) v += sums[w][e];
             g.part[slot + e] = v;
             g.part_n[slot + e] = hist[e];
         }
@@ -178,22 +190,52 @@ __global__ __launch_bounds__(kEndBlock) void k_balance_end(BalanceArgs g) {
     for (int e0 = 0; e0 < E; e0 += 256) {
         float v[4] = {};
         int m[4] = {};
-#pragma unroll 4
-        for (int c = c0 + wv; c < c1; c += kEndWaves) {
-            const int64_t slot = static_cast<int64_t>(c + s) * E + e0;
+        if (E % 4 == 0) {
+            // four experts of a lane, four shares at once
+            typedef int i32x4 __attribute__((ext_vector_type(4)));
+            const int e = e0 + 4 * lane < E ? e0 + 4 * lane : 0;
+            for (int c = c0 + wv; c < c1; c += 4 * kEndWaves) {
+                f32x4 p[4];
+                i32x4 n4[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int cc = c + u * kEndWaves < c1 ? c + u * kEndWaves : c;
+                    const int64_t slot = static_cast<int64_t>(cc + s) * E + e;
+                    p[u] = *reinterpret_cast<const f32x4 *>(g.part + slot);
+                    n4[u] = *reinterpret_cast<const i32x4 *>(g.part_n + slot);
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (c + u * kEndWaves < c1) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            v[i] += p[u][i];
+                            m[i] += n4[u][i];
+                        }
+                    }
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int e = lane + 64 * i;
-                if (e0 + e < E) {
-                    v[i] += g.part[slot + e];
-                    m[i] += g.part_n[slot + e];
+                sums[wv][4 * lane + i] = v[i];
+                counts[wv][4 * lane + i] = m[i];
+            }
+        } else {
+            for (int c = c0 + wv; c < c1; c += kEndWaves) {
+                const int64_t slot = static_cast<int64_t>(c + s) * E + e0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = lane + 64 * i;
+                    if (e0 + e < E) {
+                        v[i] += g.part[slot + e];
+                        m[i] += g.part_n[slot + e];
+                    }
                 }
             }
-        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            sums[wv][lane + 64 * i] = v[i];
-            counts[wv][lane + 64 * i] = m[i];
+            for (int i = 0; i < 4; ++i) {
+                sums[wv][lane + 64 * i] = v[i];
+                counts[wv][lane + 64 * i] = m[i];
+            }
         }
         __syncthreads();
         if (tid < 256 && e0 + tid < E) {
@@ -316,7 +358,7 @@ template <typename T, bool SIGMOID>
 void balance_any(const BalanceArgs &g, int shares, hipStream_t s) {
     with_lanes(g.E, [&](auto l, auto v) {
         hipLaunchKernelGGL((k_balance<T, decltype(l)::value, decltype(v)::value, SIGMOID>),
-                           dim3(shares), dim3(kBlock), 0, s, g);
+                           dim3(shares), dim3(kFwdBlock), 0, s, g);
     });
 }
 
@@ -362,7 +404,9 @@ hipError_t launch_balance(const ue_ctx &c, const BalanceArgs &a, hipStream_t s) 
 hipError_t launch_balance_backward(const ue_ctx &c, const BalanceBackArgs &g,
                                    hipStream_t s) {
     if (g.T == 0) return hipSuccess;
-    const int chunk = balance_chunk(g.T, c.num_cu);
+    // eight workgroups' shares per CU
+    const int chunk = (g.T + 8 * c.num_cu - 1) / (8 * c.num_cu) < 16
+                          ? 16 : (g.T + 8 * c.num_cu - 1) / (8 * c.num_cu);
     const int shares = (g.T + chunk - 1) / chunk;
     if (g.bf16)
         g.sigmoid ? backward_any<uint16_t, true>(g, chunk, shares, s)

@@ -85,37 +85,43 @@ __global__ __launch_bounds__(kBlock) void k_combine_backward(CombineArgs g, int 
     const int t = t_first + blockIdx.x;
     const int64_t o = static_cast<int64_t>(t) * g.k;
     const T *dout = static_cast<const T *>(g.dout) + t * g.lddout;
+    const T *y = static_cast<const T *>(g.y);
+    T *dy = static_cast<T *>(g.dy);
     for (int j0 = 0; j0 < g.k; j0 += kJoin) {
-        float dot[kJoin] = {};
+        // (kept in registers: the stores might be to the same memory, for all
+        // the compiler knows)
+        int pos[kJoin];
+        float w[kJoin], dot[kJoin] = {};
+#pragma unroll
+        for (int j = 0; j < kJoin; ++j) {
+            const int at = j0 + j < g.k ? j0 + j : 0;
+            const int p = g.inv[o + at];
+            pos[j] = j0 + j < g.k && static_cast<uint32_t>(p) < static_cast<uint32_t>(g.rows) ? p : -1;
+            w[j] = g.weights ? g.weights[o + at] : 1.f;
+        }
         for (int h = wv * kSeg; h < g.H; h += kWaves * kSeg) {
             const int n = g.H - h;
             float d[8], f[kJoin][8];
             load_seg<T, VEC>(dout + h, n, d);
             if (g.dweights) {
 #pragma unroll
-                for (int j = 0; j < kJoin; ++j) {
-                    const int pos = j0 + j < g.k ? g.inv[o + j0 + j] : -1;
-                    if (static_cast<uint32_t>(pos) >= static_cast<uint32_t>(g.rows)) continue;
-                    load_seg<T, VEC>(static_cast<const T *>(g.y) + pos * g.ldy + h, n, f[j]);
-                }
+                for (int j = 0; j < kJoin; ++j)
+                    if (pos[j] >= 0) load_seg<T, VEC>(y + pos[j] * g.ldy + h, n, f[j]);
             }
             if (g.dy) {
 #pragma unroll
                 for (int j = 0; j < kJoin; ++j) {
-                    const int pos = j0 + j < g.k ? g.inv[o + j0 + j] : -1;
-                    if (static_cast<uint32_t>(pos) >= static_cast<uint32_t>(g.rows)) continue;
-                    const float w = g.weights ? g.weights[o + j0 + j] : 1.f;
+                    if (pos[j] < 0) continue;
                     float v[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = w * d[i];
-                    store_seg<T, VEC>(static_cast<T *>(g.dy) + pos * g.lddy + h, n, v);
+                    for (int i = 0; i < 8; ++i) v[i] = w[j] * d[i];
+                    store_seg<T, VEC>(dy + pos[j] * g.lddy + h, n, v);
                 }
             }
             if (g.dweights) {
 #pragma unroll
                 for (int j = 0; j < kJoin; ++j) {
-                    const int pos = j0 + j < g.k ? g.inv[o + j0 + j] : -1;
-                    if (static_cast<uint32_t>(pos) >= static_cast<uint32_t>(g.rows)) continue;
+                    if (pos[j] < 0) continue;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(d[i], f[j][i], dot[j]);
                 }
