@@ -63,10 +63,11 @@ __global__ __launch_bounds__(kBlock) void k_gated(GatedArgs g, FastDiv per_row, 
         int8_t *to = g.q + m * g.ldq + k;
         uint8_t *st = g.scale + m * g.lds + c;
         uint32_t s = pack8(gate, q);
-        *reinterpret_cast<uint64_t *>(to) = q;
+        __builtin_nontemporal_store(q, reinterpret_cast<uint64_t *>(to));
         if ((threadIdx.x & 3) == 0) st[0] = static_cast<uint8_t>(s);
         s = pack8(up, q);
-        *reinterpret_cast<uint64_t *>(to + per_row.d * UE_PACK_BLOCK) = q;
+        __builtin_nontemporal_store(
+            q, reinterpret_cast<uint64_t *>(to + per_row.d * UE_PACK_BLOCK));
         if ((threadIdx.x & 3) == 0) st[per_row.d] = static_cast<uint8_t>(s);
     }
 }
@@ -80,8 +81,9 @@ __global__ __launch_bounds__(kBlock) void k_gated_backward(GatedArgs g, FastDiv 
     const int k = c * UE_PACK_BLOCK + (threadIdx.x & 3) * 8;
     const int8_t *from = g.q_in + m * g.ldq + k;
     const uint8_t *st = g.scale_in + m * g.lds + c;
-    const uint64_t qg = *reinterpret_cast<const uint64_t *>(from);
-    const uint64_t qu = *reinterpret_cast<const uint64_t *>(from + per_row.d * UE_PACK_BLOCK);
+    const uint64_t qg = __builtin_nontemporal_load(reinterpret_cast<const uint64_t *>(from));
+    const uint64_t qu = __builtin_nontemporal_load(
+        reinterpret_cast<const uint64_t *>(from + per_row.d * UE_PACK_BLOCK));
     const uint32_t sg = st[0], su = st[per_row.d];
     float d[8], gate[8], up[8], h[8];
     load8<T>(static_cast<const T *>(g.dh) + m * g.ldin + k, g.vec, g.I - k, d);
