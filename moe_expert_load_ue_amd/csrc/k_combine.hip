@@ -6,12 +6,16 @@
 //
 // Forward: a wave takes one segment of one token's row and loads that segment
 // of up to kJoin of its rows at once before it adds them, in order. Backward: a
-// workgroup takes a token, its waves the segments in turn; every element of dout
-// is read once per kJoin rows, and the dots are added over lanes, then waves,
-// in a fixed order. Tokens and their rows' places are the same for a whole wave
-// and so are read by scalar loads.
+// wave per assignment, those of a token in one workgroup (of up to kJoin waves),
+// so that dout comes from the cache for all but the first; a dot is added by
+// lanes, then over them, in a fixed order. Places and weights are the same for a
+// whole wave and so are read by scalar loads.
 //
-// Bound: HBM.
+// Bound: HBM. 16384 tokens x top-8 x 7168, bf16: forward 372 us (2.1 GB, 5.7
+// TB/s), backward 734 us (4.0 GB, 5.5 TB/s). A workgroup per token whose waves
+// shared out the segments took 880 backward; four segments ahead in place of two
+// 965, one 724 (but 10.9 us in place of 9.8 for 1021 tokens x top-6 x 1002,
+// fp32); dout past the caches too 794.
 #include "ue_train.h"
 
 namespace ue {
@@ -22,11 +26,11 @@ constexpr int kSeg = 512;     // elements of a wave's segment: 8 a lane
 
 // The lane's elements of a segment at p: 8 in a row (VEC), or every 64th. `n`:
 // elements from p to the end of the row.
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool ONCE = true>
 __device__ __forceinline__ void load_seg(const T *p, int n, float (&f)[8]) {
     const int lane = lane_id();
     if (VEC) {
-        load8<T>(p + lane * 8, true, n - lane * 8, f);
+        load8<T, ONCE>(p + lane * 8, true, n - lane * 8, f);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -77,70 +81,51 @@ __global__ __launch_bounds__(kBlock) void k_combine(CombineArgs g, FastDiv segs,
     store_seg<T, VEC>(static_cast<T *>(g.out) + t * g.ldo + h, n, sum);
 }
 
+constexpr int kAhead = 2;     // segments in flight
+
 template <typename T, bool VEC>
-__global__ __launch_bounds__(kBlock) void k_combine_backward(CombineArgs g, int t_first) {
-    __shared__ float part[kWaves][kJoin];
-    const int lane = lane_id();
+__global__ __launch_bounds__(kJoin * 64) void k_combine_backward(CombineArgs g, int t_first) {
+    const int lane = lane_id(), waves = blockDim.x >> 6;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int t = t_first + blockIdx.x;
     const int64_t o = static_cast<int64_t>(t) * g.k;
     const T *dout = static_cast<const T *>(g.dout) + t * g.lddout;
-    const T *y = static_cast<const T *>(g.y);
-    T *dy = static_cast<T *>(g.dy);
-    for (int j0 = 0; j0 < g.k; j0 += kJoin) {
-        // (kept in registers: the stores might be to the same memory, for all
-        // the compiler knows)
-        int pos[kJoin];
-        float w[kJoin], dot[kJoin] = {};
+    for (int j = wv; j < g.k; j += waves) {
+        const int pos = g.inv[o + j];
+        const float w = g.weights ? g.weights[o + j] : 1.f;
+        float dot = 0.f;
+        if (static_cast<uint32_t>(pos) < static_cast<uint32_t>(g.rows)) {
+            const T *y = static_cast<const T *>(g.y) + pos * g.ldy;
+            T *dy = static_cast<T *>(g.dy) + pos * g.lddy;
+            for (int h0 = 0; h0 < g.H; h0 += kAhead * kSeg) {
+                float d[kAhead][8], f[kAhead][8];
 #pragma unroll
-        for (int j = 0; j < kJoin; ++j) {
-            const int at = j0 + j < g.k ? j0 + j : 0;
-            const int p = g.inv[o + at];
-            pos[j] = j0 + j < g.k && static_cast<uint32_t>(p) < static_cast<uint32_t>(g.rows) ? p : -1;
-            w[j] = g.weights ? g.weights[o + at] : 1.f;
-        }
-        for (int h = wv * kSeg; h < g.H; h += kWaves * kSeg) {
-            const int n = g.H - h;
-            float d[8], f[kJoin][8];
-            load_seg<T, VEC>(dout + h, n, d);
-            if (g.dweights) {
-#pragma unroll
-                for (int j = 0; j < kJoin; ++j)
-                    if (pos[j] >= 0) load_seg<T, VEC>(y + pos[j] * g.ldy + h, n, f[j]);
-            }
-            if (g.dy) {
-#pragma unroll
-                for (int j = 0; j < kJoin; ++j) {
-                    if (pos[j] < 0) continue;
-                    float v[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = w[j] * d[i];
-                    store_seg<T, VEC>(dy + pos[j] * g.lddy + h, n, v);
+                for (int u = 0; u < kAhead; ++u) {
+                    const int h = h0 + u * kSeg;
+                    if (h >= g.H) continue;
+                    load_seg<T, VEC, false>(dout + h, g.H - h, d[u]);
+                    if (g.dweights) load_seg<T, VEC>(y + h, g.H - h, f[u]);
                 }
-            }
-            if (g.dweights) {
 #pragma unroll
-                for (int j = 0; j < kJoin; ++j) {
-                    if (pos[j] < 0) continue;
+                for (int u = 0; u < kAhead; ++u) {
+                    const int h = h0 + u * kSeg;
+                    if (h >= g.H) continue;
+                    if (g.dweights) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(d[i], f[j][i], dot[j]);
+                        for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(d[u][i], f[u][i], dot);
+                    }
+                    if (g.dy) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) d[u][i] *= w;
+                        store_seg<T, VEC>(dy + h, g.H - h, d[u]);
+                    }
                 }
             }
         }
-        if (!g.dweights) continue;
-#pragma unroll
-        for (int j = 0; j < kJoin; ++j) {
-            const float v = lanes_sum<64>(dot[j]);
-            if (lane == 0) part[wv][j] = v;
+        if (g.dweights) {
+            dot = lanes_sum<64>(dot);
+            if (lane == 0) g.dweights[o + j] = dot;
         }
-        __syncthreads();
-        if (threadIdx.x < kJoin && j0 + static_cast<int>(threadIdx.x) < g.k) {
-            float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) v += part[w][threadIdx.x];
-            g.dweights[o + j0 + threadIdx.x] = v;
-        }
-        __syncthreads();
     }
 }
 
@@ -177,7 +162,7 @@ hipError_t launch_combine(const ue_ctx &, const CombineArgs &g, hipStream_t s) {
 hipError_t launch_combine_backward(const ue_ctx &, const CombineArgs &g, hipStream_t s) {
     constexpr int kTokens = 1 << 23;         // of a launch: fewer than 2^32 threads
     for (int t = 0; t < g.T; t += kTokens) {
-        const dim3 gr(g.T - t < kTokens ? g.T - t : kTokens), bl(kBlock);
+        const dim3 gr(g.T - t < kTokens ? g.T - t : kTokens), bl(64 * (g.k < kJoin ? g.k : kJoin));
         if (g.bf16) {
             if (g.vec) hipLaunchKernelGGL((k_combine_backward<uint16_t, true>), gr, bl, 0, s, g, t);
             else hipLaunchKernelGGL((k_combine_backward<uint16_t, false>), gr, bl, 0, s, g, t);

@@ -146,13 +146,15 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // caches where time counts (gated activation of 32768 rows of 2048 with its
 // backward pass 258 us through the caches, 181 past them; gradients of the sum of
 // rows, 16384 tokens x top-8 x 7168, 1020 against 881).
-template <typename T>
+template <typename T, bool ONCE = true>
 __device__ __forceinline__ void load8(const T *p, bool vec, int n, float (&f)[8]) {
     if (vec && n >= 8) {
         struct Pack { u32x4 v[sizeof(T) / 2]; } k;
 #pragma unroll
-        for (size_t c = 0; c < sizeof(T) / 2; ++c)
-            k.v[c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p) + c);
+        for (size_t c = 0; c < sizeof(T) / 2; ++c) {
+            const u32x4 *at = reinterpret_cast<const u32x4 *>(p) + c;
+            k.v[c] = ONCE ? __builtin_nontemporal_load(at) : *at;
+        }
         struct Elements { T v[8]; };
         const Elements e = __builtin_bit_cast(Elements, k);
 #pragma unroll
