@@ -573,8 +573,9 @@ int ue_moe_tokens(ue_ctx *ctx, const void *x, int64_t ldx, int32_t T,
  *   counts   device, int32 [n_seq, E] out;  prob  device, fp32 [n_seq, E] out
  *   loss     device, fp32 [n_seq] out
  *   workspace  device, 16-byte aligned, ue_balance_workspace(ctx, T, n_seq)
- *            bytes, overwritten. Calls given the same one must not overlap,
- *            replays of captured ones included.
+ *            bytes, overwritten; may be NULL where that is 0 (few tokens). Calls
+ *            given the same one must not overlap, replays of captured ones
+ *            included.
  * T in 0..max_tokens, n_seq in 0..2^20. Sums are fp32 in a fixed order (no
  * atomics on values): results repeat bit for bit. */
 size_t ue_balance_workspace(const ue_ctx *ctx, int32_t T, int32_t n_seq);

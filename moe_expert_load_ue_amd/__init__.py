@@ -1000,12 +1000,14 @@ def ue_balance(ctx: Context, logits, ids, offsets=None, score="softmax",
         prob = _new((n, ctx.E), torch.float32, ctx, stream)
     else:
         _flat(prob, "prob", torch.float32, dev, n * ctx.E)
-    need = library().ue_balance_workspace(ctx._h, T, n)
-    workspace = _workspace(ctx, workspace, need, stream)
-    rc = library().ue_balance(ctx._h, logits.data_ptr(), _TYPES[logits.dtype],
+    lib = library()
+    need, ws = lib.ue_balance_workspace(ctx._h, T, n), None
+    if need:
+        workspace = _workspace(ctx, workspace, need, stream)
+        ws = workspace.data_ptr()
+    rc = lib.ue_balance(ctx._h, logits.data_ptr(), _TYPES[logits.dtype],
                               ld, T, score, i, po, n, counts.data_ptr(),
-                              prob.data_ptr(), loss.data_ptr(),
-                              workspace.data_ptr(),
+                              prob.data_ptr(), loss.data_ptr(), ws,
                               _on(ctx, stream, logits, ids, offsets, counts,
                                   prob, loss, workspace))
     if rc:
@@ -1041,10 +1043,11 @@ def ue_balance_backward(ctx: Context, logits, counts, dloss, offsets=None,
     if dlogits is None:
         if accumulate:
             raise ValueError("accumulate needs dlogits to add to")
-        dlogits = _new((T, ctx.E), logits.dtype, ctx, stream)
-    rows, _, ldo = _rows(dlogits, "dlogits", dev, (logits.dtype,), ctx.E)
-    if rows != T:
-        raise ValueError(f"dlogits must have {T} rows")
+        dlogits, ldo = _new((T, ctx.E), logits.dtype, ctx, stream), ctx.E
+    else:
+        rows, _, ldo = _rows(dlogits, "dlogits", dev, (logits.dtype,), ctx.E)
+        if rows != T:
+            raise ValueError(f"dlogits must have {T} rows")
     rc = library().ue_balance_backward(
         ctx._h, logits.data_ptr(), _TYPES[logits.dtype], ld, T, _score(score),
         po, n, c, d, dlogits.data_ptr(), ldo, bool(accumulate),
@@ -1094,12 +1097,14 @@ def ue_pack_rows(ctx: Context, x, q=None, scale=None, stream=None):
         raise ValueError("q and scale belong together")
     if q is None:
         q, scale = _packed_new(ctx, M, whole, stream)
+        ldq, lds, pq, ps = whole, whole // PACK_BLOCK, q.data_ptr(), scale.data_ptr()
         if whole != K:
             q = q[:, :K]
-    m, _, ldq, pq, lds, ps = _packed(ctx, q, scale, K)
-    if m != M:
-        raise ValueError(f"q must have {M} rows")
-    _reach(q, "q", M, ldq, K, PACK_BLOCK)
+    else:
+        m, _, ldq, pq, lds, ps = _packed(ctx, q, scale, K)
+        if m != M:
+            raise ValueError(f"q must have {M} rows")
+        _reach(q, "q", M, ldq, K, PACK_BLOCK)
     rc = library().ue_pack_rows(ctx._h, x.data_ptr(), _TYPES[x.dtype], ldx, M,
                                 K, pq, ldq, ps, lds,
                                 _on(ctx, stream, x, q, scale))
@@ -1126,6 +1131,15 @@ def ue_unpack_rows(ctx: Context, q, scale, out=None, out_dtype=torch.bfloat16,
     return out
 
 
+def _out(t, name, ctx, dtype, rows, cols):
+    """Distance between the rows of an output [rows, cols] given by the
+    caller."""
+    n, _, ld = _rows(t, name, ctx.device, (dtype,), cols)
+    if n != rows:
+        raise ValueError(f"{name} must have {rows} rows")
+    return ld
+
+
 def _half(I):
     """Bytes of gate, and of up, in a packed row of both."""
     return (I + PACK_BLOCK - 1) // PACK_BLOCK * PACK_BLOCK
@@ -1142,17 +1156,19 @@ def ue_gated(ctx: Context, gu, h=None, q=None, scale=None, keep=True,
         raise ValueError("gu must hold as many up as gate columns")
     I = two // 2
     if h is None:
-        h = _new((M, I), gu.dtype, ctx, stream)
-    n, _, ldh = _rows(h, "h", ctx.device, (gu.dtype,), I)
-    if n != M:
-        raise ValueError(f"h must have {M} rows")
+        h, ldh = _new((M, I), gu.dtype, ctx, stream), I
+    else:
+        ldh = _out(h, "h", ctx, gu.dtype, M, I)
     if (q is None) != (scale is None) or (q is not None and not keep):
         raise ValueError("q and scale belong together, and to keep=True")
     ldq = lds = 0
     pq = ps = None
-    if keep:
-        if q is None:
-            q, scale = _packed_new(ctx, M, 2 * _half(I), stream)
+    if keep and q is None:
+        ldq = 2 * _half(I)
+        lds = ldq // PACK_BLOCK
+        q, scale = _packed_new(ctx, M, ldq, stream)
+        pq, ps = q.data_ptr(), scale.data_ptr()
+    elif keep:
         m, _, ldq, pq, lds, ps = _packed(ctx, q, scale, 2 * _half(I))
         if m != M:
             raise ValueError(f"q must have {M} rows")
@@ -1174,17 +1190,14 @@ def ue_gated_backward(ctx: Context, dh, q, scale, dgu=None, h=None,
     if m != M:
         raise ValueError(f"q must have {M} rows")
     if dgu is None:
-        dgu = _new((M, 2 * I), dh.dtype, ctx, stream)
-    n, _, lddgu = _rows(dgu, "dgu", ctx.device, (dh.dtype,), 2 * I)
-    if n != M:
-        raise ValueError(f"dgu must have {M} rows")
-    if h is None and with_h:
-        h = _new((M, I), dh.dtype, ctx, stream)
-    ldh = 0
+        dgu, lddgu = _new((M, 2 * I), dh.dtype, ctx, stream), 2 * I
+    else:
+        lddgu = _out(dgu, "dgu", ctx, dh.dtype, M, 2 * I)
+    ldh = I
     if h is not None:
-        n, _, ldh = _rows(h, "h", ctx.device, (dh.dtype,), I)
-        if n != M:
-            raise ValueError(f"h must have {M} rows")
+        ldh = _out(h, "h", ctx, dh.dtype, M, I)
+    elif with_h:
+        h = _new((M, I), dh.dtype, ctx, stream)
     rc = library().ue_gated_backward(
         ctx._h, pq, ldq, ps, lds, dh.data_ptr(), _TYPES[dh.dtype], lddh, M, I,
         dgu.data_ptr(), lddgu, None if h is None else h.data_ptr(), ldh,
@@ -1279,15 +1292,12 @@ def ue_combine(ctx: Context, y, inv_perm, weights=None, add=None, out=None,
     T, pi, pw = _assigned(ctx, inv_perm, weights)
     pa, lda = None, 0
     if add is not None:
-        n, _, lda = _rows(add, "add", dev, (y.dtype,), H)
-        if n != T:
-            raise ValueError(f"add must have {T} rows")
+        lda = _out(add, "add", ctx, y.dtype, T, H)
         pa = add.data_ptr()
     if out is None:
-        out = _new((T, H), y.dtype, ctx, stream)
-    n, _, ldo = _rows(out, "out", dev, (y.dtype,), H)
-    if n != T:
-        raise ValueError(f"out must have {T} rows")
+        out, ldo = _new((T, H), y.dtype, ctx, stream), H
+    else:
+        ldo = _out(out, "out", ctx, y.dtype, T, H)
     rc = library().ue_combine(ctx._h, y.data_ptr(), _TYPES[y.dtype], ldy, rows,
                               pi, pw, pa, lda, T, H, out.data_ptr(), ldo,
                               _on(ctx, stream, y, inv_perm, weights, add, out))
@@ -1316,15 +1326,15 @@ def ue_combine_backward(ctx: Context, dout, inv_perm, weights=None, y=None,
             dweights = _new((T, ctx.k), torch.float32, ctx, stream)
         else:
             _flat(dweights, "dweights", torch.float32, dev, T * ctx.k)
-    lddy = 0
-    if dy is not None or with_dy:
-        if dy is None:
-            dy = _new((rows, H), dout.dtype, ctx, stream)
+    lddy = H
+    if dy is not None:
         n, _, lddy = _rows(dy, "dy", dev, (dout.dtype,), H)
         if y is None:
             rows = n
         elif n != rows:
             raise ValueError(f"dy must have {rows} rows")
+    elif with_dy:
+        dy = _new((rows, H), dout.dtype, ctx, stream)
     rc = library().ue_combine_backward(
         ctx._h, dout.data_ptr(), _TYPES[dout.dtype], lddo, pi, pw, py, ldy,
         rows, T, H, None if dy is None else dy.data_ptr(), lddy,

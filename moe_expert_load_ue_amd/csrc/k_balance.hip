@@ -109,7 +109,8 @@ struct Sequences {
 
 constexpr int kFwdWaves = 8, kFwdBlock = kFwdWaves * 64;
 
-template <typename T, int L, int VP, bool SIGMOID>
+// WHOLE: a workgroup per sequence, which writes the results itself.
+template <typename T, int L, int VP, bool SIGMOID, bool WHOLE>
 __global__ __launch_bounds__(kFwdBlock) void k_balance(BalanceArgs g) {
     constexpr int kEach = 64 / L, kAll = L * VP;
     __shared__ float sums[kFwdWaves][kAll];
@@ -117,15 +118,17 @@ __global__ __launch_bounds__(kFwdBlock) void k_balance(BalanceArgs g) {
     const int tid = threadIdx.x, lane = lane_id(), wv = tid >> 6;
     const int at = lane & (L - 1), sub = lane / L, E = g.E;
     const Sequences seqs{g.offsets, g.T, g.n_seq};
-    const int c = blockIdx.x, t0 = c * g.chunk;
-    const int t1 = g.T - t0 < g.chunk ? g.T : t0 + g.chunk;
+    const int c = blockIdx.x, t0 = WHOLE ? 0 : c * g.chunk;
+    const int t1 = WHOLE || g.T - t0 < g.chunk ? g.T : t0 + g.chunk;
     const T *logits = static_cast<const T *>(g.logits);
-    for (int s = seqs.find(t0); s < g.n_seq; ++s) {
+    for (int s = WHOLE ? c : seqs.find(t0); s < (WHOLE ? c + 1 : g.n_seq); ++s) {
         int a = seqs.begin(s), b = seqs.begin(s + 1);
-        if (a >= t1) break;
-        a = a > t0 ? a : t0;
-        b = b < t1 ? b : t1;
-        if (a >= b) continue;
+        if constexpr (!WHOLE) {
+            if (a >= t1) break;
+            a = a > t0 ? a : t0;
+            b = b < t1 ? b : t1;
+            if (a >= b) continue;
+        }
         for (int e = tid; e < E; e += kFwdBlock) hist[e] = 0;
         __syncthreads();
         for (int i = a * g.k + tid; i < b * g.k; i += kFwdBlock) {
@@ -160,13 +163,35 @@ __global__ __launch_bounds__(kFwdBlock) void k_balance(BalanceArgs g) {
             if (sub == 0) sums[wv][expert_of_slot<T, L, VP>(at, i, g.vec)] = acc[i];
         }
         __syncthreads();
-        const int64_t slot = static_cast<int64_t>(c + s) * E;
+        const int64_t slot = static_cast<int64_t>(WHOLE ? s : c + s) * E;
+        const float inv_n = b > a ? 1.0f / static_cast<float>(b - a) : 0.f;
+        float term = 0.f;
         for (int e = tid; e < E; e += kFwdBlock) {
             float v = 0.f;
 #pragma unroll
             for (int w = 0; w < kFwdWaves; ++w) v += sums[w][e];
-            g.part[slot + e] = v;
-            g.part_n[slot + e] = hist[e];
+            const int n = hist[e];
+            if constexpr (WHOLE) {
+                v *= inv_n;
+                g.prob[slot + e] = v;
+                g.counts[slot + e] = n;
+                term += static_cast<float>(n) * v;
+            } else {
+                g.part[slot + e] = v;
+                g.part_n[slot + e] = n;
+            }
+        }
+        if constexpr (WHOLE) {
+            __shared__ float terms[kFwdWaves];
+            term = lanes_sum<64>(term);
+            if (lane == 0) terms[wv] = term;
+            __syncthreads();
+            if (tid == 0) {
+                float all = 0.f;
+#pragma unroll
+                for (int w = 0; w < kFwdWaves; ++w) all += terms[w];
+                g.loss[s] = all * (static_cast<float>(E) / static_cast<float>(g.k)) * inv_n;
+            }
         }
         __syncthreads();
     }
@@ -357,8 +382,13 @@ void with_lanes(int E, F f) {
 template <typename T, bool SIGMOID>
 void balance_any(const BalanceArgs &g, int shares, hipStream_t s) {
     with_lanes(g.E, [&](auto l, auto v) {
-        hipLaunchKernelGGL((k_balance<T, decltype(l)::value, decltype(v)::value, SIGMOID>),
-                           dim3(shares), dim3(kFwdBlock), 0, s, g);
+        constexpr int L = decltype(l)::value, VP = decltype(v)::value;
+        if (g.part)
+            hipLaunchKernelGGL((k_balance<T, L, VP, SIGMOID, false>), dim3(shares),
+                               dim3(kFwdBlock), 0, s, g);
+        else
+            hipLaunchKernelGGL((k_balance<T, L, VP, SIGMOID, true>), dim3(g.n_seq),
+                               dim3(kFwdBlock), 0, s, g);
     });
 }
 
@@ -377,7 +407,12 @@ int balance_chunk(int T, int num_cu) {
     const int each = (T + 2 * num_cu - 1) / (2 * num_cu);
     return each <= 64 ? 64 : (each + 15) / 16 * 16;
 }
-int64_t balance_slots(int T, int n_seq, int num_cu) {
+// A workgroup passes over 64 tokens at once (128 experts; half as many from
+// there on): batches of up to eight such passes are left to a workgroup per
+// sequence, without partial sums and the launch that adds them.
+int64_t balance_slots(int T, int n_seq, int E, int num_cu) {
+    const int pass = E <= 128 ? 64 : E <= 256 ? 32 : E <= 512 ? 16 : 8;
+    if (T <= 8 * pass) return 0;
     const int c = balance_chunk(T, num_cu);
     return (static_cast<int64_t>(T) + c - 1) / c + n_seq;
 }
@@ -387,16 +422,14 @@ hipError_t launch_balance(const ue_ctx &c, const BalanceArgs &a, hipStream_t s) 
     BalanceArgs g = a;
     g.chunk = balance_chunk(g.T, c.num_cu);
     const int shares = (g.T + g.chunk - 1) / g.chunk;
-    if (shares > 0) {
-        if (g.bf16)
-            g.sigmoid ? balance_any<uint16_t, true>(g, shares, s)
-                      : balance_any<uint16_t, false>(g, shares, s);
-        else
-            g.sigmoid ? balance_any<float, true>(g, shares, s)
-                      : balance_any<float, false>(g, shares, s);
-        const hipError_t he = hipGetLastError();
-        if (he != hipSuccess) return he;
-    }
+    if (g.bf16)
+        g.sigmoid ? balance_any<uint16_t, true>(g, shares, s)
+                  : balance_any<uint16_t, false>(g, shares, s);
+    else
+        g.sigmoid ? balance_any<float, true>(g, shares, s)
+                  : balance_any<float, false>(g, shares, s);
+    const hipError_t he = hipGetLastError();
+    if (he != hipSuccess || !g.part) return he;
     hipLaunchKernelGGL(k_balance_end, dim3(g.n_seq), dim3(kEndBlock), 0, s, g);
     return hipGetLastError();
 }

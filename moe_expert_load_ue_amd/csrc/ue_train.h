@@ -17,7 +17,8 @@ struct BalanceArgs {
     int32_t *counts;
     float *prob, *loss;
     int chunk;                  // tokens of a workgroup's share
-    float *part;                // [slots][E] sums of p; slot: chunk + sequence
+    float *part;                // [slots][E] sums of p; slot: chunk + sequence;
+                                // null: a workgroup per sequence, no partial sums
     int32_t *part_n;            // [slots][E] assignments
 };
 struct BalanceBackArgs {
@@ -31,10 +32,10 @@ struct BalanceBackArgs {
     void *dlogits;
     int64_t ld_out;
 };
-// Tokens of a workgroup's share, and the slots of partial sums T tokens in
-// n_seq sequences may need.
+// Tokens of a workgroup's share, and the slots of partial sums that T tokens in
+// n_seq sequences need (0: none are made).
 int balance_chunk(int T, int num_cu);
-int64_t balance_slots(int T, int n_seq, int num_cu);
+int64_t balance_slots(int T, int n_seq, int E, int num_cu);
 hipError_t launch_balance(const ue_ctx &c, const BalanceArgs &g, hipStream_t s);
 hipError_t launch_balance_backward(const ue_ctx &c, const BalanceBackArgs &g,
                                    hipStream_t s);

@@ -112,7 +112,8 @@ extern "C" {
 
 size_t ue_balance_workspace(const ue_ctx *ctx, int32_t T, int32_t n_seq) {
     if (!ctx || T < 0 || n_seq < 0) return 0;
-    return static_cast<size_t>(ue::balance_slots(T, n_seq, ctx->num_cu)) * ctx->E * 8;
+    return static_cast<size_t>(ue::balance_slots(T, n_seq, ctx->E, ctx->num_cu)) *
+           ctx->E * 8;
 }
 
 int ue_balance(ue_ctx *ctx, const void *logits, int32_t type, int64_t ld, int32_t T,
@@ -122,7 +123,9 @@ int ue_balance(ue_ctx *ctx, const void *logits, int32_t type, int64_t ld, int32_
     ctx->err.clear();
     if (int rc = check_balance(ctx, "ue_balance", logits, type, ld, T, score, offsets, n_seq))
         return rc;
-    if ((T > 0 && !ids) || (n_seq > 0 && (!counts || !prob || !loss || !workspace)))
+    const int64_t slots = ue::balance_slots(T, n_seq, ctx->E, ctx->num_cu);
+    if ((T > 0 && !ids) || (n_seq > 0 && (!counts || !prob || !loss)) ||
+        (n_seq > 0 && slots > 0 && !workspace))
         return fail(ctx, UE_EINVAL, "ue_balance: null argument");
     if (!aligned(ids, 4) || !aligned(counts, 4) || !aligned(prob, 4) || !aligned(loss, 4) ||
         !aligned(workspace, 16))
@@ -143,9 +146,10 @@ int ue_balance(ue_ctx *ctx, const void *logits, int32_t type, int64_t ld, int32_
     g.counts = counts;
     g.prob = prob;
     g.loss = loss;
-    const int64_t slots = ue::balance_slots(T, n_seq, ctx->num_cu);
-    g.part = static_cast<float *>(workspace);
-    g.part_n = reinterpret_cast<int32_t *>(g.part + slots * ctx->E);
+    if (slots > 0) {
+        g.part = static_cast<float *>(workspace);
+        g.part_n = reinterpret_cast<int32_t *>(g.part + slots * ctx->E);
+    }
     hipStream_t s = static_cast<hipStream_t>(stream);
     tbegin(ctx, s);
     return done(ctx, ue::launch_balance(*ctx, g, s), s, "k_balance launch");

@@ -779,6 +779,8 @@ def test_binding_refusals():
     h, gq, gs = ue.ue_gated(ctx, x)
     b = x.bfloat16()
     small = torch.zeros(8, dtype=torch.uint8, device=DEV)
+    big = ctx_for(8, 2, 600)                 # so many tokens need a workspace
+    many, many_ids = torch.randn((600, 8), device=DEV), ids[:1].repeat(600, 1)
     for err, call in [
             (TypeError, lambda: ue.ue_balance(ctx, x.half(), ids)),
             (ValueError, lambda: ue.ue_balance(ctx, x[:, :7], ids)),
@@ -787,7 +789,7 @@ def test_binding_refusals():
             (TypeError, lambda: ue.ue_balance(ctx, x, ids, off.long())),
             (ValueError, lambda: ue.ue_balance(ctx, x, ids, [0, 4])),
             (ValueError, lambda: ue.ue_balance(ctx, x, ids, score="tanh")),
-            (ValueError, lambda: ue.ue_balance(ctx, x, ids, workspace=small)),
+            (ValueError, lambda: ue.ue_balance(big, many, many_ids, workspace=small)),
             (ValueError, lambda: ue.ue_balance(ctx, x.cpu(), ids)),
             (ue.UEError, lambda: ue.ue_balance(ctx, torch.randn((17, 8), device=DEV),
                                                torch.zeros((17, 2), dtype=torch.int32, device=DEV))),
@@ -823,4 +825,5 @@ def test_binding_refusals():
             (TypeError, lambda: ue.ue_combine_backward(ctx, x, ids, y=b))]:
         with pytest.raises(err):
             call()
+    big.close()
     ctx.close()

@@ -22,7 +22,8 @@ extern "C" void *make_ctx(int E, int k, int tokens) {
     return c;
 }
 """
-E, K, T = 8, 2, 16
+E, K, T = 8, 2, 1024
+BIG = 600                                # tokens that need a workspace
 A, ODD = 1 << 20, (1 << 20) + 1          # an address, and one aligned to nothing
 EINVAL, ESHAPE = -1, -2
 
@@ -60,14 +61,16 @@ def test_balance(ctx):
         (EINVAL, dict(ids=None)), (ESHAPE, dict(n_seq=-1)), (ESHAPE, dict(n_seq=(1 << 20) + 1)),
         (ESHAPE, dict(offsets=None)), (ESHAPE, dict(offsets=None, n_seq=0)),
         (EINVAL, dict(counts=None)), (EINVAL, dict(prob=None)), (EINVAL, dict(loss=None)),
-        (EINVAL, dict(workspace=None)), (EINVAL, dict(workspace=A + 8)),
+        (EINVAL, dict(workspace=None, T=BIG)), (EINVAL, dict(workspace=A + 8)),
         (EINVAL, dict(logits=A + 2)), (EINVAL, dict(logits=ODD, type=1)),
         (EINVAL, dict(ids=A + 2)), (EINVAL, dict(offsets=ODD)), (EINVAL, dict(counts=ODD)),
         (EINVAL, dict(prob=ODD)), (EINVAL, dict(loss=ODD))])
     lib = ue.library()
     assert lib.ue_balance_workspace(ctx, -1, 1) == 0 == lib.ue_balance_workspace(None, 1, 1)
-    # shares of 64 tokens and a slot for every share and sequence, 8 bytes an expert
-    assert lib.ue_balance_workspace(ctx, 130, 5) == (3 + 5) * E * 8
+    # shares of 64 tokens and a slot for every share and sequence, 8 bytes an
+    # expert; none for few tokens
+    assert lib.ue_balance_workspace(ctx, BIG, 5) == (10 + 5) * E * 8
+    assert lib.ue_balance_workspace(ctx, 512, 5) == 0
 
 
 def test_balance_backward(ctx):
