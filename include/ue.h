@@ -668,7 +668,9 @@ int ue_gated_backward(ue_ctx *ctx, const int8_t *q, int64_t ldq,
  *            bytes (0 for many shapes), or NULL: few matrices of many rows are
  *            then not split over the device. Calls given the same one must not
  *            overlap.
- * N and K in 0..2^20; one matrix of out, and 64 rows of dy, are below 4 GiB. */
+ * M in 0..2^30, N and K in 0..2^20; rows of dy and x are at most 2^24 apart, and
+ * one matrix of out is below 4 GiB. Of packed x, a row's bytes up to K rounded up
+ * to 16 must be readable. */
 typedef struct ue_weight_grad_product {
     const void *dy;
     const void *x;

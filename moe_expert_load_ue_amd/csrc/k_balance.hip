@@ -121,10 +121,17 @@ __global__ __launch_bounds__(kFwdBlock) void k_balance(BalanceArgs g) {
     const int c = blockIdx.x, t0 = WHOLE ? 0 : c * g.chunk;
     const int t1 = WHOLE || g.T - t0 < g.chunk ? g.T : t0 + g.chunk;
     const T *logits = static_cast<const T *>(g.logits);
-    for (int s = WHOLE ? c : seqs.find(t0); s < (WHOLE ? c + 1 : g.n_seq); ++s) {
+    // (the next sequence is looked for behind this one's end, past any number of
+    // empty ones; offsets that decrease may not lead back)
+    int s = WHOLE ? c : seqs.find(t0), after = g.n_seq;
+    for (; s < g.n_seq; s = after) {
         int a = seqs.begin(s), b = seqs.begin(s + 1);
         if constexpr (!WHOLE) {
             if (a >= t1) break;
+            if (b < t1) {
+                after = seqs.find(b);
+                after = after > s ? after : s + 1;
+            }
             a = a > t0 ? a : t0;
             b = b < t1 ? b : t1;
             if (a >= b) continue;
@@ -301,7 +308,7 @@ __global__ __launch_bounds__(kBlock) void k_balance_backward(BalanceBackArgs g, 
     T *out = static_cast<T *>(g.dlogits);
     int t = t0 + wv * kEach + sub;
     // this token's sequence; its counts times what its gradient is scaled with
-    int s = seqs.find(t), from = 0, to = -1;
+    int s = 0, from = 0, to = -1;
     float cw[VP] = {};
     for (; t - sub < t1; t += kWaves * kEach) {
         const bool real = t < t1;
@@ -309,7 +316,7 @@ __global__ __launch_bounds__(kBlock) void k_balance_backward(BalanceBackArgs g, 
         float x[VP], slope[VP];
         load_token<T, L, VP>(logits + mine * g.ld, at, E, g.vec, x);
         if (real && t >= to) {
-            while (s < g.n_seq && seqs.begin(s + 1) <= t) ++s;
+            s = seqs.find(t);
             if (s < g.n_seq) {
                 from = seqs.begin(s);
                 to = seqs.begin(s + 1);

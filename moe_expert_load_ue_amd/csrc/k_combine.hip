@@ -160,7 +160,7 @@ hipError_t launch_combine(const ue_ctx &, const CombineArgs &g, hipStream_t s) {
 }
 
 hipError_t launch_combine_backward(const ue_ctx &, const CombineArgs &g, hipStream_t s) {
-    constexpr int kTokens = 1 << 23;         // of a launch: fewer than 2^32 threads
+    constexpr int kTokens = 1 << 22;         // of a launch: fewer than 2^32 threads
     for (int t = 0; t < g.T; t += kTokens) {
         const dim3 gr(g.T - t < kTokens ? g.T - t : kTokens), bl(64 * (g.k < kJoin ? g.k : kJoin));
         if (g.bf16) {

@@ -88,14 +88,15 @@ struct Stage {
 };
 
 template <int FN, int FK, int WN, int WK, bool WHOLE, bool PACKED, bool INDEXED>
-__global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
+__global__ __launch_bounds__(WN *WK * 64, FN * FK > 8 ? 1 : 2) void k_wgrad(
     WgradArgs g, FastDiv div, int tiles_n, int tiles_k) {
     constexpr int kThreads = WN * WK * 64;
     constexpr int BN = WN * FN * 32, BK = WK * FK * 32;
     constexpr int UN = BN / kUnit, UK = BK / kUnit;          // units of a row
     constexpr int kDyBytes = kRows * BN * 2, kXBytes = kRows * BK * 2;
     constexpr int kGapX = kThreads / UK, kGapDy = kThreads / UN;
-    static_assert(kGapX * 2 == kRows && kGapDy * 2 == kRows, "two units of a thread, kGap rows apart");
+    constexpr int kUnits = kRows / kGapX;        // of a thread, kGap rows apart
+    static_assert(kGapX * kUnits == kRows && kGapDy * kUnits == kRows);
     static_assert((UN == 8 || UN == 16) && (UK == 8 || UK == 16));
     // both stages of dy, then both of x
     extern __shared__ __align__(16) char lds[];
@@ -153,12 +154,12 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
         return s.left >= kRows ? r : r < s.left ? r : s.left > 0 ? s.left - 1 : 0;
     };
 
-    // ---- loads: two units of dy and of x per thread, a half at a time. Rows
+    // ---- loads: units of dy and of x, a half at a time. Rows
     // that are not the stage's are put down as zeros; pieces past the last column
     // are read as others (results of columns that nobody stores) ----
     const int dy_row = tid / UN, dy_col = tid % UN * kUnit;
     const int x_row = tid / UK, x_col = tid % UK * kUnit;
-    Unit dyr[2];
+    Unit dyr[kUnits];
     auto fetch_dy = [&](const Stage &s, int c, int half) {
         // (a piece before the stage's first row: what is read back from the end
         // may begin there, and offsets are unsigned)
@@ -179,15 +180,15 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
         if (half) dyr[c].hi = v;
         else dyr[c].lo = v;
     };
-    int index[2] = {};
+    int index[kUnits] = {};
     auto fetch_index = [&](const Stage &s, int c) {
         if constexpr (INDEXED) index[c] = (g.index + s.m0)[row_in(s, c * kGapX + x_row)];
     };
     struct Raw { u32x4 q; uint32_t s; };
-    Raw xq[PACKED ? 2 : 1];
-    Unit xu[PACKED ? 1 : 2];
-    bool live[2];
-    uint32_t x_of[2];
+    Raw xq[PACKED ? kUnits : 1];
+    Unit xu[PACKED ? 1 : kUnits];
+    bool live[kUnits];
+    uint32_t x_of[kUnits];
     auto fetch_x = [&](const Stage &s, int c, int half) {
         if (half == 0) {
             const int r = c * kGapX + x_row, i = INDEXED ? index[c] : s.m0 + r;
@@ -332,33 +333,34 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
 #pragma unroll
         for (int j = 0; j < FK; ++j) rb[j] += delta_x;
     };
-    // What stands at 32 places of a stage: a unit is made ready and put down and
-    // its registers filled again, a load or a store at a time. Loads are waited
-    // for in their order, so each is used after about as many others.
+    // What stands at the places of a stage, 16 for each unit: a unit is made ready
+    // and put down and its registers filled again, a load or a store at a time.
+    // Loads are waited for in their order, so each is used after about as many
+    // others. All units have been put down by the middle of the stage.
     auto at_place = [&](int at) {
-        if (at < kParts) ready_x(0, at);
-        else if (at < 2 * kParts) ready_x(1, at - kParts);
-        switch (at) {
-            case 1: put_dy(put_of, 0, 0); break;
-            case 2: fetch_dy(fetch_of, 0, 0); break;
-            case 4: put_x(0, 0); break;
-            case 5: put_dy(put_of, 0, 1); break;
-            case 6: fetch_dy(fetch_of, 0, 1); break;
-            case 7: put_x(0, 1); break;
-            case 8: fetch_x(fetch_of, 0, 0); break;
-            case 9: put_dy(put_of, 1, 0); fetch_x(fetch_of, 0, 1); fetch_index(index_of, 0); break;
-            case 10: fetch_dy(fetch_of, 1, 0); break;
-            case 12: put_x(1, 0); break;
-            case 13: put_dy(put_of, 1, 1); break;
-            case 14: fetch_dy(fetch_of, 1, 1); break;
-            case 15: put_x(1, 1); break;
-            case 16: fetch_x(fetch_of, 1, 0); break;
-            case 17: fetch_x(fetch_of, 1, 1); fetch_index(index_of, 1); break;
-            default: break;
+        const int c = at / kParts, r = at % kParts;
+        if (c < kUnits) {
+            ready_x(c, r);
+            switch (r) {
+                case 1: put_dy(put_of, c, 0); break;
+                case 2: fetch_dy(fetch_of, c, 0); break;
+                case 4: put_x(c, 0); break;
+                case 5: put_dy(put_of, c, 1); break;
+                case 6: fetch_dy(fetch_of, c, 1); break;
+                case 7: put_x(c, 1); break;
+                default: break;
+            }
+        }
+        if (c > 0 && c <= kUnits) {
+            if (r == 0) fetch_x(fetch_of, c - 1, 0);
+            if (r == 1) {
+                fetch_x(fetch_of, c - 1, 1);
+                fetch_index(index_of, c - 1);
+            }
         }
     };
-    constexpr int kEach = 32 / (kSteps * kAll);
-    static_assert(kEach * kSteps * kAll == 32);
+    constexpr int kEach = 2 * kParts * kUnits / (kSteps * kAll);
+    static_assert(kEach * kSteps * kAll == 2 * kParts * kUnits);
     // The products of one step on `use`, while the operands of `step` are read
     // into `load`. A wave issues in order, and what stands between matrix
     // instructions runs beside them.
@@ -436,20 +438,20 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void k_wgrad(
     index_of = fetch_of;
     next_stage(index_of);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) fetch_index(put_of, c);
+    for (int c = 0; c < kUnits; ++c) fetch_index(put_of, c);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) fetch_dy(put_of, c / 2, c % 2);
+    for (int c = 0; c < 2 * kUnits; ++c) fetch_dy(put_of, c / 2, c % 2);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) fetch_x(put_of, c / 2, c % 2);
+    for (int c = 0; c < 2 * kUnits; ++c) fetch_x(put_of, c / 2, c % 2);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) fetch_index(fetch_of, c);
+    for (int c = 0; c < kUnits; ++c) fetch_index(fetch_of, c);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < 2 * kUnits; ++c) {
         put_dy(put_of, c / 2, c % 2);
         fetch_dy(fetch_of, c / 2, c % 2);
     }
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < kUnits; ++c) {
 #pragma unroll
         for (int part = 0; part < kParts; ++part) ready_x(c, part);
         put_x(c, 0);
@@ -579,7 +581,7 @@ hipError_t wgrad_as(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_larg
     constexpr int BN = WN * FN * 32, BK = WK * FK * 32, kThreads = WN * WK * 64;
     constexpr int kLds = 2 * kRows * (BN + BK) * 2;
     // as many workgroups as fit at once: two waves per SIMD
-    constexpr int kPerCu = 512 / kThreads;
+    constexpr int kPerCu = FN * FK > 8 ? 1 : 512 / kThreads;
     const int64_t tn = (g.N + BN - 1) / BN, tk = (g.K + BK - 1) / BK, total = tn * tk * g.G * g.parts;
     too_large = total > 0x7FFFFFFF - kPerCu * c.num_cu;
     if (too_large) return hipSuccess;

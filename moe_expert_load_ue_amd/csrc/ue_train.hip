@@ -78,8 +78,8 @@ int check_rows(ue_ctx *c, const char *what, const char *name, const void *p, int
 int check_wgrad(ue_ctx *c, const ue_weight_grad_product *p) {
     const char *what = "ue_weight_grad";
     if (!p) return fail(c, UE_EINVAL, "%s: null product", what);
-    if (p->M < 0 || p->N < 0 || p->K < 0 || p->N > kMaxCols || p->K > kMaxCols ||
-        p->x_rows < 0)
+    if (p->M < 0 || p->M > (1 << 30) || p->N < 0 || p->K < 0 || p->N > kMaxCols ||
+        p->K > kMaxCols || p->x_rows < 0)
         return fail(c, UE_ESHAPE, "%s: M=%d N=%d K=%d x_rows=%d", what, p->M, p->N, p->K,
                     p->x_rows);
     if (p->offsets ? p->groups < 0 || p->groups > kMaxGroups : p->groups != 1)

@@ -151,6 +151,35 @@ def test_balance_many_and_clamped_sequences():
     ctx.close()
 
 
+def test_balance_among_empty_sequences():
+    """A million empty sequences in one place, and offsets that decrease: each
+    workgroup looks past them, none goes round in circles."""
+    say("balance among empty sequences")
+    T, E, k = 1000, 32, 2
+    ctx = ctx_for(E, k, T)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.randn((T, E), generator=g, device=DEV)
+    ids = x.topk(k, 1).indices.int()
+    n = 1 << 20
+    off = torch.full((n + 1,), 333, dtype=torch.int32, device=DEV)
+    off[0], off[-2:] = 0, torch.tensor([700, 1000], dtype=torch.int32)
+    loss, counts, prob = ue.ue_balance(ctx, x, ids, off)
+    few = torch.tensor([0, 333, 700, 1000], dtype=torch.int32, device=DEV)
+    want = ue.ue_balance(ctx, x, ids, few)
+    keep = torch.tensor([0, n - 2, n - 1], device=DEV)
+    assert torch.equal(loss[keep], want[0]) and torch.equal(counts[keep], want[1])
+    assert torch.equal(prob[keep], want[2])
+    assert int((loss != 0).sum()) == 3 and int(counts.sum()) == T * k
+    d = ue.ue_balance_backward(ctx, x, counts, torch.ones(n, device=DEV), off)
+    assert torch.equal(d, ue.ue_balance_backward(ctx, x, want[1], torch.ones(3, device=DEV), few))
+    for bad in ([1000, 500, 0], [0, 900, 100, 1000, 50, 600], [-7, 2000, -7, 2000]):
+        bad = torch.tensor(bad, dtype=torch.int32, device=DEV)
+        loss, counts, _ = ue.ue_balance(ctx, x, ids, bad)
+        ue.ue_balance_backward(ctx, x, counts, loss, bad)
+    torch.cuda.synchronize()
+    ctx.close()
+
+
 @pytest.mark.parametrize("E", [24, 30])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_balance_strides(E, dtype):
@@ -698,6 +727,32 @@ def test_combine_past_4_gib():
     size = (dout[t].double() * y[at].double()).abs().sum(1)
     assert bool(((dw[t, j].double() - want).abs() <= (H / 64 + 20) * U * size).all())
     assert int((dy != 0).any(1).sum()) == at.numel()
+    ctx.close()
+
+
+def test_more_than_one_launch_holds():
+    """Tokens and rows past what a launch's threads reach: the parts behind the
+    first launch are done too."""
+    say("combine in parts")
+    T = (1 << 25) + 3
+    ctx = ue.Context(2, 1, 0, 1, T, device=DEV)
+    inv = torch.arange(T, device=DEV, dtype=torch.int32).flip(0).contiguous().view(T, 1)
+    y = (torch.arange(T, device=DEV) % 251).bfloat16().view(T, 1)
+    out = ue.ue_combine(ctx, y, inv)
+    assert torch.equal(out, y.flip(0))
+    w = torch.full((T, 1), 2.0, device=DEV)
+    dy, dw = ue.ue_combine_backward(ctx, y, inv, w, y)
+    assert torch.equal(dy, 2 * y.flip(0))
+    assert torch.equal(dw, y.float() * y.flip(0).float())
+    del inv, out, w, dy, dw
+    say("pack in parts")
+    M = (1 << 29) + 5
+    x = torch.zeros((M, 1), dtype=BF16, device=DEV)
+    at = torch.tensor([0, 1, (1 << 29) - 1, 1 << 29, M - 1], device=DEV)
+    x[at, 0] = torch.tensor([1.0, -3.0, 127.0, 5.0, -0.5], device=DEV).bfloat16()
+    q, s = ue.ue_pack_rows(ctx, x)
+    assert torch.equal(ue.ue_unpack_rows(ctx, q, s), x)
+    assert int((q[:, 0] != 0).sum()) == 5
     ctx.close()
 
 

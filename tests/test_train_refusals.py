@@ -127,7 +127,7 @@ def test_weight_grad(ctx):
         return lib.ue_weight_grad(ctx, ctypes.byref(p), None)
     assert lib.ue_weight_grad(ctx, None, None) == EINVAL
     assert lib.ue_weight_grad(None, None, None) == EINVAL
-    for kw in (dict(M=-1), dict(N=-1), dict(K=-1), dict(N=(1 << 20) + 1), dict(K=(1 << 20) + 1),
+    for kw in (dict(M=-1), dict(M=(1 << 30) + 1, x_rows=1 << 30), dict(N=-1), dict(K=-1), dict(N=(1 << 20) + 1), dict(K=(1 << 20) + 1),
                dict(x_rows=-1), dict(x_rows=0), dict(groups=-1), dict(groups=1 << 20),
                dict(offsets=None), dict(lddy=23), dict(ldx=40), dict(ldx=56), dict(lds=1),
                dict(ldo=39), dict(out_stride=24 * 40 - 1), dict(index_div=0), dict(index=None),
