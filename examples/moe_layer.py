@@ -4,8 +4,9 @@ computes it, on one MI355X:
 - many tokens (prefill, training): router logits -> ue_gate -> ue_rebalance ->
   ue_quantize_rows -> ue_matmul_i8 over the plan's slots (gated, the tokens
   gathered through the dispatch permutation) -> ue_quantize_rows ->
-  ue_matmul_i8 -> weighted sum through the inverse permutation; and the
-  router's gradient from the weights' (ue_gate_backward);
+  ue_matmul_i8 -> weighted sum through the inverse permutation (ue_combine);
+  and the router's gradient from the weights' (ue_combine_backward,
+  ue_gate_backward); examples/moe_train.py has a whole training step;
 - a few tokens (decode): ue_register_layer once, then ue_moe_tokens.
 
 Both use the same weights; the script prints how far the two are apart on the
@@ -23,6 +24,16 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import moe_expert_load_ue_amd as ue  # noqa: E402
+
+
+class Saved(dict):
+    """What the passes between need; the experts' rows by token and place on
+    request."""
+
+    def __missing__(self, key):
+        if key != "rows":
+            raise KeyError(key)
+        return self["y"][self["inv"].long()]                   # [T, k, H]
 
 
 class Layer:
@@ -69,17 +80,18 @@ class Layer:
                             out_dtype=torch.float32, **slots)
         q, qs = ue.ue_quantize_rows(ctx, h)
         y = ue.ue_matmul_i8(ctx, q, qs, self.down, self.down_scale, **slots)
-        rows = y[r["inv_perm"][0].view(-1, k).long()]          # [T, k, H]
-        out = (rows.float() * weights[..., None]).sum(1).bfloat16()
-        return out, dict(logits=logits, ids=ids, rows=rows, plan=plan,
-                         counts=r["counts"])
+        inv = r["inv_perm"][0].view(-1, k)
+        out = ue.ue_combine(ctx, y, inv, weights)
+        return out, Saved(logits=logits, ids=ids, weights=weights, y=y, inv=inv,
+                          plan=plan, counts=r["counts"])
 
     def router_gradient(self, x, saved, dout):
         """Gradient of the router's matrix from that of the output (the part
         that flows through the routing weights)."""
-        dw = (saved["rows"].float() * dout.float()[:, None, :]).sum(-1)
-        dlogits = ue.ue_gate_backward(self.ctx, saved["logits"], saved["ids"],
-                                      dw.contiguous(), **self.rule)
+        _, dw = ue.ue_combine_backward(self.ctx, dout, saved["inv"], saved["weights"],
+                                       y=saved["y"], with_dy=False)
+        dlogits = ue.ue_gate_backward(self.ctx, saved["logits"], saved["ids"], dw,
+                                      **self.rule)
         return dlogits.t() @ x.float()
 
     def few(self, x):
