@@ -88,8 +88,9 @@ class Layer:
     def router_gradient(self, x, saved, dout):
         """Gradient of the router's matrix from that of the output (the part
         that flows through the routing weights)."""
+        y = saved["y"] if dout.dtype == saved["y"].dtype else saved["y"].to(dout.dtype)
         _, dw = ue.ue_combine_backward(self.ctx, dout, saved["inv"], saved["weights"],
-                                       y=saved["y"], with_dy=False)
+                                       y=y, with_dy=False)
         dlogits = ue.ue_gate_backward(self.ctx, saved["logits"], saved["ids"], dw,
                                       **self.rule)
         return dlogits.t() @ x.float()
