@@ -23,32 +23,23 @@ namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-template <typename T, int L, int VP>
-__device__ __forceinline__ int expert_of_slot(int at, int i, bool vec) {
-    return vec ? 4 * (at + L * (i / 4)) + i % 4 : at + L * i;
+// Slot i of lane `at` holds this expert: four in a row, so that a lane loads 16
+// bytes (8 of bf16) and the lanes of a token 64 and more side by side.
+template <int L>
+__device__ __forceinline__ int expert_of_slot(int at, int i) {
+    return 4 * (at + L * (i / 4)) + i % 4;
 }
 
 // The logits of one row that lane `at` holds, -inf past the last expert.
 template <typename T, int L, int VP>
-__device__ __forceinline__ void load_token(const T *row, int at, int E, bool vec,
-                                           float (&x)[VP]) {
-    if (vec) {
-        struct alignas(4 * sizeof(T)) Pack { T v[4]; };
+__device__ __forceinline__ void load_token(const T *row, int at, int E, float (&x)[VP]) {
 #pragma unroll
-        for (int c = 0; c < VP / 4; ++c) {
-            const int e = 4 * (at + L * c);
-            Pack p;
-            if (e < E) p = *reinterpret_cast<const Pack *>(row + e);
+    for (int c = 0; c < VP / 4; ++c) {
+        const int e = expert_of_slot<L>(at, 4 * c);
+        float f[4];
+        load_run<4, false>(row + e, E - e, f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[4 * c + i] = e < E ? widen<T>(p.v[i]) : -__builtin_inff();
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < VP; ++i) {
-            const int e = at + L * i;
-            x[i] = e < E ? widen<T>(row[e]) : -__builtin_inff();
-        }
+        for (int i = 0; i < 4; ++i) x[4 * c + i] = e + i < E ? f[i] : -__builtin_inff();
     }
 }
 
@@ -85,6 +76,9 @@ __device__ __forceinline__ void scores(float (&x)[VP], float (&slope)[SLOPE ? VP
 #pragma unroll
     for (int i = 0; i < VP; ++i) x[i] *= inv;
 }
+
+// Experts of a row of partial sums: rows in pieces of four.
+__device__ __forceinline__ int padded(int E) { return (E + 3) & ~3; }
 
 // Bounds of sequences, clamped to the tokens there are.
 struct Sequences {
@@ -123,9 +117,9 @@ __global__ __launch_bounds__(kFwdBlock) void k_balance(BalanceArgs g) {
     const T *logits = static_cast<const T *>(g.logits);
     // (the next sequence is looked for behind this one's end, past any number of
     // empty ones; offsets that decrease may not lead back)
-    int s = WHOLE ? c : seqs.find(t0), after = g.n_seq;
-    for (; s < g.n_seq; s = after) {
+    for (int s = WHOLE ? c : seqs.find(t0), after; s < g.n_seq; s = after) {
         int a = seqs.begin(s), b = seqs.begin(s + 1);
+        after = g.n_seq;
         if constexpr (!WHOLE) {
             if (a >= t1) break;
             if (b < t1) {
@@ -149,7 +143,7 @@ __global__ __launch_bounds__(kFwdBlock) void k_balance(BalanceArgs g) {
         float x[VP], next[VP], none[1];
         auto load = [&](int t, float (&to)[VP]) {
             const int mine = t + sub < b ? t + sub : b - 1;
-            load_token<T, L, VP>(logits + mine * g.ld, at, E, g.vec, to);
+            load_token<T, L, VP>(logits + mine * g.ld, at, E, to);
         };
         int t = a + wv * kEach;
         if (t < b) load(t, x);
@@ -167,10 +161,10 @@ __global__ __launch_bounds__(kFwdBlock) void k_balance(BalanceArgs g) {
         for (int i = 0; i < VP; ++i) {
 #pragma unroll
             for (int d = L; d < 64; d <<= 1) acc[i] += __shfl_xor(acc[i], d);
-            if (sub == 0) sums[wv][expert_of_slot<T, L, VP>(at, i, g.vec)] = acc[i];
+            if (sub == 0) sums[wv][expert_of_slot<L>(at, i)] = acc[i];
         }
         __syncthreads();
-        const int64_t slot = static_cast<int64_t>(WHOLE ? s : c + s) * E;
+        const int64_t slot = static_cast<int64_t>(WHOLE ? s : c + s) * (WHOLE ? E : padded(E));
         const float inv_n = b > a ? 1.0f / static_cast<float>(b - a) : 0.f;
         float term = 0.f;
         for (int e = tid; e < E; e += kFwdBlock) {
@@ -222,52 +216,33 @@ __global__ __launch_bounds__(kEndBlock) void k_balance_end(BalanceArgs g) {
     for (int e0 = 0; e0 < E; e0 += 256) {
         float v[4] = {};
         int m[4] = {};
-        if (E % 4 == 0) {
-            // four experts of a lane, four shares at once
-            typedef int i32x4 __attribute__((ext_vector_type(4)));
-            const int e = e0 + 4 * lane < E ? e0 + 4 * lane : 0;
-            for (int c = c0 + wv; c < c1; c += 4 * kEndWaves) {
-                f32x4 p[4];
-                i32x4 n4[4];
+        // four experts of a lane, four shares at once
+        typedef int i32x4 __attribute__((ext_vector_type(4)));
+        const int EP = padded(E), e = e0 + 4 * lane < EP ? e0 + 4 * lane : 0;
+        for (int c = c0 + wv; c < c1; c += 4 * kEndWaves) {
+            f32x4 p[4];
+            i32x4 n4[4];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int cc = c + u * kEndWaves < c1 ? c + u * kEndWaves : c;
-                    const int64_t slot = static_cast<int64_t>(cc + s) * E + e;
-                    p[u] = *reinterpret_cast<const f32x4 *>(g.part + slot);
-                    n4[u] = *reinterpret_cast<const i32x4 *>(g.part_n + slot);
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (c + u * kEndWaves < c1) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            v[i] += p[u][i];
-                            m[i] += n4[u][i];
-                        }
-                    }
+            for (int u = 0; u < 4; ++u) {
+                const int cc = c + u * kEndWaves < c1 ? c + u * kEndWaves : c;
+                const int64_t slot = static_cast<int64_t>(cc + s) * EP + e;
+                p[u] = *reinterpret_cast<const f32x4 *>(g.part + slot);
+                n4[u] = *reinterpret_cast<const i32x4 *>(g.part_n + slot);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sums[wv][4 * lane + i] = v[i];
-                counts[wv][4 * lane + i] = m[i];
-            }
-        } else {
-            for (int c = c0 + wv; c < c1; c += kEndWaves) {
-                const int64_t slot = static_cast<int64_t>(c + s) * E + e0;
+            for (int u = 0; u < 4; ++u)
+                if (c + u * kEndWaves < c1) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int e = lane + 64 * i;
-                    if (e0 + e < E) {
-                        v[i] += g.part[slot + e];
-                        m[i] += g.part_n[slot + e];
+                    for (int i = 0; i < 4; ++i) {
+                        v[i] += p[u][i];
+                        m[i] += n4[u][i];
                     }
                 }
-            }
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sums[wv][lane + 64 * i] = v[i];
-                counts[wv][lane + 64 * i] = m[i];
-            }
+        for (int i = 0; i < 4; ++i) {
+            sums[wv][4 * lane + i] = v[i];
+            counts[wv][4 * lane + i] = m[i];
         }
         __syncthreads();
         if (tid < 256 && e0 + tid < E) {
@@ -314,7 +289,7 @@ __global__ __launch_bounds__(kBlock) void k_balance_backward(BalanceBackArgs g, 
         const bool real = t < t1;
         const int mine = real ? t : t1 - 1;
         float x[VP], slope[VP];
-        load_token<T, L, VP>(logits + mine * g.ld, at, E, g.vec, x);
+        load_token<T, L, VP>(logits + mine * g.ld, at, E, x);
         if (real && t >= to) {
             s = seqs.find(t);
             if (s < g.n_seq) {
@@ -325,7 +300,7 @@ __global__ __launch_bounds__(kBlock) void k_balance_backward(BalanceBackArgs g, 
                     (static_cast<float>(E) / (static_cast<float>(g.k) * n)) / n;
 #pragma unroll
                 for (int i = 0; i < VP; ++i) {
-                    const int e = expert_of_slot<T, L, VP>(at, i, g.vec);
+                    const int e = expert_of_slot<L>(at, i);
                     cw[i] = e < E ? static_cast<float>(
                                 g.counts[static_cast<int64_t>(s) * E + e]) * f : 0.f;
                 }
@@ -347,30 +322,15 @@ __global__ __launch_bounds__(kBlock) void k_balance_backward(BalanceBackArgs g, 
         }
         if (!real || (g.accumulate && !inside)) continue;
         T *row = out + t * g.ld_out;
-        if (g.vec) {
-            struct alignas(4 * sizeof(T)) Pack { T v[4]; };
 #pragma unroll
-            for (int c = 0; c < VP / 4; ++c) {
-                const int e = 4 * (at + L * c);
-                if (e >= E) continue;
-                Pack p;
-                if (g.accumulate) {
-                    p = *reinterpret_cast<const Pack *>(row + e);
+        for (int c = 0; c < VP / 4; ++c) {
+            const int e = expert_of_slot<L>(at, 4 * c);
+            if (e >= E) continue;
+            float f[4];
+            if (g.accumulate) load_run<4, false>(row + e, E - e, f);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[4 * c + i] += widen<T>(p.v[i]);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) p.v[i] = narrow<T>(x[4 * c + i]);
-                *reinterpret_cast<Pack *>(row + e) = p;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < VP; ++i) {
-                const int e = at + L * i;
-                if (e >= E) continue;
-                if (g.accumulate) x[i] += widen<T>(row[e]);
-                row[e] = narrow<T>(x[i]);
-            }
+            for (int i = 0; i < 4; ++i) f[i] = (g.accumulate ? f[i] : 0.f) + x[4 * c + i];
+            store_run<4, false>(row + e, E - e, f);
         }
     }
 }

@@ -26,7 +26,7 @@ __global__ __launch_bounds__(kBlock) void k_pack(PackArgs g, FastDiv per_row, ui
     const uint32_t m = div_by(b, per_row), c = b - m * per_row.d;
     const int k = c * UE_PACK_BLOCK + (threadIdx.x & 3) * 8;
     float f[8];
-    load8<T>(static_cast<const T *>(g.x) + m * g.ldx + k, g.vec, g.K - k, f);
+    load8<T>(static_cast<const T *>(g.x) + m * g.ldx + k, g.K - k, f);
     uint64_t q;
     const uint32_t s = pack8(f, q);
     *reinterpret_cast<uint64_t *>(g.q + m * g.ldq + k) = q;
@@ -42,7 +42,7 @@ __global__ __launch_bounds__(kBlock) void k_unpack(PackArgs g, FastDiv per_row, 
     const uint64_t q = *reinterpret_cast<const uint64_t *>(g.q_in + m * g.ldq + k);
     float f[8];
     unpack8(q, g.scale_in[m * g.lds + c], f);
-    store8<T>(static_cast<T *>(g.out) + m * g.ldx + k, g.vec, g.K - k, f);
+    store8<T>(static_cast<T *>(g.out) + m * g.ldx + k, g.K - k, f);
 }
 
 template <typename T, bool KEEP>
@@ -53,11 +53,11 @@ __global__ __launch_bounds__(kBlock) void k_gated(GatedArgs g, FastDiv per_row, 
     const int k = c * UE_PACK_BLOCK + (threadIdx.x & 3) * 8;
     const T *row = static_cast<const T *>(g.gu) + m * g.ldin + k;
     float gate[8], up[8], h[8];
-    load8<T>(row, g.vec, g.I - k, gate);
-    load8<T>(row + g.I, g.vec, g.I - k, up);
+    load8<T>(row, g.I - k, gate);
+    load8<T>(row + g.I, g.I - k, up);
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = silu_of(gate[i]) * up[i];
-    store8<T>(static_cast<T *>(g.h) + m * g.ldh + k, g.vec, g.I - k, h);
+    store8<T>(static_cast<T *>(g.h) + m * g.ldh + k, g.I - k, h);
     if (KEEP) {
         uint64_t q;
         int8_t *to = g.q + m * g.ldq + k;
@@ -86,7 +86,7 @@ __global__ __launch_bounds__(kBlock) void k_gated_backward(GatedArgs g, FastDiv 
         reinterpret_cast<const uint64_t *>(from + per_row.d * UE_PACK_BLOCK));
     const uint32_t sg = st[0], su = st[per_row.d];
     float d[8], gate[8], up[8], h[8];
-    load8<T>(static_cast<const T *>(g.dh) + m * g.ldin + k, g.vec, g.I - k, d);
+    load8<T>(static_cast<const T *>(g.dh) + m * g.ldin + k, g.I - k, d);
     unpack8(qg, sg, gate);
     unpack8(qu, su, up);
 #pragma unroll
@@ -101,9 +101,9 @@ __global__ __launch_bounds__(kBlock) void k_gated_backward(GatedArgs g, FastDiv 
         up[i] = d[i] * silu;
     }
     T *row = static_cast<T *>(g.dgu) + m * g.lddgu + k;
-    store8<T>(row, g.vec, g.I - k, gate);
-    store8<T>(row + g.I, g.vec, g.I - k, up);
-    if (g.h) store8<T>(static_cast<T *>(g.h) + m * g.ldh + k, g.vec, g.I - k, h);
+    store8<T>(row, g.I - k, gate);
+    store8<T>(row + g.I, g.I - k, up);
+    if (g.h) store8<T>(static_cast<T *>(g.h) + m * g.ldh + k, g.I - k, h);
 }
 
 // Rows of `per_row` blocks each, in launches of at most kLaunchBlocks blocks:

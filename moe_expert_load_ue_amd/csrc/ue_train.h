@@ -9,23 +9,21 @@ namespace ue {
 struct BalanceArgs {
     const void *logits;         // [T] rows of E, ld elements apart
     int64_t ld;
-    bool bf16, vec;             // vec: four logits load (and store) at once
-    bool sigmoid;
+    bool bf16, sigmoid;
     int E, k, T, n_seq;
     const int32_t *ids;
     const int32_t *offsets;     // [n_seq + 1] or null (one sequence)
     int32_t *counts;
     float *prob, *loss;
     int chunk;                  // tokens of a workgroup's share
-    float *part;                // [slots][E] sums of p; slot: chunk + sequence;
+    float *part;                // [slots][E up to 4 n] sums of p; slot: chunk + sequence;
                                 // null: a workgroup per sequence, no partial sums
-    int32_t *part_n;            // [slots][E] assignments
+    int32_t *part_n;            // likewise: assignments
 };
 struct BalanceBackArgs {
     const void *logits;
     int64_t ld;
-    bool bf16, vec;             // vec: of the gradient's rows too
-    bool sigmoid, accumulate;
+    bool bf16, sigmoid, accumulate;
     int E, k, T, n_seq;
     const int32_t *offsets, *counts;
     const float *dloss;
@@ -40,12 +38,12 @@ hipError_t launch_balance(const ue_ctx &c, const BalanceArgs &g, hipStream_t s);
 hipError_t launch_balance_backward(const ue_ctx &c, const BalanceBackArgs &g,
                                    hipStream_t s);
 
-// Rows and their packed form. `vec`: the unpacked rows start 16-byte aligned.
+// Rows and their packed form.
 struct PackArgs {
     const void *x;
     void *out;                  // unpacking: where the values go
     int64_t ldx;
-    bool bf16, vec;
+    bool bf16;
     int M, K;
     int8_t *q;
     const int8_t *q_in;
@@ -61,7 +59,7 @@ struct GatedArgs {
     const void *gu;             // forward: [M] rows of 2 I
     const void *dh;             // backward: [M] rows of I
     int64_t ldin;
-    bool bf16, vec;             // vec: every row's pieces are 16-byte aligned
+    bool bf16;
     int M, I;
     void *h;                    // may be null backward
     int64_t ldh;
@@ -81,7 +79,7 @@ struct CombineArgs {
     const void *y;              // [rows] rows of H
     int64_t ldy;
     int rows;
-    bool bf16, vec;             // vec: all rows are 16-byte aligned
+    bool bf16;
     const int32_t *inv;
     const float *weights;       // or null (ones)
     int T, k, H;
@@ -140,47 +138,65 @@ __device__ __forceinline__ float narrow<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ uint16_t narrow<uint16_t>(float v) { return f32_to_bf16(v); }
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
-// Eight elements, or those of them before `n`, at p. Past the caches, both ways:
-// what these kernels read and write is used once each, and is larger than the
-// caches where time counts (gated activation of 32768 rows of 2048 with its
-// backward pass 258 us through the caches, 181 past them; gradients of the sum of
-// rows, 16384 tokens x top-8 x 7168, 1020 against 881).
-template <typename T, bool ONCE = true>
-__device__ __forceinline__ void load8(const T *p, bool vec, int n, float (&f)[8]) {
-    if (vec && n >= 8) {
-        struct Pack { u32x4 v[sizeof(T) / 2]; } k;
+// N elements, or those of them before `n`, at p, in loads and stores of up to 16
+// bytes whatever p's alignment (the device takes any). ONCE: past the caches, both
+// ways: most of what these kernels read and write is used once each, and is
+// larger than the caches where time counts (gated activation of 32768 rows of
+// 2048 with its backward pass 258 us through the caches, 181 past them; gradients
+// of the sum of rows, 16384 tokens x top-8 x 7168, 1020 against 881).
+template <int BYTES>
+struct Words {
+    typedef uint32_t type __attribute__((ext_vector_type(BYTES / 4), aligned(2)));
+};
+template <int N, bool ONCE, typename T>
+__device__ __forceinline__ void load_run(const T *p, int n, float (&f)[N]) {
+    constexpr int kBytes = N * sizeof(T), kPiece = kBytes < 16 ? kBytes : 16;
+    typedef typename Words<kPiece>::type W;
+    if (n >= N) {
+        struct Pack { W v[kBytes / kPiece]; } k;
 #pragma unroll
-        for (size_t c = 0; c < sizeof(T) / 2; ++c) {
-            const u32x4 *at = reinterpret_cast<const u32x4 *>(p) + c;
+        for (int c = 0; c < kBytes / kPiece; ++c) {
+            const W *at = reinterpret_cast<const W *>(p) + c;
             k.v[c] = ONCE ? __builtin_nontemporal_load(at) : *at;
         }
-        struct Elements { T v[8]; };
+        struct Elements { T v[N]; };
         const Elements e = __builtin_bit_cast(Elements, k);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = widen<T>(e.v[i]);
+        for (int i = 0; i < N; ++i) f[i] = widen<T>(e.v[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = i < n ? widen<T>(p[i]) : 0.f;
+        for (int i = 0; i < N; ++i) f[i] = i < n ? widen<T>(p[i]) : 0.f;
+    }
+}
+template <int N, bool ONCE, typename T>
+__device__ __forceinline__ void store_run(T *p, int n, const float (&f)[N]) {
+    constexpr int kBytes = N * sizeof(T), kPiece = kBytes < 16 ? kBytes : 16;
+    typedef typename Words<kPiece>::type W;
+    if (n >= N) {
+        struct Elements { T v[N]; } e;
+#pragma unroll
+        for (int i = 0; i < N; ++i) e.v[i] = narrow<T>(f[i]);
+        struct Pack { W v[kBytes / kPiece]; };
+        const Pack k = __builtin_bit_cast(Pack, e);
+#pragma unroll
+        for (int c = 0; c < kBytes / kPiece; ++c) {
+            W *at = reinterpret_cast<W *>(p) + c;
+            if (ONCE) __builtin_nontemporal_store(k.v[c], at);
+            else *at = k.v[c];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n) p[i] = narrow<T>(f[i]);
     }
 }
 template <typename T>
-__device__ __forceinline__ void store8(T *p, bool vec, int n, const float (&f)[8]) {
-    if (vec && n >= 8) {
-        struct Elements { T v[8]; } e;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) e.v[i] = narrow<T>(f[i]);
-        struct Pack { u32x4 v[sizeof(T) / 2]; };
-        const Pack k = __builtin_bit_cast(Pack, e);
-#pragma unroll
-        for (size_t c = 0; c < sizeof(T) / 2; ++c)
-            __builtin_nontemporal_store(k.v[c], reinterpret_cast<u32x4 *>(p) + c);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = narrow<T>(f[i]);
-    }
+__device__ __forceinline__ void load8(const T *p, int n, float (&f)[8]) {
+    load_run<8, true>(p, n, f);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T *p, int n, const float (&f)[8]) {
+    store_run<8, true>(p, n, f);
 }
 
 // The power of two of a block whose largest magnitude has these bits, biased

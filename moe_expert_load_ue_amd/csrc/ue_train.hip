@@ -113,7 +113,7 @@ extern "C" {
 size_t ue_balance_workspace(const ue_ctx *ctx, int32_t T, int32_t n_seq) {
     if (!ctx || T < 0 || n_seq < 0) return 0;
     return static_cast<size_t>(ue::balance_slots(T, n_seq, ctx->E, ctx->num_cu)) *
-           ctx->E * 8;
+           ((ctx->E + 3) / 4 * 4) * 8;
 }
 
 int ue_balance(ue_ctx *ctx, const void *logits, int32_t type, int64_t ld, int32_t T,
@@ -131,11 +131,9 @@ int ue_balance(ue_ctx *ctx, const void *logits, int32_t type, int64_t ld, int32_
         !aligned(workspace, 16))
         return fail(ctx, UE_EINVAL, "ue_balance: unaligned argument");
     ue::BalanceArgs g{};
-    const size_t es = type_bytes(type);
     g.logits = logits;
     g.ld = ld;
     g.bf16 = type == UE_BF16;
-    g.vec = ctx->E % 4 == 0 && rows_aligned(logits, ld, es, 4 * es);
     g.sigmoid = score == UE_SCORE_SIGMOID;
     g.E = ctx->E;
     g.k = ctx->k;
@@ -148,7 +146,7 @@ int ue_balance(ue_ctx *ctx, const void *logits, int32_t type, int64_t ld, int32_
     g.loss = loss;
     if (slots > 0) {
         g.part = static_cast<float *>(workspace);
-        g.part_n = reinterpret_cast<int32_t *>(g.part + slots * ctx->E);
+        g.part_n = reinterpret_cast<int32_t *>(g.part + slots * ((ctx->E + 3) / 4 * 4));
     }
     hipStream_t s = static_cast<hipStream_t>(stream);
     tbegin(ctx, s);
@@ -169,15 +167,12 @@ int ue_balance_backward(ue_ctx *ctx, const void *logits, int32_t type, int64_t l
                     static_cast<ll>(ld_out));
     if ((T > 0 && !dlogits) || (n_seq > 0 && (!counts || !dloss)))
         return fail(ctx, UE_EINVAL, "ue_balance_backward: null argument");
-    const size_t es = type_bytes(type);
-    if (!aligned(counts, 4) || !aligned(dloss, 4) || !aligned(dlogits, es))
+    if (!aligned(counts, 4) || !aligned(dloss, 4) || !aligned(dlogits, type_bytes(type)))
         return fail(ctx, UE_EINVAL, "ue_balance_backward: unaligned argument");
     ue::BalanceBackArgs g{};
     g.logits = logits;
     g.ld = ld;
     g.bf16 = type == UE_BF16;
-    g.vec = ctx->E % 4 == 0 && rows_aligned(logits, ld, es, 4 * es) &&
-            rows_aligned(dlogits, ld_out, es, 4 * es);
     g.sigmoid = score == UE_SCORE_SIGMOID;
     g.accumulate = accumulate != 0;
     g.E = ctx->E;
@@ -209,7 +204,6 @@ int ue_pack_rows(ue_ctx *ctx, const void *x, int32_t type, int64_t ldx, int32_t 
     g.x = x;
     g.ldx = ldx;
     g.bf16 = type == UE_BF16;
-    g.vec = rows_aligned(x, ldx, type_bytes(type), 16);
     g.M = M;
     g.K = K;
     g.q = q;
@@ -237,7 +231,6 @@ int ue_unpack_rows(ue_ctx *ctx, const int8_t *q, int64_t ldq, const uint8_t *sca
     g.out = x;
     g.ldx = ldx;
     g.bf16 = type == UE_BF16;
-    g.vec = rows_aligned(x, ldx, type_bytes(type), 16);
     g.M = M;
     g.K = K;
     g.q_in = q;
@@ -264,12 +257,10 @@ int ue_gated(ue_ctx *ctx, const void *gu, int32_t type, int64_t ldgu, int32_t M,
         if (int rc = check_packed(ctx, "ue_gated", q, ldq, scale, lds, M,
                                   2 * nb * UE_PACK_BLOCK, 2 * nb))
             return rc;
-    const size_t es = type_bytes(type);
     ue::GatedArgs g{};
     g.gu = gu;
     g.ldin = ldgu;
     g.bf16 = type == UE_BF16;
-    g.vec = I * es % 16 == 0 && rows_aligned(gu, ldgu, es, 16) && rows_aligned(h, ldh, es, 16);
     g.M = M;
     g.I = I;
     g.h = h;
@@ -298,13 +289,10 @@ int ue_gated_backward(ue_ctx *ctx, const int8_t *q, int64_t ldq, const uint8_t *
     const int64_t nb = blocks_of(I);
     if (int rc = check_packed(ctx, what, q, ldq, scale, lds, M, 2 * nb * UE_PACK_BLOCK, 2 * nb))
         return rc;
-    const size_t es = type_bytes(type);
     ue::GatedArgs g{};
     g.dh = dh;
     g.ldin = lddh;
     g.bf16 = type == UE_BF16;
-    g.vec = I * es % 16 == 0 && rows_aligned(dh, lddh, es, 16) &&
-            rows_aligned(dgu, lddgu, es, 16) && (!h || rows_aligned(h, ldh, es, 16));
     g.M = M;
     g.I = I;
     g.h = h;
@@ -386,14 +374,11 @@ int ue_combine(ue_ctx *ctx, const void *y, int32_t type, int64_t ldy, int32_t ro
     if (T > 0 && !inv_perm) return fail(ctx, UE_EINVAL, "ue_combine: null inv_perm");
     if (!aligned(inv_perm, 4) || !aligned(weights, 4))
         return fail(ctx, UE_EINVAL, "ue_combine: unaligned argument");
-    const size_t es = type_bytes(type);
     ue::CombineArgs g{};
     g.y = y;
     g.ldy = ldy;
     g.rows = rows;
     g.bf16 = type == UE_BF16;
-    g.vec = rows_aligned(y, ldy, es, 16) && rows_aligned(out, ldo, es, 16) &&
-            (!add || rows_aligned(add, ldadd, es, 16));
     g.inv = inv_perm;
     g.weights = weights;
     g.T = T;
@@ -426,14 +411,11 @@ int ue_combine_backward(ue_ctx *ctx, const void *dout, int32_t type, int64_t ldd
     if (T > 0 && !inv_perm) return fail(ctx, UE_EINVAL, "%s: null inv_perm", what);
     if (!aligned(inv_perm, 4) || !aligned(weights, 4) || !aligned(dweights, 4))
         return fail(ctx, UE_EINVAL, "%s: unaligned argument", what);
-    const size_t es = type_bytes(type);
     ue::CombineArgs g{};
     g.y = y;
     g.ldy = ldy;
     g.rows = rows;
     g.bf16 = type == UE_BF16;
-    g.vec = rows_aligned(dout, lddout, es, 16) && (!dweights || rows_aligned(y, ldy, es, 16)) &&
-            (!dy || rows_aligned(dy, lddy, es, 16));
     g.inv = inv_perm;
     g.weights = weights;
     g.T = T;
