@@ -31,16 +31,20 @@ __device__ __forceinline__ int expert_of_slot(int at, int i) {
 }
 
 // The logits of one row that lane `at` holds, -inf past the last expert.
-template <typename T, int L, int VP>
+// FOURS: E % 4 == 0, so that a piece is whole or nobody's; those are loaded
+// without a branch, all at once.
+template <typename T, int L, int VP, bool FOURS>
 __device__ __forceinline__ void load_token(const T *row, int at, int E, float (&x)[VP]) {
+    float f[VP / 4][4];
 #pragma unroll
     for (int c = 0; c < VP / 4; ++c) {
         const int e = expert_of_slot<L>(at, 4 * c);
-        float f[4];
-        load_run<4, false>(row + e, E - e, f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[4 * c + i] = e + i < E ? f[i] : -__builtin_inff();
+        if (FOURS) load_run<4, false>(row + (e < E ? e : 0), 4, f[c]);
+        else load_run<4, false>(row + e, E - e, f[c]);
     }
+#pragma unroll
+    for (int i = 0; i < VP; ++i)
+        x[i] = expert_of_slot<L>(at, i) < E ? f[i / 4][i % 4] : -__builtin_inff();
 }
 
 // Scores of a token in place of its logits, 0 where all are masked; `slope`:
@@ -140,23 +144,27 @@ __global__ __launch_bounds__(kFwdBlock) void k_balance(BalanceArgs g) {
         float acc[VP] = {};
         constexpr int kStep = kFwdWaves * kEach;
         // a token's logits are on their way while the one before is summed
-        float x[VP], next[VP], none[1];
-        auto load = [&](int t, float (&to)[VP]) {
-            const int mine = t + sub < b ? t + sub : b - 1;
-            load_token<T, L, VP>(logits + mine * g.ld, at, E, to);
-        };
-        int t = a + wv * kEach;
-        if (t < b) load(t, x);
-        for (; t < b; t += kStep) {
-            if (t + kStep < b) load(t + kStep, next);
-            scores<L, VP, SIGMOID, false>(x, none);
-            if (t + sub < b) {
+        auto tokens = [&](auto fours) {
+            float x[VP], next[VP], none[1];
+            auto load = [&](int t, float (&to)[VP]) {
+                const int mine = t + sub < b ? t + sub : b - 1;
+                load_token<T, L, VP, decltype(fours)::value>(logits + mine * g.ld, at, E, to);
+            };
+            int t = a + wv * kEach;
+            if (t < b) load(t, x);
+            for (; t < b; t += kStep) {
+                if (t + kStep < b) load(t + kStep, next);
+                scores<L, VP, SIGMOID, false>(x, none);
+                if (t + sub < b) {
 #pragma unroll
-                for (int i = 0; i < VP; ++i) acc[i] += x[i];
+                    for (int i = 0; i < VP; ++i) acc[i] += x[i];
+                }
+#pragma unroll
+                for (int i = 0; i < VP; ++i) x[i] = next[i];
             }
-#pragma unroll
-            for (int i = 0; i < VP; ++i) x[i] = next[i];
-        }
+        };
+        if (E % 4 == 0) tokens(std::true_type{});
+        else tokens(std::false_type{});
 #pragma unroll
         for (int i = 0; i < VP; ++i) {
 #pragma unroll
@@ -281,58 +289,64 @@ __global__ __launch_bounds__(kBlock) void k_balance_backward(BalanceBackArgs g, 
     const int t1 = g.T - t0 < chunk ? g.T : t0 + chunk;
     const T *logits = static_cast<const T *>(g.logits);
     T *out = static_cast<T *>(g.dlogits);
-    int t = t0 + wv * kEach + sub;
-    // this token's sequence; its counts times what its gradient is scaled with
-    int s = 0, from = 0, to = -1;
-    float cw[VP] = {};
-    for (; t - sub < t1; t += kWaves * kEach) {
-        const bool real = t < t1;
-        const int mine = real ? t : t1 - 1;
-        float x[VP], slope[VP];
-        load_token<T, L, VP>(logits + mine * g.ld, at, E, x);
-        if (real && t >= to) {
-            s = seqs.find(t);
-            if (s < g.n_seq) {
-                from = seqs.begin(s);
-                to = seqs.begin(s + 1);
-                const float n = static_cast<float>(to - from);
-                const float f = g.dloss[s] *
-                    (static_cast<float>(E) / (static_cast<float>(g.k) * n)) / n;
+    auto tokens = [&](auto fours) {
+        constexpr bool FOURS = decltype(fours)::value;
+        int t = t0 + wv * kEach + sub;
+        // this token's sequence; its counts times what its gradient is scaled with
+        int s = 0, from = 0, to = -1;
+        float cw[VP] = {};
+        for (; t - sub < t1; t += kWaves * kEach) {
+            const bool real = t < t1;
+            const int mine = real ? t : t1 - 1;
+            float x[VP], slope[VP];
+            load_token<T, L, VP, FOURS>(logits + mine * g.ld, at, E, x);
+            if (real && t >= to) {
+                s = seqs.find(t);
+                if (s < g.n_seq) {
+                    from = seqs.begin(s);
+                    to = seqs.begin(s + 1);
+                    const float n = static_cast<float>(to - from);
+                    const float f = g.dloss[s] *
+                        (static_cast<float>(E) / (static_cast<float>(g.k) * n)) / n;
 #pragma unroll
-                for (int i = 0; i < VP; ++i) {
-                    const int e = expert_of_slot<L>(at, i);
-                    cw[i] = e < E ? static_cast<float>(
-                                g.counts[static_cast<int64_t>(s) * E + e]) * f : 0.f;
+                    for (int i = 0; i < VP; ++i) {
+                        const int e = expert_of_slot<L>(at, i);
+                        cw[i] = e < E ? static_cast<float>(
+                                    g.counts[static_cast<int64_t>(s) * E + e]) * f : 0.f;
+                    }
+                } else {
+                    from = to = g.T;       // behind the last sequence
                 }
-            } else {
-                from = to = g.T;       // behind the last sequence
+            }
+            const bool inside = real && t >= from && t < to;
+            scores<L, VP, SIGMOID, true>(x, slope);
+            float dot = 0.f;
+#pragma unroll
+            for (int i = 0; i < VP; ++i) dot = __builtin_fmaf(x[i], cw[i], dot);
+            dot = lanes_sum<L>(dot);
+#pragma unroll
+            for (int i = 0; i < VP; ++i) {
+                x[i] *= cw[i] - dot;
+                if (SIGMOID) x[i] *= slope[i];
+                if (!inside) x[i] = 0.f;
+            }
+            if (!real || (g.accumulate && !inside)) continue;
+            T *row = out + t * g.ld_out;
+#pragma unroll
+            for (int c = 0; c < VP / 4; ++c) {
+                const int e = expert_of_slot<L>(at, 4 * c);
+                if (e >= E) continue;
+                const int n = FOURS ? 4 : E - e;
+                float f[4];
+                if (g.accumulate) load_run<4, false>(row + e, n, f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = (g.accumulate ? f[i] : 0.f) + x[4 * c + i];
+                store_run<4, true>(row + e, n, f);
             }
         }
-        const bool inside = real && t >= from && t < to;
-        scores<L, VP, SIGMOID, true>(x, slope);
-        float dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < VP; ++i) dot = __builtin_fmaf(x[i], cw[i], dot);
-        dot = lanes_sum<L>(dot);
-#pragma unroll
-        for (int i = 0; i < VP; ++i) {
-            x[i] *= cw[i] - dot;
-            if (SIGMOID) x[i] *= slope[i];
-            if (!inside) x[i] = 0.f;
-        }
-        if (!real || (g.accumulate && !inside)) continue;
-        T *row = out + t * g.ld_out;
-#pragma unroll
-        for (int c = 0; c < VP / 4; ++c) {
-            const int e = expert_of_slot<L>(at, 4 * c);
-            if (e >= E) continue;
-            float f[4];
-            if (g.accumulate) load_run<4, false>(row + e, E - e, f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = (g.accumulate ? f[i] : 0.f) + x[4 * c + i];
-            store_run<4, false>(row + e, E - e, f);
-        }
-    }
+    };
+    if (E % 4 == 0) tokens(std::true_type{});
+    else tokens(std::false_type{});
 }
 
 // The lanes and slots that hold E experts: f<L, VP>().
