@@ -47,10 +47,10 @@ __device__ __forceinline__ void load_token(const T *row, int at, int E, float (&
         x[i] = expert_of_slot<L>(at, i) < E ? f[i / 4][i % 4] : -__builtin_inff();
 }
 
-// Scores of a token in place of its logits, 0 where all are masked; `slope`:
-// 1 - sigmoid (untouched for the softmax).
+// Scores of a token in place of its logits, 0 where all are masked, but for the
+// factor that is returned; `slope`: 1 - sigmoid (untouched for the softmax).
 template <int L, int VP, bool SIGMOID, bool SLOPE>
-__device__ __forceinline__ void scores(float (&x)[VP], float (&slope)[SLOPE ? VP : 1]) {
+__device__ __forceinline__ float scores(float (&x)[VP], float (&slope)[SLOPE ? VP : 1]) {
     float sum = 0.f;
     if (SIGMOID) {
 #pragma unroll
@@ -76,9 +76,7 @@ __device__ __forceinline__ void scores(float (&x)[VP], float (&slope)[SLOPE ? VP
         sum = lanes_sum<L>(sum);
         if (sum == 0.f) sum = 1.f;
     }
-    const float inv = 1.0f / sum;
-#pragma unroll
-    for (int i = 0; i < VP; ++i) x[i] *= inv;
+    return 1.0f / sum;
 }
 
 // Experts of a row of partial sums: rows in pieces of four.
@@ -93,7 +91,22 @@ struct Sequences {
         const int o = offsets[s];
         return o < 0 ? 0 : o > T ? T : o;
     }
-    // the first sequence that ends behind token t
+    // the first sequence that ends behind token t, all lanes of a wave looking for
+    // the same: of 64 (the loads that follow on each other are what it costs)
+    __device__ __forceinline__ int find_wave(int t, int lane) const {
+        int lo = 0, hi = n;
+        while (lo < hi) {
+            const int step = (hi - lo + 63) >> 6, last = lo + (lane + 1) * step - 1;
+            // lane i: does sequence lo + (i + 1) step - 1 end behind t?
+            const uint64_t m = __ballot(last >= hi || begin(last + 1) > t);
+            if (m == 0) return hi;
+            const int i = __builtin_ctzll(m), from = lo + i * step;
+            hi = from + step - 1 < hi ? from + step - 1 : hi;
+            lo = from;
+        }
+        return lo;
+    }
+    // the same, for a lane on its own
     __device__ __forceinline__ int find(int t) const {
         int lo = 0, hi = n;
         while (lo < hi) {
@@ -121,13 +134,13 @@ __global__ __launch_bounds__(kFwdBlock) void k_balance(BalanceArgs g) {
     const T *logits = static_cast<const T *>(g.logits);
     // (the next sequence is looked for behind this one's end, past any number of
     // empty ones; offsets that decrease may not lead back)
-    for (int s = WHOLE ? c : seqs.find(t0), after; s < g.n_seq; s = after) {
+    for (int s = WHOLE ? c : seqs.find_wave(t0, lane), after; s < g.n_seq; s = after) {
         int a = seqs.begin(s), b = seqs.begin(s + 1);
         after = g.n_seq;
         if constexpr (!WHOLE) {
             if (a >= t1) break;
             if (b < t1) {
-                after = seqs.find(b);
+                after = seqs.find_wave(b, lane);
                 after = after > s ? after : s + 1;
             }
             a = a > t0 ? a : t0;
@@ -136,14 +149,10 @@ __global__ __launch_bounds__(kFwdBlock) void k_balance(BalanceArgs g) {
         }
         for (int e = tid; e < E; e += kFwdBlock) hist[e] = 0;
         __syncthreads();
-        for (int i = a * g.k + tid; i < b * g.k; i += kFwdBlock) {
-            const int id = g.ids[i];
-            if (static_cast<uint32_t>(id) < static_cast<uint32_t>(E))
-                atomicAdd(&hist[id], 1);
-        }
         float acc[VP] = {};
         constexpr int kStep = kFwdWaves * kEach;
-        // a token's logits are on their way while the one before is summed
+        // a token's logits are on their way while the one before is summed, the
+        // first ones' while the ids are counted
         auto tokens = [&](auto fours) {
             float x[VP], next[VP], none[1];
             auto load = [&](int t, float (&to)[VP]) {
@@ -152,13 +161,17 @@ __global__ __launch_bounds__(kFwdBlock) void k_balance(BalanceArgs g) {
             };
             int t = a + wv * kEach;
             if (t < b) load(t, x);
+            for (int i = a * g.k + tid; i < b * g.k; i += kFwdBlock) {
+                const int id = g.ids[i];
+                if (static_cast<uint32_t>(id) < static_cast<uint32_t>(E))
+                    atomicAdd(&hist[id], 1);
+            }
             for (; t < b; t += kStep) {
                 if (t + kStep < b) load(t + kStep, next);
-                scores<L, VP, SIGMOID, false>(x, none);
-                if (t + sub < b) {
+                float inv = scores<L, VP, SIGMOID, false>(x, none);
+                if (t + sub >= b) inv = 0.f;
 #pragma unroll
-                    for (int i = 0; i < VP; ++i) acc[i] += x[i];
-                }
+                for (int i = 0; i < VP; ++i) acc[i] = __builtin_fmaf(x[i], inv, acc[i]);
 #pragma unroll
                 for (int i = 0; i < VP; ++i) x[i] = next[i];
             }
@@ -289,6 +302,9 @@ __global__ __launch_bounds__(kBlock) void k_balance_backward(BalanceBackArgs g, 
     const int t1 = g.T - t0 < chunk ? g.T : t0 + chunk;
     const T *logits = static_cast<const T *>(g.logits);
     T *out = static_cast<T *>(g.dlogits);
+    // most tokens are of the sequence of the wave's first one
+    const int first = seqs.find_wave(t0 + wv * kEach, lane);
+    const int first_to = first < g.n_seq ? seqs.begin(first + 1) : 0x7FFFFFFF;
     auto tokens = [&](auto fours) {
         constexpr bool FOURS = decltype(fours)::value;
         int t = t0 + wv * kEach + sub;
@@ -301,7 +317,7 @@ __global__ __launch_bounds__(kBlock) void k_balance_backward(BalanceBackArgs g, 
             float x[VP], slope[VP];
             load_token<T, L, VP, FOURS>(logits + mine * g.ld, at, E, x);
             if (real && t >= to) {
-                s = seqs.find(t);
+                s = t < first_to ? first : seqs.find(t);
                 if (s < g.n_seq) {
                     from = seqs.begin(s);
                     to = seqs.begin(s + 1);
@@ -319,10 +335,13 @@ __global__ __launch_bounds__(kBlock) void k_balance_backward(BalanceBackArgs g, 
                 }
             }
             const bool inside = real && t >= from && t < to;
-            scores<L, VP, SIGMOID, true>(x, slope);
+            const float inv = scores<L, VP, SIGMOID, true>(x, slope);
             float dot = 0.f;
 #pragma unroll
-            for (int i = 0; i < VP; ++i) dot = __builtin_fmaf(x[i], cw[i], dot);
+            for (int i = 0; i < VP; ++i) {
+                x[i] *= inv;
+                dot = __builtin_fmaf(x[i], cw[i], dot);
+            }
             dot = lanes_sum<L>(dot);
 #pragma unroll
             for (int i = 0; i < VP; ++i) {
