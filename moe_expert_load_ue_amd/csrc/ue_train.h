@@ -32,7 +32,7 @@ struct BalanceBackArgs {
 };
 // Tokens of a workgroup's share, and the slots of partial sums that T tokens in
 // n_seq sequences need (0: none are made).
-int balance_chunk(int T, int num_cu);
+int balance_chunk(int T, int E, int num_cu);
 int64_t balance_slots(int T, int n_seq, int E, int num_cu);
 hipError_t launch_balance(const ue_ctx &c, const BalanceArgs &g, hipStream_t s);
 hipError_t launch_balance_backward(const ue_ctx &c, const BalanceBackArgs &g,
