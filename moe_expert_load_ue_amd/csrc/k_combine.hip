@@ -4,15 +4,14 @@
 //   out_t = add_t + sum_j w_tj y[inv_tj];  dy[inv_tj] = w_tj dout_t;
 //   dw_tj = <dout_t, y[inv_tj]>
 //
-// Forward: a wave takes one segment of one token's row and loads that segment
-// of up to kJoin of its rows at once before it adds them, in order. Backward: a
-// wave per assignment, those of a token in one workgroup (of up to kJoin waves),
-// so that dout comes from the cache for all but the first; a dot is added by
-// lanes, then over them, in a fixed order. Places and weights are the same for a
-// whole wave and so are read by scalar loads.
+// Forward: the lanes of one segment of one token's row load that segment of up
+// to kJoin of its rows at once before they add them, in order. Backward: those of
+// an assignment go along its row, a token's side by side, so that dout comes from
+// the caches for all but the first; a dot is added by lanes, then over them, in a
+// fixed order. Rows take a wave's 64 lanes or, short ones, 16 or 32 of them.
 //
-// Bound: HBM. 16384 tokens x top-8 x 7168, bf16: forward 372 us (2.1 GB, 5.7
-// TB/s), backward 734 us (4.0 GB, 5.5 TB/s). A workgroup per token whose waves
+// Bound: HBM. 16384 tokens x top-8 x 7168, bf16: forward 367 us (2.1 GB, 5.7
+// TB/s), backward 730 us (4.0 GB, 5.5 TB/s). A workgroup per token whose waves
 // shared out the segments took 880 backward; four segments ahead in place of two
 // 965, one 724 (but 10.9 us in place of 9.8 for 1021 tokens x top-6 x 1002,
 // fp32); dout past the caches too 794.
@@ -22,46 +21,118 @@ namespace ue {
 namespace {
 
 constexpr int kJoin = 8;      // rows of a token in flight
-constexpr int kEach = 8;      // elements of a lane
+constexpr int kEach = 8;      // elements of a lane, in runs of 16 bytes
+
+// A lane's elements of the LANES lanes' segment of a row that begins at h: runs
+// lie lane after lane. A run that the row's end would cut lies at that end
+// instead, and its first few elements, `over` of them, are others' and left
+// alone: so all lanes load without a branch, whatever the row's length. (With
+// branches on a run's length, rows' loads waited for each other: 1021 tokens x
+// top-6 x 1002, fp32, 23 us both ways, now 18; 25517 x top-5 x 166 89 and 77.)
+// SHORT: rows of less than a run, element by element.
+template <typename T, int LANES, bool SHORT>
+struct Segment {
+    static constexpr int kRun = 16 / sizeof(T), kRuns = kEach / kRun;
+    typedef typename Words<16>::type W;
+    W v[kRuns];
+
+    static __device__ __forceinline__ int over(int h, int lane, int c, int H) {
+        const int o = h + (c * LANES + lane + 1) * kRun - H;
+        return !SHORT && o > 0 ? o : 0;
+    }
+    template <bool ONCE>
+    __device__ __forceinline__ void load(const T *row, int h, int lane, int H) {
+#pragma unroll
+        for (int c = 0; c < kRuns; ++c) {
+            const int at = h + (c * LANES + lane) * kRun;
+            if constexpr (!SHORT) {
+                const W *p = reinterpret_cast<const W *>(row + (at < H - kRun ? at : H - kRun));
+                v[c] = ONCE ? __builtin_nontemporal_load(p) : *p;
+            } else {
+                struct { T e[kRun]; } few = {};
+#pragma unroll
+                for (int i = 0; i < kRun; ++i)
+                    if (at + i < H) few.e[i] = row[at + i];
+                v[c] = __builtin_bit_cast(W, few);
+            }
+        }
+    }
+    __device__ __forceinline__ void get(float (&f)[kEach]) const {
+        struct Elements { T e[kEach]; };
+        const Elements e = __builtin_bit_cast(Elements, v);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) f[i] = widen<T>(e.e[i]);
+    }
+    // Others' elements as zeros.
+    static __device__ __forceinline__ void own(int h, int lane, int H, float (&f)[kEach]) {
+        if (H % (LANES * kEach) == 0) return;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (i % kRun < over(h, lane, i / kRun, H)) f[i] = 0.f;
+    }
+    static __device__ __forceinline__ void store(T *row, int h, int lane, int H,
+                                                 const float (&f)[kEach]) {
+#pragma unroll
+        for (int c = 0; c < kRuns; ++c) {
+            const int at = h + (c * LANES + lane) * kRun, o = over(h, lane, c, H);
+            if (at >= H) continue;
+            float r[kRun];
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) r[i] = f[c * kRun + i];
+            if (o == 0) {
+                store_run<kRun, true>(row + at, H - at, r);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kRun; ++i)
+                    if (i >= o) row[at - o + i] = narrow<T>(r[i]);
+            }
+        }
+    }
+};
 
 // LANES: of a row's segment. Rows shorter than a wave's 512 elements share it.
-template <typename T, int LANES>
+template <typename T, int LANES, bool SHORT>
 __global__ __launch_bounds__(kBlock) void k_combine(CombineArgs g, FastDiv segs, uint32_t items) {
     constexpr int kItems = kBlock / LANES;
     uint32_t item = blockIdx.x * kItems + threadIdx.x / LANES;
     if (LANES == 64) item = __builtin_amdgcn_readfirstlane(item);
     if (item >= items) return;
     const int t = div_by(item, segs);
-    const int h = (item - t * segs.d) * LANES * kEach + threadIdx.x % LANES * kEach;
-    const int n = g.H - h;
+    const int h = (item - t * segs.d) * LANES * kEach, lane = threadIdx.x % LANES;
     const int64_t o = static_cast<int64_t>(t) * g.k;
-    const T *y = static_cast<const T *>(g.y) + h;
+    const T *y = static_cast<const T *>(g.y);
+    typedef Segment<T, LANES, SHORT> Seg;
     float sum[kEach] = {};
-    if (g.add) load8(static_cast<const T *>(g.add) + t * g.ldadd + h, n, sum);
+    Seg first;
+    if (g.add) first.template load<true>(static_cast<const T *>(g.add) + t * g.ldadd, h, lane, g.H);
     for (int j0 = 0; j0 < g.k; j0 += kJoin) {
-        float f[kJoin][kEach], w[kJoin];
+        Seg rows[kJoin];
+        float w[kJoin];
         bool has[kJoin];
 #pragma unroll
         for (int j = 0; j < kJoin; ++j) {
             const int at = j0 + j < g.k ? j0 + j : 0, pos = g.inv[o + at];
             has[j] = j0 + j < g.k && static_cast<uint32_t>(pos) < static_cast<uint32_t>(g.rows);
             w[j] = g.weights ? g.weights[o + at] : 1.f;
-            if (has[j]) load8(y + pos * g.ldy, n, f[j]);
+            if (has[j]) rows[j].template load<true>(y + pos * g.ldy, h, lane, g.H);
         }
+        if (j0 == 0 && g.add) first.get(sum);
 #pragma unroll
         for (int j = 0; j < kJoin; ++j) {
             if (!has[j]) continue;
+            float f[kEach];
+            rows[j].get(f);
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) sum[i] = __builtin_fmaf(w[j], f[j][i], sum[i]);
+            for (int i = 0; i < kEach; ++i) sum[i] = __builtin_fmaf(w[j], f[i], sum[i]);
         }
     }
-    store8(static_cast<T *>(g.out) + t * g.ldo + h, n, sum);
+    Seg::store(static_cast<T *>(g.out) + t * g.ldo, h, lane, g.H, sum);
 }
 
 constexpr int kAhead = 2;     // segments in flight
 constexpr int kBackBlock = 512;
 
-template <typename T, int LANES>
+template <typename T, int LANES, bool SHORT>
 __global__ __launch_bounds__(kBackBlock) void k_combine_backward(CombineArgs g, FastDiv topk,
                                                                  uint32_t assignments) {
     constexpr int kItems = kBackBlock / LANES, kSeg = LANES * kEach;
@@ -69,35 +140,44 @@ __global__ __launch_bounds__(kBackBlock) void k_combine_backward(CombineArgs g, 
     if (LANES == 64) a = __builtin_amdgcn_readfirstlane(a);
     if (a >= assignments) return;                   // (whole rows of lanes)
     const int lane = threadIdx.x % LANES, t = div_by(a, topk);
-    const T *dout = static_cast<const T *>(g.dout) + t * g.lddout + lane * kEach;
+    const T *dout = static_cast<const T *>(g.dout) + t * g.lddout;
     const int pos = g.inv[a];
     const float w = g.weights ? g.weights[a] : 1.f;
     float dot = 0.f;
     if (static_cast<uint32_t>(pos) < static_cast<uint32_t>(g.rows)) {
-        const T *y = static_cast<const T *>(g.y) + pos * g.ldy + lane * kEach;
-        T *dy = static_cast<T *>(g.dy) + pos * g.lddy + lane * kEach;
-        const int n = g.H - lane * kEach;
+        const T *y = static_cast<const T *>(g.y) + pos * g.ldy;
+        T *dy = static_cast<T *>(g.dy) + pos * g.lddy;
+        typedef Segment<T, LANES, SHORT> Seg;
         for (int h0 = 0; h0 < g.H; h0 += kAhead * kSeg) {
-            float d[kAhead][kEach], f[kAhead][kEach];
+            Seg d[kAhead], f[kAhead];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const int h = h0 + u * kSeg;
                 if (h >= g.H) continue;
-                load_run<kEach, false>(dout + h, n - h, d[u]);
-                if (g.dweights) load8(y + h, n - h, f[u]);
+                d[u].template load<false>(dout, h, lane, g.H);
+                if (g.dweights) f[u].template load<true>(y, h, lane, g.H);
             }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const int h = h0 + u * kSeg;
                 if (h >= g.H) continue;
+                float dv[kEach];
+                d[u].get(dv);
                 if (g.dweights) {
+                    float fv[kEach];
+                    f[u].get(fv);
+                    float mine[kEach];
 #pragma unroll
-                    for (int i = 0; i < kEach; ++i) dot = __builtin_fmaf(d[u][i], f[u][i], dot);
+                    for (int i = 0; i < kEach; ++i) mine[i] = dv[i];
+                    Seg::own(h, lane, g.H, fv);
+                    Seg::own(h, lane, g.H, mine);
+#pragma unroll
+                    for (int i = 0; i < kEach; ++i) dot = __builtin_fmaf(mine[i], fv[i], dot);
                 }
                 if (g.dy) {
 #pragma unroll
-                    for (int i = 0; i < kEach; ++i) d[u][i] *= w;
-                    store8(dy + h, n - h, d[u]);
+                    for (int i = 0; i < kEach; ++i) dv[i] *= w;
+                    Seg::store(dy, h, lane, g.H, dv);
                 }
             }
         }
@@ -108,12 +188,14 @@ __global__ __launch_bounds__(kBackBlock) void k_combine_backward(CombineArgs g, 
     }
 }
 
-// The lanes a row of H takes: f(lanes).
+// The lanes a row of H takes, and whether it is less than a run.
 template <class F>
-void with_row_lanes(int H, F f) {
-    if (H <= 16 * kEach) f(std::integral_constant<int, 16>{});
-    else if (H <= 32 * kEach) f(std::integral_constant<int, 32>{});
-    else f(std::integral_constant<int, 64>{});
+void with_row_lanes(const CombineArgs &g, F f) {
+    typedef std::false_type No;
+    if (g.H < (g.bf16 ? 8 : 4)) f(std::integral_constant<int, 16>{}, std::true_type{});
+    else if (g.H <= 16 * kEach) f(std::integral_constant<int, 16>{}, No{});
+    else if (g.H <= 32 * kEach) f(std::integral_constant<int, 32>{}, No{});
+    else f(std::integral_constant<int, 64>{}, No{});
 }
 
 // A launch has fewer than 2^32 threads, of at most 64 for a row's segment.
@@ -137,7 +219,8 @@ CombineArgs from_token(const CombineArgs &g, int64_t t, int64_t n) {
 
 hipError_t launch_combine(const ue_ctx &, const CombineArgs &g, hipStream_t s) {
     hipError_t he = hipSuccess;
-    with_row_lanes(g.H, [&](auto l) {
+    with_row_lanes(g, [&](auto l, auto few) {
+        constexpr bool kShort = decltype(few)::value;
         constexpr int kLanes = decltype(l)::value;
         const int segs = (g.H + kLanes * kEach - 1) / (kLanes * kEach);
         const int64_t tokens = kLaunchItems / segs;
@@ -146,10 +229,10 @@ hipError_t launch_combine(const ue_ctx &, const CombineArgs &g, hipStream_t s) {
             const uint32_t items = static_cast<uint32_t>(p.T) * segs;
             const dim3 gr((items + kBlock / kLanes - 1) / (kBlock / kLanes));
             if (g.bf16)
-                hipLaunchKernelGGL((k_combine<uint16_t, kLanes>), gr, dim3(kBlock), 0, s, p,
+                hipLaunchKernelGGL((k_combine<uint16_t, kLanes, kShort>), gr, dim3(kBlock), 0, s, p,
                                    fast_div(segs), items);
             else
-                hipLaunchKernelGGL((k_combine<float, kLanes>), gr, dim3(kBlock), 0, s, p,
+                hipLaunchKernelGGL((k_combine<float, kLanes, kShort>), gr, dim3(kBlock), 0, s, p,
                                    fast_div(segs), items);
             he = hipGetLastError();
         }
@@ -159,7 +242,8 @@ hipError_t launch_combine(const ue_ctx &, const CombineArgs &g, hipStream_t s) {
 
 hipError_t launch_combine_backward(const ue_ctx &, const CombineArgs &g, hipStream_t s) {
     hipError_t he = hipSuccess;
-    with_row_lanes(g.H, [&](auto l) {
+    with_row_lanes(g, [&](auto l, auto few) {
+        constexpr bool kShort = decltype(few)::value;
         constexpr int kLanes = decltype(l)::value, kItems = kBackBlock / kLanes;
         const int64_t tokens = kLaunchItems / g.k;
         for (int64_t t = 0; t < g.T && he == hipSuccess; t += tokens) {
@@ -167,10 +251,10 @@ hipError_t launch_combine_backward(const ue_ctx &, const CombineArgs &g, hipStre
             const uint32_t items = static_cast<uint32_t>(p.T) * g.k;
             const dim3 gr((items + kItems - 1) / kItems);
             if (g.bf16)
-                hipLaunchKernelGGL((k_combine_backward<uint16_t, kLanes>), gr, dim3(kBackBlock), 0,
+                hipLaunchKernelGGL((k_combine_backward<uint16_t, kLanes, kShort>), gr, dim3(kBackBlock), 0,
                                    s, p, fast_div(g.k), items);
             else
-                hipLaunchKernelGGL((k_combine_backward<float, kLanes>), gr, dim3(kBackBlock), 0, s,
+                hipLaunchKernelGGL((k_combine_backward<float, kLanes, kShort>), gr, dim3(kBackBlock), 0, s,
                                    p, fast_div(g.k), items);
             he = hipGetLastError();
         }

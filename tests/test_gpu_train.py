@@ -671,6 +671,41 @@ def test_combine(T, k, H, dtype):
     ctx.close()
 
 
+@pytest.mark.parametrize("H", (3, 5, 9, 17, 131, 257, 513, 515, 1027))
+@pytest.mark.parametrize("dtype", TYPES)
+def test_combine_rows_that_end_inside_a_piece(dtype, H):
+    """Rows whose last piece reaches back into the one before: added to in place,
+    with nothing written past their ends, infinities in that piece."""
+    say("combine ends", H, dtype)
+    T, k = 700, 2
+    rng = np.random.default_rng(H)
+    ctx = ctx_for(8, k, T)
+    inv = rng.permutation(T * k).astype(np.int32).reshape(T, k)
+    y = rounded(rng.normal(size=(T * k, H)), dtype)
+    add = rounded(rng.normal(size=(T, H)), dtype)
+    dout = rounded(1.0 + rng.random(size=(T, H)), dtype)
+    w = rng.normal(size=(T, k)).astype(np.float32)
+    wide = torch.full((T, H + 9), -7.0, dtype=dtype, device=DEV)
+    res = wide[:, 4:4 + H]
+    res.copy_(dev(add, dtype))
+    assert ue.ue_combine(ctx, dev(y, dtype), dev(inv), dev(w), add=res, out=res) is res
+    want, size = R.combine(y, inv, w, add)
+    close(host(res), want, (k + 2) * U * size + half_step(dtype, want))
+    assert bool((wide[:, :4] == -7).all()) and bool((wide[:, 4 + H:] == -7).all())
+    y[5, H - 2] = INF
+    wide = torch.full((T * k, H + 9), -7.0, dtype=dtype, device=DEV)
+    dy, dw = ue.ue_combine_backward(ctx, dev(dout, dtype), dev(inv), dev(w), dev(y, dtype),
+                                    dy=wide[:, 4:4 + H])
+    wy, wd, ws = R.combine_backward(dout, y, inv, w)
+    close(host(dy), wy, half_step(dtype, wy) + 1e-40)
+    assert bool((wide[:, :4] == -7).all()) and bool((wide[:, 4 + H:] == -7).all())
+    at = inv == 5
+    got = host(dw)
+    assert got[at] == INF
+    close(got[~at], wd[~at], (H / 64 + 20) * U * ws[~at])
+    ctx.close()
+
+
 def test_combine_edges():
     """No tokens, no rows, infinities beside ordinary rows, the gather's
     gradient."""
