@@ -35,8 +35,9 @@
  *    streams. Calls of ue_moe_tokens have a workspace of their own and must
  *    not overlap one another, replays of captured ones included.
  *    ue_weight_sync, ue_grad_reduce, ue_gather_rows, ue_gate,
- *    ue_gate_backward, ue_quantize_rows and ue_matmul_i8 use no
- *    workspace and may run on another stream beside them (the next layer's
+ *    ue_gate_backward, ue_quantize_rows, ue_matmul_i8 and the calls of the
+ *    training step (ue_balance to ue_combine_backward) use no workspace but
+ *    what they are given, and may run on another stream beside them (the next layer's
  *    rebalance beside this layer's sync), while kernel timing is off and
  *    the registered tables are not replaced meanwhile.
  *  - All shapes are int32; the number of assignments per layer, T*k, must

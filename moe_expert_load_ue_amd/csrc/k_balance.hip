@@ -16,6 +16,13 @@
 // either grows by one, so no two meetings share a slot, and shares + sequences
 // slots are enough for any lengths. A second launch adds a sequence's rows,
 // shares in order.
+//
+// Bound: 65536 tokens of 256 experts, fp32, sigmoid: HBM going back (31 us, 134 MB,
+// 4.3 TB/s); forward (24 us, 69 MB, 2.9 TB/s, and 7 us for the launch that adds the
+// partial sums) instruction issue (20 per logit, 40% of the cycles) and the start
+// and end of workgroups that pass over their share four times. A few thousand
+// tokens are bound by the latency of the two launches (3001 tokens of 60 experts
+// 7 and 3 us), a few hundred take one launch, which the host's calls outlast.
 #include "ue_train.h"
 
 namespace ue {

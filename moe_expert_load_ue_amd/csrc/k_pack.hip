@@ -9,7 +9,12 @@
 // round them by two lane moves. The blocks of all rows are one list, so rows of
 // any length fill the waves.
 //
-// Bound: HBM.
+// Bound: HBM. 32768 rows of 2048, bf16: gated activation, keeping gate and up, 87
+// us (541 MB, 6.2 TB/s), its backward pass with the activation again 107 us (675
+// MB, 6.3 TB/s); 8192 rows of 7168 packed in 19 us (178 MB, 9 TB/s, half of it
+// found in the cache). A quad of lanes takes one block and no loop: what is in
+// flight is other waves'. 13358 rows of 302, fp32, both ways 35 us (element by
+// element, as rows that are no multiple of 16 bytes were read once, 68).
 #include "ue_train.h"
 
 namespace ue {

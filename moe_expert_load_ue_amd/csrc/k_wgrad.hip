@@ -1,17 +1,29 @@
 // Gradients of the matrices of row groups (ue_weight_grad):
 //   out[g, n, k] (+)= sum over the rows m of group g of dy[m, n] x[r(m), k]
 //
-// A workgroup makes a tile of one group's matrix. Both operands lie row by row,
+// A workgroup makes tiles of the groups' matrices. Both operands lie row by row,
 // with the sum going down the rows, while a matrix instruction wants each lane's
 // eight terms side by side. So rows go to LDS as they are, in bf16, and come
 // out transposed: a transposing LDS read gives each of 16 lanes one column of
-// four rows. A stage is kRows rows; dy comes by direct loads two stages ahead,
-// . Which four rows a lane's terms
-// come from does not matter as long as both operands take the same.
+// four rows. A stage is kRows rows, which come to registers, packed x is widened
+// on the way down to LDS. Which four rows a lane's terms come from does not
+// matter as long as both operands take the same.
 //
-// Rows in LDS are units of 16 columns (32 bytes); unit u of row r sits at
-// u ^ (r mod units), so that the four rows a transposing read touches fall on
-// different banks.
+// Rows in LDS are units of 16 columns (32 bytes), placed so that neither what is
+// put down nor what is read back transposed meets a bank twice (no conflicts
+// counted).
+//
+// Bound: the clock under load, taken to be the power limit's. One group of 8192 x
+// 4096 x 7168, packed x, takes 465-475 us (1.02 PFLOP/s; bf16 x 451-456) at 1.97
+// GHz of 2.4, with the matrix units busy 46% of the cycles: a stage takes 3900
+// cycles, of which the matrix instructions need 2048 and LDS 1290. Changes that
+// took waiting away left its time alone: loads used a whole stage after they are
+// issued in place of half of one (465-473 us, bf16 x 458-470), workgroups started
+// apart from each other (466-483). Without its loads it takes 388 us, without what
+// it puts down in LDS either 312. Four waves of 128 x 128 spilled (3.7 ms); tiles
+// of 256 x 128 on four waves, two workgroups per CU, 575 us against 483; rows
+// straight to LDS wait for each other, since the compiler puts a wait for all of
+// them ahead of every LDS read.
 #include "ue_train.h"
 
 #include <atomic>
@@ -71,9 +83,10 @@ constexpr int kPiece = 8;
 // stage's products run, the next one's rows go to LDS, those of the one after
 // are on their way to registers, and the row numbers of the third too, whichever
 // tiles they are of. So the first stages of a tile are there when the results of
-// the one before have been stored. (A workgroup per tile, with nothing under its
-// first loads and its stores, took 870 us for 72 groups of 2048x4096 with 455
-// rows each; its stores alone 500, all but the stores 737.)
+// the one before have been stored. (72 groups of 2048x4096 with 455 rows each
+// take 752-778 us, in one run of calls on some devices 870; a workgroup per tile,
+// with nothing under its first loads and its stores, took 870 where this takes
+// 794. The stores alone take 500.)
 //
 // A stage is four steps of 16 rows. A step's operands are read from LDS during
 // the step before, and the next stage is put down during the first three. So by
@@ -155,9 +168,9 @@ __global__ __launch_bounds__(WN *WK * 64, FN * FK > 8 ? 1 : 2) void k_wgrad(
         return s.left >= kRows ? r : r < s.left ? r : s.left > 0 ? s.left - 1 : 0;
     };
 
-    // ---- loads: units of dy and of x, a half at a time. Rows
-    // that are not the stage's are put down as zeros; pieces past the last column
-    // are read as others (results of columns that nobody stores) ----
+    // ---- loads: units of dy and of x, a half at a time. Rows that are not the
+    // stage's are put down as zeros; pieces past the last column are read as others
+    // (results of columns that nobody stores) ----
     const int dy_row = tid / UN, dy_col = tid % UN * kUnit;
     const int x_row = tid / UK, x_col = tid % UK * kUnit;
     Unit dyr[kUnits];
@@ -388,7 +401,8 @@ __global__ __launch_bounds__(WN *WK * 64, FN * FK > 8 ? 1 : 2) void k_wgrad(
 
     // ---- results: lane l holds column l mod 32, rows 8 (r / 4) + 4 (l / 32) +
     // r mod 4 of each fragment: whole lines of 128 bytes per store, which nobody
-    // reads soon (past the caches 870 us, through them 1030, of the size above) ----
+    // reads soon (past the caches 870 us, through them 1030, of the size above when
+    // a workgroup made one tile) ----
     auto results = [&](const Stage &s) {
         const int nb = s.n0 + wn * FN * 32 + 4 * (lane >> 5);
         const int kb = s.k0 + wk * FK * 32 + (lane & 31);

@@ -110,7 +110,7 @@ struct WgradArgs {
     const int32_t *index;       // [M] or null
     int index_div;
     int M, N, K;
-    bool accumulate, vec_dy, vec_x, vec_out;   // rows in 16-byte pieces
+    bool accumulate, vec_dy, vec_x;            // rows in 16-byte pieces
     float *out;
     int64_t ldo, out_stride;
     float *part;                // [parts][G][N][K] of a split sum, or null

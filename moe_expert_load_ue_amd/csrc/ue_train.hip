@@ -342,8 +342,6 @@ int ue_weight_grad(ue_ctx *ctx, const ue_weight_grad_product *p, void *stream) {
     g.accumulate = p->accumulate != 0;
     g.vec_dy = rows_aligned(p->dy, p->lddy, 2, 16);
     g.vec_x = p->x_scale || rows_aligned(p->x, p->ldx, 2, 16);
-    g.vec_out = rows_aligned(p->out, p->ldo, 4, 16) &&
-                (p->groups == 1 || p->out_stride % 4 == 0);
     g.out = p->out;
     g.ldo = p->ldo;
     g.out_stride = p->out_stride;
