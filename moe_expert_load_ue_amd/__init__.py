@@ -694,12 +694,25 @@ def _flat(t, name, dtype, device, numel):
     return t.data_ptr()
 
 
+# Makes an uninitialised tensor on the current device (which `_on` checks to be
+# the context's): what generated code of torch.compile calls, 0.8 us on the host
+# where torch.empty takes 1.7, of the 10 that a call with three outputs took.
+_guards = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
+_empty = getattr(_guards, "_empty_strided_cuda", None)
+
+
 def _new(shape, dtype, ctx, stream):
     """An output tensor whose memory belongs to the stream that writes it."""
-    if stream is None:
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=ctx.device)
+    if _empty is None or _device() != ctx._index:
         return torch.empty(shape, dtype=dtype, device=ctx.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=ctx.device)
+    if len(shape) == 1:
+        return _empty(shape, (1,), dtype)
+    cols = shape[-1] or 1
+    return _empty(shape, (cols, 1) if len(shape) == 2 else
+                  ((shape[1] or 1) * cols, cols, 1), dtype)
 
 
 _device = torch._C._cuda_getDevice \

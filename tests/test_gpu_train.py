@@ -706,6 +706,20 @@ def test_combine_rows_that_end_inside_a_piece(dtype, H):
     ctx.close()
 
 
+@pytest.mark.parametrize("shape", ((0,), (5,), (3, 7), (3, 0), (0, 4), (2, 3, 5), (2, 0, 5), (2, 3, 0)))
+def test_outputs_made_here_are_ordinary_tensors(shape):
+    """Their layout and device are torch.empty's, on the default stream and on
+    another."""
+    ctx = ctx_for(8, 2, 8)
+    for stream in (None, torch.cuda.Stream()):
+        for dtype in (torch.float32, torch.bfloat16, torch.int8, torch.int32):
+            t = ue._new(shape, dtype, ctx, stream)
+            w = torch.empty(shape, dtype=dtype, device=DEV)
+            assert t.shape == w.shape and t.stride() == w.stride() and t.dtype == w.dtype
+            assert t.device == w.device and t.is_contiguous() and not t.requires_grad
+    ctx.close()
+
+
 def test_combine_edges():
     """No tokens, no rows, infinities beside ordinary rows, the gather's
     gradient."""
