@@ -667,24 +667,27 @@ _raw_stream = torch._C._cuda_getCurrentRawStream \
 def _rows(t, name, device, types, cols=None):
     """A matrix [rows, cols] whose rows are contiguous; returns (rows, cols,
     distance between rows in elements)."""
+    try:
+        n, c = t.shape
+        if t.dtype in types and t.device == device and (c == cols or
+                                                        cols is None):
+            ld, one = t.stride()
+            if one == 1 or c <= 1:
+                # a single row has no distance to the next: one that meets
+                # every call
+                return n, c, ld if n > 1 else (c + 15) // 16 * 16
+    except (AttributeError, TypeError, ValueError):
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype not in types:
         raise TypeError(f"{name} must be one of {list(types)}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    shape = t.shape
-    if len(shape) != 2 or (cols is not None and shape[1] != cols):
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
         raise ValueError(f"{name} must be [rows, {cols or 'cols'}], is "
-                         f"{tuple(shape)}")
-    n, c = shape
-    ld, one = t.stride()
-    if c > 1 and one != 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    if n <= 1:
-        # a single row has no distance to the next: one that meets every call
-        ld = (c + 15) // 16 * 16
-    return n, c, ld
+                         f"{tuple(t.shape)}")
+    raise ValueError(f"{name} must have contiguous rows")
 
 
 def _flat(t, name, dtype, device, numel):
@@ -694,25 +697,29 @@ def _flat(t, name, dtype, device, numel):
     return t.data_ptr()
 
 
-# Makes an uninitialised tensor on the current device (which `_on` checks to be
-# the context's): what generated code of torch.compile calls, 0.8 us on the host
-# where torch.empty takes 1.7, of the 10 that a call with three outputs took.
+# Makes an uninitialised tensor on the current device: what generated code of
+# torch.compile calls, 0.8 us on the host where torch.empty takes 1.7, of the 10
+# that a call with three outputs took.
 _guards = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
 _empty = getattr(_guards, "_empty_strided_cuda", None)
 
 
 def _new(shape, dtype, ctx, stream):
-    """An output tensor whose memory belongs to the stream that writes it."""
+    """An output tensor whose memory belongs to the stream that writes it. (Every
+    call passes through `_on` before its launch, which refuses it where the
+    current device is not the context's.)"""
     if stream is not None:
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=ctx.device)
-    if _empty is None or _device() != ctx._index:
+    if _empty is None:
         return torch.empty(shape, dtype=dtype, device=ctx.device)
-    if len(shape) == 1:
+    dims = len(shape)
+    if dims == 2:
+        return _empty(shape, (shape[1] or 1, 1), dtype)
+    if dims == 1:
         return _empty(shape, (1,), dtype)
-    cols = shape[-1] or 1
-    return _empty(shape, (cols, 1) if len(shape) == 2 else
-                  ((shape[1] or 1) * cols, cols, 1), dtype)
+    cols = shape[2] or 1
+    return _empty(shape, ((shape[1] or 1) * cols, cols, 1), dtype)
 
 
 _device = torch._C._cuda_getDevice \
