@@ -17,12 +17,12 @@
 // slots are enough for any lengths. A second launch adds a sequence's rows,
 // shares in order.
 //
-// Bound: 65536 tokens of 256 experts, fp32, sigmoid: HBM going back (31 us, 134 MB,
-// 4.3 TB/s); forward (24 us, 69 MB, 2.9 TB/s, and 7 us for the launch that adds the
-// partial sums) instruction issue (20 per logit, 40% of the cycles) and the start
-// and end of workgroups that pass over their share four times. A few thousand
-// tokens are bound by the latency of the two launches (3001 tokens of 60 experts
-// 7 and 3 us), a few hundred take one launch, which the host's calls outlast.
+// Bound: 65536 tokens of 256 experts, fp32, sigmoid: HBM going back (23 us, 134 MB,
+// 5.8 TB/s); forward (26 us, 69 MB) instruction issue (20 per logit) and the start
+// and end of workgroups, 7 us of it the launch that adds the partial sums. A few
+// thousand tokens are bound by the latency of the launches (3001 tokens of 60
+// experts 11 us, back 7), a few hundred take one launch, which the host's calls
+// outlast.
 #include "ue_train.h"
 
 namespace ue {
@@ -89,18 +89,33 @@ __device__ __forceinline__ float scores(float (&x)[VP], float (&slope)[SLOPE ? V
 // Experts of a row of partial sums: rows in pieces of four.
 __device__ __forceinline__ int padded(int E) { return (E + 3) & ~3; }
 
-// Bounds of sequences, clamped to the tokens there are.
+// Bounds of sequences, clamped to the tokens there are. What is asked for by a
+// whole wave alike comes, of up to 63 sequences, from one load that every lane
+// makes at the start (the loads that follow on each other are what bounds of
+// sequences cost).
 struct Sequences {
     const int32_t *offsets;
     int T, n;
+    int held;                   // begin(lane), if there are few
     __device__ __forceinline__ int begin(int s) const {
         if (!offsets) return s ? T : 0;
         const int o = offsets[s];
         return o < 0 ? 0 : o > T ? T : o;
     }
+    __device__ __forceinline__ Sequences(const int32_t *o, int T, int n, int lane)
+        : offsets(o), T(T), n(n), held(0) {
+        if (n < 64) held = begin(lane < n ? lane : n);
+    }
+    __device__ __forceinline__ int begin_wave(int s) const {
+        return n < 64 ? __builtin_amdgcn_readlane(held, s) : begin(s);
+    }
     // the first sequence that ends behind token t, all lanes of a wave looking for
-    // the same: of 64 (the loads that follow on each other are what it costs)
+    // the same: of 64 at once
     __device__ __forceinline__ int find_wave(int t, int lane) const {
+        if (n < 64) {
+            const uint64_t m = __ballot(lane > 0 && lane <= n && held > t);
+            return m ? __builtin_ctzll(m) - 1 : n;
+        }
         int lo = 0, hi = n;
         while (lo < hi) {
             const int step = (hi - lo + 63) >> 6, last = lo + (lane + 1) * step - 1;
@@ -135,14 +150,14 @@ __global__ __launch_bounds__(kFwdBlock) void k_balance(BalanceArgs g) {
     __shared__ int hist[kAll];
     const int tid = threadIdx.x, lane = lane_id(), wv = tid >> 6;
     const int at = lane & (L - 1), sub = lane / L, E = g.E;
-    const Sequences seqs{g.offsets, g.T, g.n_seq};
+    const Sequences seqs(g.offsets, g.T, g.n_seq, lane);
     const int c = blockIdx.x, t0 = WHOLE ? 0 : c * g.chunk;
     const int t1 = WHOLE || g.T - t0 < g.chunk ? g.T : t0 + g.chunk;
     const T *logits = static_cast<const T *>(g.logits);
     // (the next sequence is looked for behind this one's end, past any number of
     // empty ones; offsets that decrease may not lead back)
     for (int s = WHOLE ? c : seqs.find_wave(t0, lane), after; s < g.n_seq; s = after) {
-        int a = seqs.begin(s), b = seqs.begin(s + 1);
+        int a = seqs.begin_wave(s), b = seqs.begin_wave(s + 1);
         after = g.n_seq;
         if constexpr (!WHOLE) {
             if (a >= t1) break;
@@ -187,9 +202,8 @@ __global__ __launch_bounds__(kFwdBlock) void k_balance(BalanceArgs g) {
         else tokens(std::false_type{});
 #pragma unroll
         for (int i = 0; i < VP; ++i) {
-#pragma unroll
-            for (int d = L; d < 64; d <<= 1) acc[i] += __shfl_xor(acc[i], d);
-            if (sub == 0) sums[wv][expert_of_slot<L>(at, i)] = acc[i];
+            const float all = sum_across<L>(acc[i]);
+            if (sub == 0) sums[wv][expert_of_slot<L>(at, i)] = all;
         }
         __syncthreads();
         const int64_t slot = static_cast<int64_t>(WHOLE ? s : c + s) * (WHOLE ? E : padded(E));
@@ -236,8 +250,8 @@ __global__ __launch_bounds__(kEndBlock) void k_balance_end(BalanceArgs g) {
     __shared__ float terms[4];
     const int tid = threadIdx.x, lane = lane_id(), wv = tid >> 6, E = g.E;
     const int s = blockIdx.x;
-    const Sequences seqs{g.offsets, g.T, g.n_seq};
-    const int a = seqs.begin(s), b = seqs.begin(s + 1), n = b > a ? b - a : 0;
+    const Sequences seqs(g.offsets, g.T, g.n_seq, lane);
+    const int a = seqs.begin_wave(s), b = seqs.begin_wave(s + 1), n = b > a ? b - a : 0;
     const int c0 = n ? a / g.chunk : 0, c1 = n ? (b - 1) / g.chunk + 1 : 0;
     const float inv_n = n ? 1.0f / static_cast<float>(n) : 0.f;
     float term = 0.f;
@@ -304,14 +318,11 @@ __global__ __launch_bounds__(kBlock) void k_balance_backward(BalanceBackArgs g, 
     constexpr int kEach = 64 / L;
     const int lane = lane_id(), wv = threadIdx.x >> 6;
     const int at = lane & (L - 1), sub = lane / L, E = g.E;
-    const Sequences seqs{g.offsets, g.T, g.n_seq};
+    const Sequences seqs(g.offsets, g.T, g.n_seq, lane);
     const int t0 = blockIdx.x * chunk;
     const int t1 = g.T - t0 < chunk ? g.T : t0 + chunk;
     const T *logits = static_cast<const T *>(g.logits);
     T *out = static_cast<T *>(g.dlogits);
-    // most tokens are of the sequence of the wave's first one
-    const int first = seqs.find_wave(t0 + wv * kEach, lane);
-    const int first_to = first < g.n_seq ? seqs.begin(first + 1) : 0x7FFFFFFF;
     auto tokens = [&](auto fours) {
         constexpr bool FOURS = decltype(fours)::value;
         int t = t0 + wv * kEach + sub;
@@ -323,22 +334,62 @@ __global__ __launch_bounds__(kBlock) void k_balance_backward(BalanceBackArgs g, 
             const int mine = real ? t : t1 - 1;
             float x[VP], slope[VP];
             load_token<T, L, VP, FOURS>(logits + mine * g.ld, at, E, x);
-            if (real && t >= to) {
-                s = t < first_to ? first : seqs.find(t);
-                if (s < g.n_seq) {
-                    from = seqs.begin(s);
-                    to = seqs.begin(s + 1);
+            const bool look = real && t >= to;
+            if (__any(look)) {
+                if (g.n_seq < 64) {
+                    // the tokens of the wave one by one, without a load
+#pragma unroll
+                    for (int u = 0; u < kEach; ++u) {
+                        const int tu = __builtin_amdgcn_readfirstlane(t - sub) + u;
+                        const int su = seqs.find_wave(tu, lane);
+                        const bool past = su >= g.n_seq;
+                        const int a = past ? g.T : seqs.begin_wave(su);
+                        const int b = past ? g.T : seqs.begin_wave(su + 1);
+                        if (look && sub == u) {
+                            s = su;
+                            from = a;
+                            to = b;
+                        }
+                    }
+                } else {
+                    // the sequence of the wave's first token is most tokens'
+                    const int tw = __builtin_amdgcn_readfirstlane(t - sub);
+                    const int sw = seqs.find_wave(tw, lane);
+                    const bool past = sw >= g.n_seq;
+                    const int a = past ? g.T : seqs.begin(sw);
+                    const int b = past ? g.T : seqs.begin(sw + 1);
+                    if (look && t < b) {
+                        s = sw;
+                        from = a;
+                        to = b;
+                    } else if (look) {
+                        s = seqs.find(t);
+                        from = s < g.n_seq ? seqs.begin(s) : g.T;
+                        to = s < g.n_seq ? seqs.begin(s + 1) : g.T;
+                    }
+                }
+                // (behind the last sequence from and to are T)
+                if (look && s < g.n_seq) {
                     const float n = static_cast<float>(to - from);
                     const float f = g.dloss[s] *
                         (static_cast<float>(E) / (static_cast<float>(g.k) * n)) / n;
+                    const int32_t *counts = g.counts + static_cast<int64_t>(s) * E;
 #pragma unroll
-                    for (int i = 0; i < VP; ++i) {
-                        const int e = expert_of_slot<L>(at, i);
-                        cw[i] = e < E ? static_cast<float>(
-                                    g.counts[static_cast<int64_t>(s) * E + e]) * f : 0.f;
+                    for (int c = 0; c < VP / 4; ++c) {
+                        const int e = expert_of_slot<L>(at, 4 * c);
+                        typedef int32_t Four __attribute__((ext_vector_type(4), aligned(4)));
+                        Four q = {};
+                        if (FOURS || e + 4 <= E) {
+                            q = *reinterpret_cast<const Four *>(counts + (e < E ? e : 0));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (e + i < E) q[i] = counts[e + i];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            cw[4 * c + i] = e + i < E ? static_cast<float>(q[i]) * f : 0.f;
                     }
-                } else {
-                    from = to = g.T;       // behind the last sequence
                 }
             }
             const bool inside = real && t >= from && t < to;
@@ -412,10 +463,12 @@ void backward_any(const BalanceBackArgs &g, int chunk, int shares, hipStream_t s
 // Tokens that a workgroup passes over at once.
 static int pass(int E) { return E <= 128 ? 64 : E <= 256 ? 32 : E <= 512 ? 16 : 8; }
 
-// Two workgroups' shares per CU, of one pass at least (2221 tokens of 442 experts:
-// 18 us, with 64 tokens 23; 3001 of 60 the same).
+// A share per CU, of one pass at least: a workgroup's start and end cost more than
+// waves beside it hide (65536 tokens of 256 experts 26 us, two shares per CU 27.5,
+// four 35; of at least 64 tokens 2221 tokens of 442 experts took 23 us, of one
+// pass, 16 of them, 18).
 int balance_chunk(int T, int E, int num_cu) {
-    const int each = (T + 2 * num_cu - 1) / (2 * num_cu);
+    const int each = (T + num_cu - 1) / num_cu;
     return each <= pass(E) ? pass(E) : (each + 15) / 16 * 16;
 }
 // Batches of up to eight passes are left to a workgroup per sequence, without
