@@ -19,9 +19,9 @@
 //
 // Bound: 65536 tokens of 256 experts, fp32, sigmoid: HBM going back (23 us, 134 MB,
 // 5.8 TB/s); forward (26 us, 69 MB) instruction issue (20 per logit) and the start
-// and end of workgroups, 7 us of it the launch that adds the partial sums. A few
+// and end of workgroups, 4.5 us of it the launch that adds the partial sums. A few
 // thousand tokens are bound by the latency of the launches (3001 tokens of 60
-// experts 11 us, back 7), a few hundred take one launch, which the host's calls
+// experts 10.6 us, back 7), a few hundred take one launch, which the host's calls
 // outlast.
 #include "ue_train.h"
 
