@@ -208,6 +208,22 @@ def test_balance_strides(E, dtype):
     ctx.close()
 
 
+@pytest.mark.parametrize("E", [2, 3, 5, 30, 131, 442, 777])
+@pytest.mark.parametrize("n", [1, 9, 62, 63, 64, 65, 300])
+def test_balance_in_shares(E, n):
+    """Batches that many workgroups share, of few and of many sequences, with
+    experts that are no multiple of four and padding ahead and behind."""
+    say("balance in shares", E, n)
+    rng = np.random.default_rng(E * 1000 + n)
+    T, k = 1237, 2
+    ctx = ctx_for(E, k, T)
+    assert ue.ue_balance_workspace(ctx, T, n) > 0
+    x, ids = balance_case(rng, T, E, k, F32, False)
+    off = np.sort(rng.integers(0, T + 1, size=n + 1))
+    check_balance(ctx, x, ids, off, F32, "sigmoid" if n % 2 else "softmax")
+    ctx.close()
+
+
 def test_balance_special_values():
     """NaN spoils its sequence's loss and prob and its own token's gradient
     only; +inf is the largest float; ids outside the experts are not counted."""
