@@ -28,7 +28,8 @@ constexpr int kEach = 8;      // elements of a lane, in runs of 16 bytes
 // instead, and its first few elements, `over` of them, are others' and left
 // alone: so all lanes load without a branch, whatever the row's length. (With
 // branches on a run's length, rows' loads waited for each other: 1021 tokens x
-// top-6 x 1002, fp32, 23 us both ways, now 18; 25517 x top-5 x 166 89 and 77.)
+// top-6 x 1002, fp32, 23 us both ways, without 18; 25517 x top-5 x 166 89 and 77;
+// 16 and 59 with rows through the caches.)
 // SHORT: rows of less than a run, element by element.
 template <typename T, int LANES, bool SHORT>
 struct Segment {
@@ -91,7 +92,7 @@ struct Segment {
 };
 
 // LANES: of a row's segment. Rows shorter than a wave's 512 elements share it.
-template <typename T, int LANES, bool SHORT>
+template <typename T, int LANES, bool SHORT, bool ONCE>
 __global__ __launch_bounds__(kBlock) void k_combine(CombineArgs g, FastDiv segs, uint32_t items) {
     constexpr int kItems = kBlock / LANES;
     uint32_t item = blockIdx.x * kItems + threadIdx.x / LANES;
@@ -104,7 +105,7 @@ __global__ __launch_bounds__(kBlock) void k_combine(CombineArgs g, FastDiv segs,
     typedef Segment<T, LANES, SHORT> Seg;
     float sum[kEach] = {};
     Seg first;
-    if (g.add) first.template load<true>(static_cast<const T *>(g.add) + t * g.ldadd, h, lane, g.H);
+    if (g.add) first.template load<ONCE>(static_cast<const T *>(g.add) + t * g.ldadd, h, lane, g.H);
     for (int j0 = 0; j0 < g.k; j0 += kJoin) {
         Seg rows[kJoin];
         float w[kJoin];
@@ -114,7 +115,7 @@ __global__ __launch_bounds__(kBlock) void k_combine(CombineArgs g, FastDiv segs,
             const int at = j0 + j < g.k ? j0 + j : 0, pos = g.inv[o + at];
             has[j] = j0 + j < g.k && static_cast<uint32_t>(pos) < static_cast<uint32_t>(g.rows);
             w[j] = g.weights ? g.weights[o + at] : 1.f;
-            if (has[j]) rows[j].template load<true>(y + pos * g.ldy, h, lane, g.H);
+            if (has[j]) rows[j].template load<ONCE>(y + pos * g.ldy, h, lane, g.H);
         }
         if (j0 == 0 && g.add) first.get(sum);
 #pragma unroll
@@ -132,7 +133,7 @@ __global__ __launch_bounds__(kBlock) void k_combine(CombineArgs g, FastDiv segs,
 constexpr int kAhead = 2;     // segments in flight
 constexpr int kBackBlock = 512;
 
-template <typename T, int LANES, bool SHORT>
+template <typename T, int LANES, bool SHORT, bool ONCE>
 __global__ __launch_bounds__(kBackBlock) void k_combine_backward(CombineArgs g, FastDiv topk,
                                                                  uint32_t assignments) {
     constexpr int kItems = kBackBlock / LANES, kSeg = LANES * kEach;
@@ -155,7 +156,7 @@ __global__ __launch_bounds__(kBackBlock) void k_combine_backward(CombineArgs g, 
                 const int h = h0 + u * kSeg;
                 if (h >= g.H) continue;
                 d[u].template load<false>(dout, h, lane, g.H);
-                if (g.dweights) f[u].template load<true>(y, h, lane, g.H);
+                if (g.dweights) f[u].template load<ONCE>(y, h, lane, g.H);
             }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
@@ -228,12 +229,12 @@ hipError_t launch_combine(const ue_ctx &, const CombineArgs &g, hipStream_t s) {
             const CombineArgs p = from_token(g, t, g.T - t < tokens ? g.T - t : tokens);
             const uint32_t items = static_cast<uint32_t>(p.T) * segs;
             const dim3 gr((items + kBlock / kLanes - 1) / (kBlock / kLanes));
-            if (g.bf16)
-                hipLaunchKernelGGL((k_combine<uint16_t, kLanes, kShort>), gr, dim3(kBlock), 0, s, p,
-                                   fast_div(segs), items);
-            else
-                hipLaunchKernelGGL((k_combine<float, kLanes, kShort>), gr, dim3(kBlock), 0, s, p,
-                                   fast_div(segs), items);
+            const int64_t bytes = static_cast<int64_t>(g.T) * g.k * g.H * (g.bf16 ? 2 : 4);
+            with_rows(g.bf16, bytes, [&](auto type, auto once) {
+                hipLaunchKernelGGL(
+                    (k_combine<decltype(type), kLanes, kShort, decltype(once)::value>), gr,
+                    dim3(kBlock), 0, s, p, fast_div(segs), items);
+            });
             he = hipGetLastError();
         }
     });
@@ -250,12 +251,12 @@ hipError_t launch_combine_backward(const ue_ctx &, const CombineArgs &g, hipStre
             const CombineArgs p = from_token(g, t, g.T - t < tokens ? g.T - t : tokens);
             const uint32_t items = static_cast<uint32_t>(p.T) * g.k;
             const dim3 gr((items + kItems - 1) / kItems);
-            if (g.bf16)
-                hipLaunchKernelGGL((k_combine_backward<uint16_t, kLanes, kShort>), gr, dim3(kBackBlock), 0,
-                                   s, p, fast_div(g.k), items);
-            else
-                hipLaunchKernelGGL((k_combine_backward<float, kLanes, kShort>), gr, dim3(kBackBlock), 0, s,
-                                   p, fast_div(g.k), items);
+            const int64_t bytes = static_cast<int64_t>(g.T) * g.k * g.H * (g.bf16 ? 2 : 4);
+            with_rows(g.bf16, bytes, [&](auto type, auto once) {
+                hipLaunchKernelGGL(
+                    (k_combine_backward<decltype(type), kLanes, kShort, decltype(once)::value>),
+                    gr, dim3(kBackBlock), 0, s, p, fast_div(g.k), items);
+            });
             he = hipGetLastError();
         }
     });

@@ -13,8 +13,9 @@
 // us (541 MB, 6.2 TB/s), its backward pass with the activation again 107 us (675
 // MB, 6.3 TB/s); 8192 rows of 7168 packed in 19 us (178 MB, 9 TB/s, half of it
 // found in the cache). A quad of lanes takes one block and no loop: what is in
-// flight is other waves'. 13358 rows of 302, fp32, both ways 35 us (element by
-// element, as rows that are no multiple of 16 bytes were read once, 68).
+// flight is other waves'. 13358 rows of 302, fp32, both ways 27 us (element by
+// element, as rows that are no multiple of 16 bytes were read once, 68; past the
+// caches what is read 35).
 #include "ue_train.h"
 
 namespace ue {
@@ -24,14 +25,14 @@ namespace {
 // 2^32 threads; FastDiv takes numbers below 2^31).
 constexpr int64_t kLaunchBlocks = int64_t(1) << 29;
 
-template <typename T>
+template <typename T, bool ONCE>
 __global__ __launch_bounds__(kBlock) void k_pack(PackArgs g, FastDiv per_row, uint32_t blocks) {
     const uint32_t b = blockIdx.x * (kBlock / 4) + (threadIdx.x >> 2);
     if (b >= blocks) return;                       // (whole quads)
     const uint32_t m = div_by(b, per_row), c = b - m * per_row.d;
     const int k = c * UE_PACK_BLOCK + (threadIdx.x & 3) * 8;
     float f[8];
-    load8<T>(static_cast<const T *>(g.x) + m * g.ldx + k, g.K - k, f);
+    load8<ONCE>(static_cast<const T *>(g.x) + m * g.ldx + k, g.K - k, f);
     uint64_t q;
     const uint32_t s = pack8(f, q);
     *reinterpret_cast<uint64_t *>(g.q + m * g.ldq + k) = q;
@@ -50,7 +51,7 @@ __global__ __launch_bounds__(kBlock) void k_unpack(PackArgs g, FastDiv per_row, 
     store8<T>(static_cast<T *>(g.out) + m * g.ldx + k, g.K - k, f);
 }
 
-template <typename T, bool KEEP>
+template <typename T, bool KEEP, bool ONCE>
 __global__ __launch_bounds__(kBlock) void k_gated(GatedArgs g, FastDiv per_row, uint32_t blocks) {
     const uint32_t b = blockIdx.x * (kBlock / 4) + (threadIdx.x >> 2);
     if (b >= blocks) return;
@@ -58,8 +59,8 @@ __global__ __launch_bounds__(kBlock) void k_gated(GatedArgs g, FastDiv per_row, 
     const int k = c * UE_PACK_BLOCK + (threadIdx.x & 3) * 8;
     const T *row = static_cast<const T *>(g.gu) + m * g.ldin + k;
     float gate[8], up[8], h[8];
-    load8<T>(row, g.I - k, gate);
-    load8<T>(row + g.I, g.I - k, up);
+    load8<ONCE>(row, g.I - k, gate);
+    load8<ONCE>(row + g.I, g.I - k, up);
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = silu_of(gate[i]) * up[i];
     store8<T>(static_cast<T *>(g.h) + m * g.ldh + k, g.I - k, h);
@@ -77,7 +78,7 @@ __global__ __launch_bounds__(kBlock) void k_gated(GatedArgs g, FastDiv per_row, 
     }
 }
 
-template <typename T>
+template <typename T, bool ONCE>
 __global__ __launch_bounds__(kBlock) void k_gated_backward(GatedArgs g, FastDiv per_row,
                                                            uint32_t blocks) {
     const uint32_t b = blockIdx.x * (kBlock / 4) + (threadIdx.x >> 2);
@@ -86,12 +87,13 @@ __global__ __launch_bounds__(kBlock) void k_gated_backward(GatedArgs g, FastDiv 
     const int k = c * UE_PACK_BLOCK + (threadIdx.x & 3) * 8;
     const int8_t *from = g.q_in + m * g.ldq + k;
     const uint8_t *st = g.scale_in + m * g.lds + c;
-    const uint64_t qg = __builtin_nontemporal_load(reinterpret_cast<const uint64_t *>(from));
-    const uint64_t qu = __builtin_nontemporal_load(
-        reinterpret_cast<const uint64_t *>(from + per_row.d * UE_PACK_BLOCK));
+    const uint64_t *pg = reinterpret_cast<const uint64_t *>(from);
+    const uint64_t *pu = reinterpret_cast<const uint64_t *>(from + per_row.d * UE_PACK_BLOCK);
+    const uint64_t qg = ONCE ? __builtin_nontemporal_load(pg) : *pg;
+    const uint64_t qu = ONCE ? __builtin_nontemporal_load(pu) : *pu;
     const uint32_t sg = st[0], su = st[per_row.d];
     float d[8], gate[8], up[8], h[8];
-    load8<T>(static_cast<const T *>(g.dh) + m * g.ldin + k, g.I - k, d);
+    load8<ONCE>(static_cast<const T *>(g.dh) + m * g.ldin + k, g.I - k, d);
     unpack8(qg, sg, gate);
     unpack8(qu, su, up);
 #pragma unroll
@@ -148,12 +150,11 @@ hipError_t launch_pack(const ue_ctx &, const PackArgs &g, hipStream_t s) {
         p.x = ahead(g.x, m * g.ldx * (g.bf16 ? 2 : 4));
         p.q = g.q + m * g.ldq;
         p.scale = g.scale + m * g.lds;
-        if (g.bf16)
-            hipLaunchKernelGGL(k_pack<uint16_t>, grid_of(blocks), dim3(kBlock), 0, s, p,
-                               fast_div(nb), blocks);
-        else
-            hipLaunchKernelGGL(k_pack<float>, grid_of(blocks), dim3(kBlock), 0, s, p,
-                               fast_div(nb), blocks);
+        const int64_t bytes = static_cast<int64_t>(g.M) * g.K * (g.bf16 ? 2 : 4);
+        with_rows(g.bf16, bytes, [&](auto t, auto once) {
+            hipLaunchKernelGGL((k_pack<decltype(t), decltype(once)::value>), grid_of(blocks),
+                               dim3(kBlock), 0, s, p, fast_div(nb), blocks);
+        });
     });
 }
 
@@ -181,15 +182,17 @@ hipError_t launch_gated(const ue_ctx &, const GatedArgs &g, hipStream_t s) {
         p.h = ahead(g.h, m * g.ldh * es);
         p.q = ahead(g.q, m * g.ldq);
         p.scale = ahead(g.scale, m * g.lds);
-        const dim3 gr = grid_of(blocks), bl(kBlock);
-        const FastDiv d = fast_div(nb);
-        if (g.bf16) {
-            if (g.q) hipLaunchKernelGGL((k_gated<uint16_t, true>), gr, bl, 0, s, p, d, blocks);
-            else hipLaunchKernelGGL((k_gated<uint16_t, false>), gr, bl, 0, s, p, d, blocks);
-        } else {
-            if (g.q) hipLaunchKernelGGL((k_gated<float, true>), gr, bl, 0, s, p, d, blocks);
-            else hipLaunchKernelGGL((k_gated<float, false>), gr, bl, 0, s, p, d, blocks);
-        }
+        const int64_t bytes = static_cast<int64_t>(g.M) * g.I * 2 * es;
+        with_rows(g.bf16, bytes, [&](auto t, auto once) {
+            typedef decltype(t) T;
+            constexpr bool kOnce = decltype(once)::value;
+            if (g.q)
+                hipLaunchKernelGGL((k_gated<T, true, kOnce>), grid_of(blocks), dim3(kBlock), 0, s,
+                                   p, fast_div(nb), blocks);
+            else
+                hipLaunchKernelGGL((k_gated<T, false, kOnce>), grid_of(blocks), dim3(kBlock), 0,
+                                   s, p, fast_div(nb), blocks);
+        });
     });
 }
 
@@ -202,12 +205,11 @@ hipError_t launch_gated_backward(const ue_ctx &, const GatedArgs &g, hipStream_t
         p.h = ahead(g.h, m * g.ldh * es);
         p.q_in = g.q_in + m * g.ldq;
         p.scale_in = g.scale_in + m * g.lds;
-        if (g.bf16)
-            hipLaunchKernelGGL(k_gated_backward<uint16_t>, grid_of(blocks), dim3(kBlock), 0, s,
-                               p, fast_div(nb), blocks);
-        else
-            hipLaunchKernelGGL(k_gated_backward<float>, grid_of(blocks), dim3(kBlock), 0, s, p,
-                               fast_div(nb), blocks);
+        const int64_t bytes = static_cast<int64_t>(g.M) * g.I * (es + 2);
+        with_rows(g.bf16, bytes, [&](auto t, auto once) {
+            hipLaunchKernelGGL((k_gated_backward<decltype(t), decltype(once)::value>),
+                               grid_of(blocks), dim3(kBlock), 0, s, p, fast_div(nb), blocks);
+        });
     });
 }
 

@@ -4,6 +4,8 @@
 
 #include "ue_gate.h"
 
+#include <type_traits>
+
 namespace ue {
 
 struct BalanceArgs {
@@ -121,6 +123,19 @@ hipError_t launch_wgrad(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_
 // Parts each group's rows are split into (1: no workspace).
 int wgrad_parts(int M, int N, int K, int G, int num_cu);
 
+// What a call reads is not kept in the caches where it is more than half of what
+// the last of them holds (256 MB; the rest is for what the call writes): the sum of
+// 25517 tokens' top-5 rows of 166, fp32, 85 MB, both ways 59 us through the caches
+// and 77 past them, gated activation of 32768 rows of 2048, 268 MB, both ways 198
+// and 193, 16384 tokens' top-8 rows of 7168, 1.9 GB, 1168 and 1100.
+// f(type of the rows, past the caches).
+template <class F>
+void with_rows(bool bf16, int64_t bytes_read, F f) {
+    const bool once = bytes_read > (int64_t(128) << 20);
+    if (bf16) once ? f(uint16_t{}, std::true_type{}) : f(uint16_t{}, std::false_type{});
+    else once ? f(float{}, std::true_type{}) : f(float{}, std::false_type{});
+}
+
 // ---------------------------------------------------------------------
 // device helpers
 
@@ -139,11 +154,10 @@ template <>
 __device__ __forceinline__ uint16_t narrow<uint16_t>(float v) { return f32_to_bf16(v); }
 
 // N elements, or those of them before `n`, at p, in loads and stores of up to 16
-// bytes whatever p's alignment (the device takes any). ONCE: past the caches, both
-// ways: most of what these kernels read and write is used once each, and is
-// larger than the caches where time counts (gated activation of 32768 rows of
-// 2048 with its backward pass 258 us through the caches, 181 past them; gradients
-// of the sum of rows, 16384 tokens x top-8 x 7168, 1020 against 881).
+// bytes whatever p's alignment (the device takes any). ONCE: past the caches, as
+// results go always (gated activation of 32768 rows of 2048 with its backward pass
+// 258 us with results through the caches, 198 past them), and what a call reads
+// where it is large (`with_rows`).
 template <int BYTES>
 struct Words {
     typedef uint32_t type __attribute__((ext_vector_type(BYTES / 4), aligned(2)));
@@ -190,9 +204,9 @@ __device__ __forceinline__ void store_run(T *p, int n, const float (&f)[N]) {
             if (i < n) p[i] = narrow<T>(f[i]);
     }
 }
-template <typename T>
+template <bool ONCE, typename T>
 __device__ __forceinline__ void load8(const T *p, int n, float (&f)[8]) {
-    load_run<8, true>(p, n, f);
+    load_run<8, ONCE>(p, n, f);
 }
 template <typename T>
 __device__ __forceinline__ void store8(T *p, int n, const float (&f)[8]) {
