@@ -736,6 +736,59 @@ def test_outputs_made_here_are_ordinary_tensors(shape):
     ctx.close()
 
 
+@pytest.mark.parametrize("H", (3, 100, 250, 2056))
+@pytest.mark.parametrize("dtype", TYPES)
+def test_large_sums_of_rows_are_the_small_ones(dtype, H):
+    """A call that reads more than is kept in the caches, against two that read
+    half of it: bit for bit."""
+    say("large combine", H, dtype)
+    k, es = 2, torch.finfo(dtype).bits // 8
+    T = (140 << 20) // (H * es * k)
+    ctx = ctx_for(8, k, T)
+    g = torch.Generator(device=DEV).manual_seed(H)
+    y = torch.randn((T * k, H), generator=g, device=DEV, dtype=dtype)
+    dout = torch.randn((T, H), generator=g, device=DEV, dtype=dtype)
+    w = torch.rand((T, k), generator=g, device=DEV)
+    inv = torch.randperm(T * k, generator=g, device=DEV).int().view(T, k)
+    out = ue.ue_combine(ctx, y, inv, w, add=dout)
+    dy, dw = ue.ue_combine_backward(ctx, dout, inv, w, y)
+    dy2 = torch.empty_like(dy)
+    for part in (slice(0, T // 2), slice(T // 2, T)):
+        assert torch.equal(out[part], ue.ue_combine(ctx, y, inv[part], w[part], add=dout[part]))
+        _, dw2 = ue.ue_combine_backward(ctx, dout[part], inv[part], w[part], y, dy=dy2)
+        assert torch.equal(dw[part], dw2)
+    assert torch.equal(dy, dy2)
+    ctx.close()
+
+
+@pytest.mark.parametrize("I", (5, 302, 2048))
+@pytest.mark.parametrize("dtype", TYPES)
+def test_large_gated_rows_are_the_small_ones(dtype, I):
+    """The same of the gated activation, its backward pass and packed rows."""
+    say("large gated", I, dtype)
+    es = torch.finfo(dtype).bits // 8
+    M = (280 << 20) // (I * 2 * es)
+    ctx = ctx_for(8, 2, 8)
+    g = torch.Generator(device=DEV).manual_seed(I)
+    gu = torch.randn((M, 2 * I), generator=g, device=DEV, dtype=dtype)
+    dh = torch.randn((M, I), generator=g, device=DEV, dtype=dtype)
+    h, q, s = ue.ue_gated(ctx, gu)
+    dgu, h2 = ue.ue_gated_backward(ctx, dh, q, s)
+    pq, ps = ue.ue_pack_rows(ctx, gu)
+    bare = ue.ue_gated(ctx, gu, keep=False)[0]
+    assert torch.equal(bare, h)
+    for i in range(4):
+        part = slice(M * i // 4, M * (i + 1) // 4)
+        a = ue.ue_gated(ctx, gu[part])
+        assert torch.equal(h[part], a[0]) and torch.equal(q[part], a[1]) and torch.equal(s[part], a[2])
+        assert torch.equal(h[part], ue.ue_gated(ctx, gu[part], keep=False)[0])
+        b = ue.ue_gated_backward(ctx, dh[part], q[part], s[part])
+        assert torch.equal(dgu[part], b[0]) and torch.equal(h2[part], b[1])
+        c = ue.ue_pack_rows(ctx, gu[part])
+        assert torch.equal(pq[part], c[0]) and torch.equal(ps[part], c[1])
+    ctx.close()
+
+
 def test_combine_edges():
     """No tokens, no rows, infinities beside ordinary rows, the gather's
     gradient."""
