@@ -36,7 +36,7 @@
  *    not overlap one another, replays of captured ones included.
  *    ue_weight_sync, ue_grad_reduce, ue_gather_rows, ue_gate,
  *    ue_gate_backward, ue_quantize_rows, ue_matmul_i8 and the calls of the
- *    training step (ue_balance to ue_combine_backward) use no workspace but
+ *    training step (ue_balance to ue_combine_backward_all) use no workspace but
  *    what they are given, and may run on another stream beside them (the next layer's
  *    rebalance beside this layer's sync), while kernel timing is off and
  *    the registered tables are not replaced meanwhile.
@@ -716,6 +716,19 @@ int ue_combine_backward(ue_ctx *ctx, const void *dout, int32_t type,
                         const float *weights, const void *y, int64_t ldy,
                         int32_t rows, int32_t T, int32_t H, void *dy,
                         int64_t lddy, float *dweights, void *stream);
+/* The same with the whole gradient: rows of dy that no assignment names are
+ * written with zeros. dy may be NULL only if rows is 0.
+ *   workspace  device, 16-byte aligned, ue_combine_backward_workspace(ctx, T,
+ *              rows) bytes, overwritten; may be NULL where that is 0 (few
+ *              assignments). Calls given the same one must not overlap, replays
+ *              of captured ones included. */
+size_t ue_combine_backward_workspace(const ue_ctx *ctx, int32_t T, int32_t rows);
+int ue_combine_backward_all(ue_ctx *ctx, const void *dout, int32_t type,
+                            int64_t lddout, const int32_t *inv_perm,
+                            const float *weights, const void *y, int64_t ldy,
+                            int32_t rows, int32_t T, int32_t H, void *dy,
+                            int64_t lddy, float *dweights, void *workspace,
+                            void *stream);
 
 #ifdef __cplusplus
 }

@@ -157,6 +157,10 @@ SIGNATURES = {
     "ue_combine_backward": (ctypes.c_int, [_vp, _vp, _i32, _i64, _vp, _vp, _vp,
                                            _i64, _i32, _i32, _i32, _vp, _i64,
                                            _vp, _vp]),
+    "ue_combine_backward_workspace": (ctypes.c_size_t, [_vp, _i32, _i32]),
+    "ue_combine_backward_all": (ctypes.c_int, [_vp, _vp, _i32, _i64, _vp, _vp,
+                                               _vp, _i64, _i32, _i32, _i32,
+                                               _vp, _i64, _vp, _vp, _vp]),
     "ue_rebalance_static": (ctypes.c_int, [ctypes.POINTER(ue_config), _vp,
                                            _i32, _i32, _vp, _vp, _vp, _vp,
                                            _vp, _vp, _vp, _vp, _vp]),
@@ -1330,7 +1334,8 @@ def ue_combine_backward(ctx: Context, dout, inv_perm, weights=None, y=None,
                         dy=None, dweights=None, with_dy=True, stream=None):
     """Gradients of :func:`ue_combine` from dout [T, H]: (dy, dweights). dy is
     as y (or, without y, [T * k, H]); its rows that inv_perm does not name are
-    left as they are. dweights fp32 [T, k] needs y and is None without it."""
+    zeros, and left as they are in a ``dy`` given by the caller. dweights fp32
+    [T, k] needs y and is None without it."""
     dev = ctx.device
     T, H, lddo = _rows(dout, "dout", dev, _FLOATS)
     n, pi, pw = _assigned(ctx, inv_perm, weights)
@@ -1346,7 +1351,8 @@ def ue_combine_backward(ctx: Context, dout, inv_perm, weights=None, y=None,
             dweights = _new((T, ctx.k), torch.float32, ctx, stream)
         else:
             _flat(dweights, "dweights", torch.float32, dev, T * ctx.k)
-    lddy = H
+    lib, lddy = library(), H
+    call, ws, workspace = lib.ue_combine_backward, (), None
     if dy is not None:
         n, _, lddy = _rows(dy, "dy", dev, (dout.dtype,), H)
         if y is None:
@@ -1355,11 +1361,16 @@ def ue_combine_backward(ctx: Context, dout, inv_perm, weights=None, y=None,
             raise ValueError(f"dy must have {rows} rows")
     elif with_dy:
         dy = _new((rows, H), dout.dtype, ctx, stream)
-    rc = library().ue_combine_backward(
+        call, ws = lib.ue_combine_backward_all, (None,)
+        need = lib.ue_combine_backward_workspace(ctx._h, T, rows)
+        if need:
+            workspace = _new((need,), torch.uint8, ctx, stream)
+            ws = (workspace.data_ptr(),)
+    rc = call(
         ctx._h, dout.data_ptr(), _TYPES[dout.dtype], lddo, pi, pw, py, ldy,
         rows, T, H, None if dy is None else dy.data_ptr(), lddy,
-        None if dweights is None else dweights.data_ptr(),
-        _on(ctx, stream, dout, inv_perm, weights, y, dy, dweights))
+        None if dweights is None else dweights.data_ptr(), *ws,
+        _on(ctx, stream, dout, inv_perm, weights, y, dy, dweights, workspace))
     if rc:
         ctx._check(rc, "ue_combine_backward")
     return dy, dweights

@@ -133,11 +133,99 @@ __global__ __launch_bounds__(kBlock) void k_combine(CombineArgs g, FastDiv segs,
 constexpr int kAhead = 2;     // segments in flight
 constexpr int kBackBlock = 512;
 
+// Zeros in a row of dy, by the lanes of one.
+template <typename T, int LANES, bool SHORT>
+__device__ __forceinline__ void zero_row(const CombineArgs &g, int64_t row, int lane) {
+    const float none[kEach] = {};
+    for (int h = 0; h < g.H; h += LANES * kEach)
+        Segment<T, LANES, SHORT>::store(static_cast<T *>(g.dy) + row * g.lddy, h, lane, g.H, none);
+}
+
+// Rows of dy that no assignment names, where all are to be written: the first
+// `clear` workgroups of the launch (a power of two) take rows clear apart (the
+// unnamed ones are often the last), find the named ones of theirs and write zeros to
+// the others, while the rest of the launch writes the named ones.
+// A few assignments are all looked at by each of these workgroups. Of many, a launch
+// ahead notes for each row an assignment that names it: what was noted is true if
+// that assignment does, and a row that none names holds anything, so the notes need
+// not be cleared. Calls of top-8, all rows named, us without and with this:
+//    32768 rows of 512 bytes      8.9    8.9    looked at
+//    32768 rows of 16 KB        220    220
+//    32776 rows of 512 bytes      8.9   12.1    noted
+//   131072 rows of 240 bytes     17.0   20.7    (each assignment looked at: 25)
+//   131072 rows of 16 KB        865    873
+//   524288 rows of 240 bytes     66     76      (each assignment looked at: 102)
+// Zeros in all of dy ahead of the launch took 11 us for the first of these, 23, 1276
+// and 87 for the last three.
+constexpr int kLookAt = 1 << 15;           // assignments
+constexpr int kClearBlocks = 256, kClearRows = 4096;
+
+template <typename T, int LANES, bool SHORT>
+__device__ __forceinline__ void clear_unnamed(const CombineArgs &g) {
+    __shared__ uint32_t named[kClearRows / 32];
+    const uint32_t mine = blockIdx.x, rows = g.rows, all = g.all;
+    const uint32_t shift = __builtin_ctz(g.clear);
+    auto mark = [&](uint32_t i) { atomicOr(&named[i >> 5], 1u << (i & 31)); };
+    // (rows counted in steps of `clear`; more than kClearRows of them only with notes)
+    const uint32_t steps = mine < rows ? ((rows - 1 - mine) >> shift) + 1 : 0;
+    for (uint32_t from = 0; from < steps; from += kClearRows) {
+        const uint32_t n = steps - from < kClearRows ? steps - from : kClearRows;
+        if (threadIdx.x < kClearRows / 32) named[threadIdx.x] = 0;
+        __syncthreads();
+        if (g.named_by) {
+            for (uint32_t i = threadIdx.x; i < n; i += kBackBlock) {
+                const uint32_t row = ((from + i) << shift) + mine, by = g.named_by[row];
+                if (by < all && static_cast<uint32_t>(g.inv[by]) == row) mark(i);
+            }
+        } else {
+            typedef uint32_t Four __attribute__((ext_vector_type(4), aligned(4)));
+            constexpr uint32_t kLoads = 4;
+            const uint32_t fours = all / 4;
+            auto look = [&](uint32_t row) {
+                if (row < rows && (row & (g.clear - 1)) == mine) mark(row >> shift);
+            };
+            for (uint32_t a = threadIdx.x; a < fours; a += kLoads * kBackBlock) {
+                Four row[kLoads];
+#pragma unroll
+                for (uint32_t u = 0; u < kLoads; ++u) {
+                    const uint32_t at = a + u * kBackBlock;
+                    row[u] = *reinterpret_cast<const Four *>(g.inv + 4 * (at < fours ? at : a));
+                    if (at >= fours) row[u] = ~Four{};
+                }
+#pragma unroll
+                for (uint32_t u = 0; u < kLoads; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) look(row[u][e]);
+            }
+            if (threadIdx.x < (all & 3)) look(g.inv[4 * fours + threadIdx.x]);
+        }
+        __syncthreads();
+        const int lane = threadIdx.x % LANES;
+        for (uint32_t i = threadIdx.x / LANES; i < n; i += kBackBlock / LANES)
+            if (!(named[i >> 5] >> (i & 31) & 1))
+                zero_row<T, LANES, SHORT>(g, ((from + i) << shift) + mine, lane);
+        __syncthreads();
+    }
+}
+
+__global__ __launch_bounds__(kBlock) void k_combine_note(CombineArgs g) {
+    const uint32_t a = blockIdx.x * kBlock + threadIdx.x;
+    if (a >= g.all) return;
+    const uint32_t row = g.inv[a];
+    if (row < static_cast<uint32_t>(g.rows)) g.named_by[row] = a;
+}
+
+// (four workgroups of rows of 64 lanes per CU, which 65 registers of fp32 rows
+// would make three)
 template <typename T, int LANES, bool SHORT, bool ONCE>
-__global__ __launch_bounds__(kBackBlock) void k_combine_backward(CombineArgs g, FastDiv topk,
-                                                                 uint32_t assignments) {
+__global__ __launch_bounds__(kBackBlock, LANES == 64 ? 8 : 6) void k_combine_backward(
+    CombineArgs g, FastDiv topk, uint32_t assignments) {
     constexpr int kItems = kBackBlock / LANES, kSeg = LANES * kEach;
-    uint32_t a = blockIdx.x * kItems + threadIdx.x / LANES;
+    if (blockIdx.x < g.clear) {
+        clear_unnamed<T, LANES, SHORT>(g);
+        return;
+    }
+    uint32_t a = (blockIdx.x - g.clear) * kItems + threadIdx.x / LANES;
     if (LANES == 64) a = __builtin_amdgcn_readfirstlane(a);
     if (a >= assignments) return;                   // (whole rows of lanes)
     const int lane = threadIdx.x % LANES, t = div_by(a, topk);
@@ -241,16 +329,35 @@ hipError_t launch_combine(const ue_ctx &, const CombineArgs &g, hipStream_t s) {
     return he;
 }
 
-hipError_t launch_combine_backward(const ue_ctx &, const CombineArgs &g, hipStream_t s) {
+bool combine_notes(int T, int k, int rows) {
+    return static_cast<int64_t>(T) * k > kLookAt || rows > kClearBlocks * kClearRows;
+}
+
+hipError_t launch_combine_backward(const ue_ctx &, const CombineArgs &a, bool every_row,
+                                   hipStream_t s) {
     hipError_t he = hipSuccess;
+    CombineArgs g = a;
+    g.all = static_cast<uint32_t>(g.T) * g.k;
+    g.clear = 0;
+    if (every_row && g.rows > 0) {
+        for (g.clear = 1; g.clear < kClearBlocks && g.clear * kBackBlock < static_cast<uint32_t>(g.rows);)
+            g.clear *= 2;
+        if (g.named_by && g.all > 0) {
+            hipLaunchKernelGGL(k_combine_note, dim3((g.all + kBlock - 1) / kBlock), dim3(kBlock), 0, s,
+                               g);
+            he = hipGetLastError();
+        }
+    }
     with_row_lanes(g, [&](auto l, auto few) {
         constexpr bool kShort = decltype(few)::value;
         constexpr int kLanes = decltype(l)::value, kItems = kBackBlock / kLanes;
         const int64_t tokens = kLaunchItems / g.k;
-        for (int64_t t = 0; t < g.T && he == hipSuccess; t += tokens) {
-            const CombineArgs p = from_token(g, t, g.T - t < tokens ? g.T - t : tokens);
+        // (no token is a launch all the same if rows are to be cleared)
+        for (int64_t t = 0; (t < g.T || (t == 0 && g.clear)) && he == hipSuccess; t += tokens) {
+            CombineArgs p = from_token(g, t, g.T - t < tokens ? g.T - t : tokens);
+            if (t > 0) p.clear = 0;
             const uint32_t items = static_cast<uint32_t>(p.T) * g.k;
-            const dim3 gr((items + kItems - 1) / kItems);
+            const dim3 gr((items + kItems - 1) / kItems + p.clear);
             const int64_t bytes = static_cast<int64_t>(g.T) * g.k * g.H * (g.bf16 ? 2 : 4);
             with_rows(g.bf16, bytes, [&](auto type, auto once) {
                 hipLaunchKernelGGL(

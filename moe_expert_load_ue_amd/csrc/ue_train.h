@@ -94,9 +94,15 @@ struct CombineArgs {
     void *dy;                   // or null
     int64_t lddy;
     float *dweights;            // or null
+    uint32_t *named_by;         // [rows] notes of who names a row, or null
+    uint32_t clear, all;        // set at launch: workgroups that clear rows of dy, and
+                                // all assignments
 };
 hipError_t launch_combine(const ue_ctx &c, const CombineArgs &g, hipStream_t s);
-hipError_t launch_combine_backward(const ue_ctx &c, const CombineArgs &g,
+// Whether rows that no assignment names are found with notes (4 bytes a row).
+bool combine_notes(int T, int k, int rows);
+// every_row: rows of dy that no assignment names are written too, with zeros.
+hipError_t launch_combine_backward(const ue_ctx &c, const CombineArgs &g, bool every_row,
                                    hipStream_t s);
 
 struct WgradArgs {

@@ -391,25 +391,30 @@ int ue_combine(ue_ctx *ctx, const void *y, int32_t type, int64_t ldy, int32_t ro
     return done(ctx, ue::launch_combine(*ctx, g, s), s, "k_combine launch");
 }
 
-int ue_combine_backward(ue_ctx *ctx, const void *dout, int32_t type, int64_t lddout,
-                        const int32_t *inv_perm, const float *weights, const void *y,
-                        int64_t ldy, int32_t rows, int32_t T, int32_t H, void *dy,
-                        int64_t lddy, float *dweights, void *stream) {
+static int combine_backward(ue_ctx *ctx, const char *what, bool every_row, const void *dout,
+                            int32_t type, int64_t lddout, const int32_t *inv_perm,
+                            const float *weights, const void *y, int64_t ldy, int32_t rows,
+                            int32_t T, int32_t H, void *dy, int64_t lddy, float *dweights,
+                            void *workspace, void *stream) {
     if (!ctx) return UE_EINVAL;
     ctx->err.clear();
-    const char *what = "ue_combine_backward";
     if (T < 0 || T > ctx->cfg.max_tokens || H < 1 || H > kMaxCols || rows < 0)
         return fail(ctx, UE_ESHAPE, "%s: T=%d (0..%d) H=%d rows=%d", what, T,
                     ctx->cfg.max_tokens, H, rows);
     if (int rc = check_rows(ctx, what, "dout", dout, type, lddout, T, H)) return rc;
     if (dweights)
         if (int rc = check_rows(ctx, what, "y", y, type, ldy, T > 0 ? rows : 0, H)) return rc;
+    const bool notes = every_row && ue::combine_notes(T, ctx->k, rows);
+    if (every_row && rows > 0 && (!dy || (notes && !workspace)))
+        return fail(ctx, UE_EINVAL, "%s: null dy or workspace", what);
     if (dy)
         if (int rc = check_rows(ctx, what, "dy", dy, type, lddy, T > 0 ? rows : 0, H)) return rc;
     if (T > 0 && !inv_perm) return fail(ctx, UE_EINVAL, "%s: null inv_perm", what);
-    if (!aligned(inv_perm, 4) || !aligned(weights, 4) || !aligned(dweights, 4))
+    if (!aligned(inv_perm, 4) || !aligned(weights, 4) || !aligned(dweights, 4) ||
+        !aligned(workspace, 16))
         return fail(ctx, UE_EINVAL, "%s: unaligned argument", what);
     ue::CombineArgs g{};
+    g.named_by = notes ? static_cast<uint32_t *>(workspace) : nullptr;
     g.y = y;
     g.ldy = ldy;
     g.rows = rows;
@@ -426,8 +431,31 @@ int ue_combine_backward(ue_ctx *ctx, const void *dout, int32_t type, int64_t ldd
     g.dweights = dweights;
     hipStream_t s = static_cast<hipStream_t>(stream);
     tbegin(ctx, s);
-    const hipError_t he = dy || dweights ? ue::launch_combine_backward(*ctx, g, s) : hipSuccess;
+    const hipError_t he = dy || dweights ? ue::launch_combine_backward(*ctx, g, every_row, s)
+                                         : hipSuccess;
     return done(ctx, he, s, "k_combine_backward launch");
 }
+
+int ue_combine_backward(ue_ctx *ctx, const void *dout, int32_t type, int64_t lddout,
+                        const int32_t *inv_perm, const float *weights, const void *y,
+                        int64_t ldy, int32_t rows, int32_t T, int32_t H, void *dy,
+                        int64_t lddy, float *dweights, void *stream) {
+    return combine_backward(ctx, "ue_combine_backward", false, dout, type, lddout, inv_perm,
+                            weights, y, ldy, rows, T, H, dy, lddy, dweights, nullptr, stream);
+}
+
+size_t ue_combine_backward_workspace(const ue_ctx *ctx, int32_t T, int32_t rows) {
+    if (!ctx || T < 0 || rows < 0 || !ue::combine_notes(T, ctx->k, rows)) return 0;
+    return static_cast<size_t>(rows) * 4;
+}
+
+int ue_combine_backward_all(ue_ctx *ctx, const void *dout, int32_t type, int64_t lddout,
+                            const int32_t *inv_perm, const float *weights, const void *y,
+                            int64_t ldy, int32_t rows, int32_t T, int32_t H, void *dy,
+                            int64_t lddy, float *dweights, void *workspace, void *stream) {
+    return combine_backward(ctx, "ue_combine_backward_all", true, dout, type, lddout, inv_perm,
+                            weights, y, ldy, rows, T, H, dy, lddy, dweights, workspace, stream);
+}
+
 
 }  // extern "C"
