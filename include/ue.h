@@ -608,7 +608,8 @@ int ue_balance_backward(ue_ctx *ctx, const void *logits, int32_t type,
  * magnitude, e the smallest exponent from -126 with top <= 127 * 2^e:
  *   q = rint(x / 2^e) (to even),  scale = e + 127 as a byte
  * so |x - q 2^e| <= 2^(e-1), every quotient is exact, and q 2^e is a bf16
- * number. A block of zeros has scale 1. A block that holds an infinity or a NaN
+ * number. e is at most 121, so that q 2^e is finite: of larger magnitudes than
+ * 127 * 2^121 (3.376e38) q is +-127, less than a step away. A block of zeros has scale 1. A block that holds an infinity or a NaN
  * has q = 0 and scale 255 and stands for NaNs.
  *   x      device, [M] rows of K, UE_F32 or UE_BF16, ldx apart
  *   q      device, int8, 16-byte aligned rows ldq apart (a multiple of 16, at

@@ -221,16 +221,18 @@ __device__ __forceinline__ void store8(T *p, int n, const float (&f)[8]) {
 
 // The power of two of a block whose largest magnitude has these bits, biased
 // by 127: its exponent less 6, one more above 127/64 of its power of two, and
-// at least 1 (so that it and its inverse are normal numbers); 255 for a block
-// that holds an infinity or a NaN.
+// at least 1 (so that it and its inverse are normal numbers); at most 248, whose
+// 127-fold is still a float (64 times the next one is 2^128); 255 for a block that
+// holds an infinity or a NaN.
 __device__ __forceinline__ uint32_t block_scale(uint32_t top) {
     if (top >= 0x7F800000u) return 255u;
-    const uint32_t e = (top + 0x1FFFFu) >> 23;
+    uint32_t e = (top + 0x1FFFFu) >> 23;
+    e = e < 254u ? e : 254u;
     return e > 7u ? e - 6u : 1u;
 }
 // 2^e, infinity for 255 (which q = 0 turns into the block's NaNs).
 __device__ __forceinline__ float scale_step(uint32_t s) { return __uint_as_float(s << 23); }
-// 2^-e, 0 for 255 (254 - e is 0 only for e = 254, which no finite block has).
+// 2^-e, 0 for 255.
 __device__ __forceinline__ float scale_inverse(uint32_t s) {
     return s >= 254u ? 0.f : __uint_as_float((254u - s) << 23);
 }
@@ -256,8 +258,11 @@ __device__ __forceinline__ uint32_t pack8(const float (&f)[8], uint64_t &q) {
     const float inv = scale_inverse(s);
     union { int8_t b[8]; uint64_t w; } u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        u.b[i] = static_cast<int8_t>(s == 255u ? 0 : static_cast<int>(rintf(f[i] * inv)));
+    for (int i = 0; i < 8; ++i) {
+        // (up to 128 steps where they are the largest)
+        const float r = __builtin_amdgcn_fmed3f(rintf(f[i] * inv), -127.f, 127.f);
+        u.b[i] = static_cast<int8_t>(s == 255u ? 0 : static_cast<int>(r));
+    }
     q = u.w;
     return s;
 }

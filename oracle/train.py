@@ -71,7 +71,8 @@ def balance_backward(logits, counts, dloss, k, offsets=None, score="softmax"):
 
 def pack(x):
     """(q int8 [M, K], scale uint8 [M, blocks]), block by block from the
-    definition: the smallest e >= -126 with top <= 127 * 2^e."""
+    definition: the smallest e >= -126 with top <= 127 * 2^e, but 121 at most,
+    whose 127-fold is the last that is a float; past that q is +-127."""
     x = np.asarray(x, np.float64)
     M, K = x.shape
     nb = -(-K // BLOCK)
@@ -86,12 +87,13 @@ def pack(x):
             e = -126
             if top > 0:
                 e = max(-126, math.frexp(top)[1] - 8)
-                while top > math.ldexp(127.0, e):
+                while top > math.ldexp(127.0, e) and e < 121:
                     e += 1
+                e = min(e, 121)
                 while e > -126 and top <= math.ldexp(127.0, e - 1):
                     e -= 1
             scale[m, c] = e + 127
-            q[m, c * BLOCK:(c + 1) * BLOCK] = np.rint(v * math.ldexp(1.0, -e))
+            q[m, c * BLOCK:(c + 1) * BLOCK] = np.clip(np.rint(v * math.ldexp(1.0, -e)), -127, 127)
     return q, scale
 
 
