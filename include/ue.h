@@ -322,7 +322,9 @@ int ue_rebalance_static(const ue_config *cfg, const int32_t *routing,
  * stream before its first kernel and after each kernel it launches.
  * ue_kernel_times waits for the latest call's last event and writes the
  * duration in milliseconds of each of its kernels, in launch order, to
- * ms[0 .. *n-1] (at most max_n values; *n is the number that call launched).
+ * ms[0 .. *n-1] (at most max_n values; *n is the number that call launched; a
+ * kernel that takes several launches, for more rows than the threads of one
+ * reach, counts as one).
  * Off by default; enabling it costs one event per kernel. Errors:
  * UE_ESTATE if timing is off or no call has run since it was enabled. */
 int ue_set_timing(ue_ctx *ctx, int enable);

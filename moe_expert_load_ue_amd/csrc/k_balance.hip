@@ -527,7 +527,7 @@ int64_t balance_slots(int T, int n_seq, int E, int num_cu) {
     return (static_cast<int64_t>(T) + c - 1) / c + n_seq;
 }
 
-hipError_t launch_balance(const ue_ctx &c, const BalanceArgs &a, hipStream_t s) {
+hipError_t launch_balance(ue_ctx &c, const BalanceArgs &a, hipStream_t s) {
     if (a.n_seq == 0) return hipSuccess;
     BalanceArgs g = a;
     g.chunk = balance_chunk(g.T, g.E, c.num_cu);
@@ -540,6 +540,7 @@ hipError_t launch_balance(const ue_ctx &c, const BalanceArgs &a, hipStream_t s) 
                   : balance_any<float, false>(g, shares, s);
     const hipError_t he = hipGetLastError();
     if (he != hipSuccess || !g.part) return he;
+    tmark(&c, s);
     hipLaunchKernelGGL(k_balance_end, dim3(g.n_seq), dim3(kEndBlock), 0, s, g);
     return hipGetLastError();
 }

@@ -333,7 +333,7 @@ bool combine_notes(int T, int k, int rows) {
     return static_cast<int64_t>(T) * k > kLookAt || rows > kClearBlocks * kClearRows;
 }
 
-hipError_t launch_combine_backward(const ue_ctx &, const CombineArgs &a, bool every_row,
+hipError_t launch_combine_backward(ue_ctx &c, const CombineArgs &a, bool every_row,
                                    hipStream_t s) {
     hipError_t he = hipSuccess;
     CombineArgs g = a;
@@ -346,6 +346,7 @@ hipError_t launch_combine_backward(const ue_ctx &, const CombineArgs &a, bool ev
             hipLaunchKernelGGL(k_combine_note, dim3((g.all + kBlock - 1) / kBlock), dim3(kBlock), 0, s,
                                g);
             he = hipGetLastError();
+            tmark(&c, s);
         }
     }
     with_row_lanes(g, [&](auto l, auto few) {

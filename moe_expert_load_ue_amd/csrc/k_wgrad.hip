@@ -682,6 +682,7 @@ hipError_t launch_wgrad(ue_ctx &c, const WgradArgs &a, hipStream_t s, bool &too_
     g.accumulate = false;
     const hipError_t he = wgrad_tiles(c, g, s, too_large);
     if (he != hipSuccess || too_large) return he;
+    tmark(&c, s);
     hipLaunchKernelGGL(k_wgrad_join, per_row, dim3(kBlock), 0, s, a);
     return hipGetLastError();
 }

@@ -8,6 +8,10 @@
 
 namespace ue {
 
+// A launcher that starts several kernels one after another marks the end of each
+// but the last (tmark); a kernel in several launches, for more rows than one's
+// threads reach, is one.
+
 struct BalanceArgs {
     const void *logits;         // [T] rows of E, ld elements apart
     int64_t ld;
@@ -36,7 +40,7 @@ struct BalanceBackArgs {
 // n_seq sequences need (0: none are made).
 int balance_chunk(int T, int E, int num_cu);
 int64_t balance_slots(int T, int n_seq, int E, int num_cu);
-hipError_t launch_balance(const ue_ctx &c, const BalanceArgs &g, hipStream_t s);
+hipError_t launch_balance(ue_ctx &c, const BalanceArgs &g, hipStream_t s);
 hipError_t launch_balance_backward(const ue_ctx &c, const BalanceBackArgs &g,
                                    hipStream_t s);
 
@@ -102,7 +106,7 @@ hipError_t launch_combine(const ue_ctx &c, const CombineArgs &g, hipStream_t s);
 // Whether rows that no assignment names are found with notes (4 bytes a row).
 bool combine_notes(int T, int k, int rows);
 // every_row: rows of dy that no assignment names are written too, with zeros.
-hipError_t launch_combine_backward(const ue_ctx &c, const CombineArgs &g, bool every_row,
+hipError_t launch_combine_backward(ue_ctx &c, const CombineArgs &g, bool every_row,
                                    hipStream_t s);
 
 struct WgradArgs {
