@@ -535,6 +535,13 @@ int64_t tiles_of(int N, int K, int b) {
 WgradTile wgrad_tile(int N, int K, int64_t G, int num_cu) {
     return tiles_of(N, K, 256) * G >= num_cu * 3 / 4 ? kTile256 : kTile128;
 }
+constexpr int per_cu(int tile) { return tile == 256 ? 1 : 2; }      // workgroups
+
+// Matrices too small to be read in pieces.
+bool wgrad_tiny(const WgradArgs &g) {
+    auto tiny = [](int64_t rows, int64_t ld, int cols) { return (rows - 1) * ld + cols < kPiece; };
+    return tiny(g.M, g.lddy, g.N) || (!g.x_scale && tiny(g.x_rows, g.ldx, g.K));
+}
 // A part has at least kPartRows rows (on average), so that what it writes and
 // reads again, 128 KB for a tile of 128, is less than the rows it saves others.
 constexpr int kPartRows = 256, kMaxParts = 64;
@@ -548,7 +555,7 @@ __global__ __launch_bounds__(kBlock) void k_wgrad_zero(WgradArgs g) {
     }
 }
 
-// Matrices too small to be read in pieces: a thread per result.
+// Those too small to be read in pieces: a thread per result.
 __global__ __launch_bounds__(kBlock) void k_wgrad_tiny(WgradArgs g) {
     const int64_t each = static_cast<int64_t>(g.N) * g.K, all = each * g.G;
     for (int64_t i = blockIdx.x * kBlock + threadIdx.x; i < all; i += gridDim.x * kBlock) {
@@ -592,14 +599,13 @@ __global__ __launch_bounds__(kBlock) void k_wgrad_join(WgradArgs g) {
 }
 
 template <int FN, int FK, int WN, int WK, bool WHOLE, bool PACKED, bool INDEXED>
-hipError_t wgrad_as(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_large) {
+hipError_t wgrad_as(ue_ctx &c, const WgradArgs &g, hipStream_t s) {
     constexpr int BN = WN * FN * 32, BK = WK * FK * 32, kThreads = WN * WK * 64;
     constexpr int kLds = 2 * kRows * (BN + BK) * 2;
     // as many workgroups as fit at once: two waves per SIMD
-    constexpr int kPerCu = FN * FK > 8 ? 1 : 512 / kThreads;
+    constexpr int kPerCu = 512 / kThreads;
+    static_assert(BN == BK && kPerCu == per_cu(BN));
     const int64_t tn = (g.N + BN - 1) / BN, tk = (g.K + BK - 1) / BK, total = tn * tk * g.G * g.parts;
-    too_large = total > 0x7FFFFFFF - kPerCu * c.num_cu;
-    if (too_large) return hipSuccess;
     const auto kernel = k_wgrad<FN, FK, WN, WK, WHOLE, PACKED, INDEXED>;
     if (kLds > 65536) {
         // once per kernel and device (a grant is the device's); one that fails is
@@ -622,25 +628,25 @@ hipError_t wgrad_as(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_larg
 }
 
 template <int FN, int FK, int WN, int WK, bool WHOLE, bool PACKED>
-hipError_t wgrad_rows(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_large) {
-    return g.index ? wgrad_as<FN, FK, WN, WK, WHOLE, PACKED, true>(c, g, s, too_large)
-                   : wgrad_as<FN, FK, WN, WK, WHOLE, PACKED, false>(c, g, s, too_large);
+hipError_t wgrad_rows(ue_ctx &c, const WgradArgs &g, hipStream_t s) {
+    return g.index ? wgrad_as<FN, FK, WN, WK, WHOLE, PACKED, true>(c, g, s)
+                   : wgrad_as<FN, FK, WN, WK, WHOLE, PACKED, false>(c, g, s);
 }
 
 template <int FN, int FK, int WN, int WK>
-hipError_t wgrad_any(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_large) {
+hipError_t wgrad_any(ue_ctx &c, const WgradArgs &g, hipStream_t s) {
     const bool whole = g.vec_dy && g.N % 8 == 0 && (g.x_scale || (g.vec_x && g.K % 8 == 0));
     if (g.x_scale)
-        return whole ? wgrad_rows<FN, FK, WN, WK, true, true>(c, g, s, too_large)
-                     : wgrad_rows<FN, FK, WN, WK, false, true>(c, g, s, too_large);
-    return whole ? wgrad_rows<FN, FK, WN, WK, true, false>(c, g, s, too_large)
-                 : wgrad_rows<FN, FK, WN, WK, false, false>(c, g, s, too_large);
+        return whole ? wgrad_rows<FN, FK, WN, WK, true, true>(c, g, s)
+                     : wgrad_rows<FN, FK, WN, WK, false, true>(c, g, s);
+    return whole ? wgrad_rows<FN, FK, WN, WK, true, false>(c, g, s)
+                 : wgrad_rows<FN, FK, WN, WK, false, false>(c, g, s);
 }
 
-hipError_t wgrad_tiles(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_large) {
+hipError_t wgrad_tiles(ue_ctx &c, const WgradArgs &g, hipStream_t s) {
     if (wgrad_tile(g.N, g.K, static_cast<int64_t>(g.G) * g.parts, c.num_cu) == kTile256)
-        return wgrad_any<4, 2, 2, 4>(c, g, s, too_large);
-    return wgrad_any<2, 2, 2, 2>(c, g, s, too_large);
+        return wgrad_any<4, 2, 2, 4>(c, g, s);
+    return wgrad_any<2, 2, 2, 2>(c, g, s);
 }
 
 }  // namespace
@@ -655,8 +661,15 @@ int wgrad_parts(int M, int N, int K, int G, int num_cu) {
     return parts > 1 ? static_cast<int>(parts) : 1;
 }
 
-hipError_t launch_wgrad(ue_ctx &c, const WgradArgs &a, hipStream_t s, bool &too_large) {
-    too_large = false;
+bool wgrad_too_large(const WgradArgs &g, int num_cu) {
+    if (g.M == 0 || wgrad_tiny(g)) return false;
+    const int64_t mats = static_cast<int64_t>(g.G) * g.parts;
+    const int tile = wgrad_tile(g.N, g.K, mats, num_cu) == kTile256 ? 256 : 128;
+    // (a workgroup's next tile is a launch's workgroups on)
+    return tiles_of(g.N, g.K, tile) * mats > 0x7FFFFFFF - per_cu(tile) * num_cu;
+}
+
+hipError_t launch_wgrad(ue_ctx &c, const WgradArgs &a, hipStream_t s) {
     if (a.N == 0 || a.K == 0 || a.G == 0) return hipSuccess;
     WgradArgs g = a;
     const int64_t rows = static_cast<int64_t>(g.G) * g.N, most = 64 * c.num_cu;
@@ -666,22 +679,19 @@ hipError_t launch_wgrad(ue_ctx &c, const WgradArgs &a, hipStream_t s, bool &too_
         hipLaunchKernelGGL(k_wgrad_zero, per_row, dim3(kBlock), 0, s, g);
         return hipGetLastError();
     }
-    auto tiny = [](int64_t rows, int64_t ld, int cols) {
-        return (rows - 1) * ld + cols < kPiece;
-    };
-    if (tiny(g.M, g.lddy, g.N) || (!g.x_scale && tiny(g.x_rows, g.ldx, g.K))) {
+    if (wgrad_tiny(g)) {
         const int64_t blocks = (rows * g.K + kBlock - 1) / kBlock;
         hipLaunchKernelGGL(k_wgrad_tiny, dim3(static_cast<uint32_t>(blocks < most ? blocks : most)),
                            dim3(kBlock), 0, s, a);
         return hipGetLastError();
     }
-    if (g.parts == 1) return wgrad_tiles(c, g, s, too_large);
+    if (g.parts == 1) return wgrad_tiles(c, g, s);
     g.out = g.part;
     g.ldo = g.K;
     g.out_stride = static_cast<int64_t>(g.N) * g.K;
     g.accumulate = false;
-    const hipError_t he = wgrad_tiles(c, g, s, too_large);
-    if (he != hipSuccess || too_large) return he;
+    const hipError_t he = wgrad_tiles(c, g, s);
+    if (he != hipSuccess) return he;
     tmark(&c, s);
     hipLaunchKernelGGL(k_wgrad_join, per_row, dim3(kBlock), 0, s, a);
     return hipGetLastError();

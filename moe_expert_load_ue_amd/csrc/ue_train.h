@@ -128,8 +128,9 @@ struct WgradArgs {
     float *part;                // [parts][G][N][K] of a split sum, or null
     int parts;
 };
-// too_large: nothing was launched, the launch would have 2^32 threads or more.
-hipError_t launch_wgrad(ue_ctx &c, const WgradArgs &g, hipStream_t s, bool &too_large);
+// More tiles than the workgroups of a launch number with 31 bits.
+bool wgrad_too_large(const WgradArgs &g, int num_cu);
+hipError_t launch_wgrad(ue_ctx &c, const WgradArgs &g, hipStream_t s);
 // Parts each group's rows are split into (1: no workspace).
 int wgrad_parts(int M, int N, int K, int G, int num_cu);
 

@@ -348,13 +348,11 @@ int ue_weight_grad(ue_ctx *ctx, const ue_weight_grad_product *p, void *stream) {
     g.parts = p->workspace ? ue::wgrad_parts(p->M, p->N, p->K, p->groups, ctx->num_cu)
                            : 1;
     g.part = static_cast<float *>(p->workspace);
+    if (ue::wgrad_too_large(g, ctx->num_cu))
+        return fail(ctx, UE_ESHAPE, "ue_weight_grad: more tiles than a launch holds");
     hipStream_t s = static_cast<hipStream_t>(stream);
     tbegin(ctx, s);
-    bool too_large = false;
-    const hipError_t he = ue::launch_wgrad(*ctx, g, s, too_large);
-    if (too_large)
-        return fail(ctx, UE_ESHAPE, "ue_weight_grad: a launch of 2^32 threads or more");
-    return done(ctx, he, s, "k_wgrad launch");
+    return done(ctx, ue::launch_wgrad(*ctx, g, s), s, "k_wgrad launch");
 }
 
 int ue_combine(ue_ctx *ctx, const void *y, int32_t type, int64_t ldy, int32_t rows,
