@@ -701,22 +701,31 @@ def _flat(t, name, dtype, device, numel):
     return t.data_ptr()
 
 
+_device = torch._C._cuda_getDevice \
+    if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
 # Makes an uninitialised tensor on the current device: what generated code of
 # torch.compile calls, 0.8 us on the host where torch.empty takes 1.7, of the 10
-# that a call with three outputs took.
-_guards = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
-_empty = getattr(_guards, "_empty_strided_cuda", None)
+# that a call with three outputs took. It goes past torch's dispatcher, so it is
+# taken only where that has nothing to do: no dispatch or function mode is on, and
+# none but ordinary memory is asked for (deterministic mode fills it).
+def _torch(*path):
+    at = torch._C
+    for name in path:
+        at = getattr(at, name, None)
+    return at
 
 
-def _new(shape, dtype, ctx, stream):
-    """An output tensor whose memory belongs to the stream that writes it. (Every
-    call passes through `_on` before its launch, which refuses it where the
-    current device is not the context's.)"""
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=ctx.device)
-    if _empty is None:
-        return torch.empty(shape, dtype=dtype, device=ctx.device)
+_empty = _torch("_dynamo", "guards", "_empty_strided_cuda")
+_dispatch_modes = _torch("_len_torch_dispatch_stack")
+_function_modes = _torch("_len_torch_function_stack")
+_deterministic = _torch("_get_deterministic_algorithms")
+if None in (_dispatch_modes, _function_modes, _deterministic):
+    _empty = None
+
+
+def _short(shape, dtype):
     dims = len(shape)
     if dims == 2:
         return _empty(shape, (shape[1] or 1, 1), dtype)
@@ -726,8 +735,24 @@ def _new(shape, dtype, ctx, stream):
     return _empty(shape, ((shape[1] or 1) * cols, cols, 1), dtype)
 
 
-_device = torch._C._cuda_getDevice \
-    if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+def _maker(ctx, stream):
+    """What makes a call's output tensors, whose memory belongs to the stream
+    that writes them: f(shape, dtype). (Looking costs 0.25 us, so calls of
+    several outputs look once.)"""
+    if stream is None and _empty is not None and _device() == ctx._index and \
+            not (_dispatch_modes() or _function_modes() or _deterministic()):
+        return _short
+
+    def make(shape, dtype):
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=ctx.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=ctx.device)
+    return make
+
+
+def _new(shape, dtype, ctx, stream):
+    return _maker(ctx, stream)(shape, dtype)
 
 
 def _on(ctx, stream, *tensors):
@@ -753,12 +778,14 @@ def _score(score):
 
 def _choice(ctx, T, ids, weights, stream):
     """ids and weights of T tokens, made if not given: (ids, weights)."""
+    if ids is None or weights is None:
+        make = _maker(ctx, stream)
     if ids is None:
-        ids = _new((T, ctx.k), torch.int32, ctx, stream)
+        ids = make((T, ctx.k), torch.int32)
     else:
         _flat(ids, "ids", torch.int32, ctx.device, T * ctx.k)
     if weights is None:
-        weights = _new((T, ctx.k), torch.float32, ctx, stream)
+        weights = make((T, ctx.k), torch.float32)
     else:
         _flat(weights, "weights", torch.float32, ctx.device, T * ctx.k)
     return ids, weights
@@ -1012,16 +1039,18 @@ def ue_balance(ctx: Context, logits, ids, offsets=None, score="softmax",
     i = _flat(ids, "ids", torch.int32, dev, T * ctx.k)
     po, n = _sequences(ctx, offsets)
     score = _score(score)
+    if loss is None or counts is None or prob is None:
+        make = _maker(ctx, stream)
     if loss is None:
-        loss = _new((n,), torch.float32, ctx, stream)
+        loss = make((n,), torch.float32)
     else:
         _flat(loss, "loss", torch.float32, dev, n)
     if counts is None:
-        counts = _new((n, ctx.E), torch.int32, ctx, stream)
+        counts = make((n, ctx.E), torch.int32)
     else:
         _flat(counts, "counts", torch.int32, dev, n * ctx.E)
     if prob is None:
-        prob = _new((n, ctx.E), torch.float32, ctx, stream)
+        prob = make((n, ctx.E), torch.float32)
     else:
         _flat(prob, "prob", torch.float32, dev, n * ctx.E)
     lib = library()
@@ -1081,10 +1110,10 @@ def ue_balance_backward(ctx: Context, logits, counts, dloss, offsets=None,
     return dlogits
 
 
-def _packed_new(ctx, M, columns, stream):
+def _packed_new(make, M, columns):
     """Packed rows of whole blocks: (q int8 [M, P], scale uint8 [M, P / 32])."""
-    return (_new((M, columns), torch.int8, ctx, stream),
-            _new((M, columns // PACK_BLOCK), torch.uint8, ctx, stream))
+    return (make((M, columns), torch.int8),
+            make((M, columns // PACK_BLOCK), torch.uint8))
 
 
 def _packed(ctx, q, scale, columns=None):
@@ -1120,7 +1149,7 @@ def ue_pack_rows(ctx: Context, x, q=None, scale=None, stream=None):
     if (q is None) != (scale is None):
         raise ValueError("q and scale belong together")
     if q is None:
-        q, scale = _packed_new(ctx, M, whole, stream)
+        q, scale = _packed_new(_maker(ctx, stream), M, whole)
         ldq, lds, pq, ps = whole, whole // PACK_BLOCK, q.data_ptr(), scale.data_ptr()
         if whole != K:
             q = q[:, :K]
@@ -1179,8 +1208,9 @@ def ue_gated(ctx: Context, gu, h=None, q=None, scale=None, keep=True,
     if two % 2:
         raise ValueError("gu must hold as many up as gate columns")
     I = two // 2
+    make = _maker(ctx, stream) if h is None or (keep and q is None) else None
     if h is None:
-        h, ldh = _new((M, I), gu.dtype, ctx, stream), I
+        h, ldh = make((M, I), gu.dtype), I
     else:
         ldh = _out(h, "h", ctx, gu.dtype, M, I)
     if (q is None) != (scale is None) or (q is not None and not keep):
@@ -1190,7 +1220,7 @@ def ue_gated(ctx: Context, gu, h=None, q=None, scale=None, keep=True,
     if keep and q is None:
         ldq = 2 * _half(I)
         lds = ldq // PACK_BLOCK
-        q, scale = _packed_new(ctx, M, ldq, stream)
+        q, scale = _packed_new(make, M, ldq)
         pq, ps = q.data_ptr(), scale.data_ptr()
     elif keep:
         m, _, ldq, pq, lds, ps = _packed(ctx, q, scale, 2 * _half(I))
@@ -1213,15 +1243,16 @@ def ue_gated_backward(ctx: Context, dh, q, scale, dgu=None, h=None,
     m, _, ldq, pq, lds, ps = _packed(ctx, q, scale, 2 * _half(I))
     if m != M:
         raise ValueError(f"q must have {M} rows")
+    make = _maker(ctx, stream) if dgu is None or (with_h and h is None) else None
     if dgu is None:
-        dgu, lddgu = _new((M, 2 * I), dh.dtype, ctx, stream), 2 * I
+        dgu, lddgu = make((M, 2 * I), dh.dtype), 2 * I
     else:
         lddgu = _out(dgu, "dgu", ctx, dh.dtype, M, 2 * I)
     ldh = I
     if h is not None:
         ldh = _out(h, "h", ctx, dh.dtype, M, I)
     elif with_h:
-        h = _new((M, I), dh.dtype, ctx, stream)
+        h = make((M, I), dh.dtype)
     rc = library().ue_gated_backward(
         ctx._h, pq, ldq, ps, lds, dh.data_ptr(), _TYPES[dh.dtype], lddh, M, I,
         dgu.data_ptr(), lddgu, None if h is None else h.data_ptr(), ldh,
@@ -1344,11 +1375,13 @@ def ue_combine_backward(ctx: Context, dout, inv_perm, weights=None, y=None,
     if y is None and dweights is not None:
         raise ValueError("dweights needs y")
     rows, ldy, py = T * ctx.k, 0, None
+    if (y is not None and dweights is None) or (dy is None and with_dy):
+        make = _maker(ctx, stream)
     if y is not None:
         rows, _, ldy = _rows(y, "y", dev, (dout.dtype,), H)
         py = y.data_ptr()
         if dweights is None:
-            dweights = _new((T, ctx.k), torch.float32, ctx, stream)
+            dweights = make((T, ctx.k), torch.float32)
         else:
             _flat(dweights, "dweights", torch.float32, dev, T * ctx.k)
     lib, lddy = library(), H
@@ -1360,11 +1393,11 @@ def ue_combine_backward(ctx: Context, dout, inv_perm, weights=None, y=None,
         elif n != rows:
             raise ValueError(f"dy must have {rows} rows")
     elif with_dy:
-        dy = _new((rows, H), dout.dtype, ctx, stream)
+        dy = make((rows, H), dout.dtype)
         call, ws = lib.ue_combine_backward_all, (None,)
         need = lib.ue_combine_backward_workspace(ctx._h, T, rows)
         if need:
-            workspace = _new((need,), torch.uint8, ctx, stream)
+            workspace = make((need,), torch.uint8)
             ws = (workspace.data_ptr(),)
     rc = call(
         ctx._h, dout.data_ptr(), _TYPES[dout.dtype], lddo, pi, pw, py, ldy,
