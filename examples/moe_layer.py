@@ -26,16 +26,6 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import moe_expert_load_ue_amd as ue  # noqa: E402
 
 
-class Saved(dict):
-    """What the passes between need; the experts' rows by token and place on
-    request."""
-
-    def __missing__(self, key):
-        if key != "rows":
-            raise KeyError(key)
-        return self["y"][self["inv"].long()]                   # [T, k, H]
-
-
 class Layer:
     """Router and int8 experts of one layer on one device, with E/R experts
     per simulated rank and S spare slots each."""
@@ -82,15 +72,18 @@ class Layer:
         y = ue.ue_matmul_i8(ctx, q, qs, self.down, self.down_scale, **slots)
         inv = r["inv_perm"][0].view(-1, k)
         out = ue.ue_combine(ctx, y, inv, weights)
-        return out, Saved(logits=logits, ids=ids, weights=weights, y=y, inv=inv,
-                          plan=plan, counts=r["counts"])
+        return out, dict(logits=logits, ids=ids, weights=weights, y=y, inv=inv,
+                         rows=y[inv.long()], plan=plan, counts=r["counts"])
 
     def router_gradient(self, x, saved, dout):
         """Gradient of the router's matrix from that of the output (the part
-        that flows through the routing weights)."""
-        y = saved["y"] if dout.dtype == saved["y"].dtype else saved["y"].to(dout.dtype)
-        _, dw = ue.ue_combine_backward(self.ctx, dout, saved["inv"], saved["weights"],
-                                       y=y, with_dy=False)
+        that flows through the routing weights). dout: of any float type and
+        strides."""
+        y = saved["y"]
+        if dout.dtype != y.dtype:
+            y, dout = y.float(), dout.float()
+        _, dw = ue.ue_combine_backward(self.ctx, dout.contiguous(), saved["inv"],
+                                       saved["weights"], y=y, with_dy=False)
         dlogits = ue.ue_gate_backward(self.ctx, saved["logits"], saved["ids"], dw,
                                       **self.rule)
         return dlogits.t() @ x.float()
