@@ -18,8 +18,11 @@
 // shares in order.
 //
 // Bound: 65536 tokens of 256 experts, fp32, sigmoid: HBM going back (23 us, 134 MB,
-// 5.8 TB/s); forward (26 us, 69 MB) instruction issue (20 per logit) and the start
-// and end of workgroups, 4.5 us of it the launch that adds the partial sums. A few
+// 5.8 TB/s); forward (25 us, 69 MB, of which 4.5 are the launch that adds the partial
+// sums) about half instruction issue (20 per logit, 5.2 M a wave's: 8-9 us of the 21,
+// 11 with the quarter-rate exponentials and reciprocals) and half latency: eight
+// tokens of a wave one after another with one ahead, the ids' counts ahead of the
+// first, a workgroup's start and end; which of them most has not been measured. A few
 // thousand tokens are bound by the latency of the launches (3001 tokens of 60
 // experts 10.6 us, back 7), a few hundred take one launch, which the host's calls
 // outlast.

@@ -11,8 +11,9 @@
 //
 // Bound: HBM. 32768 rows of 2048, bf16: gated activation, keeping gate and up, 87
 // us (541 MB, 6.2 TB/s), its backward pass with the activation again 107 us (675
-// MB, 6.3 TB/s); 8192 rows of 7168 packed in 19 us (178 MB, 9 TB/s, half of it
-// found in the cache). A quad of lanes takes one block and no loop: what is in
+// MB, 6.3 TB/s), one after the other 194; in short runs with pauses 113 and 111 at
+// the median. 4096 rows of 7168 packed in 17-19 us (89 MB), calls for 8192 29 us (178
+// MB, 6.1 TB/s) and back to bf16 27, to fp32 87 (294 MB, 3.4 TB/s). A quad of lanes takes one block and no loop: what is in
 // flight is other waves'. 13358 rows of 302, fp32, both ways 27 us (element by
 // element, as rows that are no multiple of 16 bytes were read once, 68; past the
 // caches what is read 35).

@@ -13,14 +13,17 @@
 // put down nor what is read back transposed meets a bank twice (no conflicts
 // counted).
 //
-// Bound: the clock under load, taken to be the power limit's. One group of 8192 x
-// 4096 x 7168, packed x, takes 465-475 us (1.02 PFLOP/s; bf16 x 451-456) at 1.97
-// GHz of 2.4, with the matrix units busy 46% of the cycles: a stage takes 3900
-// cycles, of which the matrix instructions need 2048 and LDS 1290. Changes that
-// took waiting away left its time alone: loads used a whole stage after they are
-// issued in place of half of one (465-473 us, bf16 x 458-470), workgroups started
-// apart from each other (466-483). Without its loads it takes 388 us, without what
-// it puts down in LDS either 312. Four waves of 128 x 128 spilled (3.7 ms); tiles
+// Bound: not the products alone. One group of 8192 x 4096 x 7168, packed x, takes
+// 465-475 us (1.02 PFLOP/s; bf16 x 451-456) at 1.97 GHz of 2.4, with the matrix units
+// busy 46% of the cycles (five groups 51%): a stage takes 3900 cycles, of which the
+// matrix instructions need 2048 and LDS 1290. Without its loads it takes 388 us,
+// without what it puts down in LDS either 312: bringing rows to LDS through
+// registers is a third of the time, and 120 of a wave's 215 vector instructions of a
+// stage are addresses. Changes that took waiting away left the time alone: loads
+// used a whole stage after they are issued in place of half of one (465-473 us, bf16
+// x 458-470), workgroups started apart from each other (466-483). The clock falls
+// under load, but power has not been measured, and the library's product of the same
+// operand layout reaches 1180 TFLOP/s on the device. Four waves of 128 x 128 spilled (3.7 ms); tiles
 // of 256 x 128 on four waves, two workgroups per CU, 575 us against 483; rows
 // straight to LDS wait for each other, since the compiler puts a wait for all of
 // them ahead of every LDS read.
@@ -83,10 +86,10 @@ constexpr int kPiece = 8;
 // stage's products run, the next one's rows go to LDS, those of the one after
 // are on their way to registers, and the row numbers of the third too, whichever
 // tiles they are of. So the first stages of a tile are there when the results of
-// the one before have been stored. (72 groups of 2048x4096 with 455 rows each
-// take 752-778 us, in one run of calls on some devices 870; a workgroup per tile,
-// with nothing under its first loads and its stores, took 870 where this takes
-// 794. The stores alone take 500.)
+// the one before have been stored. (72 groups of 2048x4096 with 455 rows each on
+// average take 780 us where they are even and 825-860 where their rows differ as
+// routing's do; 752 at the least. A workgroup per tile, with nothing under its first
+// loads and its stores, took 870 where this took 794. The stores alone take 500.)
 //
 // A stage is four steps of 16 rows. A step's operands are read from LDS during
 // the step before, and the next stage is put down during the first three. So by
@@ -526,7 +529,10 @@ __global__ __launch_bounds__(WN *WK * 64, FN * FK > 8 ? 1 : 2) void k_wgrad(
 //     4 of 2048x1024x2048      87     67   (128)
 //     8 of  600x 480x 352      30     23   (32)
 //          32768x 128x 256      50     41   (in parts)
-// So the large ones when they make work for three CUs of four.
+// So the large ones when they make work for three CUs of four. Added to what out
+// holds (written), even groups: 5 of 1638x4096x7168 607 us (518), 72 of 455x2048x4096
+// 1169 (780), 64 of 256x1024x2048 241 (125): one more read of out, with nothing
+// under its loads.
 enum WgradTile { kTile256, kTile128 };
 
 int64_t tiles_of(int N, int K, int b) {

@@ -166,9 +166,10 @@ __device__ __forceinline__ uint16_t narrow<uint16_t>(float v) { return f32_to_bf
 
 // N elements, or those of them before `n`, at p, in loads and stores of up to 16
 // bytes whatever p's alignment (the device takes any). ONCE: past the caches, as
-// results go always (gated activation of 32768 rows of 2048 with its backward pass
-// 258 us with results through the caches, 198 past them), and what a call reads
-// where it is large (`with_rows`).
+// results go (gated activation of 32768 rows of 2048 with its backward pass 258 us
+// with results through the caches, 198 past them; not the packed rows that
+// ue_pack_rows makes, which a product reads next), and what a call reads where it is
+// large (`with_rows`).
 template <int BYTES>
 struct Words {
     typedef uint32_t type __attribute__((ext_vector_type(BYTES / 4), aligned(2)));
